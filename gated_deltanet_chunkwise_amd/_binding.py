@@ -17,7 +17,10 @@ GDN_F16 = 2  # KDA gate only
 SYMBOLS = ("gdn_fwd_workspace_size", "gdn_fwd_workspace_layout", "gdn_fwd_check",
            "gdn_fwd", "gdn_fwd_timed", "gdn_fwd_stages", "gdn_decode", "gdn_kda_gate",
            "gdn_bwd_workspace_size", "gdn_bwd", "gdn_bwd_timed", "gdn_status_string",
-           "gdn_fwd_fuses_output", "gdn_fwd_noalloc", "gdn_fwd_seg_chunks")
+           "gdn_fwd_fuses_output", "gdn_fwd_noalloc", "gdn_fwd_seg_chunks",
+           "gdn_conv_fwd", "gdn_conv_decode", "gdn_conv_bwd_workspace_size", "gdn_conv_bwd",
+           "gdn_scan_fwd_workspace_size", "gdn_scan_fwd", "gdn_scan_decode",
+           "gdn_scan_bwd_workspace_size", "gdn_scan_bwd", "gdn_pack8", "gdn_unpack8")
 GDN_SEG_AUTO = -1  # include/gdn.h: seg_chunks chosen per call
 GDN_SCRATCH_BYTES = 64 << 20  # include/gdn.h: the static workspace of gdn_fwd_noalloc
 NUM_STAGES = 4
@@ -110,6 +113,8 @@ def _declare(lib):
     lib.gdn_fwd_noalloc.argtypes = [P] + [vp] * 11 + [fp]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_status_string.argtypes = [ctypes.c_int]
+    from . import _layers
+    _layers.declare(lib)
     return lib
 
 
@@ -575,21 +580,27 @@ def _gated_delta_rule_fn():
     global _GATED_DELTA_RULE
     if _GATED_DELTA_RULE is None:
         torch = _torch()
+        from . import _layers
 
         class GatedDeltaRule(torch.autograd.Function):
             @staticmethod
             def forward(ctx, q, k, v, g_raw, beta, A_log, dt_bias, cu_seqlens, initial_state,
-                        scale):
+                        scale, bits):
                 o, fin = fwd(q, k, v, g_raw, beta, A_log, dt_bias, cu_seqlens, initial_state,
                              scale=scale)
-                ctx.save_for_backward(q, k, v, g_raw, beta, A_log, dt_bias, cu_seqlens,
-                                      initial_state)
-                ctx.scale = scale
+                pairs = [_layers.keep(t, bits)[0] for t in (q, k, v)]
+                ctx.save_for_backward(*(t for pair in pairs for t in pair), g_raw, beta, A_log,
+                                      dt_bias, cu_seqlens, initial_state)
+                ctx.scale, ctx.dtype = scale, q.dtype
                 return o, fin
 
             @staticmethod
             def backward(ctx, d_o, d_fin):
-                q, k, v, g_raw, beta, A_log, dt_bias, cu_seqlens, h0 = ctx.saved_tensors
+                (qd, qs, kd, ks, vd, vs, g_raw, beta, A_log, dt_bias, cu_seqlens,
+                 h0) = ctx.saved_tensors
+                q, k, v = (t if sc is None else
+                           _layers.unpack8(_layers.Packed8(t, sc, ctx.dtype))
+                           for t, sc in ((qd, qs), (kd, ks), (vd, vs)))
                 B, T = q.shape[0], q.shape[1]
                 HV, V = v.shape[2], v.shape[3]
                 # torch may hand over expanded or strided gradients; the library
@@ -603,20 +614,24 @@ def _gated_delta_rule_fn():
                          cu_seqlens=cu_seqlens, initial_state=h0, scale=ctx.scale)
                 return (gr["dq"], gr["dk"], gr["dv"], gr["dg_raw"], gr["dbeta"], gr["dA_log"],
                         gr["ddt_bias"] if dt_bias is not None else None, None,
-                        gr["dh0"] if h0 is not None else None, None)
+                        gr["dh0"] if h0 is not None else None, None, None)
 
         _GATED_DELTA_RULE = GatedDeltaRule
     return _GATED_DELTA_RULE
 
 
 def gated_delta_rule(q, k, v, g_raw, beta, A_log, dt_bias=None, cu_seqlens=None,
-                     initial_state=None, scale=1.0):
+                     initial_state=None, scale=1.0, checkpoint_bits=None):
     """fwd() as a differentiable torch op: returns (o, final_state) like fwd();
     their gradients run gdn_bwd (which recomputes the forward's intermediates)
     and reach q, k, v, g_raw, beta, A_log, dt_bias and initial_state.  Inputs
-    as for fwd(): contiguous GPU tensors of the documented shapes and dtypes."""
+    as for fwd(): contiguous GPU tensors of the documented shapes and dtypes.
+    checkpoint_bits=8 keeps q, k and v for the backward pass as 8-bit checkpoints (pack8):
+    the gradients are then those at the values the checkpoints stand for."""
+    from ._layers import check_bits
+    check_bits(checkpoint_bits)
     return _gated_delta_rule_fn().apply(q, k, v, g_raw, beta, A_log, dt_bias, cu_seqlens,
-                                        initial_state, scale)
+                                        initial_state, scale, checkpoint_bits)
 
 
 def bwd(q, k, v, g_raw, beta, A_log, dt_bias, d_o, d_final_state=None, cu_seqlens=None,

@@ -2,6 +2,7 @@
 
 Usage: python -m gated_deltanet_chunkwise_amd.build   (or build() from Python)
 """
+import concurrent.futures
 import os
 import subprocess
 import sys
@@ -11,8 +12,10 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgdn.so")
-SOURCES = [os.path.join(CSRC, "gdn_api.hip")]
-HEADERS = [os.path.join(CSRC, f) for f in ("gdn_common.h", "gdn_kernels.h", "gdn_kda.h", "gdn_decode.h", "gdn_bwd.h")] + [
+SOURCES = [os.path.join(CSRC, f) for f in ("gdn_api.hip", "gdn_conv_api.hip", "gdn_scan_api.hip", "gdn_scan_bwd_api.hip")]
+HEADERS = [os.path.join(CSRC, f) for f in
+           ("gdn_common.h", "gdn_kernels.h", "gdn_kda.h", "gdn_decode.h", "gdn_bwd.h", "gdn_layer.h", "gdn_host.h",
+            "gdn_conv.h", "gdn_pack8.h", "gdn_scan.h", "gdn_scan_host.h", "gdn_scan_bwd.h")] + [
     os.path.join(INCLUDE, "gdn.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -21,7 +24,6 @@ FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-Wall",
     # Keep the compiler from forming packed fp32 VALU ops (v_pk_*_f32).
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -33,10 +35,7 @@ FLAGS = [
 ]
 
 
-def build(out=LIB, extra=(), verbose=False):
-    """Compile every HIP source into `out`.  Always recompiles."""
-    tmp = out + ".tmp%d" % os.getpid()
-    cmd = [HIPCC, *FLAGS, *extra, "-o", tmp, *SOURCES]
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -47,7 +46,24 @@ def build(out=LIB, extra=(), verbose=False):
         raise RuntimeError("hipcc failed (%d):\n%s" % (res.returncode, err))
     if err.strip() and verbose:
         print(err, file=sys.stderr)
-    os.replace(tmp, out)
+
+
+def build(out=LIB, extra=(), verbose=False):
+    """Compile every HIP source, side by side, and link them into `out`.  Always recompiles."""
+    tmp = out + ".tmp%d" % os.getpid()
+    objs = [tmp + ".%s.o" % os.path.splitext(os.path.basename(s))[0] for s in SOURCES]
+    try:
+        with concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as pool:
+            jobs = [pool.submit(_run, [HIPCC, *FLAGS, *extra, "-c", "-o", o, s], verbose)
+                    for s, o in zip(SOURCES, objs)]
+            for j in jobs:
+                j.result()
+        _run([HIPCC, FLAGS[0], *extra, "-shared", "-o", tmp, *objs], verbose)
+        os.replace(tmp, out)
+    finally:
+        for f in objs:
+            if os.path.exists(f):
+                os.remove(f)
     return out
 
 

@@ -1,0 +1,341 @@
+// gdn_conv_api.hip -- entry points of the short causal convolution and the 8-bit
+// activation checkpoints: validation and launches.  See include/gdn.h.
+#include "gdn_conv.h"
+#include "gdn_host.h"
+#include "gdn_pack8.h"
+
+namespace {
+
+struct ConvPlan {
+  gdn::ConvGeo geo;
+  int64_t ld;     // elements between x's rows
+  size_t esz;
+  int vec;        // channels per lane: 16 bytes' worth, or 1
+  int cl;         // backward: neighbouring vectors per workgroup
+  int64_t rows;   // backward: rows of partial sums
+  size_t total;   // backward workspace bytes
+};
+
+int pow2_at_least(int v) {
+  int p = 1;
+  while (p < v) p <<= 1;
+  return p;
+}
+
+// Sizes only.
+gdn_status_t conv_sizes(const gdn_conv_params_t* p, bool packed, ConvPlan* out) {
+  if (!p) return GDN_ERR_NULL;
+  if (p->dtype != GDN_F32 && p->dtype != GDN_BF16) return GDN_ERR_DTYPE;
+  if (p->C <= 0 || p->W <= 0 || (p->activation != 0 && p->activation != 1)) return GDN_ERR_SHAPE;
+  gdn_status_t st = check_batch(p->B, p->T, p->num_seqs, packed);
+  if (st != GDN_OK) return st;
+  if (p->W < 2 || p->W > 4) return GDN_ERR_UNSUPPORTED;
+  if (p->x_stride != 0 && p->x_stride < p->C) return GDN_ERR_SHAPE;
+  ConvPlan pl{};
+  pl.ld = p->x_stride ? p->x_stride : p->C;
+  pl.esz = p->dtype == GDN_BF16 ? 2 : 4;
+  gdn::ConvGeo& g = pl.geo;
+  g.B = p->B; g.T = p->T; g.C = p->C;
+  g.N = packed ? p->num_seqs : p->B;
+  g.silu = p->activation;
+  g.nblk = (int)ceil_div(p->C, gdn::kPackBlock);
+  if ((int64_t)g.N * 3 * p->C > ((int64_t)1 << 38)) return GDN_ERR_UNSUPPORTED;  // grid range
+  // 16-byte vectors if the channels divide into them; the smaller tile of the two
+  // paths below bounds the workspace, so it does not depend on pointers
+  const int wide = (int)(16 / pl.esz);
+  pl.vec = p->C % wide == 0 ? wide : 1;
+  *out = pl;
+  return GDN_OK;
+}
+
+// The backward pass's tiles: each lane's tile as long as leaves about 8 waves per
+// CU (256 CUs are taken for granted, so that the workspace is the same on every
+// device), 16 tokens at least (its W-1 tokens of overlap are then at most a fifth)
+// and 256 at most.
+void conv_bwd_tiles(const gdn_conv_params_t* p, bool packed, int vec, ConvPlan* pl) {
+  gdn::ConvGeo& g = pl->geo;
+  pl->vec = vec;
+  g.cvn = p->C / vec;
+  const int64_t ntok = (int64_t)p->B * p->T;
+  int64_t tile = ntok * g.cvn / (256 * 8 * 64);
+  tile = std::min<int64_t>(std::max<int64_t>(tile, 16), 256);
+  g.tile = (int)tile;
+  g.ntiles = (int)std::max<int64_t>(ceil_div(p->T, tile), 1);
+  pl->cl = std::min(64, pow2_at_least(g.cvn));
+  const int64_t tiles = (int64_t)g.ntiles * (packed ? 1 : p->B);
+  pl->rows = ceil_div(tiles, 256 / pl->cl);
+  pl->total = align_up((size_t)pl->rows * (p->W + 1) * p->C * 4);
+}
+
+size_t conv_ws(const gdn_conv_params_t* p, bool packed, ConvPlan pl) {
+  conv_bwd_tiles(p, packed, pl.vec, &pl);
+  size_t total = pl.total;
+  conv_bwd_tiles(p, packed, 1, &pl);  // what misaligned pointers would take
+  return std::max(total, pl.total);
+}
+
+bool vec_ok(const ConvPlan& pl, std::initializer_list<const void*> rows) {
+  if (pl.vec == 1 || pl.ld % pl.vec) return false;
+  for (const void* q : rows)
+    if (!aligned(q, 16)) return false;
+  return true;
+}
+
+template <typename E, int W, int VEC>
+gdn_status_t conv_fwd_run(ConvPlan pl, const void* x, const float* w, const float* b,
+                          const void* h0, void* y, void* fin, hipStream_t s) {
+  gdn::ConvGeo& g = pl.geo;
+  g.cvn = g.C / VEC;
+  // Tokens per lane: as long as leaves about 8 waves per CU, at least one group of
+  // loads, at most 64.
+  const int64_t ntok = (int64_t)g.B * g.T;
+  const int64_t lanes = (int64_t)device_cus() * 8 * 64;
+  const int64_t tile = ntok * g.cvn / std::max<int64_t>(lanes, 1) / gdn::kConvGroup * gdn::kConvGroup;
+  g.tile = (int)std::min<int64_t>(std::max<int64_t>(tile, gdn::kConvGroup), 64);
+  g.ntiles = (int)ceil_div(g.T, g.tile);
+  const int64_t units = (int64_t)g.ntiles * (g.cu ? 1 : g.B) + (fin ? (int64_t)g.N * (W - 1) : 0);
+  const int64_t blocks = ceil_div(units * g.cvn, 256);
+  if (blocks == 0) return GDN_OK;
+  if (blocks > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  return launch(gdn::gdn_conv_fwd_kernel<E, W, VEC>, dim3((unsigned)blocks), dim3(256), s, g,
+                gdn::Src{x, nullptr, pl.ld}, w, b, static_cast<const E*>(h0), static_cast<E*>(y),
+                static_cast<E*>(fin)) == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+template <typename E, int W, int VEC>
+gdn_status_t conv_decode_run(ConvPlan pl, const void* x, const float* w, const float* b,
+                             const void* in, void* out, void* y, hipStream_t s) {
+  gdn::ConvGeo& g = pl.geo;
+  g.cvn = g.C / VEC;
+  const int64_t blocks = ceil_div((int64_t)g.B * g.cvn, 256);
+  if (blocks > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  return launch(gdn::gdn_conv_decode_kernel<E, W, VEC>, dim3((unsigned)blocks), dim3(256), s, g,
+                gdn::Src{x, nullptr, pl.ld}, w, b, static_cast<const E*>(in), static_cast<E*>(out),
+                static_cast<E*>(y)) == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+struct ConvBwdArgs {
+  const void* x;
+  const uint8_t* scales;
+  const float *w, *b;
+  const void *h0, *dy, *dfin;
+  void* dx;
+  float *dw, *db;
+  void* dh0;
+};
+
+template <typename E, int W, int VEC>
+gdn_status_t conv_bwd_run(const ConvPlan& pl, const ConvBwdArgs& a, void* ws, hipStream_t s) {
+  const gdn::ConvGeo& g = pl.geo;
+  const gdn::Src x{a.x, a.scales, pl.ld};
+  float* partial = static_cast<float*>(ws);
+  hipError_t err = hipSuccess;
+  auto ok = [&](hipError_t e) {
+    if (e != hipSuccess && err == hipSuccess) err = e;
+  };
+  const bool tokens = (int64_t)g.B * g.T > 0;
+  const int cgroups = (int)ceil_div(g.cvn, pl.cl);
+  if (tokens)
+    ok(launch(gdn::gdn_conv_bwd_kernel<E, W, VEC>, dim3((unsigned)(pl.rows * cgroups)), dim3(256), s, g, x, a.w, a.b, static_cast<const E*>(a.h0), static_cast<const E*>(a.dy),
+              static_cast<const E*>(a.dfin), static_cast<E*>(a.dx), partial, pl.cl, cgroups));
+  if (a.dh0 && g.N > 0)
+    ok(launch(gdn::gdn_conv_bwd_state_kernel<E, W, VEC>, dim3((unsigned)ceil_div((int64_t)g.N * g.cvn, 256)),
+              dim3(256), s, g, x, a.w, a.b, static_cast<const E*>(a.h0), static_cast<const E*>(a.dy),
+              static_cast<const E*>(a.dfin), static_cast<E*>(a.dh0)));
+  ok(launch(gdn::gdn_conv_bwd_sums_kernel<W>, dim3((unsigned)ceil_div((int64_t)(W + 1) * g.C, 64)),
+            dim3(256), s, partial, tokens ? (int)pl.rows : 0, g.C, a.dw, a.db));
+  return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+// F<E, W, VEC>::run for the plan's type, width and vector length.
+template <template <typename, int, int> class F, typename... A>
+gdn_status_t conv_dispatch(const gdn_conv_params_t* p, bool vec, A&&... a) {
+  auto width = [&](auto e, auto v) {
+    using E = decltype(e);
+    constexpr int V = decltype(v)::value;
+    if (p->W == 2) return F<E, 2, V>::run(a...);
+    if (p->W == 3) return F<E, 3, V>::run(a...);
+    return F<E, 4, V>::run(a...);
+  };
+  using One = std::integral_constant<int, 1>;
+  if (p->dtype == GDN_BF16)
+    return vec ? width(gdn::bf16{}, std::integral_constant<int, 8>{}) : width(gdn::bf16{}, One{});
+  return vec ? width(0.f, std::integral_constant<int, 4>{}) : width(0.f, One{});
+}
+template <typename E, int W, int VEC> struct FwdRun {
+  template <typename... A> static gdn_status_t run(A&&... a) { return conv_fwd_run<E, W, VEC>(a...); }
+};
+template <typename E, int W, int VEC> struct DecodeRun {
+  template <typename... A> static gdn_status_t run(A&&... a) { return conv_decode_run<E, W, VEC>(a...); }
+};
+template <typename E, int W, int VEC> struct BwdRun {
+  template <typename... A> static gdn_status_t run(A&&... a) { return conv_bwd_run<E, W, VEC>(a...); }
+};
+
+gdn_status_t pack_sizes(int dt, int64_t rows, int32_t C) {
+  if (dt != GDN_F32 && dt != GDN_BF16) return GDN_ERR_DTYPE;
+  if (rows < 0 || C < 1) return GDN_ERR_SHAPE;
+  if (rows > INT64_MAX / 8 / C) return GDN_ERR_SHAPE;
+  return GDN_OK;
+}
+
+template <typename E>
+gdn_status_t pack_run(const void* xv, int64_t ld, int64_t rows, int C, int8_t* codes,
+                      uint8_t* scales, hipStream_t s) {
+  const E* x = static_cast<const E*>(xv);
+  const int nblk = (int)ceil_div(C, gdn::kPackBlock);
+  const int64_t cap = (int64_t)device_cus() * 16;  // workgroups beyond that loop
+  const bool vec = C % 8 == 0 && ld % (16 / (int)sizeof(E)) == 0 && aligned(x, 16) && aligned(codes, 8);
+  if (!vec) {
+    const int64_t blocks = std::min(ceil_div(rows * nblk, 8), cap);
+    return launch(gdn::gdn_pack8_scalar_kernel<E>, dim3((unsigned)blocks), dim3(256), s, x, ld, codes,
+                  scales, rows, C, nblk) == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+  }
+  const int64_t vpr = (int64_t)nblk * 4;
+  const int64_t most = std::max<int64_t>(((int64_t)1 << 30) / vpr, 1);  // rows per launch
+  for (int64_t r = 0; r < rows; r += most) {
+    const int64_t n = std::min(most, rows - r);
+    const int64_t blocks = std::min(ceil_div(n * vpr, 256 * gdn::kPackUnroll), cap);
+    if (launch(gdn::gdn_pack8_vec_kernel<E>, dim3((unsigned)blocks), dim3(256), s, x + r * ld, ld,
+               codes + r * C, scales + r * nblk, (uint32_t)n, C, (uint32_t)vpr) != hipSuccess)
+      return GDN_ERR_LAUNCH;
+  }
+  return GDN_OK;
+}
+
+template <typename E>
+gdn_status_t unpack_run(const int8_t* codes, const uint8_t* scales, int64_t rows, int C, void* yv,
+                        hipStream_t s) {
+  E* y = static_cast<E*>(yv);
+  const int nblk = (int)ceil_div(C, gdn::kPackBlock);
+  const int64_t cap = (int64_t)device_cus() * 16;
+  if (C % 8 != 0 || !aligned(y, 16) || !aligned(codes, 8)) {
+    const int64_t blocks = std::min(ceil_div(rows * C, 256), 2 * cap);
+    return launch(gdn::gdn_unpack8_scalar_kernel<E>, dim3((unsigned)blocks), dim3(256), s, codes, scales,
+                  y, rows * C, C, nblk) == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+  }
+  const int64_t vpr = C / 8, most = std::max<int64_t>(((int64_t)1 << 30) / vpr, 1);
+  for (int64_t r = 0; r < rows; r += most) {
+    const int64_t n = std::min(most, rows - r);
+    const int64_t blocks = std::min(ceil_div(n * vpr, 256 * gdn::kPackUnroll), cap);
+    if (launch(gdn::gdn_unpack8_vec_kernel<E>, dim3((unsigned)blocks), dim3(256), s, codes + r * C,
+               scales + r * nblk, y + r * C, (uint32_t)n, (uint32_t)vpr, (uint32_t)nblk) != hipSuccess)
+      return GDN_ERR_LAUNCH;
+  }
+  return GDN_OK;
+}
+
+int enum_int(const gdn_dtype_t& e) {  // any int may stand in an enum argument (see gdn_api.hip)
+  int v;
+  __builtin_memcpy(&v, &e, sizeof v);
+  return v;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status_t gdn_conv_fwd(const gdn_conv_params_t* p, const void* x, const float* weight,
+                          const float* bias, const int64_t* cu_seqlens, const void* initial_state,
+                          void* y, void* final_state, void* stream) {
+  ConvPlan pl;
+  gdn_status_t st = conv_sizes(p, cu_seqlens != nullptr, &pl);
+  if (st != GDN_OK) return st;
+  const bool tokens = (int64_t)p->B * p->T > 0;
+  if (tokens && (!x || !weight || !y)) return GDN_ERR_NULL;
+  if (!aligned(x, pl.esz) || !aligned(y, pl.esz) || !aligned(initial_state, pl.esz) ||
+      !aligned(final_state, pl.esz) || !aligned(weight, 4) || !aligned(bias, 4) || !aligned(cu_seqlens, 8))
+    return GDN_ERR_ALIGN;
+  pl.geo.cu = cu_seqlens;
+  return conv_dispatch<FwdRun>(p, vec_ok(pl, {x, y, initial_state, final_state}), pl, x, weight, bias,
+                               initial_state, y, final_state, static_cast<hipStream_t>(stream));
+}
+
+gdn_status_t gdn_conv_decode(const gdn_conv_params_t* p, const void* x, const float* weight,
+                             const float* bias, const void* state, void* new_state, void* y,
+                             void* stream) {
+  ConvPlan pl;
+  gdn_status_t st = conv_sizes(p, false, &pl);
+  if (st != GDN_OK) return st;
+  if (p->num_seqs != 0) return GDN_ERR_SHAPE;
+  if (p->B > 0 && (!state || !new_state)) return GDN_ERR_NULL;
+  if ((int64_t)p->B * p->T > 0 && (!x || !weight || !y)) return GDN_ERR_NULL;
+  if (!aligned(x, pl.esz) || !aligned(y, pl.esz) || !aligned(state, pl.esz) ||
+      !aligned(new_state, pl.esz) || !aligned(weight, 4) || !aligned(bias, 4))
+    return GDN_ERR_ALIGN;
+  if (p->B == 0 || (p->T == 0 && state == new_state)) return GDN_OK;
+  if (p->T == 0) {  // no weights to read: the state passes through
+    pl.geo.cu = nullptr;
+    return conv_dispatch<FwdRun>(p, vec_ok(pl, {state, new_state}), pl, x, weight, bias, state, y,
+                                 new_state, static_cast<hipStream_t>(stream));
+  }
+  return conv_dispatch<DecodeRun>(p, vec_ok(pl, {x, y, state, new_state}), pl, x, weight, bias, state,
+                                  new_state, y, static_cast<hipStream_t>(stream));
+}
+
+size_t gdn_conv_bwd_workspace_size(const gdn_conv_params_t* p, int packed) {
+  ConvPlan pl;
+  if (conv_sizes(p, packed != 0, &pl) != GDN_OK) return 0;
+  return conv_ws(p, packed != 0, pl);
+}
+
+gdn_status_t gdn_conv_bwd(const gdn_conv_params_t* p, const void* x, const uint8_t* x_scales,
+                          const float* weight, const float* bias, const int64_t* cu_seqlens,
+                          const void* initial_state, const void* d_y, const void* d_final_state,
+                          void* dx, float* dweight, float* dbias, void* d_initial_state,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  const bool packed = cu_seqlens != nullptr;
+  ConvPlan pl;
+  gdn_status_t st = conv_sizes(p, packed, &pl);
+  if (st != GDN_OK) return st;
+  if (x_scales && p->x_stride != 0 && p->x_stride != p->C) return GDN_ERR_SHAPE;  // codes are dense
+  const bool tokens = (int64_t)p->B * p->T > 0;
+  if ((tokens && (!x || !weight || !d_y || !dx)) || !dweight) return GDN_ERR_NULL;
+  const size_t need = conv_ws(p, packed, pl);
+  if (need > 0 && !workspace) return GDN_ERR_NULL;
+  const size_t xa = x_scales ? 1 : pl.esz;
+  if (!aligned(x, xa) || !aligned(d_y, pl.esz) || !aligned(dx, pl.esz) ||
+      !aligned(initial_state, pl.esz) || !aligned(d_final_state, pl.esz) ||
+      !aligned(d_initial_state, pl.esz) || !aligned(weight, 4) || !aligned(bias, 4) ||
+      !aligned(dweight, 4) || !aligned(dbias, 4) || !aligned(cu_seqlens, 8) || !aligned(workspace, kWsAlign))
+    return GDN_ERR_ALIGN;
+  if (workspace_bytes < need) return GDN_ERR_WORKSPACE;
+  const bool vec = vec_ok(pl, {x_scales ? nullptr : x, d_y, dx, initial_state, d_final_state, d_initial_state}) &&
+                   aligned(x, 8);
+  conv_bwd_tiles(p, packed, vec ? pl.vec : 1, &pl);
+  if (pl.rows * ceil_div(pl.geo.cvn, pl.cl) > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  pl.geo.cu = cu_seqlens;
+  const ConvBwdArgs a{x, x_scales, weight, bias, initial_state, d_y, d_final_state,
+                      dx, dweight, dbias, d_initial_state};
+  return conv_dispatch<BwdRun>(p, vec, pl, a, workspace, static_cast<hipStream_t>(stream));
+}
+
+gdn_status_t gdn_pack8(const void* x, gdn_dtype_t dtype, int64_t rows, int32_t C, int64_t x_stride,
+                       int8_t* codes, uint8_t* scales, void* stream) {
+  const int dt = enum_int(dtype);
+  gdn_status_t st = pack_sizes(dt, rows, C);
+  if (st != GDN_OK) return st;
+  if (x_stride != 0 && x_stride < C) return GDN_ERR_SHAPE;
+  if (rows == 0) return GDN_OK;
+  if (!x || !codes || !scales) return GDN_ERR_NULL;
+  if (!aligned(x, dt == GDN_F32 ? 4 : 2)) return GDN_ERR_ALIGN;
+  const int64_t ld = x_stride ? x_stride : C;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return dt == GDN_F32 ? pack_run<float>(x, ld, rows, C, codes, scales, s)
+                       : pack_run<gdn::bf16>(x, ld, rows, C, codes, scales, s);
+}
+
+gdn_status_t gdn_unpack8(const int8_t* codes, const uint8_t* scales, int64_t rows, int32_t C, void* y,
+                         gdn_dtype_t dtype, void* stream) {
+  const int dt = enum_int(dtype);
+  gdn_status_t st = pack_sizes(dt, rows, C);
+  if (st != GDN_OK) return st;
+  if (rows == 0) return GDN_OK;
+  if (!codes || !scales || !y) return GDN_ERR_NULL;
+  if (!aligned(y, dt == GDN_F32 ? 4 : 2)) return GDN_ERR_ALIGN;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return dt == GDN_F32 ? unpack_run<float>(codes, scales, rows, C, y, s)
+                       : unpack_run<gdn::bf16>(codes, scales, rows, C, y, s);
+}
+
+}  // extern "C"

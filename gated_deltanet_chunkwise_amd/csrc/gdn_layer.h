@@ -1,0 +1,203 @@
+// gdn_layer.h -- device helpers shared by the layer operators around the gated
+// delta rule (short causal convolution, selective scan, 8-bit checkpoints).
+#pragma once
+#include "gdn_common.h"
+
+namespace gdn {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kPackBlock = 32;  // channels that share one checkpoint scale
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// 1 / (1 + e^-x).  v_exp_f32 and v_rcp_f32 are within about 1 ulp; e^-x
+// overflowing to infinity gives exactly 0.
+__device__ __forceinline__ float fast_sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-x * kLog2e));
+}
+
+// gate_softplus (gdn_common.h: the same steps and error) without branches, for a
+// value that every lane needs.
+__device__ __forceinline__ float softplus_flat(float x) {
+  const float t = x * kLog2e;
+  const bool deep = t < -64.f;
+  const float y = __builtin_amdgcn_exp2f(deep ? t + 64.f : t) * (deep ? 0x1p-64f : 1.f);
+  const float u = 1.f + y;
+  const float r = __builtin_amdgcn_logf(u) * 0.693147180559945309f * (y * __builtin_amdgcn_rcpf(u - 1.f));
+  return x > 20.f ? x : u == 1.f ? y : r;
+}
+
+// The checkpoint scale of a stored byte b: 2^(b - 127), and NaN for 255 (a block
+// that held an infinity or a NaN).
+__device__ __forceinline__ float pack_scale(uint32_t b) {
+  return __uint_as_float(b == 255u ? 0x7fc00000u : b ? b << 23 : 0x00400000u);
+}
+
+// Activations [tokens][C] as a kernel reads them: rows of E with a row stride, or
+// (scales != nullptr) a checkpoint's codes [tokens][C] and scales [tokens][ceil(C/32)].
+struct Src {
+  const void* p;
+  const uint8_t* scales;
+  int64_t ld;  // elements between rows (codes: C)
+};
+
+// VEC consecutive channels of one row, as loaded (not yet converted), so that
+// loads can be issued well before their use.
+template <typename E, int VEC> struct RawVec;
+template <> struct RawVec<bf16, 8> { u32x4 w; };
+template <> struct RawVec<float, 4> { u32x4 w; };
+template <typename E> struct RawVec<E, 1> { uint32_t w, s; };
+
+template <typename E, int VEC>
+__device__ __forceinline__ RawVec<E, VEC> raw_load(const Src& s, int64_t row, int c, int nblk) {
+  RawVec<E, VEC> r;
+  if constexpr (VEC == 1) {
+    if (s.scales) {
+      r.w = static_cast<const uint8_t*>(s.p)[row * s.ld + c];
+      r.s = s.scales[row * nblk + (c >> 5)];
+    } else {
+      const E* q = static_cast<const E*>(s.p) + row * s.ld + c;
+      if constexpr (sizeof(E) == 2) r.w = *reinterpret_cast<const uint16_t*>(q);
+      else r.w = *reinterpret_cast<const uint32_t*>(q);
+      r.s = 0;
+    }
+  } else {
+    if (s.scales) {  // VEC divides 32: one scale for the vector
+      const uint8_t* q = static_cast<const uint8_t*>(s.p) + row * s.ld + c;
+      if constexpr (VEC == 8) {
+        const u32x2 d = *reinterpret_cast<const u32x2*>(q);
+        r.w.x = d.x;
+        r.w.y = d.y;
+      } else {
+        r.w.x = *reinterpret_cast<const uint32_t*>(q);
+        r.w.y = 0;
+      }
+      r.w.z = s.scales[row * nblk + (c >> 5)];
+      r.w.w = 0;
+    } else {
+      r.w = *reinterpret_cast<const u32x4*>(static_cast<const E*>(s.p) + row * s.ld + c);
+    }
+  }
+  return r;
+}
+
+// The raw vector as fp32; `packed` as the load's (s.scales != nullptr).
+template <typename E, int VEC>
+__device__ __forceinline__ void raw_unpack(const RawVec<E, VEC>& r, bool packed, float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    if (packed) v[0] = (float)(int8_t)r.w * pack_scale(r.s);
+    else v[0] = sizeof(E) == 2 ? __uint_as_float(r.w << 16) : __uint_as_float(r.w);
+  } else {
+    if (packed) {
+      const float sc = pack_scale(r.w.z);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = (float)(int8_t)(r.w[i >> 2] >> (8 * (i & 3))) * sc;
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        if constexpr (sizeof(E) == 2) v[i] = (i & 1) ? bf16_hi(r.w[i >> 1]) : bf16_lo(r.w[i >> 1]);
+        else v[i] = __uint_as_float(r.w[i]);
+      }
+    }
+  }
+}
+
+// VEC consecutive elements of E from a plain pointer, and to one (round to nearest even).
+template <typename E, int VEC>
+__device__ __forceinline__ void vec_load(const E* p, float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    v[0] = (float)*p;
+  } else {
+    const Src s{p, nullptr, 0};
+    raw_unpack<E, VEC>(raw_load<E, VEC>(s, 0, 0, 0), false, v);
+  }
+}
+template <typename E, int VEC>
+__device__ __forceinline__ void vec_store(E* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    *p = (E)v[0];
+  } else if constexpr (sizeof(E) == 2) {
+    const f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+    const bf16x4 a = to_bf16x4(lo), b = to_bf16x4(hi);
+    *reinterpret_cast<bf16x8*>(p) = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  } else {
+    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+  }
+}
+
+// Packed sequences.  Offsets are read clamped to [0, T], so that ill-formed ones
+// never lead outside the buffers.
+__device__ __forceinline__ int seq_offset(const int64_t* cu, int n, int T) {
+  const int64_t v = cu[n];
+  return v < 0 ? 0 : v > T ? T : (int)v;
+}
+// The last n in [0, N) whose offset is at most t (0 if there is none): the sequence
+// of token t, unless t lies behind the last sequence.
+__device__ __forceinline__ int seq_of_token(const int64_t* cu, int N, int T, int t) {
+  int lo = 0, hi = N;  // offset[lo] <= t is taken for granted, offset[hi] > t or hi == N
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (seq_offset(cu, mid, T) <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// A wave-uniform value that the compiler cannot see to be one, in a scalar register.
+template <bool UNIFORM> __device__ __forceinline__ int uniform(int v) {
+  return UNIFORM ? __builtin_amdgcn_readfirstlane(v) : v;
+}
+
+// A maximal stretch [ta, tb) of a tile within one sequence n = [start, end), all in
+// tokens of the flattened batch; done() once the tile is exhausted.  Every step
+// moves n or ta forward, so the walk ends for any offsets.  UNIFORM: all lanes of the
+// wave walk the same tile.
+template <bool UNIFORM> struct Run {
+  int n, N, T, start, end, ta, tb, t1;
+  const int64_t* cu;
+
+  __device__ __forceinline__ void init(const int64_t* cu_, int T_, int N_, int tile, int ntiles, int len) {
+    cu = cu_;
+    T = T_;
+    N = N_;
+    if (cu) {
+      ta = tile * len;
+      t1 = min(ta + len, T);
+      n = uniform<UNIFORM>(seq_of_token(cu, N, T, ta));
+      fit();
+    } else {
+      n = tile / ntiles;
+      start = n * T;
+      end = start + T;
+      ta = start + (tile - n * ntiles) * len;
+      t1 = tb = min(ta + len, end);
+    }
+  }
+  __device__ __forceinline__ bool done() const { return ta >= t1; }
+  __device__ __forceinline__ void next() {
+    ta = tb;
+    if (cu && ta < t1) {
+      ++n;
+      fit();
+    }
+  }
+  // The sequence that holds token ta, from n on: skips empty ones; behind the last
+  // sequence the walk ends.
+  __device__ __forceinline__ void fit() {
+    for (; n < N; ++n) {
+      start = uniform<UNIFORM>(seq_offset(cu, n, T));
+      end = uniform<UNIFORM>(seq_offset(cu, n + 1, T));
+      if (end > ta) {
+        if (start > ta) ta = min(start, t1);  // only for ill-formed offsets
+        tb = min(end, t1);
+        return;
+      }
+    }
+    ta = tb = t1;
+  }
+};
+
+}  // namespace gdn

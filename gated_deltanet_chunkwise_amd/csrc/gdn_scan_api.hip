@@ -1,0 +1,182 @@
+// gdn_scan_api.hip -- entry points of the selective scan's forward pass and decode
+// step: validation, tiles and launches.  See include/gdn.h.
+#include "gdn_scan_host.h"
+
+namespace {
+
+gdn_status_t fwd_sizes(const gdn_scan_params_t* p, bool packed, ScanPlan* pl) {
+  const gdn_status_t st = scan_sizes(p, packed, pl);
+  if (st == GDN_OK) scan_waves(pl, p->N <= 8 ? 8 : 16);
+  return st;
+}
+
+// Tokens per tile.  One tile per sequence where its waves alone keep the device busy
+// (or the sequences are short); else tiles for about kWaves waves per CU, of kLeast
+// tokens at least.
+constexpr int kWavesPerCu = 16, kLeastTile = 64;
+
+int scan_fwd_len(const ScanPlan& pl, int cus) {
+  const gdn::ScanGeo& g = pl.geo;
+  const int64_t waves = (int64_t)g.cgroups * g.nw * (pl.packed ? 1 : g.B);  // of one tile per row
+  const int64_t want = (int64_t)cus * kWavesPerCu;
+  if (g.T <= kLeastTile || (!pl.packed && waves * 4 >= want)) return std::max(g.T, 1);
+  const int64_t tiles = std::max<int64_t>(want / std::max<int64_t>(waves, 1), 1);
+  const int64_t len = ceil_div(ceil_div(g.T, tiles), gdn::kScanGroup) * gdn::kScanGroup;
+  return (int)std::max<int64_t>(len, kLeastTile);
+}
+
+// f(E, BE, NS, SPLIT) as default-constructed tags.
+template <typename F> gdn_status_t scan_dispatch(const ScanPlan& pl, bool direct, F&& f) {
+  auto split = [&](auto e, auto be, auto ns) {
+    return pl.geo.nw > 1 ? f(e, be, ns, std::true_type{}) : f(e, be, ns, std::false_type{});
+  };
+  auto states = [&](auto e, auto be) {
+    if (pl.ns == 8) return f(e, be, std::integral_constant<int, 8>{}, std::false_type{});
+    return split(e, be, std::integral_constant<int, 16>{});
+  };
+  if (pl.esz == 4) return states(0.f, 0.f);
+  return direct ? states(gdn::bf16{}, gdn::bf16{}) : states(gdn::bf16{}, 0.f);
+}
+
+struct FwdSpace {
+  size_t states, sums, rows, total;
+};
+// For tiles of kLeastTile tokens, the shortest there are: the choice depends on the
+// device, the size of the workspace does not.
+FwdSpace fwd_space(ScanPlan pl) {
+  FwdSpace w{};
+  const bool one = pl.geo.T <= kLeastTile;
+  scan_tiles(&pl, one ? std::max(pl.geo.T, 1) : kLeastTile);
+  const size_t tiles = one ? 0 : (size_t)scan_all_tiles(pl);
+  size_t off = 0;
+  w.states = off; off = align_up(off + tiles * pl.geo.np * pl.geo.D * 4);
+  w.sums = off;   off = align_up(off + tiles * pl.geo.D * 4);
+  w.rows = off;   off += 2 * scan_rows_bytes(pl);
+  w.total = off;
+  return w;
+}
+
+struct FwdArgs {
+  const void *x, *dt;
+  const float* A_log;
+  const void *Bm, *Cm;
+  const float* skip;
+  const void* z;
+  const float *dt_bias, *h0;
+  void* y;
+  float* fin;
+};
+
+gdn_status_t scan_fwd_run(ScanPlan pl, const FwdArgs& a, void* ws, hipStream_t s) {
+  gdn::ScanGeo& g = pl.geo;
+  const FwdSpace sp = fwd_space(pl);
+  char* w = static_cast<char*>(ws);
+  float* states = reinterpret_cast<float*>(w + sp.states);
+  float* sums = reinterpret_cast<float*>(w + sp.sums);
+  scan_tiles(&pl, scan_fwd_len(pl, device_cus()));
+  const bool direct = scan_rows_direct(pl, a.Bm, a.Cm);
+  const void *Bm = a.Bm, *Cm = a.Cm;
+  hipError_t err = hipSuccess;
+  auto ok = [&](hipError_t e) {
+    if (e != hipSuccess && err == hipSuccess) err = e;
+  };
+  if (!direct && pl.tok > 0) {
+    float* Bw = reinterpret_cast<float*>(w + sp.rows);
+    float* Cw = reinterpret_cast<float*>(w + sp.rows + scan_rows_bytes(pl));
+    ok(pl.esz == 2 ? scan_copy_rows<gdn::bf16>(&pl, Bm, Cm, Bw, Cw, s) : scan_copy_rows<float>(&pl, Bm, Cm, Bw, Cw, s));
+    Bm = Bw;
+    Cm = Cw;
+  }
+  const int64_t main_blocks = pl.tok > 0 ? scan_all_tiles(pl) * g.cgroups : 0;
+  const int64_t empties = (g.cu || g.T == 0) && a.fin ? g.S : 0;
+  if (main_blocks + empties > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  if (pl.tok == 0) g.ntiles = 0;  // no tile blocks: the first block is the first sequence's
+  if (main_blocks + empties == 0) return GDN_OK;
+  gdn_status_t st = scan_dispatch(pl, direct, [&](auto e, auto be, auto ns, auto split) {
+    using E = decltype(e);
+    using BE = decltype(be);
+    constexpr int NS = decltype(ns)::value;
+    constexpr bool SPLIT = decltype(split)::value;
+    const gdn::Src x{a.x, nullptr, pl.ldx}, z{a.z, nullptr, pl.ldz};
+    const E* dt = static_cast<const E*>(a.dt);
+    const BE *b = static_cast<const BE*>(Bm), *c = static_cast<const BE*>(Cm);
+    E* y = static_cast<E*>(a.y);
+    const dim3 block(64 * g.nw);
+    if (g.ntiles > 1) {
+      ok(launch(gdn::gdn_scan_kernel<E, BE, NS, SPLIT, true>, dim3((unsigned)main_blocks), block, s, g, x, dt, z,
+                a.A_log, b, c, a.skip, a.dt_bias, a.h0, states, sums, y, a.fin));
+      const int64_t lanes = (int64_t)(g.cu ? 1 : g.B) * g.np * g.D;
+      ok(launch(gdn::gdn_scan_join_kernel, dim3((unsigned)ceil_div(lanes, 256)), dim3(256), s, g, a.A_log, a.h0,
+                states, sums));
+    }
+    ok(launch(gdn::gdn_scan_kernel<E, BE, NS, SPLIT, false>, dim3((unsigned)(main_blocks + empties)), block, s, g, x,
+              dt, z, a.A_log, b, c, a.skip, a.dt_bias, a.h0, states, sums, y, a.fin));
+    return GDN_OK;
+  });
+  if (st != GDN_OK) return st;
+  return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gdn_scan_fwd_workspace_size(const gdn_scan_params_t* p, int packed) {
+  ScanPlan pl;
+  return fwd_sizes(p, packed != 0, &pl) == GDN_OK ? fwd_space(pl).total : 0;
+}
+
+gdn_status_t gdn_scan_fwd(const gdn_scan_params_t* p, const void* x, const void* dt, const float* A_log,
+                          const void* Bm, const void* Cm, const float* skip, const void* z,
+                          const float* dt_bias, const int64_t* cu_seqlens, const float* initial_state,
+                          void* y, float* final_state, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  ScanPlan pl;
+  gdn_status_t st = fwd_sizes(p, cu_seqlens != nullptr, &pl);
+  if (st != GDN_OK) return st;
+  if (pl.tok > 0 && (!x || !dt || !A_log || !Bm || !Cm || !y)) return GDN_ERR_NULL;
+  const size_t need = fwd_space(pl).total;
+  if (need > 0 && !workspace) return GDN_ERR_NULL;
+  for (const void* q : {x, dt, Bm, Cm, z, (const void*)y})
+    if (!aligned(q, pl.esz)) return GDN_ERR_ALIGN;
+  for (const float* q : {A_log, skip, dt_bias, initial_state, (const float*)final_state})
+    if (!aligned(q, 4)) return GDN_ERR_ALIGN;
+  if (!aligned(cu_seqlens, 8) || !aligned(workspace, kWsAlign)) return GDN_ERR_ALIGN;
+  if (workspace_bytes < need) return GDN_ERR_WORKSPACE;
+  pl.geo.cu = cu_seqlens;
+  return scan_fwd_run(pl, {x, dt, A_log, Bm, Cm, skip, z, dt_bias, initial_state, y, final_state},
+                      workspace, static_cast<hipStream_t>(stream));
+}
+
+gdn_status_t gdn_scan_decode(const gdn_scan_params_t* p, const void* x, const void* dt, const float* A_log,
+                             const void* Bm, const void* Cm, const float* skip, const void* z,
+                             const float* dt_bias, const float* state, float* new_state, void* y,
+                             void* stream) {
+  ScanPlan pl;
+  gdn_status_t st = scan_sizes(p, false, &pl);
+  if (st != GDN_OK) return st;
+  if (p->num_seqs != 0) return GDN_ERR_SHAPE;
+  if (p->B > 0 && (!state || !new_state)) return GDN_ERR_NULL;
+  if ((pl.tok > 0 && (!x || !dt || !Bm || !Cm || !y)) || (p->B > 0 && !A_log)) return GDN_ERR_NULL;
+  for (const void* q : {x, dt, Bm, Cm, z, (const void*)y})
+    if (!aligned(q, pl.esz)) return GDN_ERR_ALIGN;
+  for (const float* q : {A_log, skip, dt_bias, state, (const float*)new_state})
+    if (!aligned(q, 4)) return GDN_ERR_ALIGN;
+  if (p->B == 0) return GDN_OK;
+  const gdn::ScanGeo& g = pl.geo;
+  int nl = 1;
+  while (nl * 4 < g.N) nl <<= 1;
+  const int vec = g.N % 4 == 0 && aligned(state, 16) && aligned(new_state, 16);
+  const int64_t blocks = ceil_div((int64_t)g.B * g.D * nl, 256);
+  if (blocks > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  auto go = [&](auto e) {
+    using E = decltype(e);
+    return launch(gdn::gdn_scan_decode_kernel<E>, dim3((unsigned)blocks), dim3(256),
+                  static_cast<hipStream_t>(stream), g, gdn::Src{x, nullptr, pl.ldx}, static_cast<const E*>(dt),
+                  gdn::Src{z, nullptr, pl.ldz}, A_log, static_cast<const E*>(Bm), static_cast<const E*>(Cm),
+                  skip, dt_bias, state, new_state, static_cast<E*>(y), nl, vec);
+  };
+  return (p->dtype == GDN_BF16 ? go(gdn::bf16{}) : go(0.f)) == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+}  // extern "C"

@@ -1,0 +1,92 @@
+// gdn_scan_host.h -- sizes, tiles and workspace that the scan's entry points share.
+#pragma once
+#include "gdn_host.h"
+#include "gdn_scan.h"
+
+namespace {
+
+struct ScanPlan {
+  gdn::ScanGeo geo;
+  int64_t ldx, ldz;
+  size_t esz;
+  int ns;        // states per lane
+  int64_t tok;   // tokens in all
+  bool packed;
+};
+
+// Sizes only.
+inline gdn_status_t scan_sizes(const gdn_scan_params_t* p, bool packed, ScanPlan* out) {
+  if (!p) return GDN_ERR_NULL;
+  if (p->dtype != GDN_F32 && p->dtype != GDN_BF16) return GDN_ERR_DTYPE;
+  if (p->D <= 0 || p->G <= 0 || p->N <= 0 || p->D % p->G) return GDN_ERR_SHAPE;
+  gdn_status_t st = check_batch(p->B, p->T, p->num_seqs, packed);
+  if (st != GDN_OK) return st;
+  if (p->N > 64) return GDN_ERR_UNSUPPORTED;
+  const int64_t bn = (int64_t)p->G * p->N;
+  if (bn > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  auto bad = [](int64_t ld, int64_t least) { return ld != 0 && ld < least; };
+  if (bad(p->x_stride, p->D) || bad(p->dt_stride, p->D) || bad(p->z_stride, p->D) ||
+      bad(p->b_stride, bn) || bad(p->c_stride, bn))
+    return GDN_ERR_SHAPE;
+  ScanPlan pl{};
+  pl.packed = packed;
+  pl.esz = p->dtype == GDN_BF16 ? 2 : 4;
+  pl.tok = (int64_t)p->B * p->T;
+  pl.ldx = p->x_stride ? p->x_stride : p->D;
+  pl.ldz = p->z_stride ? p->z_stride : p->D;
+  gdn::ScanGeo& g = pl.geo;
+  g.B = p->B; g.T = p->T; g.D = p->D; g.G = p->G; g.N = p->N;
+  g.S = packed ? p->num_seqs : p->B;
+  g.DG = p->D / p->G;
+  g.wpg = (int)ceil_div(g.DG, 64);
+  g.cgroups = g.G * g.wpg;
+  g.lddt = p->dt_stride ? p->dt_stride : p->D;
+  g.ldb = p->b_stride ? p->b_stride : bn;
+  g.ldc = p->c_stride ? p->c_stride : bn;
+  g.bgs = g.cgs = p->N;
+  *out = pl;
+  return GDN_OK;
+}
+
+// ns states per lane, as many waves per workgroup as that takes.
+inline void scan_waves(ScanPlan* pl, int ns) {
+  pl->ns = ns;
+  pl->geo.nw = (int)ceil_div(pl->geo.N, ns);
+  pl->geo.np = pl->geo.nw * ns;
+}
+
+inline void scan_tiles(ScanPlan* pl, int len) {
+  pl->geo.len = len;
+  pl->geo.ntiles = (int)std::max<int64_t>(ceil_div(pl->geo.T, len), 1);
+}
+inline int64_t scan_all_tiles(const ScanPlan& pl) {
+  return (int64_t)pl.geo.ntiles * (pl.packed ? 1 : pl.geo.B);
+}
+
+// Whether Bm and Cm can be read in place: whole rows of np states at 4-byte aligned
+// addresses (fp32: the addresses are always aligned).
+inline bool scan_rows_direct(const ScanPlan& pl, const void* Bm, const void* Cm) {
+  const gdn::ScanGeo& g = pl.geo;
+  if (g.N != g.np) return false;
+  if (pl.esz == 4) return true;
+  return g.ldb % 2 == 0 && g.ldc % 2 == 0 && aligned(Bm, 4) && aligned(Cm, 4);
+}
+// Bytes of one of the two fp32 copies otherwise.
+inline size_t scan_rows_bytes(const ScanPlan& pl) {
+  return align_up((size_t)pl.tok * pl.geo.G * pl.geo.np * 4);
+}
+
+template <typename E>
+hipError_t scan_copy_rows(ScanPlan* pl, const void* Bm, const void* Cm, float* Bw, float* Cw, hipStream_t s) {
+  gdn::ScanGeo& g = pl->geo;
+  const int64_t n = pl->tok * g.G * g.np;
+  const int64_t blocks = std::min(ceil_div(n, 256), (int64_t)device_cus() * 16);
+  const hipError_t e = launch(gdn::gdn_scan_rows_kernel<E>, dim3((unsigned)blocks), dim3(256), s,
+                              static_cast<const E*>(Bm), static_cast<const E*>(Cm), g.ldb, g.ldc, pl->tok,
+                              g.G, g.N, g.np, Bw, Cw);
+  g.ldb = g.ldc = (int64_t)g.G * g.np;
+  g.bgs = g.cgs = g.np;
+  return e;
+}
+
+}  // namespace

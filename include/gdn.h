@@ -419,6 +419,159 @@ gdn_status_t gdn_kda_gate(const void *g, gdn_dtype_t g_dtype, const float *A_log
                           const float *dt_bias, void *yg, gdn_dtype_t yg_dtype, int64_t T,
                           int32_t H, int32_t D, void *stream);
 
+/* ---- Short causal convolution ---------------------------------------------------
+ * The depthwise convolution that a gated delta rule or selective scan layer puts
+ * its projections through, with an optional SiLU:
+ *     s[t,c] = bias[c] + sum_{j<W} weight[c,j] x[t-W+1+j,c]
+ *     y[t,c] = s (activation 0) or s / (1 + exp(-s)) (activation 1)
+ * per sequence; inputs before its first token are its initial state's rows, or 0.
+ * The final state is the sequence's last W-1 inputs (rows of the initial state
+ * where the sequence is shorter), so a prompt's final state is what gdn_conv_decode
+ * continues from.
+ *   p            sizes; W = 2, 3 or 4; num_seqs = N with cu_seqlens (then B = 1)
+ *   x            [B][T] rows of C channels, p->x_stride elements apart (0: C), dtype:
+ *                a slice of a wider projection is read in place
+ *   weight       [C][W] fp32; bias [C] fp32 or NULL (0)
+ *   cu_seqlens   [N+1] int64 or NULL, as for gdn_fwd, except that it may end before T:
+ *                rows of y behind the last sequence are left as they were, rows of dx
+ *                are set to 0
+ *   initial_state, final_state  [N][W-1][C], dtype, oldest row first, or NULL
+ *   y            [B][T][C] contiguous, dtype, written
+ * Sums are fp32, rounded once.  dtype: GDN_F32 or GDN_BF16.  Alignment: element
+ * size (rows of 16-byte aligned, 16-byte divisible vectors are faster); cu_seqlens
+ * 8; workspace 256.  B * T below 2^31 - 4096.  Errors as for gdn_fwd, all checked
+ * before anything is enqueued; GDN_ERR_UNSUPPORTED for another W.  Outputs must not
+ * overlap inputs or each other (gdn_conv_decode: new_state may be state).
+ * Enqueued on `stream`; nothing is allocated. */
+typedef struct {
+  int32_t B, T, C, W;
+  int32_t num_seqs;   /* N with cu_seqlens; ignored (N = B) without */
+  int32_t dtype;      /* gdn_dtype_t of x, y and the states */
+  int32_t activation; /* 0: none, 1: SiLU */
+  int64_t x_stride;   /* elements between x's rows, 0 = C */
+} gdn_conv_params_t;
+
+gdn_status_t gdn_conv_fwd(const gdn_conv_params_t *p, const void *x, const float *weight,
+                          const float *bias, const int64_t *cu_seqlens,
+                          const void *initial_state, void *y, void *final_state,
+                          void *stream);
+
+/* T tokens (1: a decode step) of each of B sequences after `state` [B][W-1][C]; the
+ * state after them is written to new_state, which may be `state` (in place) and must
+ * not overlap it otherwise.  num_seqs = 0. */
+gdn_status_t gdn_conv_decode(const gdn_conv_params_t *p, const void *x, const float *weight,
+                             const float *bias, const void *state, void *new_state, void *y,
+                             void *stream);
+
+/* Gradients for L = sum <d_y, y> + <d_final_state, final_state>.
+ *   x             as for gdn_conv_fwd, or a checkpoint of it: with x_scales not NULL x
+ *                 is the codes and x_scales the scales of gdn_pack8 (rows = B T, dense),
+ *                 read in place; the gradients are those at the values the checkpoint
+ *                 stands for
+ *   d_y           [B][T][C], d_final_state [N][W-1][C] or NULL (0), dtype
+ *   dx            [B][T][C] dtype; dweight [C][W] fp32; dbias [C] fp32 or NULL;
+ *   d_initial_state [N][W-1][C] dtype or NULL; all written
+ *   workspace     gdn_conv_bwd_workspace_size() bytes
+ * Sums run in a fixed order: the same call gives the same bits. */
+size_t gdn_conv_bwd_workspace_size(const gdn_conv_params_t *p, int packed);
+
+gdn_status_t gdn_conv_bwd(const gdn_conv_params_t *p, const void *x, const uint8_t *x_scales,
+                          const float *weight, const float *bias, const int64_t *cu_seqlens,
+                          const void *initial_state, const void *d_y,
+                          const void *d_final_state, void *dx, float *dweight, float *dbias,
+                          void *d_initial_state, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/* ---- Selective state space scan -------------------------------------------------
+ * The diagonal recurrence next to the gated delta rule, one state of N values per
+ * channel, its gate per channel and state:
+ *     D[t,d]   = softplus(dt[t,d] + dt_bias[d])           (softplus as for gdn_fwd)
+ *     h_t[d,n] = exp(-exp(A_log[d,n]) D[t,d]) h_{t-1}[d,n] + D[t,d] Bm[t,g,n] x[t,d]
+ *     y[t,d]   = (sum_n Cm[t,g,n] h_t[d,n] + skip[d] x[t,d]) * silu(z[t,d])
+ * with g = d / (D/G), the channel's group of Bm and Cm.
+ *   p             sizes; 1 <= N <= 64, D % G == 0; num_seqs with cu_seqlens (then B = 1)
+ *   x, dt, z      [B][T] rows of D channels, x_stride, dt_stride, z_stride elements
+ *                 apart (0: D), dtype; z may be NULL (no gate)
+ *   Bm, Cm        [B][T] rows of G*N, b_stride, c_stride elements apart (0: G*N), dtype
+ *   A_log         [D][N] fp32; skip [D] fp32 or NULL (0); dt_bias [D] fp32 or NULL (0)
+ *   cu_seqlens    [num_seqs+1] int64 or NULL, as for gdn_conv_fwd
+ *   initial_state, final_state  [sequences][D][N] fp32 or NULL
+ *   y             [B][T][D] contiguous, dtype, written
+ *   workspace     gdn_scan_fwd_workspace_size() bytes
+ * All arithmetic is fp32; y is rounded once.  Long sequences are cut into tiles of
+ * tokens that run side by side (three kernels); where the channels alone fill the
+ * device, one kernel runs each sequence through.  The cut is chosen from the sizes
+ * and the current device's compute units.  dtype, alignment, limits and errors as for
+ * gdn_conv_fwd; GDN_ERR_UNSUPPORTED for N > 64.  Outputs must not overlap inputs or
+ * each other (gdn_scan_decode: new_state may be state).  Enqueued on `stream`;
+ * nothing is allocated. */
+typedef struct {
+  int32_t B, T, D, G, N;
+  int32_t num_seqs; /* sequences with cu_seqlens; ignored (B) without */
+  int32_t dtype;    /* gdn_dtype_t of x, dt, z, Bm, Cm and y */
+  int64_t x_stride, dt_stride, z_stride, b_stride, c_stride; /* elements between rows, 0 = dense */
+} gdn_scan_params_t;
+
+size_t gdn_scan_fwd_workspace_size(const gdn_scan_params_t *p, int packed);
+
+gdn_status_t gdn_scan_fwd(const gdn_scan_params_t *p, const void *x, const void *dt,
+                          const float *A_log, const void *Bm, const void *Cm,
+                          const float *skip, const void *z, const float *dt_bias,
+                          const int64_t *cu_seqlens, const float *initial_state, void *y,
+                          float *final_state, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/* T tokens (1: a decode step) of each of B sequences after `state` [B][D][N] fp32; the
+ * state after them is written to new_state, which may be `state` (in place) and must
+ * not overlap it otherwise.  num_seqs = 0. */
+gdn_status_t gdn_scan_decode(const gdn_scan_params_t *p, const void *x, const void *dt,
+                             const float *A_log, const void *Bm, const void *Cm,
+                             const float *skip, const void *z, const float *dt_bias,
+                             const float *state, float *new_state, void *y, void *stream);
+
+/* Gradients for L = sum <d_y, y> + <d_final_state, final_state>.  The states are
+ * formed again tile by tile; nothing of the forward pass is needed but its inputs.
+ *   x, z          as for gdn_scan_fwd, or checkpoints: with x_scales (z_scales) not NULL
+ *                 the codes and scales of gdn_pack8, dense, read in place; the gradients
+ *                 are those at the values they stand for
+ *   d_y           [B][T][D] dtype; d_final_state [sequences][D][N] fp32 or NULL (0)
+ *   dx, ddt       [B][T][D]; dz [B][T][D] (required with z, unused without); dBm, dCm
+ *                 [B][T][G][N]: dtype, written (rows behind the last sequence: 0)
+ *   dA_log        [D][N] fp32; dskip, ddt_bias [D] fp32 or NULL; d_initial_state
+ *                 [sequences][D][N] fp32 or NULL; written
+ *   workspace     gdn_scan_bwd_workspace_size() bytes
+ * Sums run in a fixed order: the same call gives the same bits. */
+size_t gdn_scan_bwd_workspace_size(const gdn_scan_params_t *p, int packed);
+
+gdn_status_t gdn_scan_bwd(const gdn_scan_params_t *p, const void *x, const uint8_t *x_scales,
+                          const void *dt, const float *A_log, const void *Bm, const void *Cm,
+                          const float *skip, const void *z, const uint8_t *z_scales,
+                          const float *dt_bias, const int64_t *cu_seqlens,
+                          const float *initial_state, const void *d_y,
+                          const float *d_final_state, void *dx, void *ddt, float *dA_log,
+                          void *dBm, void *dCm, float *dskip, void *dz, float *ddt_bias,
+                          float *d_initial_state, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/* ---- Activation checkpoints in 8 bits --------------------------------------------
+ * What a training step keeps of an activation until its backward pass, in 1 + 1/32
+ * bytes per element.  Each row of C channels is held in blocks of 32 (the last may be
+ * shorter): a scale s = 2^(b-127), stored as the byte b, the least power of two with
+ * max|x| <= 127 s (b between 1 and 248), and one signed code per channel, x / s rounded
+ * to the nearest integer, ties to even, within [-127, 127].  The checkpoint stands for
+ * code * s, at most max|x| / 127 from x.  A block that holds an infinity or a NaN gets
+ * b = 255, which stands for NaN.
+ *   x        rows of C channels, x_stride elements apart (0: C), dtype (GDN_F32, GDN_BF16)
+ *   codes    [rows][C] int8;  scales [rows][ceil(C/32)] uint8
+ *   y        [rows][C] contiguous, dtype: code * s (exact in either type, short of
+ *            denormal results in bf16)
+ * Errors as for gdn_kda_gate.  rows = 0 enqueues nothing.  Enqueued on `stream`. */
+gdn_status_t gdn_pack8(const void *x, gdn_dtype_t dtype, int64_t rows, int32_t C,
+                       int64_t x_stride, int8_t *codes, uint8_t *scales, void *stream);
+
+gdn_status_t gdn_unpack8(const int8_t *codes, const uint8_t *scales, int64_t rows, int32_t C,
+                         void *y, gdn_dtype_t dtype, void *stream);
+
 /* Static description of a status code. */
 const char *gdn_status_string(gdn_status_t s);
 
