@@ -395,12 +395,14 @@ def scan_fwd(x, dt, A_log, Bm, Cm, skip=None, z=None, dt_bias=None, cu_seqlens=N
 def scan_bwd(x, dt, A_log, Bm, Cm, d_y, d_final_state=None, skip=None, z=None, dt_bias=None, cu_seqlens=None,
              initial_state=None, stream=None):
     """Gradients of scan_fwd through gdn_scan_bwd: dict of dx, ddt, dBm, dCm (and dz with
-    z) in x's dtype, dA_log, dskip, ddt_bias and dh0 in fp32.  x and z may be their
+    z) in x's dtype, dA_log, dskip, ddt_bias and dh0 in fp32.  x and z may both be their
     checkpoints (Packed8)."""
     torch = _torch()
     f32 = torch.float32
     xd, xs, dtype = _maybe_packed("x", x)
     zd, zs, z_dtype = (None, None, None) if z is None else _maybe_packed("z", z)
+    if z is not None and (xs is None) != (zs is None):
+        raise ValueError("x and z must both be checkpoints, or neither")
     p, B, T, D, G, N, S = _scan_sizes(xd, dtype, dt, A_log, Bm, Cm, skip, zd, z_dtype, dt_bias, cu_seqlens)
     _check_tensor("d_y", d_y, (B, T, D), dtype)
     _check_tensor("d_final_state", d_final_state, (S, D, N), f32, required=False)

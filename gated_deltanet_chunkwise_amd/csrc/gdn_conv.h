@@ -279,7 +279,7 @@ __global__ __launch_bounds__(256) void gdn_conv_bwd_kernel(ConvGeo g, Src x,
             for (int i = 0; i < VEC; ++i)
 #pragma unroll
               for (int j = 0; j < W; ++j) out[i] = fmaf(w[i][j], p[j][i], out[i]);
-            vec_store<E, VEC>(dx + (int64_t)o * g.C + c, out);
+            vec_store<E, VEC, true>(dx + (int64_t)o * g.C + c, out);
           }
         }
       }

@@ -8,6 +8,9 @@ namespace gdn {
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
+// A pointer into global memory with its address space spelled out.
+template <typename E> using Global = __attribute__((address_space(1))) E*;
+
 constexpr int kPackBlock = 32;  // channels that share one checkpoint scale
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -19,14 +22,13 @@ __device__ __forceinline__ float fast_sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-x * kLog2e));
 }
 
-// gate_softplus (gdn_common.h: the same steps and error) without branches, for a
-// value that every lane needs.
+// gate_softplus (gdn_common.h: the same formula and error) without branches, for a value
+// that every lane needs, and without its range below 2^-126: a time step that small
+// changes no state, and here is 0.
 __device__ __forceinline__ float softplus_flat(float x) {
-  const float t = x * kLog2e;
-  const bool deep = t < -64.f;
-  const float y = __builtin_amdgcn_exp2f(deep ? t + 64.f : t) * (deep ? 0x1p-64f : 1.f);
+  const float y = __builtin_amdgcn_exp2f(x * kLog2e);
   const float u = 1.f + y;
-  const float r = __builtin_amdgcn_logf(u) * 0.693147180559945309f * (y * __builtin_amdgcn_rcpf(u - 1.f));
+  const float r = (__builtin_amdgcn_logf(u) * __builtin_amdgcn_rcpf(u - 1.f)) * (y * 0.693147180559945309f);
   return x > 20.f ? x : u == 1.f ? y : r;
 }
 
@@ -115,16 +117,21 @@ __device__ __forceinline__ void vec_load(const E* p, float (&v)[VEC]) {
     raw_unpack<E, VEC>(raw_load<E, VEC>(s, 0, 0, 0), false, v);
   }
 }
-template <typename E, int VEC>
+// NT: streamed past the caches (nobody reads it soon).
+template <typename E, int VEC, bool NT = false>
 __device__ __forceinline__ void vec_store(E* p, const float (&v)[VEC]) {
   if constexpr (VEC == 1) {
     *p = (E)v[0];
   } else if constexpr (sizeof(E) == 2) {
     const f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
     const bf16x4 a = to_bf16x4(lo), b = to_bf16x4(hi);
-    *reinterpret_cast<bf16x8*>(p) = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    const bf16x8 w = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    if constexpr (NT) __builtin_nontemporal_store(w, reinterpret_cast<bf16x8*>(p));
+    else *reinterpret_cast<bf16x8*>(p) = w;
   } else {
-    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    const f32x4 w = {v[0], v[1], v[2], v[3]};
+    if constexpr (NT) __builtin_nontemporal_store(w, reinterpret_cast<f32x4*>(p));
+    else *reinterpret_cast<f32x4*>(p) = w;
   }
 }
 

@@ -43,7 +43,7 @@ typedef const __attribute__((address_space(4))) uint32_t* scalar_ptr;
 template <typename BE, int NS> struct ScalarRow {
   static constexpr int kWords = NS * (int)sizeof(BE) / 4;
   uint32_t w[kWords];
-  __device__ __forceinline__ void load(const BE* p) {
+  __device__ __forceinline__ void load(Global<const BE> p) {
     scalar_ptr q = (scalar_ptr)(uintptr_t)p;
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = q[i];
@@ -54,36 +54,115 @@ template <typename BE, int NS> struct ScalarRow {
   }
 };
 
-// One channel of one row as loaded.
-template <typename E> __device__ __forceinline__ uint32_t load1(const E* p) {
-  if constexpr (sizeof(E) == 2) return *reinterpret_cast<const uint16_t*>(p);
-  else return *reinterpret_cast<const uint32_t*>(p);
+// Brings the rows of Bm and Cm of 64 tokens from `t` on (those before `end`) into the L2,
+// a lane per token, by loading a value of each.  The scalar loads that follow token by
+// token wait for one row at a time: from memory that is 1 to 2 us for every cache line of
+// two rows (the backward pass's first kernel: 73 us for 64 tokens, however few waves), from
+// the L2 it is hidden behind the token before.  The values are of no use: land() takes them,
+// late enough that nothing waits for them.
+struct RowAhead {
+  uint32_t b = 0, c = 0;
+  template <typename BE>
+  __device__ __forceinline__ void send(Global<const BE> Bt, Global<const BE> Ct, int64_t ldb, int64_t ldc, int t, int end) {
+    const int q = min(t + (int)(threadIdx.x & 63), end - 1);
+    b = *(Global<const uint16_t>)(Bt + q * ldb);
+    c = *(Global<const uint16_t>)(Ct + q * ldc);
+  }
+  __device__ __forceinline__ void land() { asm volatile("" ::"v"(b), "v"(c)); }
+};
+
+// One channel of one row as loaded: `row` is wave-uniform, `off` the lane's offset in
+// bytes, so that the address takes no vector arithmetic.
+template <typename E> __device__ __forceinline__ uint32_t load1(Global<const E> row, uint32_t off) {
+  Global<const char> p = (Global<const char>)row + off;
+  if constexpr (sizeof(E) == 2) return *(Global<const uint16_t>)p;
+  else return *(Global<const uint32_t>)p;
+}
+template <typename E> __device__ __forceinline__ uint32_t load1(const E* row, uint32_t off) {
+  return load1<E>((Global<const E>)row, off);
+}
+template <typename E> __device__ __forceinline__ void store1(Global<E> row, uint32_t off, float v) {
+  *(Global<E>)((Global<char>)row + off) = (E)v;
+}
+// A lane's offset, in a form that the compiler adds to a uniform pointer within the load
+// itself (it would otherwise form 64-bit sums in vector registers).
+__device__ __forceinline__ uint32_t lane_offset(uint32_t bytes) {
+  asm("" : "+v"(bytes));
+  return bytes;
+}
+
+// p + n, in a form that the compiler does not fold into other sums: the walks below step
+// their row pointers token by token, and without this it keeps every multiple of every
+// stride in scalar registers, which then spill.
+template <typename T> __device__ __forceinline__ Global<T> stepped(Global<T> p, int64_t n) {
+  p += n;
+  asm("" : "+s"(p));
+  return p;
+}
+
+// Waits for the scalar loads in flight, and lets nothing later move before the wait.
+// Scalar loads return out of order, so the compiler's own wait for one row would, placed
+// at its first use, also wait for the next row's loads issued meanwhile.
+__device__ __forceinline__ void scalar_loads_done() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_sched_barrier(0);
 }
 template <typename E> __device__ __forceinline__ float value1(uint32_t w) {
   return __uint_as_float(sizeof(E) == 2 ? w << 16 : w);
 }
 
-// -exp(A_log) log2(e), the rate in base 2 that the kernels hold.  0 beyond N: such a
-// state keeps the 0 it starts with.
-template <int NS>
-__device__ __forceinline__ void scan_rates(const float* A_log, const ScanGeo& g, int d, int n0, float (&A2)[NS]) {
+// NS consecutive values of a row of N from n0 on, 0 beyond the row.  WHOLE: the row is a
+// multiple of NS, and is read four values at a time (dword alignment is enough for that).
+typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
+template <int NS, bool WHOLE>
+__device__ __forceinline__ void row_load(const float* p, int N, int n0, float (&v)[NS]) {
+  if constexpr (WHOLE) {
 #pragma unroll
-  for (int j = 0; j < NS; ++j)
-    A2[j] = n0 + j < g.N ? -expf(A_log[(int64_t)d * g.N + n0 + j]) * kLog2e : 0.f;
+    for (int j = 0; j < NS; j += 4) {
+      const f32x4 q = *reinterpret_cast<const f32x4_u*>(p + n0 + j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[j + i] = q[i];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      const float q = p[min(n0 + j, N - 1)];
+      v[j] = n0 + j < N ? q : 0.f;
+    }
+  }
 }
 
-template <int NS>
-__device__ __forceinline__ void state_load(const float* st, const ScanGeo& g, int n, int d, int n0, float (&h)[NS]) {
-  const float* p = st ? st + ((int64_t)n * g.D + d) * g.N : nullptr;
+// -exp(A_log) log2(e), the rate in base 2 that the kernels hold.  0 beyond N: such a
+// state keeps the 0 it starts with.
+__device__ __forceinline__ float scan_rate(float a_log) { return -fast_exp2(a_log * kLog2e) * kLog2e; }
+template <int NS, bool WHOLE>
+__device__ __forceinline__ void scan_rates(const float* A_log, const ScanGeo& g, int d, int n0, float (&A2)[NS]) {
+  row_load<NS, WHOLE>(A_log + (int64_t)d * g.N, g.N, n0, A2);
 #pragma unroll
-  for (int j = 0; j < NS; ++j) h[j] = p && n0 + j < g.N ? p[n0 + j] : 0.f;
+  for (int j = 0; j < NS; ++j) A2[j] = WHOLE || n0 + j < g.N ? scan_rate(A2[j]) : 0.f;
 }
-template <int NS>
+
+template <int NS, bool WHOLE>
+__device__ __forceinline__ void state_load(const float* st, const ScanGeo& g, int n, int d, int n0, float (&h)[NS]) {
+  if (st) {
+    row_load<NS, WHOLE>(st + ((int64_t)n * g.D + d) * g.N, g.N, n0, h);
+  } else {
+#pragma unroll
+    for (int j = 0; j < NS; ++j) h[j] = 0.f;
+  }
+}
+template <int NS, bool WHOLE>
 __device__ __forceinline__ void state_store(float* st, const ScanGeo& g, int n, int d, int n0, const float (&h)[NS]) {
   float* p = st + ((int64_t)n * g.D + d) * g.N;
+  if constexpr (WHOLE) {
 #pragma unroll
-  for (int j = 0; j < NS; ++j)
-    if (n0 + j < g.N) p[n0 + j] = h[j];
+    for (int j = 0; j < NS; j += 4)
+      *reinterpret_cast<f32x4_u*>(p + n0 + j) = f32x4{h[j], h[j + 1], h[j + 2], h[j + 3]};
+  } else {
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+      if (n0 + j < g.N) p[n0 + j] = h[j];
+  }
 }
 
 // Block id -> (tile of the whole batch, group of 64 channels); the lane's channel d,
@@ -104,6 +183,22 @@ struct ScanPlace {
   }
 };
 
+// The lane's states in [tile][np][D].
+template <int NS>
+__device__ __forceinline__ void tile_state_load(const float* st, const ScanGeo& g, const ScanPlace& w, float (&h)[NS]) {
+  Global<const float> row = (Global<const float>)st + ((int64_t)w.tile * g.np + w.n0) * g.D;
+  const uint32_t off = lane_offset(w.d * 4u);
+#pragma unroll
+  for (int j = 0; j < NS; ++j, row = stepped<const float>(row, g.D)) h[j] = __uint_as_float(load1<float>(row, off));
+}
+template <int NS>
+__device__ __forceinline__ void tile_state_store(float* st, const ScanGeo& g, const ScanPlace& w, const float (&h)[NS]) {
+  Global<float> row = (Global<float>)st + ((int64_t)w.tile * g.np + w.n0) * g.D;
+  const uint32_t off = lane_offset(w.d * 4u);
+#pragma unroll
+  for (int j = 0; j < NS; ++j, row = stepped<float>(row, g.D)) store1<float>(row, off, h[j]);
+}
+
 // A sequence without tokens ends as it starts.
 __device__ __forceinline__ void scan_empty_state(const ScanGeo& g, int n, const float* from, float* to) {
   const int64_t start = g.cu ? seq_offset(g.cu, n, g.T) : 0;
@@ -117,7 +212,7 @@ __device__ __forceinline__ void scan_empty_state(const ScanGeo& g, int n, const 
 // [tile][D] written; a sum of -1 says that a sequence starts in the tile, so nothing
 // passes through it), or the outputs (`states` holds the tiles' start states).
 // Blocks behind the last tile's copy the states of empty sequences (not ENDS).
-template <typename E, typename BE, int NS, bool SPLIT, bool ENDS>
+template <typename E, typename BE, int NS, bool WHOLE, bool SPLIT, bool ENDS>
 __global__ __launch_bounds__(SPLIT ? 64 * kScanMaxWaves : 64) void gdn_scan_kernel(
     ScanGeo g, Src x, const E* __restrict__ dt, Src z, const float* __restrict__ A_log,
     const BE* __restrict__ Bm, const BE* __restrict__ Cm, const float* __restrict__ skip,
@@ -136,14 +231,10 @@ __global__ __launch_bounds__(SPLIT ? 64 * kScanMaxWaves : 64) void gdn_scan_kern
   ScanPlace w;
   w.init<NS>(g, blockIdx.x);
   float A2[NS], h[NS];
-  scan_rates<NS>(A_log, g, w.d, w.n0, A2);
+  scan_rates<NS, WHOLE>(A_log, g, w.d, w.n0, A2);
   const float bias = dt_bias ? dt_bias[w.d] : 0.f, sk = skip ? skip[w.d] : 0.f;
-  const E* xd = static_cast<const E*>(x.p) + w.d;
-  const E* dtd = dt + w.d;
-  const E* zd = static_cast<const E*>(z.p) + w.d;
-  const bool gate = z.p != nullptr && !ENDS;
-  const BE* bp = Bm + (int64_t)w.gi * g.bgs + w.n0;
-  const BE* cp = Cm + (int64_t)w.gi * g.cgs + w.n0;
+  const uint32_t off = lane_offset(w.d * (uint32_t)sizeof(E));
+  const bool gate = !ENDS && z.p != nullptr;
   float sum = 0.f;
   int buf = 0;
 
@@ -153,123 +244,207 @@ __global__ __launch_bounds__(SPLIT ? 64 * kScanMaxWaves : 64) void gdn_scan_kern
   for (int j = 0; j < NS; ++j) h[j] = 0.f;
   for (; !run.done(); run.next()) {
     if (run.ta > run.start) {
-      if constexpr (!ENDS) {
-        const float* p = states + ((int64_t)w.tile * g.np + w.n0) * g.D + w.d;
-#pragma unroll
-        for (int j = 0; j < NS; ++j) h[j] = p[(int64_t)j * g.D];
-      }
+      if constexpr (!ENDS) tile_state_load<NS>(states, g, w, h);
     } else {
-      state_load<NS>(h0, g, run.n, w.d, w.n0, h);
+      state_load<NS, WHOLE>(h0, g, run.n, w.d, w.n0, h);
       sum = -1.f;
     }
-    uint32_t rx[U], rd[U], rz[U] = {};
-    auto fetch = [&](int t) {
+    Global<const E> xr = (Global<const E>)x.p + run.ta * x.ld, dr = (Global<const E>)dt + run.ta * g.lddt;
+    Global<const E> zr = (Global<const E>)z.p + run.ta * z.ld;
+    Global<E> yr = (Global<E>)y + (int64_t)run.ta * g.D;
+    Global<const BE> br = (Global<const BE>)Bm + run.ta * g.ldb + (int64_t)w.gi * g.bgs + w.n0;
+    Global<const BE> cr = (Global<const BE>)Cm + run.ta * g.ldc + (int64_t)w.gi * g.cgs + w.n0;
+    const Global<const BE> b0 = (Global<const BE>)Bm + (int64_t)w.gi * g.bgs + w.n0;
+    const Global<const BE> c0 = (Global<const BE>)Cm + (int64_t)w.gi * g.cgs + w.n0;
+    RowAhead ahead;
+    ahead.send<BE>(b0, ENDS ? b0 : c0, g.ldb, ENDS ? g.ldb : g.ldc, run.ta, run.tb);
+    ScalarRow<BE, NS> b, c;
+    b.load(br);
+    if constexpr (!ENDS) c.load(cr);
+    // One token with its row of Bm and Cm in flight; `more`: the run goes on, so the next
+    // token's rows are sent for.  Returns sum_n Cm h.
+    auto step = [&](float xv, float dl, bool more) {
+      scalar_loads_done();
+      const ScalarRow<BE, NS> bt = b, ct = c;
+      if (more) {
+        br = stepped<const BE>(br, g.ldb);
+        cr = stepped<const BE>(cr, g.ldc);
+      }
+      b.load(br);
+      if constexpr (!ENDS) c.load(cr);
+      const float u = dl * xv;
+      float a[NS];
+#pragma unroll
+      for (int j = 0; j < NS; ++j) a[j] = fast_exp2(dl * A2[j]);
+      __builtin_amdgcn_sched_barrier(0);
+      float acc0 = 0.f, acc1 = 0.f;
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        h[j] = fmaf(a[j], h[j], bt[j] * u);
+        if constexpr (!ENDS) {
+          if (j & 1) acc1 = fmaf(ct[j], h[j], acc1);
+          else acc0 = fmaf(ct[j], h[j], acc0);
+        }
+      }
+      return acc0 + acc1;
+    };
+    auto finish = [&](float acc, float xv, float gv, Global<E> row) {
+      const float o = fmaf(sk, xv, acc) * gv;
+      if (w.on) store1<E>(row, off, o);
+    };
+    // SPLIT: the waves' parts of a group's outputs are added through LDS, each wave
+    // finishing every nw-th token.  The other buffer is written next, and the barrier
+    // after that keeps this one until all have read it.
+    auto add_waves = [&](const float (&xv)[U], const float (&gv)[U], int n) {
+      __syncthreads();
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        const int64_t q = min(t + k, run.tb - 1);
-        rx[k] = load1<E>(xd + q * x.ld);
-        rd[k] = load1<E>(dtd + q * g.lddt);
-        if (gate) rz[k] = load1<E>(zd + q * z.ld);
+        if (k >= n || k % g.nw != w.wave) continue;
+        float acc = 0.f;
+        for (int q = 0; q < g.nw; ++q) acc += part[buf][q][k][w.lane];
+        finish(acc, xv[k], gv[k], yr + (int64_t)k * g.D);
+      }
+      buf ^= 1;
+    };
+    // first what is over whole groups, token by token, then the groups, the next one's
+    // rows on their way while one is computed
+    const int over = (run.tb - run.ta) % U;
+    for (int k = 0; k < over; ++k) {
+      const float xv = value1<E>(load1<E>(xr, off)), dl = softplus_flat(value1<E>(load1<E>(dr, off)) + bias);
+      float gv = 1.f;
+      if (gate) {
+        const float zv = value1<E>(load1<E>(zr, off));
+        gv = zv * fast_sigmoid(zv);
+      }
+      const float acc = step(xv, dl, run.ta + k + 1 < run.tb);
+      if constexpr (ENDS) {
+        if (sum >= 0.f) sum += dl;
+      } else if constexpr (SPLIT) {
+        float xs[U] = {xv}, gs[U] = {gv};
+        part[buf][w.wave][0][w.lane] = acc;
+        add_waves(xs, gs, 1);
+      } else {
+        finish(acc, xv, gv, yr);
+      }
+      xr += x.ld;
+      dr += g.lddt;
+      zr += z.ld;
+      yr += g.D;
+    }
+    uint32_t rx[U], rd[U], rz[U] = {};
+    auto fetch = [&]() {
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        rx[k] = load1<E>(xr, off);
+        rd[k] = load1<E>(dr, off);
+        xr = stepped<const E>(xr, x.ld);
+        dr = stepped<const E>(dr, g.lddt);
+      }
+      if (gate) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          rz[k] = load1<E>(zr, off);
+          zr = stepped<const E>(zr, z.ld);
+        }
       }
     };
-    ScalarRow<BE, NS> b, c;
-    fetch(run.ta);
-    b.load(bp + run.ta * g.ldb);
-    if constexpr (!ENDS) c.load(cp + run.ta * g.ldc);
-    for (int t = run.ta; t < run.tb; t += U) {
-      float xv[U], dl[U], zv[U];
+    if (run.ta + over < run.tb) fetch();
+    for (int t = run.ta + over; t < run.tb; t += U) {
+      float xv[U], dl[U], gv[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         xv[k] = value1<E>(rx[k]);
-        zv[k] = value1<E>(rz[k]);
         dl[k] = softplus_flat(value1<E>(rd[k]) + bias);
+        gv[k] = 1.f;
       }
-      if (t + U < run.tb) fetch(t + U);
+      if (gate) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const float zv = value1<E>(rz[k]);
+          gv[k] = zv * fast_sigmoid(zv);
+        }
+      }
+      const bool more = t + U < run.tb;
+      if (more) fetch();
+      if (((t - run.ta - over) & 63) == 0 && t + 64 < run.tb) {
+        ahead.land();
+        ahead.send<BE>(b0, ENDS ? b0 : c0, g.ldb, ENDS ? g.ldb : g.ldc, t + 64, run.tb);
+      }
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        if (t + k >= run.tb) break;
-        const ScalarRow<BE, NS> bt = b, ct = c;
-        const int64_t q = min(t + k + 1, run.tb - 1);
-        b.load(bp + q * g.ldb);
-        if constexpr (!ENDS) c.load(cp + q * g.ldc);
-        const float u = dl[k] * xv[k];
-        float acc0 = 0.f, acc1 = 0.f;
-#pragma unroll
-        for (int j = 0; j < NS; ++j) {
-          h[j] = fmaf(fast_exp2(dl[k] * A2[j]), h[j], bt[j] * u);
-          if constexpr (!ENDS) {
-            if (j & 1) acc1 = fmaf(ct[j], h[j], acc1);
-            else acc0 = fmaf(ct[j], h[j], acc0);
-          }
-        }
+        const float acc = step(xv[k], dl[k], k + 1 < U || more);
         if constexpr (ENDS) {
           if (sum >= 0.f) sum += dl[k];
         } else if constexpr (SPLIT) {
-          part[buf][w.wave][k][w.lane] = acc0 + acc1;
+          part[buf][w.wave][k][w.lane] = acc;
         } else {
-          float o = fmaf(sk, xv[k], acc0 + acc1);
-          if (gate) o *= zv[k] * fast_sigmoid(zv[k]);
-          if (w.on) y[(int64_t)(t + k) * g.D + w.d] = (E)o;
+          finish(acc, xv[k], gv[k], yr);
+          yr = stepped<E>(yr, g.D);
         }
       }
       if constexpr (SPLIT && !ENDS) {
-        // each wave finishes every nw-th token; the other buffer is written next, and
-        // the barrier after that keeps this one until all have read it
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-          if (k % g.nw != w.wave || t + k >= run.tb) continue;
-          float o = sk * xv[k];
-          for (int q = 0; q < g.nw; ++q) o += part[buf][q][k][w.lane];
-          if (gate) o *= zv[k] * fast_sigmoid(zv[k]);
-          if (w.on) y[(int64_t)(t + k) * g.D + w.d] = (E)o;
-        }
-        buf ^= 1;
+        add_waves(xv, gv, U);
+        yr += (int64_t)U * g.D;
       }
     }
+    ahead.land();
     if constexpr (!ENDS)
-      if (fin && w.on && run.tb == run.end) state_store<NS>(fin, g, run.n, w.d, w.n0, h);
+      if (fin && w.on && run.tb == run.end) state_store<NS, WHOLE>(fin, g, run.n, w.d, w.n0, h);
   }
   if constexpr (ENDS) {
     if (!w.on) return;
-    float* p = states + ((int64_t)w.tile * g.np + w.n0) * g.D + w.d;
-#pragma unroll
-    for (int j = 0; j < NS; ++j) p[(int64_t)j * g.D] = h[j];
+    tile_state_store<NS>(states, g, w, h);
     if (w.wave == 0) sums[(int64_t)w.tile * g.D + w.d] = sum;
   }
 }
 
 // (2): states [row of the batch][tile][np][D] from end states to start states, in
-// place; one lane per (row, state, channel).
-static __global__ __launch_bounds__(256) void gdn_scan_join_kernel(ScanGeo g, const float* __restrict__ A_log,
+// place; one lane per (row, state, channel).  BACK: from the last tile to the first, from
+// what each tile adds to the state gradient before it to the gradient of its end state
+// (the backward pass's).  A chain of a few operations per tile: what it takes is the
+// latency of its loads, so U tiles are sent for ahead of the U being joined, and before
+// anything else.
+template <bool BACK>
+__global__ __launch_bounds__(256) void gdn_scan_join_kernel(ScanGeo g, const float* __restrict__ A_log,
                                                             const float* __restrict__ h0,
                                                             float* __restrict__ states,
                                                             const float* __restrict__ sums) {
-  constexpr int U = 8;
-  const int64_t per = (int64_t)g.np * g.D;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int rows = g.cu ? 1 : g.B;
-  if (i >= rows * per) return;
-  const int row = (int)(i / per);
-  const int64_t r = i - row * per;
-  const int n = (int)(r / g.D), d = (int)(r - (int64_t)n * g.D);
-  const float A2 = n < g.N ? -expf(A_log[(int64_t)d * g.N + n]) * kLog2e : 0.f;
-  float H = !g.cu && h0 && n < g.N ? h0[((int64_t)row * g.D + d) * g.N + n] : 0.f;
-  float* p = states + (int64_t)row * g.ntiles * per + r;
-  const float* s = sums + (int64_t)row * g.ntiles * g.D + d;
-  for (int t = 0; t < g.ntiles; t += U) {
-    float e[U], sm[U];
+  constexpr int U = 16;
+  const uint32_t per = (uint32_t)g.np * g.D;  // checked on the host: below 2^31
+  const uint32_t r = blockIdx.x * 256u + threadIdx.x;
+  if (r >= per) return;
+  const int row = blockIdx.y, last = g.ntiles - 1;
+  const uint32_t n = r / g.D, d = r - n * g.D;
+  float* p = states + (int64_t)row * g.ntiles * per;
+  const float* s = sums + (int64_t)row * g.ntiles * g.D;
+  float e[U], sm[U];
+  auto fetch = [&](int t) {
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const int q = min(t + k, g.ntiles - 1);
-      e[k] = p[q * per];  // the last tile's is not written by (1) and not used
-      sm[k] = s[(int64_t)q * g.D];
+      const int q = min(t + k, last);
+      const int64_t at = BACK ? last - q : q;
+      e[k] = (p + at * per)[r];
+      sm[k] = (s + at * g.D)[d];
     }
+  };
+  fetch(0);
+  const int64_t sd = (int64_t)d * g.N + min(n, (uint32_t)g.N - 1);
+  const bool in = n < (uint32_t)g.N;
+  float H = !BACK && !g.cu && h0 ? h0[(int64_t)row * g.D * g.N + sd] : 0.f;
+  H = in ? H : 0.f;
+  const float A2 = in ? scan_rate(A_log[sd]) : 0.f;
+  for (int t = 0; t <= last; t += U) {
+    float out[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {  // beyond the last tile: not stored
+      out[k] = H;
+      H = sm[k] < 0.f ? e[k] : fmaf(fast_exp2(A2 * sm[k]), H, e[k]);
+    }
+    if (t + U <= last) fetch(t + U);
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      if (t + k >= g.ntiles) break;
-      p[(t + k) * per] = H;
-      H = sm[k] < 0.f ? e[k] : fmaf(fast_exp2(A2 * sm[k]), H, e[k]);
+      if (t + k > last) break;
+      (p + (int64_t)(BACK ? last - (t + k) : t + k) * per)[r] = out[k];
     }
   }
 }
@@ -318,7 +493,7 @@ __global__ __launch_bounds__(256) void gdn_scan_decode_kernel(
 #pragma unroll
     for (int j = 0; j < 4; ++j) h[j] = n0 + j < g.N ? hp[j] : 0.f;
   }
-  scan_rates<4>(A_log, g, d, n0, A2);
+  scan_rates<4, false>(A_log, g, d, n0, A2);
   const float bias = dt_bias ? dt_bias[d] : 0.f, sk = skip ? skip[d] : 0.f;
   for (int t = 0; t < g.T; ++t) {
     const int64_t tok = b * g.T + t;

@@ -1,53 +1,54 @@
 // gdn_scan_api.hip -- entry points of the selective scan's forward pass and decode
 // step: validation, tiles and launches.  See include/gdn.h.
 #include "gdn_scan_host.h"
+#include <cstdlib>
 
 namespace {
 
-gdn_status_t fwd_sizes(const gdn_scan_params_t* p, bool packed, ScanPlan* pl) {
-  const gdn_status_t st = scan_sizes(p, packed, pl);
-  if (st == GDN_OK) scan_waves(pl, p->N <= 8 ? 8 : 16);
-  return st;
-}
+// Tokens per tile: as many as leave about 16 waves per CU (256 CUs taken for granted, so
+// that sizes alone decide), 16 at least; one tile per sequence where its waves alone come
+// to a quarter of that.
+// TODO measured
+constexpr int kTileWaves = 256 * 16, kLeastTile = 16;
 
-// Tokens per tile.  One tile per sequence where its waves alone keep the device busy
-// (or the sequences are short); else tiles for about kWaves waves per CU, of kLeast
-// tokens at least.
-constexpr int kWavesPerCu = 16, kLeastTile = 64;
-
-int scan_fwd_len(const ScanPlan& pl, int cus) {
+int scan_fwd_len(const ScanPlan& pl) {
+  if (getenv("TILE")) return atoi(getenv("TILE"));
   const gdn::ScanGeo& g = pl.geo;
   const int64_t waves = (int64_t)g.cgroups * g.nw * (pl.packed ? 1 : g.B);  // of one tile per row
-  const int64_t want = (int64_t)cus * kWavesPerCu;
-  if (g.T <= kLeastTile || (!pl.packed && waves * 4 >= want)) return std::max(g.T, 1);
-  const int64_t tiles = std::max<int64_t>(want / std::max<int64_t>(waves, 1), 1);
+  if (g.T <= kLeastTile || (!pl.packed && waves * 4 >= kTileWaves)) return std::max(g.T, 1);
+  const int64_t tiles = std::max<int64_t>(kTileWaves / waves, 1);
   const int64_t len = ceil_div(ceil_div(g.T, tiles), gdn::kScanGroup) * gdn::kScanGroup;
   return (int)std::max<int64_t>(len, kLeastTile);
 }
 
-// f(E, BE, NS, SPLIT) as default-constructed tags.
+gdn_status_t fwd_sizes(const gdn_scan_params_t* p, bool packed, ScanPlan* pl) {
+  const gdn_status_t st = scan_sizes(p, packed, pl);
+  if (st != GDN_OK) return st;
+  const int ns = p->N <= 8 ? 8 : 16;
+  scan_waves(pl, ns, (int)ceil_div(p->N, ns));
+  scan_tiles(pl, scan_fwd_len(*pl));
+  return GDN_OK;
+}
+
+// f(E, BE, NS, WHOLE, SPLIT) as default-constructed tags.
 template <typename F> gdn_status_t scan_dispatch(const ScanPlan& pl, bool direct, F&& f) {
-  auto split = [&](auto e, auto be, auto ns) {
-    return pl.geo.nw > 1 ? f(e, be, ns, std::true_type{}) : f(e, be, ns, std::false_type{});
+  using Yes = std::true_type;
+  using No = std::false_type;
+  auto states = [&](auto e, auto be, auto whole) {
+    if (pl.ns == 8) return f(e, be, std::integral_constant<int, 8>{}, whole, No{});
+    const std::integral_constant<int, 16> ns;
+    return pl.geo.nw > 1 ? f(e, be, ns, whole, Yes{}) : f(e, be, ns, whole, No{});
   };
-  auto states = [&](auto e, auto be) {
-    if (pl.ns == 8) return f(e, be, std::integral_constant<int, 8>{}, std::false_type{});
-    return split(e, be, std::integral_constant<int, 16>{});
-  };
-  if (pl.esz == 4) return states(0.f, 0.f);
-  return direct ? states(gdn::bf16{}, gdn::bf16{}) : states(gdn::bf16{}, 0.f);
+  if (pl.esz == 4) return direct ? states(0.f, 0.f, Yes{}) : states(0.f, 0.f, No{});
+  return direct ? states(gdn::bf16{}, gdn::bf16{}, Yes{}) : states(gdn::bf16{}, 0.f, No{});
 }
 
 struct FwdSpace {
   size_t states, sums, rows, total;
 };
-// For tiles of kLeastTile tokens, the shortest there are: the choice depends on the
-// device, the size of the workspace does not.
-FwdSpace fwd_space(ScanPlan pl) {
+FwdSpace fwd_space(const ScanPlan& pl) {
   FwdSpace w{};
-  const bool one = pl.geo.T <= kLeastTile;
-  scan_tiles(&pl, one ? std::max(pl.geo.T, 1) : kLeastTile);
-  const size_t tiles = one ? 0 : (size_t)scan_all_tiles(pl);
+  const size_t tiles = pl.geo.ntiles > 1 ? (size_t)scan_all_tiles(pl) : 0;
   size_t off = 0;
   w.states = off; off = align_up(off + tiles * pl.geo.np * pl.geo.D * 4);
   w.sums = off;   off = align_up(off + tiles * pl.geo.D * 4);
@@ -73,7 +74,6 @@ gdn_status_t scan_fwd_run(ScanPlan pl, const FwdArgs& a, void* ws, hipStream_t s
   char* w = static_cast<char*>(ws);
   float* states = reinterpret_cast<float*>(w + sp.states);
   float* sums = reinterpret_cast<float*>(w + sp.sums);
-  scan_tiles(&pl, scan_fwd_len(pl, device_cus()));
   const bool direct = scan_rows_direct(pl, a.Bm, a.Cm);
   const void *Bm = a.Bm, *Cm = a.Cm;
   hipError_t err = hipSuccess;
@@ -92,24 +92,22 @@ gdn_status_t scan_fwd_run(ScanPlan pl, const FwdArgs& a, void* ws, hipStream_t s
   if (main_blocks + empties > INT32_MAX) return GDN_ERR_UNSUPPORTED;
   if (pl.tok == 0) g.ntiles = 0;  // no tile blocks: the first block is the first sequence's
   if (main_blocks + empties == 0) return GDN_OK;
-  gdn_status_t st = scan_dispatch(pl, direct, [&](auto e, auto be, auto ns, auto split) {
+  gdn_status_t st = scan_dispatch(pl, direct, [&](auto e, auto be, auto ns, auto whole, auto split) {
     using E = decltype(e);
     using BE = decltype(be);
     constexpr int NS = decltype(ns)::value;
-    constexpr bool SPLIT = decltype(split)::value;
+    constexpr bool WHOLE = decltype(whole)::value, SPLIT = decltype(split)::value;
     const gdn::Src x{a.x, nullptr, pl.ldx}, z{a.z, nullptr, pl.ldz};
     const E* dt = static_cast<const E*>(a.dt);
     const BE *b = static_cast<const BE*>(Bm), *c = static_cast<const BE*>(Cm);
     E* y = static_cast<E*>(a.y);
     const dim3 block(64 * g.nw);
     if (g.ntiles > 1) {
-      ok(launch(gdn::gdn_scan_kernel<E, BE, NS, SPLIT, true>, dim3((unsigned)main_blocks), block, s, g, x, dt, z,
+      ok(launch(gdn::gdn_scan_kernel<E, BE, NS, WHOLE, SPLIT, true>, dim3((unsigned)main_blocks), block, s, g, x, dt, z,
                 a.A_log, b, c, a.skip, a.dt_bias, a.h0, states, sums, y, a.fin));
-      const int64_t lanes = (int64_t)(g.cu ? 1 : g.B) * g.np * g.D;
-      ok(launch(gdn::gdn_scan_join_kernel, dim3((unsigned)ceil_div(lanes, 256)), dim3(256), s, g, a.A_log, a.h0,
-                states, sums));
+      ok(launch(gdn::gdn_scan_join_kernel<false>, scan_join_grid(g), dim3(256), s, g, a.A_log, a.h0, states, sums));
     }
-    ok(launch(gdn::gdn_scan_kernel<E, BE, NS, SPLIT, false>, dim3((unsigned)(main_blocks + empties)), block, s, g, x,
+    ok(launch(gdn::gdn_scan_kernel<E, BE, NS, WHOLE, SPLIT, false>, dim3((unsigned)(main_blocks + empties)), block, s, g, x,
               dt, z, a.A_log, b, c, a.skip, a.dt_bias, a.h0, states, sums, y, a.fin));
     return GDN_OK;
   });

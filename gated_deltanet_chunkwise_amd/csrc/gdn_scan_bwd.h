@@ -28,18 +28,47 @@ namespace gdn {
 
 constexpr int kScanBwdStates = 8;  // states per lane
 constexpr int kScanBwdSub = 8;     // tokens per group
-// Tokens per tile: 64, or 32 where the kept states of eight waves would not fit in LDS.
-constexpr int scan_bwd_tile(int waves) { return waves > 4 ? 32 : 64; }
+// Tokens per tile.  The states that a tile keeps take 32 bytes of LDS per token and lane:
+// 64 tokens leave room for 8 waves per CU with up to two waves per workgroup (256
+// registers allow no more), 32 with more waves.
+constexpr int scan_bwd_tile(int waves) { return waves > 2 ? 32 : 64; }
 
-// One channel of one row, codes and scale of a checkpoint in one word.
-template <typename E> __device__ __forceinline__ uint32_t src_load1(const Src& s, int64_t row, int d, int nblk) {
-  if (s.scales)
-    return static_cast<const uint8_t*>(s.p)[row * s.ld + d] | (uint32_t)s.scales[row * nblk + (d >> 5)] << 8;
-  return load1<E>(static_cast<const E*>(s.p) + row * s.ld + d);
-}
-template <typename E> __device__ __forceinline__ float src_value1(const Src& s, uint32_t w) {
-  return s.scales ? (float)(int8_t)(w & 255u) * pack_scale(w >> 8) : value1<E>(w);
-}
+// U tokens' values of one channel as loaded, so that the loads are all in flight before
+// the first is converted.  CK: from a checkpoint, code and scale.
+template <typename E, int U, bool CK> struct TokenVals {
+  uint32_t w[U], s[CK ? U : 1];
+  // tokens t .. t + U - 1, those from `end` on held to the last before it; `off`: the
+  // lane's offset in bytes (CK: d and d / 32)
+  __device__ __forceinline__ void fetch(const Src& src, int t, int end, uint32_t off, uint32_t soff, int nblk) {
+    if (t + U <= end) walk(src, t, off, soff, nblk, [](int) { return true; });
+    else walk(src, t, off, soff, nblk, [&](int k) { return t + k + 1 < end; });
+  }
+  template <typename F>
+  __device__ __forceinline__ void walk(const Src& src, int t, uint32_t off, uint32_t soff, int nblk, F&& more) {
+    if constexpr (CK) {
+      Global<const uint8_t> p = (Global<const uint8_t>)src.p + (int64_t)t * src.ld;
+      Global<const uint8_t> q = (Global<const uint8_t>)src.scales + (int64_t)t * nblk;
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        w[k] = p[off];
+        s[k] = q[soff];
+        p = stepped<const uint8_t>(p, more(k) ? src.ld : 0);
+        q = stepped<const uint8_t>(q, more(k) ? nblk : 0);
+      }
+    } else {
+      Global<const E> p = (Global<const E>)src.p + (int64_t)t * src.ld;
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        w[k] = load1<E>(p, off);
+        p = stepped<const E>(p, more(k) ? src.ld : 0);
+      }
+    }
+  }
+  __device__ __forceinline__ float operator[](int k) const {
+    if constexpr (CK) return (float)(int8_t)w[k] * pack_scale(s[k]);
+    else return value1<E>(w[k]);
+  }
+};
 
 // Sums over the wave's 64 lanes of V values each (V = 16 or 32): returns the sum of
 // value lane / (64 / V).
@@ -84,12 +113,22 @@ struct ScanBwdGeo {
   int nblk;  // checkpoint scales per row
 };
 
+// softplus_flat(x) and its derivative, sigmoid(x) (1 where softplus is taken as x).
+__device__ __forceinline__ float softplus_both(float x, float& slope) {
+  const float y = __builtin_amdgcn_exp2f(x * kLog2e);
+  const float u = 1.f + y;
+  const float r = (__builtin_amdgcn_logf(u) * __builtin_amdgcn_rcpf(u - 1.f)) * (y * 0.693147180559945309f);
+  slope = x > 20.f ? 1.f : y * __builtin_amdgcn_rcpf(u);
+  return x > 20.f ? x : u == 1.f ? y : r;
+}
+
 // silu'(z) = s + z s (1 - s), s = sigmoid(z); 1 - s as sigmoid(-z).
 __device__ __forceinline__ float dsilu(float z, float s) { return fmaf(z * s, fast_sigmoid(-z), s); }
 
 // (1).  states, rev [tile][np][D]; sums, rsums [tile][D] (-1: nothing passes through).
-template <typename E, typename BE, int NS, int NW>
-__global__ __launch_bounds__(64 * NW) void gdn_scan_bwd_ends_kernel(
+// R needs no walk backwards: with P_t = a_1 .. a_t it is sum_t P_t Cm_t r_t.
+template <typename E, typename BE, int NS, bool WHOLE, bool CK>
+__global__ __launch_bounds__(64 * kScanMaxWaves) void gdn_scan_bwd_ends_kernel(
     ScanBwdGeo bg, Src x, const E* __restrict__ dt, Src z, const float* __restrict__ A_log,
     const BE* __restrict__ Bm, const BE* __restrict__ Cm, const float* __restrict__ dt_bias,
     const float* __restrict__ h0, const E* __restrict__ d_y, const float* __restrict__ d_fin,
@@ -100,10 +139,11 @@ __global__ __launch_bounds__(64 * NW) void gdn_scan_bwd_ends_kernel(
   ScanPlace w;
   w.init<NS>(g, blockIdx.x);
   float A2[NS], h[NS], P[NS], R[NS];
-  scan_rates<NS>(A_log, g, w.d, w.n0, A2);
+  scan_rates<NS, WHOLE>(A_log, g, w.d, w.n0, A2);
+  // lane offsets: of E, of a checkpoint's codes and scales
+  const uint32_t off = lane_offset(w.d * (uint32_t)sizeof(E)), xoff = CK ? lane_offset(w.d) : off;
+  const uint32_t soff = CK ? lane_offset((uint32_t)w.d >> 5) : 0;
   const float bias = dt_bias ? dt_bias[w.d] : 0.f;
-  const BE* bp = Bm + (int64_t)w.gi * g.bgs + w.n0;
-  const BE* cp = Cm + (int64_t)w.gi * g.cgs + w.n0;
   float sum = 0.f, rsum = -1.f;
 #pragma unroll
   for (int j = 0; j < NS; ++j) {
@@ -115,56 +155,78 @@ __global__ __launch_bounds__(64 * NW) void gdn_scan_bwd_ends_kernel(
   for (; !run.done(); run.next()) {
     const bool cont = run.ta > run.start;  // only a tile's first run can be
     if (!cont) {
-      state_load<NS>(h0, g, run.n, w.d, w.n0, h);
+      state_load<NS, WHOLE>(h0, g, run.n, w.d, w.n0, h);
       sum = -1.f;
     }
     float pass = 0.f;
+    Global<const BE> br = (Global<const BE>)Bm + run.ta * g.ldb + (int64_t)w.gi * g.bgs + w.n0;
+    Global<const BE> cr = (Global<const BE>)Cm + run.ta * g.ldc + (int64_t)w.gi * g.cgs + w.n0;
+    TokenVals<E, U, CK> rx, rz = {};
+    TokenVals<E, U, false> rd, ry = {};
+    auto fetch = [&](int t) {
+      rx.fetch(x, t, run.tb, xoff, soff, bg.nblk);
+      rd.fetch(Src{dt, nullptr, g.lddt}, t, run.tb, off, 0, 0);
+      if (cont) {
+        ry.fetch(Src{d_y, nullptr, g.D}, t, run.tb, off, 0, 0);
+        if (z.p) rz.fetch(z, t, run.tb, xoff, soff, bg.nblk);
+      }
+    };
+    RowAhead ahead;  // a tile is 64 tokens at most
+    ahead.send<BE>((Global<const BE>)Bm + (int64_t)w.gi * g.bgs + w.n0, (Global<const BE>)Cm + (int64_t)w.gi * g.cgs + w.n0,
+                   g.ldb, g.ldc, run.ta, run.tb);
+    ScalarRow<BE, NS> b, c;
+    b.load(br);
+    c.load(cr);
+    fetch(run.ta);
     for (int t = run.ta; t < run.tb; t += U) {
-      uint32_t rx[U], rd[U], ry[U] = {}, rz[U] = {};
+      float u[U], dl[U], r[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        const int64_t q = min(t + k, run.tb - 1);
-        rx[k] = src_load1<E>(x, q, w.d, bg.nblk);
-        rd[k] = load1<E>(dt + q * g.lddt + w.d);
-        if (cont) {
-          ry[k] = load1<E>(d_y + q * g.D + w.d);
-          if (z.p) rz[k] = src_load1<E>(z, q, w.d, bg.nblk);
+        dl[k] = softplus_flat(rd[k] + bias);
+        u[k] = dl[k] * rx[k];
+        r[k] = ry[k];
+      }
+      if (z.p) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const float zv = rz[k];
+          r[k] *= zv * fast_sigmoid(zv);
         }
       }
+      if (t + U < run.tb) fetch(t + U);
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         if (t + k >= run.tb) break;
-        ScalarRow<BE, NS> b;
-        b.load(bp + (int64_t)(t + k) * g.ldb);
-        const float dl = softplus_flat(value1<E>(rd[k]) + bias);
-        const float u = dl * src_value1<E>(x, rx[k]);
+        scalar_loads_done();
+        const ScalarRow<BE, NS> bt = b, ct = c;
+        if (t + k + 1 < run.tb) {
+          br = stepped<const BE>(br, g.ldb);
+          cr = stepped<const BE>(cr, g.ldc);
+        }
+        b.load(br);
+        c.load(cr);
+        float a[NS];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) a[j] = fast_exp2(dl[k] * A2[j]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < NS; ++j) h[j] = fmaf(a[j], h[j], bt[j] * u[k]);
         if (cont) {
-          ScalarRow<BE, NS> c;
-          c.load(cp + (int64_t)(t + k) * g.ldc);
-          float r = value1<E>(ry[k]);
-          if (z.p) {
-            const float zv = src_value1<E>(z, rz[k]);
-            r *= zv * fast_sigmoid(zv);
-          }
-          pass += dl;
+          pass += dl[k];
 #pragma unroll
           for (int j = 0; j < NS; ++j) {
-            const float a = fast_exp2(dl * A2[j]);
-            h[j] = fmaf(a, h[j], b[j] * u);
-            P[j] *= a;
-            R[j] = fmaf(P[j], c[j] * r, R[j]);
+            P[j] *= a[j];
+            R[j] = fmaf(P[j], ct[j] * r[k], R[j]);
           }
-        } else {
-#pragma unroll
-          for (int j = 0; j < NS; ++j) h[j] = fmaf(fast_exp2(dl * A2[j]), h[j], b[j] * u);
         }
       }
     }
+    ahead.land();
     if (sum >= 0.f) sum += pass;
     if (cont) {
       if (run.tb == run.end) {
         float f[NS];
-        state_load<NS>(d_fin, g, run.n, w.d, w.n0, f);
+        state_load<NS, WHOLE>(d_fin, g, run.n, w.d, w.n0, f);
 #pragma unroll
         for (int j = 0; j < NS; ++j) R[j] = fmaf(P[j], f[j], R[j]);
       } else {
@@ -173,49 +235,11 @@ __global__ __launch_bounds__(64 * NW) void gdn_scan_bwd_ends_kernel(
     }
   }
   if (!w.on) return;
-  const int64_t at = ((int64_t)w.tile * g.np + w.n0) * g.D + w.d;
-#pragma unroll
-  for (int j = 0; j < NS; ++j) {
-    states[at + (int64_t)j * g.D] = h[j];
-    rev[at + (int64_t)j * g.D] = R[j];
-  }
+  tile_state_store<NS>(states, g, w, h);
+  tile_state_store<NS>(rev, g, w, R);
   if (w.wave == 0) {
     sums[(int64_t)w.tile * g.D + w.d] = sum;
     rsums[(int64_t)w.tile * g.D + w.d] = rsum;
-  }
-}
-
-// (2), backwards: rev from what each tile sends to the state before it to the gradient
-// of each tile's end state, in place.
-__global__ __launch_bounds__(256) void gdn_scan_bwd_join_kernel(ScanGeo g, const float* __restrict__ A_log,
-                                                                float* __restrict__ rev,
-                                                                const float* __restrict__ rsums) {
-  constexpr int U = 8;
-  const int64_t per = (int64_t)g.np * g.D;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int rows = g.cu ? 1 : g.B;
-  if (i >= rows * per) return;
-  const int row = (int)(i / per);
-  const int64_t r = i - row * per;
-  const int n = (int)(r / g.D), d = (int)(r - (int64_t)n * g.D);
-  const float A2 = n < g.N ? -expf(A_log[(int64_t)d * g.N + n]) * kLog2e : 0.f;
-  float G = 0.f;
-  float* p = rev + (int64_t)row * g.ntiles * per + r;
-  const float* s = rsums + (int64_t)row * g.ntiles * g.D + d;
-  for (int t = g.ntiles - 1; t >= 0; t -= U) {
-    float e[U], sm[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int q = max(t - k, 0);
-      e[k] = p[q * per];
-      sm[k] = s[(int64_t)q * g.D];
-    }
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      if (t - k < 0) break;
-      p[(t - k) * per] = G;
-      G = sm[k] < 0.f ? e[k] : fmaf(fast_exp2(A2 * sm[k]), G, e[k]);
-    }
   }
 }
 
@@ -223,8 +247,11 @@ __global__ __launch_bounds__(256) void gdn_scan_bwd_join_kernel(ScanGeo g, const
 // sum_t D q; rev the end states' gradients.  pbc [channel wave][token][2][np]: the
 // wave's parts of dBm and dCm.  psum [tile][NW][2][D]: of dskip and ddt_bias.  Blocks
 // behind the last tile's copy d_final to d_initial for empty sequences.
-template <typename E, typename BE, int NS, int NW, int SUB>
-__global__ __launch_bounds__(64 * NW) void gdn_scan_bwd_kernel(
+//
+// The waves of a workgroup (NS states each) add their sums over the states, three per
+// token, through LDS: token k of a group is finished by wave k % NW.
+template <typename E, typename BE, int NS, bool WHOLE, int NW, int SUB, bool CK>
+__global__ __launch_bounds__(64 * NW, 2) void gdn_scan_bwd_kernel(
     ScanBwdGeo bg, Src x, const E* __restrict__ dt, Src z, const float* __restrict__ A_log,
     const BE* __restrict__ Bm, const BE* __restrict__ Cm, const float* __restrict__ skip,
     const float* __restrict__ dt_bias, const float* __restrict__ h0, const E* __restrict__ d_y,
@@ -232,7 +259,7 @@ __global__ __launch_bounds__(64 * NW) void gdn_scan_bwd_kernel(
     E* __restrict__ dx, E* __restrict__ ddt, E* __restrict__ dz, float* __restrict__ pbc,
     float* __restrict__ psum, float* __restrict__ dh0) {
   __shared__ float hs[scan_bwd_tile(NW) / SUB][NW][NS][64];
-  __shared__ float part[NW > 1 ? NW : 1][NW > 1 ? SUB : 1][3][NW > 1 ? 64 : 1];
+  __shared__ float part[NW > 1 ? SUB : 1][NW > 1 ? NW - 1 : 1][3][NW > 1 ? 64 : 1];
   const ScanGeo& g = bg.g;
   const int64_t ntok = (int64_t)g.B * g.T;
   const uint32_t main_blocks = (uint32_t)(g.ntiles * (g.cu ? 1 : g.B)) * g.cgroups;
@@ -243,17 +270,21 @@ __global__ __launch_bounds__(64 * NW) void gdn_scan_bwd_kernel(
   ScanPlace w;
   w.init<NS>(g, blockIdx.x);
   const int cg = blockIdx.x % g.cgroups;
+  // lane offsets: of E, of a checkpoint's codes and scales
+  const uint32_t off = lane_offset(w.d * (uint32_t)sizeof(E)), xoff = CK ? lane_offset(w.d) : off;
+  const uint32_t soff = CK ? lane_offset((uint32_t)w.d >> 5) : 0;
+  const bool gate = z.p != nullptr;
   float A2[NS], dA[NS], h[NS], l[NS];
-  scan_rates<NS>(A_log, g, w.d, w.n0, A2);
+  scan_rates<NS, WHOLE>(A_log, g, w.d, w.n0, A2);
   const float bias = dt_bias ? dt_bias[w.d] : 0.f, sk = skip ? skip[w.d] : 0.f;
-  const BE* bp = Bm + (int64_t)w.gi * g.bgs + w.n0;
-  const BE* cp = Cm + (int64_t)w.gi * g.cgs + w.n0;
+  const Global<const BE> bp = (Global<const BE>)Bm + (int64_t)w.gi * g.bgs + w.n0;
+  const Global<const BE> cp = (Global<const BE>)Cm + (int64_t)w.gi * g.cgs + w.n0;
   float dskip = 0.f, dbias = 0.f;
-  const int64_t at = ((int64_t)w.tile * g.np + w.n0) * g.D + w.d;
   // this wave's place in a token's row of pbc: lane v of dBm and dCm's 2 NS values
   constexpr int kRep = 64 / (2 * NS);
   const int v = w.lane / kRep;
-  float* pb = pbc + ((int64_t)cg * ntok) * 2 * g.np + (v / NS) * g.np + w.n0 + v % NS;
+  const Global<float> pb = (Global<float>)pbc + (int64_t)cg * ntok * 2 * g.np;
+  const uint32_t pboff = lane_offset(((v / NS) * g.np + w.n0 + v % NS) * 4u);
 #pragma unroll
   for (int j = 0; j < NS; ++j) dA[j] = 0.f;
 
@@ -261,212 +292,232 @@ __global__ __launch_bounds__(64 * NW) void gdn_scan_bwd_kernel(
     const int last = max(uniform<true>(seq_offset(g.cu, g.S, g.T)), w.tile * g.len);
     for (int t = last; t < min((w.tile + 1) * g.len, g.T); ++t) {
       if (w.on && w.wave == 0) {
-        dx[(int64_t)t * g.D + w.d] = (E)0.f;
-        ddt[(int64_t)t * g.D + w.d] = (E)0.f;
-        if (z.p) dz[(int64_t)t * g.D + w.d] = (E)0.f;
+        store1<E>((Global<E>)dx + (int64_t)t * g.D, off, 0.f);
+        store1<E>((Global<E>)ddt + (int64_t)t * g.D, off, 0.f);
+        if (gate) store1<E>((Global<E>)dz + (int64_t)t * g.D, off, 0.f);
       }
-      if (w.lane % kRep == 0) pb[(int64_t)t * 2 * g.np] = 0.f;
+      if (w.lane % kRep == 0) store1<float>(pb + (int64_t)t * 2 * g.np, pboff, 0.f);
     }
   }
 
   Run<true> run;
   run.init(g.cu, g.T, g.S, w.tile, g.ntiles, g.len);
   for (; !run.done(); run.next()) {
-    if (run.ta > run.start) {
-#pragma unroll
-      for (int j = 0; j < NS; ++j) h[j] = states[at + (int64_t)j * g.D];
-    } else {
-      state_load<NS>(h0, g, run.n, w.d, w.n0, h);
-    }
-    if (run.tb == run.end) {
-      state_load<NS>(d_fin, g, run.n, w.d, w.n0, l);
-    } else {
-#pragma unroll
-      for (int j = 0; j < NS; ++j) l[j] = rev[at + (int64_t)j * g.D];
-    }
+    if (run.ta > run.start) tile_state_load<NS>(states, g, w, h);
+    else state_load<NS, WHOLE>(h0, g, run.n, w.d, w.n0, h);
+    if (run.tb == run.end) state_load<NS, WHOLE>(d_fin, g, run.n, w.d, w.n0, l);
+    else tile_state_load<NS>(rev, g, w, l);
 #pragma unroll
     for (int j = 0; j < NS; ++j) l[j] = w.on ? l[j] : 0.f;  // lanes without a channel add nothing
 
+    // groups of SUB tokens, the last one maybe shorter (its rows held to the run's last)
     const int nsub = (run.tb - run.ta + SUB - 1) / SUB;
-    uint32_t rx[SUB], rd[SUB], ry[SUB], rz[SUB] = {};
+    TokenVals<E, SUB, CK> rx, rz = {};
+    TokenVals<E, SUB, false> rd, ry;
     auto fetch = [&](int t, bool all) {
-#pragma unroll
-      for (int k = 0; k < SUB; ++k) {
-        const int64_t q = min(t + k, run.tb - 1);
-        rx[k] = src_load1<E>(x, q, w.d, bg.nblk);
-        rd[k] = load1<E>(dt + q * g.lddt + w.d);
-        if (all) {
-          ry[k] = load1<E>(d_y + q * g.D + w.d);
-          if (z.p) rz[k] = src_load1<E>(z, q, w.d, bg.nblk);
-        }
+      rx.fetch(x, t, run.tb, xoff, soff, bg.nblk);
+      rd.fetch(Src{dt, nullptr, g.lddt}, t, run.tb, off, 0, 0);
+      if (all) {
+        ry.fetch(Src{d_y, nullptr, g.D}, t, run.tb, off, 0, 0);
+        if (gate) rz.fetch(z, t, run.tb, xoff, soff, bg.nblk);
       }
     };
+    RowAhead ahead;
+    ahead.send<BE>(bp, cp, g.ldb, g.ldc, run.ta, run.tb);
     // forwards: the state before every group
+    ScalarRow<BE, NS> b, c;
+    Global<const BE> br = bp + run.ta * g.ldb;
+    b.load(br);
     fetch(run.ta, nsub == 1);
     for (int s = 0; s < nsub; ++s) {
 #pragma unroll
       for (int j = 0; j < NS; ++j) hs[s][w.wave][j][w.lane] = h[j];
       if (s == nsub - 1) break;
-      const int t = run.ta + s * SUB;
-      float xv[SUB], dl[SUB];
+      float u[SUB], dl[SUB];
 #pragma unroll
       for (int k = 0; k < SUB; ++k) {
-        xv[k] = src_value1<E>(x, rx[k]);
-        dl[k] = softplus_flat(value1<E>(rd[k]) + bias);
+        dl[k] = softplus_flat(rd[k] + bias);
+        u[k] = dl[k] * rx[k];
       }
-      fetch(t + SUB, s + 1 == nsub - 1);
+      fetch(run.ta + (s + 1) * SUB, s + 1 == nsub - 1);
 #pragma unroll
       for (int k = 0; k < SUB; ++k) {
-        ScalarRow<BE, NS> b;
-        b.load(bp + (int64_t)(t + k) * g.ldb);
-        const float u = dl[k] * xv[k];
+        scalar_loads_done();
+        const ScalarRow<BE, NS> bt = b;
+        br = stepped<const BE>(br, g.ldb);  // there is a later group
+        b.load(br);
+        float a[NS];
 #pragma unroll
-        for (int j = 0; j < NS; ++j) h[j] = fmaf(fast_exp2(dl[k] * A2[j]), h[j], b[j] * u);
+        for (int j = 0; j < NS; ++j) a[j] = fast_exp2(dl[k] * A2[j]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < NS; ++j) h[j] = fmaf(a[j], h[j], bt[j] * u[k]);
       }
     }
+    ahead.land();
     // backwards, group by group
     for (int s = nsub - 1; s >= 0; --s) {
       const int t = run.ta + s * SUB, cnt = min(SUB, run.tb - t);
-      float xv[SUB], dl[SUB], raw[SUB], dyv[SUB], zv[SUB], hp[SUB][NS];
+      // per token: x, D, softplus', r = dy silu(z), dy silu'(z)
+      float xv[SUB], dl[SUB], sig[SUB], r[SUB], rz2[SUB], hp[SUB][NS];
 #pragma unroll
       for (int k = 0; k < SUB; ++k) {
-        xv[k] = w.on ? src_value1<E>(x, rx[k]) : 0.f;
-        raw[k] = value1<E>(rd[k]) + bias;
-        dl[k] = softplus_flat(raw[k]);
-        dyv[k] = w.on ? value1<E>(ry[k]) : 0.f;
-        zv[k] = src_value1<E>(z, rz[k]);
+        xv[k] = w.on ? rx[k] : 0.f;
+        dl[k] = softplus_both(rd[k] + bias, sig[k]);
+        r[k] = w.on ? ry[k] : 0.f;
+        rz2[k] = 0.f;
+      }
+      if (gate) {
+#pragma unroll
+        for (int k = 0; k < SUB; ++k) {
+          const float zv = rz[k], sg = fast_sigmoid(zv);
+          rz2[k] = r[k] * dsilu(zv, sg);
+          r[k] *= zv * sg;
+        }
       }
       if (s > 0) fetch(t - SUB, true);
+      br = bp + t * g.ldb;
+      b.load(br);
 #pragma unroll
       for (int j = 0; j < NS; ++j) hp[0][j] = hs[s][w.wave][j][w.lane];
 #pragma unroll
       for (int k = 0; k + 1 < SUB; ++k) {
         if (k + 1 >= cnt) break;
-        ScalarRow<BE, NS> b;
-        b.load(bp + (int64_t)(t + k) * g.ldb);
+        scalar_loads_done();
+        const ScalarRow<BE, NS> bt = b;
+        br = stepped<const BE>(br, g.ldb);
+        b.load(br);
         const float u = dl[k] * xv[k];
+        float a[NS];
 #pragma unroll
-        for (int j = 0; j < NS; ++j) hp[k + 1][j] = fmaf(fast_exp2(dl[k] * A2[j]), hp[k][j], b[j] * u);
+        for (int j = 0; j < NS; ++j) a[j] = fast_exp2(dl[k] * A2[j]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < NS; ++j) hp[k + 1][j] = fmaf(a[j], hp[k][j], bt[j] * u);
       }
-      float yraw[SUB], lb[SUB], aq[SUB];  // sums over the states: Cm h, l Bm, A q
+      float own[SUB / NW][3];  // sums over the states of the tokens this wave finishes
+      br = bp + (int64_t)(t + cnt - 1) * g.ldb;
+      Global<const BE> cr = cp + (int64_t)(t + cnt - 1) * g.ldc;
+      Global<float> pr = pb + (int64_t)(t + cnt - 1) * 2 * g.np;
+      b.load(br);
+      c.load(cr);
+      if constexpr (NW > 1) __syncthreads();  // the last group's sums are all read
 #pragma unroll
       for (int k = SUB - 1; k >= 0; --k) {
         if (k >= cnt) continue;
-        ScalarRow<BE, NS> b, c;
-        b.load(bp + (int64_t)(t + k) * g.ldb);
-        c.load(cp + (int64_t)(t + k) * g.ldc);
+        scalar_loads_done();
+        const ScalarRow<BE, NS> bt = b, ct = c;
+        if (k > 0) {
+          br = stepped<const BE>(br, -g.ldb);
+          cr = stepped<const BE>(cr, -g.ldc);
+        }
+        b.load(br);
+        c.load(cr);
         const float u = dl[k] * xv[k];
-        const float r = z.p ? dyv[k] * zv[k] * fast_sigmoid(zv[k]) : dyv[k];
-        float bc[2 * NS], sy = 0.f, sb = 0.f, sq = 0.f;
+        float a[NS], bc[2 * NS], sy = 0.f, sb = 0.f, sq = 0.f;
+#pragma unroll
+        for (int j = 0; j < NS; ++j) a[j] = fast_exp2(dl[k] * A2[j]);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
-          const float a = fast_exp2(dl[k] * A2[j]);
-          const float ah = a * hp[k][j];
-          const float ht = fmaf(b[j], u, ah);
-          const float lam = fmaf(c[j], r, l[j]);
-          sy = fmaf(c[j], ht, sy);
-          sb = fmaf(b[j], lam, sb);
+          const float ah = a[j] * hp[k][j];
+          const float ht = fmaf(bt[j], u, ah);
+          const float lam = fmaf(ct[j], r[k], l[j]);
+          sy = fmaf(ct[j], ht, sy);
+          sb = fmaf(bt[j], lam, sb);
           const float q = lam * ah;
           sq = fmaf(q, A2[j], sq);
           dA[j] = fmaf(q, dl[k], dA[j]);
           bc[j] = lam * u;
-          bc[NS + j] = ht * r;
-          l[j] = a * lam;
+          bc[NS + j] = ht * r[k];
+          l[j] = a[j] * lam;
         }
-        yraw[k] = sy;
-        lb[k] = sb;
-        aq[k] = sq;
         const float tot = wave_sums<2 * NS>(bc);
-        if (w.lane % kRep == 0) pb[(int64_t)(t + k) * 2 * g.np] = tot;
-      }
-      if constexpr (NW > 1) {
-        __syncthreads();  // the last group's sums are all read
-#pragma unroll
-        for (int k = 0; k < SUB; ++k) {
-          if (k >= cnt) break;
-          part[w.wave][k][0][w.lane] = yraw[k];
-          part[w.wave][k][1][w.lane] = lb[k];
-          part[w.wave][k][2][w.lane] = aq[k];
+        if (w.lane % kRep == 0) store1<float>(pr, pboff, tot);
+        pr = stepped<float>(pr, -2 * g.np);
+        if (NW == 1 || k % NW == w.wave) {
+          own[k / NW][0] = sy;
+          own[k / NW][1] = sb;
+          own[k / NW][2] = sq;
+        } else {
+          const int slot = w.wave - (w.wave > k % NW ? 1 : 0);
+          part[k][slot][0][w.lane] = sy;
+          part[k][slot][1][w.lane] = sb;
+          part[k][slot][2][w.lane] = sq;
         }
-        __syncthreads();
       }
+      if constexpr (NW > 1) __syncthreads();
 #pragma unroll
       for (int k = 0; k < SUB; ++k) {
         if (k >= cnt) break;
+        if (NW > 1 && k % NW != w.wave) continue;
+        float sy = own[k / NW][0], sb = own[k / NW][1], sq = own[k / NW][2];
         if constexpr (NW > 1) {
-          if (k % g.nw != w.wave) continue;
-          yraw[k] = lb[k] = aq[k] = 0.f;
-          for (int q = 0; q < g.nw; ++q) {
-            yraw[k] += part[q][k][0][w.lane];
-            lb[k] += part[q][k][1][w.lane];
-            aq[k] += part[q][k][2][w.lane];
+#pragma unroll
+          for (int q = 0; q < NW - 1; ++q) {
+            sy += part[k][q][0][w.lane];
+            sb += part[k][q][1][w.lane];
+            sq += part[k][q][2][w.lane];
           }
         }
-        float r = dyv[k];
-        const int64_t o = (int64_t)(t + k) * g.D + w.d;
-        if (z.p) {
-          const float sg = fast_sigmoid(zv[k]);
-          if (w.on) dz[o] = (E)(dyv[k] * dsilu(zv[k], sg) * fmaf(sk, xv[k], yraw[k]));
-          r *= zv[k] * sg;
-        }
-        const float dD = fmaf(lb[k], xv[k], aq[k] * 0.693147180559945309f);
-        const float dr = raw[k] > 20.f ? dD : dD * fast_sigmoid(raw[k]);
+        const int64_t o = (int64_t)(t + k) * g.D;
+        const float dr = fmaf(sb, xv[k], sq * 0.693147180559945309f) * sig[k];
         if (w.on) {
-          dx[o] = (E)fmaf(dl[k], lb[k], sk * r);
-          ddt[o] = (E)dr;
+          if (gate) store1<E>((Global<E>)dz + o, off, rz2[k] * fmaf(sk, xv[k], sy));
+          store1<E>((Global<E>)dx + o, off, fmaf(dl[k], sb, sk * r[k]));
+          store1<E>((Global<E>)ddt + o, off, dr);
         }
-        dskip = fmaf(r, xv[k], dskip);
+        dskip = fmaf(r[k], xv[k], dskip);
         dbias += dr;
       }
     }
-    if (dh0 && w.on && run.ta == run.start) state_store<NS>(dh0, g, run.n, w.d, w.n0, l);
+    if (dh0 && w.on && run.ta == run.start) state_store<NS, WHOLE>(dh0, g, run.n, w.d, w.n0, l);
   }
   if (!w.on) return;
-#pragma unroll
-  for (int j = 0; j < NS; ++j) states[at + (int64_t)j * g.D] = dA[j];
-  float* ps = psum + ((int64_t)w.tile * g.nw + w.wave) * 2 * g.D + w.d;
-  ps[0] = dskip;
-  ps[g.D] = dbias;
+  tile_state_store<NS>(states, g, w, dA);
+  Global<float> ps = (Global<float>)psum + ((int64_t)w.tile * NW + w.wave) * 2 * g.D;
+  store1<float>(ps, w.d * 4u, dskip);
+  store1<float>(ps + g.D, w.d * 4u, dbias);
 }
 
-// (4): dBm and dCm, a lane per value, summed over the group's channel waves.
+// (4).  Blocks below `row_blocks`: dBm and dCm, a lane per value, summed over the group's
+// channel waves.  The others: dA_log, dskip and ddt_bias, summed over the tiles, 64
+// neighbouring values per workgroup, four lanes of tiles each; np rows of D values for
+// dA_log, then two rows.
 template <typename E>
-__global__ __launch_bounds__(256) void gdn_scan_bwd_rows_kernel(ScanGeo g, const float* __restrict__ pbc,
-                                                                E* __restrict__ dBm, E* __restrict__ dCm) {
-  const int64_t ntok = (int64_t)g.B * g.T, total = ntok * g.G * 2 * g.np;
-  const int64_t step = (int64_t)gridDim.x * 256;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += step) {
-    const int64_t per = ntok * 2 * g.np;
+__global__ __launch_bounds__(256) void gdn_scan_bwd_sums_kernel(
+    ScanGeo g, int tiles, uint32_t row_blocks, const float* __restrict__ A_log,
+    const float* __restrict__ pbc, const float* __restrict__ states, const float* __restrict__ psum,
+    E* __restrict__ dBm, E* __restrict__ dCm, float* __restrict__ dA_log, float* __restrict__ dskip,
+    float* __restrict__ ddt_bias) {
+  __shared__ float sm[256];
+  if (blockIdx.x < row_blocks) {
+    const int64_t per = (int64_t)g.B * g.T * 2 * g.np;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int gi = (int)(i / per);
+    if (gi >= g.G) return;
     const int64_t r = i - gi * per;
-    const int64_t t = r / (2 * g.np);
-    const int m = (int)(r - t * 2 * g.np), c = m / g.np, n = m - c * g.np;
-    if (n >= g.N) continue;
+    const uint32_t w2 = 2 * g.np;
+    const int64_t t = r / w2;
+    const int m = (int)(r - t * w2), c = m >= g.np, n = m - c * g.np;
+    if (n >= g.N) return;
     const float* p = pbc + (int64_t)gi * g.wpg * per + r;
     float s = 0.f;
+#pragma unroll 8
     for (int k = 0; k < g.wpg; ++k) s += p[k * per];
     (c ? dCm : dBm)[(t * g.G + gi) * g.N + n] = (E)s;
+    return;
   }
-}
-
-// (4): dA_log, dskip and ddt_bias, summed over the tiles: 64 neighbouring values per
-// workgroup, four lanes of tiles each.  Values: np rows of D for dA_log, then two rows.
-__global__ __launch_bounds__(256) void gdn_scan_bwd_params_kernel(ScanGeo g, int tiles,
-                                                                  const float* __restrict__ A_log,
-                                                                  const float* __restrict__ states,
-                                                                  const float* __restrict__ psum,
-                                                                  float* __restrict__ dA_log,
-                                                                  float* __restrict__ dskip,
-                                                                  float* __restrict__ ddt_bias) {
-  __shared__ float sm[256];
-  const int64_t e = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63), per = (int64_t)g.np * g.D;
+  const int64_t e = (int64_t)(blockIdx.x - row_blocks) * 64 + (threadIdx.x & 63), per = (int64_t)g.np * g.D;
   const int q = threadIdx.x >> 6;
   const int64_t n = e / g.D, d = e - n * g.D;
   float s = 0.f;
   if (n < g.np) {
+#pragma unroll 8
     for (int t = q; t < tiles; t += 4) s += states[t * per + e];
   } else if (n < g.np + 2) {
     const int64_t row = (int64_t)2 * g.D;
+#pragma unroll 8
     for (int t = q; t < tiles * g.nw; t += 4) s += psum[t * row + (n - g.np) * g.D + d];
   }
   sm[threadIdx.x] = s;

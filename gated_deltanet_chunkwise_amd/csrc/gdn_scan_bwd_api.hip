@@ -29,7 +29,10 @@ BwdSpace bwd_space(const ScanPlan& pl) {
 gdn_status_t bwd_sizes(const gdn_scan_params_t* p, bool packed, ScanPlan* pl) {
   gdn_status_t st = scan_sizes(p, packed, pl);
   if (st != GDN_OK) return st;
-  scan_waves(pl, gdn::kScanBwdStates);
+  // 1, 2, 4 or 8 waves
+  int nw = 1;
+  while (nw * gdn::kScanBwdStates < p->N) nw *= 2;
+  scan_waves(pl, gdn::kScanBwdStates, nw);
   scan_tiles(pl, gdn::scan_bwd_tile(pl->geo.nw));
   return GDN_OK;
 }
@@ -68,7 +71,9 @@ gdn_status_t scan_bwd_run(ScanPlan pl, const BwdArgs& a, void* ws, hipStream_t s
   const int64_t tiles = pl.tok > 0 ? scan_all_tiles(pl) : 0;
   const int64_t main_blocks = tiles * g.cgroups;
   const int64_t empties = (g.cu || g.T == 0) && a.dh0 ? g.S : 0;
-  if (main_blocks + empties > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  const int64_t row_blocks = pl.tok > 0 ? ceil_div(pl.tok * g.G * 2 * g.np, 256) : 0;
+  const int64_t param_blocks = ceil_div((int64_t)(g.np + 2) * g.D, 64);
+  if (main_blocks + empties > INT32_MAX || row_blocks + param_blocks > INT32_MAX) return GDN_ERR_UNSUPPORTED;
   if (!direct && pl.tok > 0) {
     float *Bw = F(sp.rows), *Cw = F(sp.rows + scan_rows_bytes(pl));
     ok(pl.esz == 2 ? scan_copy_rows<gdn::bf16>(&pl, Bm, Cm, Bw, Cw, s) : scan_copy_rows<float>(&pl, Bm, Cm, Bw, Cw, s));
@@ -76,43 +81,56 @@ gdn_status_t scan_bwd_run(ScanPlan pl, const BwdArgs& a, void* ws, hipStream_t s
     Cm = Cw;
   }
   if (pl.tok == 0) g.ntiles = 0;
-  auto run = [&](auto e, auto be, auto nw) {
+  auto run = [&](auto e, auto be, auto whole, auto nw, auto ck) {
     using E = decltype(e);
     using BE = decltype(be);
     constexpr int NS = gdn::kScanBwdStates, NW = decltype(nw)::value;
+    constexpr bool WHOLE = decltype(whole)::value, CK = decltype(ck)::value;
     const gdn::ScanBwdGeo bg{g, (int)ceil_div(g.D, gdn::kPackBlock)};
     const gdn::Src x{a.x, a.x_scales, a.x_scales ? g.D : pl.ldx}, z{a.z, a.z_scales, a.z_scales ? g.D : pl.ldz};
     const E *dt = static_cast<const E*>(a.dt), *dy = static_cast<const E*>(a.dy);
     const BE *b = static_cast<const BE*>(Bm), *c = static_cast<const BE*>(Cm);
-    const dim3 block(64 * g.nw);
     if (g.ntiles > 1) {
-      ok(launch(gdn::gdn_scan_bwd_ends_kernel<E, BE, NS, NW>, dim3((unsigned)main_blocks), block, s, bg, x, dt, z,
-                a.A_log, b, c, a.dt_bias, a.h0, dy, a.dfin, F(sp.states), F(sp.rev), F(sp.sums), F(sp.rsums)));
-      const dim3 grid((unsigned)ceil_div((int64_t)(g.cu ? 1 : g.B) * g.np * g.D, 256));
-      ok(launch(gdn::gdn_scan_join_kernel, grid, dim3(256), s, g, a.A_log, a.h0, F(sp.states), F(sp.sums)));
-      ok(launch(gdn::gdn_scan_bwd_join_kernel, grid, dim3(256), s, g, a.A_log, F(sp.rev), F(sp.rsums)));
+      // sixteen states per lane where there are as many: half the work per token that
+      // does not depend on the states
+      auto ends = [&](auto n) {
+        constexpr int M = decltype(n)::value;
+        gdn::ScanBwdGeo eg = bg;
+        eg.g.nw = g.np / M;
+        ok(launch(gdn::gdn_scan_bwd_ends_kernel<E, BE, M, WHOLE, CK>, dim3((unsigned)main_blocks), dim3(64 * eg.g.nw), s, eg,
+                  x, dt, z, a.A_log, b, c, a.dt_bias, a.h0, dy, a.dfin, F(sp.states), F(sp.rev), F(sp.sums),
+                  F(sp.rsums)));
+      };
+      if constexpr (NW == 1) ends(std::integral_constant<int, 8>{});
+      else ends(std::integral_constant<int, 16>{});
+      ok(launch(gdn::gdn_scan_join_kernel<false>, scan_join_grid(g), dim3(256), s, g, a.A_log, a.h0, F(sp.states),
+                F(sp.sums)));
+      ok(launch(gdn::gdn_scan_join_kernel<true>, scan_join_grid(g), dim3(256), s, g, a.A_log, nullptr, F(sp.rev),
+                F(sp.rsums)));
     }
     if (main_blocks + empties > 0)
-      ok(launch(gdn::gdn_scan_bwd_kernel<E, BE, NS, NW, gdn::kScanBwdSub>, dim3((unsigned)(main_blocks + empties)), block, s, bg, x,
-                dt, z, a.A_log, b, c, a.skip, a.dt_bias, a.h0, dy, a.dfin, F(sp.states), F(sp.rev),
-                static_cast<E*>(a.dx), static_cast<E*>(a.ddt), static_cast<E*>(a.dz), F(sp.pbc), F(sp.psum), a.dh0));
-    if (pl.tok > 0) {
-      const int64_t n = pl.tok * g.G * 2 * g.np;
-      ok(launch(gdn::gdn_scan_bwd_rows_kernel<E>, dim3((unsigned)std::min(ceil_div(n, 256), (int64_t)1 << 20)),
-                dim3(256), s, g, F(sp.pbc), static_cast<E*>(a.dBm), static_cast<E*>(a.dCm)));
-    }
-    ok(launch(gdn::gdn_scan_bwd_params_kernel, dim3((unsigned)ceil_div((int64_t)(g.np + 2) * g.D, 64)), dim3(256), s, g,
-              (int)tiles, a.A_log, F(sp.states), F(sp.psum), a.dA_log, a.dskip, a.dbias));
+      ok(launch(gdn::gdn_scan_bwd_kernel<E, BE, NS, WHOLE, NW, gdn::kScanBwdSub, CK>, dim3((unsigned)(main_blocks + empties)),
+                dim3(64 * NW), s, bg, x, dt, z, a.A_log, b, c, a.skip, a.dt_bias, a.h0, dy, a.dfin, F(sp.states),
+                F(sp.rev), static_cast<E*>(a.dx), static_cast<E*>(a.ddt), static_cast<E*>(a.dz), F(sp.pbc), F(sp.psum),
+                a.dh0));
+    ok(launch(gdn::gdn_scan_bwd_sums_kernel<E>, dim3((unsigned)(row_blocks + param_blocks)), dim3(256), s, g, (int)tiles,
+              (uint32_t)row_blocks, a.A_log, F(sp.pbc), F(sp.states), F(sp.psum), static_cast<E*>(a.dBm),
+              static_cast<E*>(a.dCm), a.dA_log, a.dskip, a.dbias));
   };
-  auto waves = [&](auto e, auto be) {
-    if (g.nw == 1) run(e, be, std::integral_constant<int, 1>{});
-    else if (g.nw == 2) run(e, be, std::integral_constant<int, 2>{});
-    else if (g.nw <= 4) run(e, be, std::integral_constant<int, 4>{});
-    else run(e, be, std::integral_constant<int, 8>{});
+  auto waves = [&](auto e, auto be, auto whole) {
+    auto kind = [&](auto nw) {
+      if (a.x_scales) run(e, be, whole, nw, std::true_type{});
+      else run(e, be, whole, nw, std::false_type{});
+    };
+    if (g.nw == 1) kind(std::integral_constant<int, 1>{});
+    else if (g.nw == 2) kind(std::integral_constant<int, 2>{});
+    else if (g.nw == 4) kind(std::integral_constant<int, 4>{});
+    else kind(std::integral_constant<int, 8>{});
   };
-  if (pl.esz == 4) waves(0.f, 0.f);
-  else if (direct) waves(gdn::bf16{}, gdn::bf16{});
-  else waves(gdn::bf16{}, 0.f);
+  using Yes = std::true_type;
+  using No = std::false_type;
+  if (pl.esz == 4) direct ? waves(0.f, 0.f, Yes{}) : waves(0.f, 0.f, No{});
+  else direct ? waves(gdn::bf16{}, gdn::bf16{}, Yes{}) : waves(gdn::bf16{}, 0.f, No{});
   return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
@@ -135,6 +153,7 @@ gdn_status_t gdn_scan_bwd(const gdn_scan_params_t* p, const void* x, const uint8
   ScanPlan pl;
   gdn_status_t st = bwd_sizes(p, cu_seqlens != nullptr, &pl);
   if (st != GDN_OK) return st;
+  if (z && !x_scales != !z_scales) return GDN_ERR_SHAPE;
   if ((x_scales && pl.ldx != p->D) || (z_scales && pl.ldz != p->D)) return GDN_ERR_SHAPE;  // codes are dense
   if (pl.tok > 0 && (!x || !dt || !Bm || !Cm || !d_y || !dx || !ddt || !dBm || !dCm || (z && !dz)))
     return GDN_ERR_NULL;

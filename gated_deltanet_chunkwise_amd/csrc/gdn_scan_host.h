@@ -23,7 +23,8 @@ inline gdn_status_t scan_sizes(const gdn_scan_params_t* p, bool packed, ScanPlan
   if (st != GDN_OK) return st;
   if (p->N > 64) return GDN_ERR_UNSUPPORTED;
   const int64_t bn = (int64_t)p->G * p->N;
-  if (bn > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  // 32-bit indices of a row of states; rows of the batch in a grid's second dimension
+  if (bn > INT32_MAX || (int64_t)p->D * 64 > INT32_MAX || p->B > 65535) return GDN_ERR_UNSUPPORTED;
   auto bad = [](int64_t ld, int64_t least) { return ld != 0 && ld < least; };
   if (bad(p->x_stride, p->D) || bad(p->dt_stride, p->D) || bad(p->z_stride, p->D) ||
       bad(p->b_stride, bn) || bad(p->c_stride, bn))
@@ -48,11 +49,11 @@ inline gdn_status_t scan_sizes(const gdn_scan_params_t* p, bool packed, ScanPlan
   return GDN_OK;
 }
 
-// ns states per lane, as many waves per workgroup as that takes.
-inline void scan_waves(ScanPlan* pl, int ns) {
+// ns states per lane and nw waves per workgroup.
+inline void scan_waves(ScanPlan* pl, int ns, int nw) {
   pl->ns = ns;
-  pl->geo.nw = (int)ceil_div(pl->geo.N, ns);
-  pl->geo.np = pl->geo.nw * ns;
+  pl->geo.nw = nw;
+  pl->geo.np = nw * ns;
 }
 
 inline void scan_tiles(ScanPlan* pl, int len) {
@@ -61,6 +62,10 @@ inline void scan_tiles(ScanPlan* pl, int len) {
 }
 inline int64_t scan_all_tiles(const ScanPlan& pl) {
   return (int64_t)pl.geo.ntiles * (pl.packed ? 1 : pl.geo.B);
+}
+
+inline dim3 scan_join_grid(const gdn::ScanGeo& g) {
+  return dim3((unsigned)ceil_div((int64_t)g.np * g.D, 256), g.cu ? 1 : g.B);
 }
 
 // Whether Bm and Cm can be read in place: whole rows of np states at 4-byte aligned

@@ -531,9 +531,10 @@ gdn_status_t gdn_scan_decode(const gdn_scan_params_t *p, const void *x, const vo
 
 /* Gradients for L = sum <d_y, y> + <d_final_state, final_state>.  The states are
  * formed again tile by tile; nothing of the forward pass is needed but its inputs.
- *   x, z          as for gdn_scan_fwd, or checkpoints: with x_scales (z_scales) not NULL
- *                 the codes and scales of gdn_pack8, dense, read in place; the gradients
- *                 are those at the values they stand for
+ *   x, z          as for gdn_scan_fwd, or both checkpoints: with x_scales and z_scales not
+ *                 NULL the codes and scales of gdn_pack8, dense, read in place; the
+ *                 gradients are those at the values they stand for (one of the two alone:
+ *                 GDN_ERR_SHAPE)
  *   d_y           [B][T][D] dtype; d_final_state [sequences][D][N] fp32 or NULL (0)
  *   dx, ddt       [B][T][D]; dz [B][T][D] (required with z, unused without); dBm, dCm
  *                 [B][T][G][N]: dtype, written (rows behind the last sequence: 0)
