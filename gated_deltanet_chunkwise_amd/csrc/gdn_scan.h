@@ -27,7 +27,8 @@ struct ScanGeo {
   int B, T, D, G, N, S;  // S = sequences
   int DG, wpg, cgroups;  // channels per group, waves per group, waves for all channels
   int len, ntiles;       // tokens per tile; tiles per row of the batch
-  int nw, np;            // waves per workgroup; nw * NS
+  int nw, np;            // waves per 64 channels; nw * NS
+  int upw, cgb;          // units of nw waves per workgroup, workgroups for all channels
   const int64_t* cu;
   int64_t lddt;
   int64_t ldb, ldc;      // elements between rows of Bm and Cm, and between groups
@@ -165,19 +166,26 @@ __device__ __forceinline__ void state_store(float* st, const ScanGeo& g, int n, 
   }
 }
 
-// Block id -> (tile of the whole batch, group of 64 channels); the lane's channel d,
-// `on` where it has one of its own.
+// Block id -> (tile of the whole batch, upw groups of 64 channels); the lane's channel d,
+// `on` where it has one of its own; cg the wave's group, `unit` its place in the
+// workgroup.  Workgroups have four waves where they can: with one or two, the waves of a
+// launch were spread unevenly over the SIMDs (2048 of one wave each: 66 us of kernel for
+// waves that lived 41 us).
 struct ScanPlace {
-  int tile, gi, d, lane, wave, n0;
-  bool on;
+  int tile, cg, gi, d, lane, unit, wave, n0;
+  bool on, valid;
   template <int NS> __device__ __forceinline__ void init(const ScanGeo& g, uint32_t block) {
-    tile = block / g.cgroups;
-    const int cg = block - tile * g.cgroups;
-    gi = cg / g.wpg;
+    tile = block / g.cgb;
     lane = threadIdx.x & 63;
-    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    unit = w / g.nw;
+    wave = w - unit * g.nw;
+    cg = (block - tile * g.cgb) * g.upw + unit;
+    valid = cg < g.cgroups;
+    cg = min(cg, g.cgroups - 1);
+    gi = cg / g.wpg;
     const int dl = (cg - gi * g.wpg) * 64 + lane;
-    on = dl < g.DG;
+    on = valid && dl < g.DG;
     d = gi * g.DG + min(dl, g.DG - 1);
     n0 = wave * NS;
   }
@@ -213,23 +221,26 @@ __device__ __forceinline__ void scan_empty_state(const ScanGeo& g, int n, const 
 // passes through it), or the outputs (`states` holds the tiles' start states).
 // Blocks behind the last tile's copy the states of empty sequences (not ENDS).
 template <typename E, typename BE, int NS, bool WHOLE, bool SPLIT, bool ENDS>
-__global__ __launch_bounds__(SPLIT ? 64 * kScanMaxWaves : 64) void gdn_scan_kernel(
+__global__ __launch_bounds__(64 * kScanMaxWaves) void gdn_scan_kernel(
     ScanGeo g, Src x, const E* __restrict__ dt, Src z, const float* __restrict__ A_log,
     const BE* __restrict__ Bm, const BE* __restrict__ Cm, const float* __restrict__ skip,
     const float* __restrict__ dt_bias, const float* __restrict__ h0, float* __restrict__ states,
     float* __restrict__ sums, E* __restrict__ y, float* __restrict__ fin) {
   constexpr int U = kScanGroup;
+  // [buffer][unit * nw + wave]
   __shared__ float part[SPLIT && !ENDS ? 2 : 1][SPLIT && !ENDS ? kScanMaxWaves : 1][U][SPLIT && !ENDS ? 64 : 1];
+  
   const int tiles = g.ntiles * (g.cu ? 1 : g.B);
-  const uint32_t main_blocks = (uint32_t)tiles * g.cgroups;
+  const uint32_t main_blocks = (uint32_t)tiles * g.cgb;
   if constexpr (ENDS) {
-    if ((int)(blockIdx.x / g.cgroups) % g.ntiles == g.ntiles - 1) return;  // nobody starts from it
+    if ((int)(blockIdx.x / g.cgb) % g.ntiles == g.ntiles - 1) return;  // nobody starts from it
   } else if (blockIdx.x >= main_blocks) {
     scan_empty_state(g, blockIdx.x - main_blocks, h0, fin);
     return;
   }
   ScanPlace w;
   w.init<NS>(g, blockIdx.x);
+  if (!SPLIT && !w.valid) return;
   float A2[NS], h[NS];
   scan_rates<NS, WHOLE>(A_log, g, w.d, w.n0, A2);
   const float bias = dt_bias ? dt_bias[w.d] : 0.f, sk = skip ? skip[w.d] : 0.f;
@@ -301,7 +312,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * kScanMaxWaves : 64) void gdn_scan_kern
       for (int k = 0; k < U; ++k) {
         if (k >= n || k % g.nw != w.wave) continue;
         float acc = 0.f;
-        for (int q = 0; q < g.nw; ++q) acc += part[buf][q][k][w.lane];
+        for (int q = 0; q < g.nw; ++q) acc += part[buf][w.unit * g.nw + q][k][w.lane];
         finish(acc, xv[k], gv[k], yr + (int64_t)k * g.D);
       }
       buf ^= 1;
@@ -321,7 +332,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * kScanMaxWaves : 64) void gdn_scan_kern
         if (sum >= 0.f) sum += dl;
       } else if constexpr (SPLIT) {
         float xs[U] = {xv}, gs[U] = {gv};
-        part[buf][w.wave][0][w.lane] = acc;
+        part[buf][w.unit * g.nw + w.wave][0][w.lane] = acc;
         add_waves(xs, gs, 1);
       } else {
         finish(acc, xv, gv, yr);
@@ -376,7 +387,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * kScanMaxWaves : 64) void gdn_scan_kern
         if constexpr (ENDS) {
           if (sum >= 0.f) sum += dl[k];
         } else if constexpr (SPLIT) {
-          part[buf][w.wave][k][w.lane] = acc;
+          part[buf][w.unit * g.nw + w.wave][k][w.lane] = acc;
         } else {
           finish(acc, xv[k], gv[k], yr);
           yr = stepped<E>(yr, g.D);

@@ -25,7 +25,7 @@ gdn_status_t fwd_sizes(const gdn_scan_params_t* p, bool packed, ScanPlan* pl) {
   const gdn_status_t st = scan_sizes(p, packed, pl);
   if (st != GDN_OK) return st;
   const int ns = p->N <= 8 ? 8 : 16;
-  scan_waves(pl, ns, (int)ceil_div(p->N, ns));
+  scan_waves(&pl->geo, ns, (int)ceil_div(p->N, ns));
   scan_tiles(pl, scan_fwd_len(*pl));
   return GDN_OK;
 }
@@ -35,7 +35,7 @@ template <typename F> gdn_status_t scan_dispatch(const ScanPlan& pl, bool direct
   using Yes = std::true_type;
   using No = std::false_type;
   auto states = [&](auto e, auto be, auto whole) {
-    if (pl.ns == 8) return f(e, be, std::integral_constant<int, 8>{}, whole, No{});
+    if (pl.geo.np == 8) return f(e, be, std::integral_constant<int, 8>{}, whole, No{});
     const std::integral_constant<int, 16> ns;
     return pl.geo.nw > 1 ? f(e, be, ns, whole, Yes{}) : f(e, be, ns, whole, No{});
   };
@@ -87,7 +87,7 @@ gdn_status_t scan_fwd_run(ScanPlan pl, const FwdArgs& a, void* ws, hipStream_t s
     Bm = Bw;
     Cm = Cw;
   }
-  const int64_t main_blocks = pl.tok > 0 ? scan_all_tiles(pl) * g.cgroups : 0;
+  const int64_t main_blocks = pl.tok > 0 ? scan_all_tiles(pl) * g.cgb : 0;
   const int64_t empties = (g.cu || g.T == 0) && a.fin ? g.S : 0;
   if (main_blocks + empties > INT32_MAX) return GDN_ERR_UNSUPPORTED;
   if (pl.tok == 0) g.ntiles = 0;  // no tile blocks: the first block is the first sequence's
@@ -101,7 +101,7 @@ gdn_status_t scan_fwd_run(ScanPlan pl, const FwdArgs& a, void* ws, hipStream_t s
     const E* dt = static_cast<const E*>(a.dt);
     const BE *b = static_cast<const BE*>(Bm), *c = static_cast<const BE*>(Cm);
     E* y = static_cast<E*>(a.y);
-    const dim3 block(64 * g.nw);
+    const dim3 block(64 * g.nw * g.upw);
     if (g.ntiles > 1) {
       ok(launch(gdn::gdn_scan_kernel<E, BE, NS, WHOLE, SPLIT, true>, dim3((unsigned)main_blocks), block, s, g, x, dt, z,
                 a.A_log, b, c, a.skip, a.dt_bias, a.h0, states, sums, y, a.fin));

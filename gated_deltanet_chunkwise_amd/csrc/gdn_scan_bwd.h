@@ -31,6 +31,7 @@ constexpr int kScanBwdSub = 8;     // tokens per group
 // Tokens per tile.  The states that a tile keeps take 32 bytes of LDS per token and lane:
 // 64 tokens leave room for 8 waves per CU with up to two waves per workgroup (256
 // registers allow no more), 32 with more waves.
+constexpr int scan_bwd_units(int waves) { return waves >= 4 ? 1 : 4 / waves; }  // per workgroup
 constexpr int scan_bwd_tile(int waves) { return waves > 2 ? 32 : 64; }
 
 // U tokens' values of one channel as loaded, so that the loads are all in flight before
@@ -138,6 +139,7 @@ __global__ __launch_bounds__(64 * kScanMaxWaves) void gdn_scan_bwd_ends_kernel(
   const ScanGeo& g = bg.g;
   ScanPlace w;
   w.init<NS>(g, blockIdx.x);
+  if (!w.valid) return;
   float A2[NS], h[NS], P[NS], R[NS];
   scan_rates<NS, WHOLE>(A_log, g, w.d, w.n0, A2);
   // lane offsets: of E, of a checkpoint's codes and scales
@@ -251,25 +253,28 @@ __global__ __launch_bounds__(64 * kScanMaxWaves) void gdn_scan_bwd_ends_kernel(
 // The waves of a workgroup (NS states each) add their sums over the states, three per
 // token, through LDS: token k of a group is finished by wave k % NW.
 template <typename E, typename BE, int NS, bool WHOLE, int NW, int SUB, bool CK>
-__global__ __launch_bounds__(64 * NW, 2) void gdn_scan_bwd_kernel(
+__global__ __launch_bounds__(64 * NW * scan_bwd_units(NW), 2) void gdn_scan_bwd_kernel(
     ScanBwdGeo bg, Src x, const E* __restrict__ dt, Src z, const float* __restrict__ A_log,
     const BE* __restrict__ Bm, const BE* __restrict__ Cm, const float* __restrict__ skip,
     const float* __restrict__ dt_bias, const float* __restrict__ h0, const E* __restrict__ d_y,
     const float* __restrict__ d_fin, float* __restrict__ states, const float* __restrict__ rev,
     E* __restrict__ dx, E* __restrict__ ddt, E* __restrict__ dz, float* __restrict__ pbc,
     float* __restrict__ psum, float* __restrict__ dh0) {
-  __shared__ float hs[scan_bwd_tile(NW) / SUB][NW][NS][64];
-  __shared__ float part[NW > 1 ? SUB : 1][NW > 1 ? NW - 1 : 1][3][NW > 1 ? 64 : 1];
+  constexpr int UPW = scan_bwd_units(NW);
+  __shared__ float hs[scan_bwd_tile(NW) / SUB][UPW * NW][NS][64];
+  __shared__ float part_[NW > 1 ? UPW : 1][NW > 1 ? SUB : 1][NW > 1 ? NW - 1 : 1][3][NW > 1 ? 64 : 1];
   const ScanGeo& g = bg.g;
   const int64_t ntok = (int64_t)g.B * g.T;
-  const uint32_t main_blocks = (uint32_t)(g.ntiles * (g.cu ? 1 : g.B)) * g.cgroups;
+  const uint32_t main_blocks = (uint32_t)(g.ntiles * (g.cu ? 1 : g.B)) * g.cgb;
   if (blockIdx.x >= main_blocks) {
     scan_empty_state(g, blockIdx.x - main_blocks, d_fin, dh0);
     return;
   }
   ScanPlace w;
   w.init<NS>(g, blockIdx.x);
-  const int cg = blockIdx.x % g.cgroups;
+  if (NW == 1 && !w.valid) return;
+  auto& part = part_[NW > 1 ? w.unit : 0];
+  const int kept = w.unit * NW + w.wave;
   // lane offsets: of E, of a checkpoint's codes and scales
   const uint32_t off = lane_offset(w.d * (uint32_t)sizeof(E)), xoff = CK ? lane_offset(w.d) : off;
   const uint32_t soff = CK ? lane_offset((uint32_t)w.d >> 5) : 0;
@@ -283,7 +288,7 @@ __global__ __launch_bounds__(64 * NW, 2) void gdn_scan_bwd_kernel(
   // this wave's place in a token's row of pbc: lane v of dBm and dCm's 2 NS values
   constexpr int kRep = 64 / (2 * NS);
   const int v = w.lane / kRep;
-  const Global<float> pb = (Global<float>)pbc + (int64_t)cg * ntok * 2 * g.np;
+  const Global<float> pb = (Global<float>)pbc + (int64_t)w.cg * ntok * 2 * g.np;
   const uint32_t pboff = lane_offset(((v / NS) * g.np + w.n0 + v % NS) * 4u);
 #pragma unroll
   for (int j = 0; j < NS; ++j) dA[j] = 0.f;
@@ -296,7 +301,7 @@ __global__ __launch_bounds__(64 * NW, 2) void gdn_scan_bwd_kernel(
         store1<E>((Global<E>)ddt + (int64_t)t * g.D, off, 0.f);
         if (gate) store1<E>((Global<E>)dz + (int64_t)t * g.D, off, 0.f);
       }
-      if (w.lane % kRep == 0) store1<float>(pb + (int64_t)t * 2 * g.np, pboff, 0.f);
+      if (w.valid && w.lane % kRep == 0) store1<float>(pb + (int64_t)t * 2 * g.np, pboff, 0.f);
     }
   }
 
@@ -331,7 +336,7 @@ __global__ __launch_bounds__(64 * NW, 2) void gdn_scan_bwd_kernel(
     fetch(run.ta, nsub == 1);
     for (int s = 0; s < nsub; ++s) {
 #pragma unroll
-      for (int j = 0; j < NS; ++j) hs[s][w.wave][j][w.lane] = h[j];
+      for (int j = 0; j < NS; ++j) hs[s][kept][j][w.lane] = h[j];
       if (s == nsub - 1) break;
       float u[SUB], dl[SUB];
 #pragma unroll
@@ -379,7 +384,7 @@ __global__ __launch_bounds__(64 * NW, 2) void gdn_scan_bwd_kernel(
       br = bp + t * g.ldb;
       b.load(br);
 #pragma unroll
-      for (int j = 0; j < NS; ++j) hp[0][j] = hs[s][w.wave][j][w.lane];
+      for (int j = 0; j < NS; ++j) hp[0][j] = hs[s][kept][j][w.lane];
 #pragma unroll
       for (int k = 0; k + 1 < SUB; ++k) {
         if (k + 1 >= cnt) break;
@@ -433,7 +438,7 @@ __global__ __launch_bounds__(64 * NW, 2) void gdn_scan_bwd_kernel(
           l[j] = a[j] * lam;
         }
         const float tot = wave_sums<2 * NS>(bc);
-        if (w.lane % kRep == 0) store1<float>(pr, pboff, tot);
+        if (w.valid && w.lane % kRep == 0) store1<float>(pr, pboff, tot);
         pr = stepped<float>(pr, -2 * g.np);
         if (NW == 1 || k % NW == w.wave) {
           own[k / NW][0] = sy;

@@ -32,7 +32,7 @@ gdn_status_t bwd_sizes(const gdn_scan_params_t* p, bool packed, ScanPlan* pl) {
   // 1, 2, 4 or 8 waves
   int nw = 1;
   while (nw * gdn::kScanBwdStates < p->N) nw *= 2;
-  scan_waves(pl, gdn::kScanBwdStates, nw);
+  scan_waves(&pl->geo, gdn::kScanBwdStates, nw);
   scan_tiles(pl, gdn::scan_bwd_tile(pl->geo.nw));
   return GDN_OK;
 }
@@ -69,7 +69,7 @@ gdn_status_t scan_bwd_run(ScanPlan pl, const BwdArgs& a, void* ws, hipStream_t s
     if (e != hipSuccess && err == hipSuccess) err = e;
   };
   const int64_t tiles = pl.tok > 0 ? scan_all_tiles(pl) : 0;
-  const int64_t main_blocks = tiles * g.cgroups;
+  const int64_t main_blocks = tiles * g.cgb;
   const int64_t empties = (g.cu || g.T == 0) && a.dh0 ? g.S : 0;
   const int64_t row_blocks = pl.tok > 0 ? ceil_div(pl.tok * g.G * 2 * g.np, 256) : 0;
   const int64_t param_blocks = ceil_div((int64_t)(g.np + 2) * g.D, 64);
@@ -96,9 +96,9 @@ gdn_status_t scan_bwd_run(ScanPlan pl, const BwdArgs& a, void* ws, hipStream_t s
       auto ends = [&](auto n) {
         constexpr int M = decltype(n)::value;
         gdn::ScanBwdGeo eg = bg;
-        eg.g.nw = g.np / M;
-        ok(launch(gdn::gdn_scan_bwd_ends_kernel<E, BE, M, WHOLE, CK>, dim3((unsigned)main_blocks), dim3(64 * eg.g.nw), s, eg,
-                  x, dt, z, a.A_log, b, c, a.dt_bias, a.h0, dy, a.dfin, F(sp.states), F(sp.rev), F(sp.sums),
+        scan_waves(&eg.g, M, g.np / M);
+        ok(launch(gdn::gdn_scan_bwd_ends_kernel<E, BE, M, WHOLE, CK>, dim3((unsigned)(tiles * eg.g.cgb)),
+                  dim3(64 * eg.g.nw * eg.g.upw), s, eg, x, dt, z, a.A_log, b, c, a.dt_bias, a.h0, dy, a.dfin, F(sp.states), F(sp.rev), F(sp.sums),
                   F(sp.rsums)));
       };
       if constexpr (NW == 1) ends(std::integral_constant<int, 8>{});
@@ -110,7 +110,7 @@ gdn_status_t scan_bwd_run(ScanPlan pl, const BwdArgs& a, void* ws, hipStream_t s
     }
     if (main_blocks + empties > 0)
       ok(launch(gdn::gdn_scan_bwd_kernel<E, BE, NS, WHOLE, NW, gdn::kScanBwdSub, CK>, dim3((unsigned)(main_blocks + empties)),
-                dim3(64 * NW), s, bg, x, dt, z, a.A_log, b, c, a.skip, a.dt_bias, a.h0, dy, a.dfin, F(sp.states),
+                dim3(64 * NW * g.upw), s, bg, x, dt, z, a.A_log, b, c, a.skip, a.dt_bias, a.h0, dy, a.dfin, F(sp.states),
                 F(sp.rev), static_cast<E*>(a.dx), static_cast<E*>(a.ddt), static_cast<E*>(a.dz), F(sp.pbc), F(sp.psum),
                 a.dh0));
     ok(launch(gdn::gdn_scan_bwd_sums_kernel<E>, dim3((unsigned)(row_blocks + param_blocks)), dim3(256), s, g, (int)tiles,

@@ -9,7 +9,6 @@ struct ScanPlan {
   gdn::ScanGeo geo;
   int64_t ldx, ldz;
   size_t esz;
-  int ns;        // states per lane
   int64_t tok;   // tokens in all
   bool packed;
 };
@@ -49,11 +48,13 @@ inline gdn_status_t scan_sizes(const gdn_scan_params_t* p, bool packed, ScanPlan
   return GDN_OK;
 }
 
-// ns states per lane and nw waves per workgroup.
-inline void scan_waves(ScanPlan* pl, int ns, int nw) {
-  pl->ns = ns;
-  pl->geo.nw = nw;
-  pl->geo.np = nw * ns;
+// ns states per lane and nw waves per 64 channels; workgroups of four waves where nw
+// divides into them.
+inline void scan_waves(gdn::ScanGeo* g, int ns, int nw) {
+  g->nw = nw;
+  g->np = nw * ns;
+  g->upw = nw < 4 ? 4 / nw : 1;
+  g->cgb = (int)ceil_div(g->cgroups, g->upw);
 }
 
 inline void scan_tiles(ScanPlan* pl, int len) {
