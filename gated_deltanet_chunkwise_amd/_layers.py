@@ -9,11 +9,10 @@ device.  Work is enqueued on `stream`, by default torch's current stream of that
 outputs and workspaces are allocated for it.
 """
 import collections
-import contextlib
 import ctypes
 
 from . import _binding
-from ._binding import GdnError, _check_tensor, _dtype_code, _ptr, _torch
+from ._binding import GdnError, _check_tensor, _dtype_code
 
 Packed8 = collections.namedtuple("Packed8", ("codes", "scales", "dtype"))
 Packed8.__doc__ = """A checkpoint of an activation [..., C] (pack8): codes [..., C] int8, scales
@@ -21,6 +20,16 @@ Packed8.__doc__ = """A checkpoint of an activation [..., C] (pack8): codes [...,
 
 _ACTIVATIONS = {None: 0, "silu": 1}
 PACK_BLOCK = 32  # channels per checkpoint scale
+
+
+_TORCH = None
+
+
+def _torch():
+    global _TORCH
+    if _TORCH is None:
+        _TORCH = _binding._torch()
+    return _TORCH
 
 
 class ConvParams(ctypes.Structure):
@@ -59,25 +68,64 @@ def declare(lib):
 
 
 # ---------------------------------------------------------------------------
-# checks
+# checks and launches.  A call of a small problem takes the GPU a few microseconds, so
+# these take care to take the host no longer.
 
-def _place(name, t, device):
-    if not t.is_cuda or t.device != device:
-        raise ValueError("%s must be a GPU tensor on %s, got %s" % (name, device, t.device))
+_RAW_STREAM = None
 
 
-def _dense(named, device):
-    """Every given tensor contiguous and on `device` (checked after the shapes)."""
-    for name, t in named:
+def _raw_stream(index):
+    """torch's current stream of GPU `index`, as the address the library takes."""
+    global _RAW_STREAM
+    if _RAW_STREAM is None:
+        torch = _torch()
+        _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _RAW_STREAM(index)
+
+
+def _lib():
+    return _binding._LIB or _binding.load_library()
+
+
+def _fit(specs):
+    """(name, tensor, shape, dtype) each: the tensor, where given, has exactly that shape
+    and dtype."""
+    for name, t, shape, dtype in specs:
+        if t is not None and (t.dtype is not dtype or t.shape != shape):
+            _check_tensor(name, t, shape, dtype)
+
+
+def _need(**tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError("%s is required" % name)
+
+
+def _place(x, rows, dense):
+    """The GPU (its index) that x and every other given tensor live on, `dense` ones
+    contiguous; both lists (name, tensor, ...)."""
+    index = x.get_device()
+    if index < 0:
+        raise ValueError("x must be a GPU tensor, got %s" % x.device)
+    for spec in rows:
+        if spec[1] is not None and spec[1].get_device() != index:
+            raise ValueError("%s must be a GPU tensor on %s, got %s" % (spec[0], x.device, spec[1].device))
+    for spec in dense:
+        t = spec[1]
         if t is not None:
-            _place(name, t, device)
+            if t.get_device() != index:
+                raise ValueError("%s must be a GPU tensor on %s, got %s" % (spec[0], x.device, t.device))
             if not t.is_contiguous():
-                raise ValueError("%s must be contiguous" % name)
+                raise ValueError("%s must be contiguous" % spec[0])
+    return index
 
 
 def _row_stride(name, t):
-    """Elements between the tokens of t [B, T, ...]; raises unless each token's values
-    are contiguous and the tokens evenly spaced."""
+    """Elements between the tokens of t [B, T, ...] (0: dense); raises unless each token's
+    values are contiguous and the tokens evenly spaced."""
+    if t.is_contiguous():
+        return 0
     B, T = t.shape[0], t.shape[1]
     width = 1
     for size, stride in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
@@ -85,67 +133,63 @@ def _row_stride(name, t):
             raise ValueError("%s: the values of a token must be contiguous" % name)
         width *= size
     if B * T <= 1:
-        return width
+        return 0
     ld = t.stride(1) if T > 1 else t.stride(0)
     if ld < width or (T > 1 and B > 1 and t.stride(0) != T * ld):
         raise ValueError("%s: tokens must be evenly spaced and not overlap" % name)
     return ld
 
 
-def _gpu(name, t):
-    if not t.is_cuda:
-        raise ValueError("%s must be a GPU tensor, got %s" % (name, t.device))
-
-
-@contextlib.contextmanager
-def _entered(device, stream, inputs):
+def _entered(index, stream, inputs, body):
     torch = _torch()
-    with torch.cuda.device(device):
+    with torch.cuda.device(index):
         if stream is None:
-            yield torch.cuda.current_stream(device)
-            return
-        if stream.device != device:
-            raise ValueError("stream belongs to %s, the tensors to %s" % (stream.device, device))
+            return body(_raw_stream(index))
+        if stream.device.index != index:
+            raise ValueError("stream belongs to %s, the tensors to GPU %d" % (stream.device, index))
         with torch.cuda.stream(stream):
-            yield stream
+            out = body(stream.cuda_stream)
         for t in inputs:  # not to be reused before the stream is through with them
             if t is not None:
                 t.record_stream(stream)
+        return out
 
 
-def _on(device, stream, inputs=()):
-    """The GPU current and the stream to launch on, in whose order outputs and
-    workspaces are allocated."""
-    torch = _torch()
-    if stream is None and device.index == torch.cuda.current_device():
-        return contextlib.nullcontext(torch.cuda.current_stream(device))
-    return _entered(device, stream, inputs)
+def _on(index, stream, inputs, body):
+    """body(stream address), with GPU `index` current and outputs and workspaces allocated
+    in the order of the stream that it launches on."""
+    if stream is None and index == _torch().cuda.current_device():
+        return body(_raw_stream(index))
+    return _entered(index, stream, inputs, body)
 
 
 def _call(name, *args):
-    st = getattr(_binding.load_library(), name)(*args)
+    """An entry point with its arguments: integers, tensors' addresses (or None) and params."""
+    st = getattr(_binding._LIB, name)(*args)
     if st:
         raise GdnError(st, name)
 
 
-def _stream_arg(stream):
-    return ctypes.c_void_p(stream.cuda_stream)
+def _p(t):
+    return None if t is None else t.data_ptr()
 
 
-def _workspace(bytes_, device):
+def _workspace(bytes_, index):
+    """(tensor, address, size); 256-byte aligned (torch's allocator aligns to 512)."""
+    if not bytes_:
+        return None, None, 0
     torch = _torch()
-    # 256-byte aligned (torch's caching allocator aligns blocks to at least 512)
-    return torch.empty(max(int(bytes_), 256), dtype=torch.uint8, device=device)
+    t = torch.empty(bytes_, dtype=torch.uint8, device=torch.device("cuda", index))
+    return t, t.data_ptr(), bytes_
 
 
-def _sequences(cu_seqlens, B, device):
+def _sequences(cu_seqlens, B):
     """Number of sequences."""
     if cu_seqlens is None:
         return B
-    torch = _torch()
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be [N+1]")
-    if cu_seqlens.dtype != torch.int64:
+    if cu_seqlens.dtype is not _torch().int64:
         raise TypeError("cu_seqlens must be int64, got %s" % cu_seqlens.dtype)
     if B != 1:
         raise ValueError("cu_seqlens needs B == 1, got %d" % B)
@@ -162,10 +206,9 @@ def pack8(x, stream=None):
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x must be [..., C]")
     code = _dtype_code(x.dtype)
-    _gpu("x", x)
+    index = _place(x, (), ())
     C = x.shape[-1]
-    rows = x.numel() // C
-    ld = C
+    ld = 0
     if not x.is_contiguous():
         # leading dimensions that merge into evenly spaced rows
         lead = [(n, s) for n, s in zip(x.shape[:-1], x.stride()[:-1]) if n != 1]
@@ -177,39 +220,41 @@ def pack8(x, stream=None):
             step *= n
         if not ok or ld < C:
             raise ValueError("x: rows of contiguous channels must be evenly spaced and not overlap")
-    with _on(x.device, stream, (x,)) as s:
+
+    def body(s):
         codes = torch.empty(x.shape, dtype=torch.int8, device=x.device)
         scales = torch.empty(x.shape[:-1] + ((C + PACK_BLOCK - 1) // PACK_BLOCK,), dtype=torch.uint8, device=x.device)
-        _call("gdn_pack8", _ptr(x), code, rows, C, ld, _ptr(codes), _ptr(scales), _stream_arg(s))
-    return Packed8(codes, scales, x.dtype)
+        _lib()
+        _call("gdn_pack8", x.data_ptr(), code, x.numel() // C, C, ld, codes.data_ptr(), scales.data_ptr(), s)
+        return Packed8(codes, scales, x.dtype)
+    return _on(index, stream, (x,), body)
 
 
 def _check_packed(name, p):
     torch = _torch()
-    if p.codes.dim() < 1 or p.codes.shape[-1] < 1:
+    shape = p.codes.shape
+    if not shape or shape[-1] < 1:
         raise ValueError("%s.codes must be [..., C]" % name)
-    C = p.codes.shape[-1]
-    _check_tensor(name + ".codes", p.codes, p.codes.shape, torch.int8)
-    _check_tensor(name + ".scales", p.scales, tuple(p.codes.shape[:-1]) + ((C + PACK_BLOCK - 1) // PACK_BLOCK,),
-                  torch.uint8)
+    _fit(((name + ".codes", p.codes, shape, torch.int8),
+          (name + ".scales", p.scales, shape[:-1] + ((shape[-1] + PACK_BLOCK - 1) // PACK_BLOCK,), torch.uint8)))
 
 
 def unpack8(packed, out=None, stream=None):
     """The activation a Packed8 stands for, in its dtype (gdn_unpack8)."""
     torch = _torch()
+    codes, scales, dtype = packed
     _check_packed("packed", packed)
-    code = _dtype_code(packed.dtype)
-    _check_tensor("out", out, packed.codes.shape, packed.dtype, required=False)
-    _gpu("packed.codes", packed.codes)
-    device = packed.codes.device
-    _dense([("packed.codes", packed.codes), ("packed.scales", packed.scales), ("out", out)], device)
-    C = packed.codes.shape[-1]
-    with _on(device, stream, (packed.codes, packed.scales, out)) as s:
-        if out is None:
-            out = torch.empty(packed.codes.shape, dtype=packed.dtype, device=device)
-        _call("gdn_unpack8", _ptr(packed.codes), _ptr(packed.scales), packed.codes.numel() // C, C, _ptr(out), code,
-              _stream_arg(s))
-    return out
+    code = _dtype_code(dtype)
+    _fit((("out", out, codes.shape, dtype),))
+    index = _place(codes, (), (("packed.codes", codes), ("packed.scales", scales), ("out", out)))
+
+    def body(s):
+        y = torch.empty(codes.shape, dtype=dtype, device=codes.device) if out is None else out
+        C = codes.shape[-1]
+        _lib()
+        _call("gdn_unpack8", codes.data_ptr(), scales.data_ptr(), codes.numel() // C, C, y.data_ptr(), code, s)
+        return y
+    return _on(index, stream, (codes, scales, out), body)
 
 
 def _maybe_packed(name, t):
@@ -231,14 +276,13 @@ def _conv_sizes(data, dtype, weight, bias, cu_seqlens, activation):
     if weight.dim() != 2:
         raise ValueError("weight must be [C, W]")
     W = weight.shape[1]
-    _check_tensor("weight", weight, (C, W), torch.float32)
-    _check_tensor("bias", bias, (C,), torch.float32, required=False)
+    _fit((("weight", weight, (C, W), torch.float32), ("bias", bias, (C,), torch.float32)))
     if activation not in _ACTIVATIONS:
         raise ValueError("activation must be None or 'silu', got %r" % (activation,))
-    N = _sequences(cu_seqlens, B, data.device)
+    N = _sequences(cu_seqlens, B)
     p = ConvParams(B, T, C, W, 0 if cu_seqlens is None else N, _dtype_code(dtype), _ACTIVATIONS[activation],
                    _row_stride("x", data))
-    return p, B, T, C, W, N
+    return ctypes.byref(p), B, T, C, W, N
 
 
 def conv_fwd(x, weight, bias=None, cu_seqlens=None, initial_state=None, activation="silu",
@@ -247,76 +291,85 @@ def conv_fwd(x, weight, bias=None, cu_seqlens=None, initial_state=None, activati
     weight [C,W] fp32 with W in 2..4, bias [C] fp32 or None, initial_state [N,W-1,C] in
     x's dtype or None, activation "silu" or None.  Returns (y [B,T,C], final_state
     [N,W-1,C] or None)."""
-    torch = _torch()
     p, B, T, C, W, N = _conv_sizes(x, x.dtype, weight, bias, cu_seqlens, activation)
-    _check_tensor("initial_state", initial_state, (N, W - 1, C), x.dtype, required=False)
-    _gpu("x", x)
-    _dense([("weight", weight), ("bias", bias), ("cu_seqlens", cu_seqlens), ("initial_state", initial_state)],
-           x.device)
-    with _on(x.device, stream, (x, weight, bias, cu_seqlens, initial_state)) as s:
-        y = torch.empty((B, T, C), dtype=x.dtype, device=x.device)
-        fin = torch.empty((N, max(W - 1, 0), C), dtype=x.dtype, device=x.device) if output_final_state else None
-        _call("gdn_conv_fwd", ctypes.byref(p), _ptr(x), _ptr(weight), _ptr(bias), _ptr(cu_seqlens),
-              _ptr(initial_state), _ptr(y), _ptr(fin), _stream_arg(s))
-    return y, fin
+    _fit((("initial_state", initial_state, (N, W - 1, C), x.dtype),))
+    index = _place(x, (), (("weight", weight), ("bias", bias), ("cu_seqlens", cu_seqlens),
+                           ("initial_state", initial_state)))
+
+    def body(s):
+        empty = _torch().empty
+        y = empty((B, T, C), dtype=x.dtype, device=x.device)
+        fin = empty((N, max(W - 1, 0), C), dtype=x.dtype, device=x.device) if output_final_state else None
+        _lib()
+        _call("gdn_conv_fwd", p, x.data_ptr(), weight.data_ptr(), _p(bias), _p(cu_seqlens), _p(initial_state),
+              y.data_ptr(), _p(fin), s)
+        return y, fin
+    return _on(index, stream, (x, weight, bias, cu_seqlens, initial_state), body)
 
 
 def conv_bwd(x, weight, bias, d_y, d_final_state=None, cu_seqlens=None, initial_state=None, activation="silu",
              stream=None):
     """Gradients of conv_fwd through gdn_conv_bwd: dict of dx [B,T,C] and dh0 [N,W-1,C]
     in x's dtype, dweight [C,W] and dbias [C] fp32.  x may be its checkpoint (Packed8)."""
-    torch = _torch()
     data, scales, dtype = _maybe_packed("x", x)
     p, B, T, C, W, N = _conv_sizes(data, dtype, weight, bias, cu_seqlens, activation)
-    _check_tensor("d_y", d_y, (B, T, C), dtype)
-    _check_tensor("d_final_state", d_final_state, (N, W - 1, C), dtype, required=False)
-    _check_tensor("initial_state", initial_state, (N, W - 1, C), dtype, required=False)
-    _gpu("x", data)
-    device = data.device
-    _dense([("weight", weight), ("bias", bias), ("cu_seqlens", cu_seqlens), ("initial_state", initial_state),
-            ("d_y", d_y), ("d_final_state", d_final_state), ("x.scales", scales)], device)
-    ws_bytes = int(_binding.load_library().gdn_conv_bwd_workspace_size(ctypes.byref(p), int(cu_seqlens is not None)))
-    with _on(device, stream, (data, scales, weight, bias, cu_seqlens, initial_state, d_y, d_final_state)) as s:
-        dx = torch.empty((B, T, C), dtype=dtype, device=device)
-        dw = torch.empty((C, W), dtype=torch.float32, device=device)
-        db = torch.empty((C,), dtype=torch.float32, device=device)
-        dh0 = torch.empty((N, max(W - 1, 0), C), dtype=dtype, device=device)
-        ws = _workspace(ws_bytes, device)
-        _call("gdn_conv_bwd", ctypes.byref(p), _ptr(data), _ptr(scales), _ptr(weight), _ptr(bias),
-              _ptr(cu_seqlens), _ptr(initial_state), _ptr(d_y), _ptr(d_final_state), _ptr(dx), _ptr(dw), _ptr(db),
-              _ptr(dh0), _ptr(ws), ws.numel(), _stream_arg(s))
-    return dict(dx=dx, dweight=dw, dbias=db, dh0=dh0)
+    _need(d_y=d_y)
+    _fit((("d_y", d_y, (B, T, C), dtype), ("d_final_state", d_final_state, (N, W - 1, C), dtype),
+          ("initial_state", initial_state, (N, W - 1, C), dtype)))
+    index = _place(data, (), (("weight", weight), ("bias", bias), ("cu_seqlens", cu_seqlens),
+                              ("initial_state", initial_state), ("d_y", d_y), ("d_final_state", d_final_state),
+                              ("x.scales", scales)))
+    ws_bytes = _lib().gdn_conv_bwd_workspace_size(p, int(cu_seqlens is not None))
+
+    def body(s):
+        torch = _torch()
+        empty, device, f32 = torch.empty, data.device, torch.float32
+        g = dict(dx=empty((B, T, C), dtype=dtype, device=device), dweight=empty((C, W), dtype=f32, device=device),
+                 dbias=empty((C,), dtype=f32, device=device),
+                 dh0=empty((N, max(W - 1, 0), C), dtype=dtype, device=device))
+        ws, ws_ptr, ws_size = _workspace(ws_bytes, index)
+        _call("gdn_conv_bwd", p, data.data_ptr(), _p(scales), weight.data_ptr(), _p(bias), _p(cu_seqlens),
+              _p(initial_state), d_y.data_ptr(), _p(d_final_state), g["dx"].data_ptr(), g["dweight"].data_ptr(),
+              g["dbias"].data_ptr(), g["dh0"].data_ptr(), ws_ptr, ws_size, s)
+        return g
+    return _on(index, stream, (data, scales, weight, bias, cu_seqlens, initial_state, d_y, d_final_state), body)
+
+
+def _conv_decode_args(x, weight, state, bias, activation, new_state, out):
+    p, B, T, C, W, _ = _conv_sizes(x, x.dtype, weight, bias, None, activation)
+    _need(state=state)
+    shape = (B, W - 1, C)
+    _fit((("state", state, shape, x.dtype), ("new_state", new_state, shape, x.dtype), ("out", out, (B, T, C), x.dtype)))
+    index = _place(x, (), (("weight", weight), ("bias", bias), ("state", state), ("new_state", new_state), ("out", out)))
+
+    def args(s):
+        y = _torch().empty((B, T, C), dtype=x.dtype, device=x.device) if out is None else out
+        new = state if new_state is None else new_state
+        _lib()
+        return (p, x.data_ptr(), weight.data_ptr(), _p(bias), state.data_ptr(), new.data_ptr(), y.data_ptr(), s), y
+    return index, args
 
 
 def conv_decode_launcher(x, weight, state, bias=None, activation="silu", new_state=None, out=None, stream=None):
     """Check and marshal gdn_conv_decode's arguments once; returns (launch, y), where
     launch() enqueues the convolution of x's T tokens after `state` [B,W-1,C], writing
     the state after them to new_state (default: `state` itself)."""
-    torch = _torch()
-    p, B, T, C, W, _ = _conv_sizes(x, x.dtype, weight, bias, None, activation)
-    _check_tensor("state", state, (B, W - 1, C), x.dtype)
-    _check_tensor("new_state", new_state, (B, W - 1, C), x.dtype, required=False)
-    _check_tensor("out", out, (B, T, C), x.dtype, required=False)
-    _gpu("x", x)
-    _dense([("weight", weight), ("bias", bias), ("state", state), ("new_state", new_state), ("out", out)], x.device)
-    new = state if new_state is None else new_state
-    with _on(x.device, stream, (x, weight, bias, state, new_state, out)) as s:
-        if out is None:
-            out = torch.empty((B, T, C), dtype=x.dtype, device=x.device)
-    args = (ctypes.byref(p), _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(new), _ptr(out), _stream_arg(s))
-    return _launcher("gdn_conv_decode", x.device, args, (p, s, x, weight, bias, state, new, out)), out
+    index, args = _conv_decode_args(x, weight, state, bias, activation, new_state, out)
+    keep = (x, weight, state, bias, new_state, out, stream)
+    args, y = _on(index, stream, keep[:-1], args)
+    return _launcher("gdn_conv_decode", index, args, keep + (y,)), y
 
 
-def _launcher(name, device, args, keep):
+def _launcher(name, index, args, keep):
     torch = _torch()
-    fn = getattr(_binding.load_library(), name)
+    fn = getattr(_lib(), name)
 
     def launch():
         keep  # the tensors stay alive as long as the callable
-        if torch.cuda.current_device() == device.index:
+        if torch.cuda.current_device() == index:
             st = fn(*args)
         else:
-            with torch.cuda.device(device):
+            with torch.cuda.device(index):
                 st = fn(*args)
         if st:
             raise GdnError(st, name)
@@ -326,47 +379,41 @@ def _launcher(name, device, args, keep):
 def conv_decode(x, weight, state, bias=None, activation="silu", new_state=None, out=None, stream=None):
     """T tokens (1: a decode step) of each of B sequences through gdn_conv_decode: returns
     y [B,T,C]; the state after them goes to new_state, or updates `state` in place."""
-    launch, out = conv_decode_launcher(x, weight, state, bias, activation, new_state, out, stream)
-    launch()
-    return out
+    index, args = _conv_decode_args(x, weight, state, bias, activation, new_state, out)
+
+    def body(s):
+        a, y = args(s)
+        _call("gdn_conv_decode", *a)
+        return y
+    return _on(index, stream, (x, weight, state, bias, new_state, out), body)
 
 
 # ---------------------------------------------------------------------------
 # selective state space scan
 
 def _scan_sizes(x, dtype, dt, A_log, Bm, Cm, skip, z, z_dtype, dt_bias, cu_seqlens):
-    torch = _torch()
-    f32 = torch.float32
+    f32 = _torch().float32
     if x.dim() != 3:
         raise ValueError("x must be [B, T, D]")
-    B, T, D = x.shape
+    shape = x.shape
+    B, T, D = shape
     if A_log.dim() != 2 or Bm.dim() != 4:
         raise ValueError("A_log must be [D, N] and Bm [B, T, G, N]")
     N, G = A_log.shape[1], Bm.shape[2]
-    _check_tensor("dt", dt, (B, T, D), dtype)
-    _check_tensor("A_log", A_log, (D, N), f32)
-    _check_tensor("Bm", Bm, (B, T, G, N), dtype)
-    _check_tensor("Cm", Cm, (B, T, G, N), dtype)
-    _check_tensor("skip", skip, (D,), f32, required=False)
+    rows = (B, T, G, N)
+    _fit((("dt", dt, shape, dtype), ("A_log", A_log, (D, N), f32), ("Bm", Bm, rows, dtype), ("Cm", Cm, rows, dtype),
+          ("skip", skip, (D,), f32), ("dt_bias", dt_bias, (D,), f32)))
+    z_ld = 0
     if z is not None:
-        if tuple(z.shape) != (B, T, D):
+        if z.shape != shape:
             raise ValueError("z must have shape %s, got %s" % ((B, T, D), tuple(z.shape)))
-        if z_dtype != dtype:
+        if z_dtype is not dtype:
             raise TypeError("z must be %s, got %s" % (dtype, z_dtype))
-    _check_tensor("dt_bias", dt_bias, (D,), f32, required=False)
-    S = _sequences(cu_seqlens, B, x.device)
+        z_ld = _row_stride("z", z)
+    S = _sequences(cu_seqlens, B)
     p = ScanParams(B, T, D, G, N, 0 if cu_seqlens is None else S, _dtype_code(dtype), _row_stride("x", x),
-                   _row_stride("dt", dt), 0 if z is None else _row_stride("z", z), _row_stride("Bm", Bm),
-                   _row_stride("Cm", Cm))
-    return p, B, T, D, G, N, S
-
-
-def _scan_place(x, dt, Bm, Cm, z, dense):
-    _gpu("x", x)
-    for name, t in (("dt", dt), ("Bm", Bm), ("Cm", Cm), ("z", z)):
-        if t is not None:
-            _place(name, t, x.device)
-    _dense(dense, x.device)
+                   _row_stride("dt", dt), z_ld, _row_stride("Bm", Bm), _row_stride("Cm", Cm))
+    return ctypes.byref(p), B, T, D, G, N, S
 
 
 def scan_fwd(x, dt, A_log, Bm, Cm, skip=None, z=None, dt_bias=None, cu_seqlens=None, initial_state=None,
@@ -375,21 +422,24 @@ def scan_fwd(x, dt, A_log, Bm, Cm, skip=None, z=None, dt_bias=None, cu_seqlens=N
     [B,T,G,N] in bf16 or fp32, A_log [D,N], skip and dt_bias [D] fp32, initial_state
     [sequences,D,N] fp32; skip, z, dt_bias and initial_state may be None.  Returns
     (y [B,T,D], final_state [sequences,D,N] fp32 or None)."""
-    torch = _torch()
+    f32 = _torch().float32
     p, B, T, D, G, N, S = _scan_sizes(x, x.dtype, dt, A_log, Bm, Cm, skip, z, None if z is None else z.dtype,
                                       dt_bias, cu_seqlens)
-    _check_tensor("initial_state", initial_state, (S, D, N), torch.float32, required=False)
-    _scan_place(x, dt, Bm, Cm, z, [("A_log", A_log), ("skip", skip), ("dt_bias", dt_bias),
-                                   ("cu_seqlens", cu_seqlens), ("initial_state", initial_state)])
-    ws_bytes = int(_binding.load_library().gdn_scan_fwd_workspace_size(ctypes.byref(p), int(cu_seqlens is not None)))
-    with _on(x.device, stream, (x, dt, A_log, Bm, Cm, skip, z, dt_bias, cu_seqlens, initial_state)) as s:
-        y = torch.empty((B, T, D), dtype=x.dtype, device=x.device)
-        fin = torch.empty((S, D, N), dtype=torch.float32, device=x.device) if output_final_state else None
-        ws = _workspace(ws_bytes, x.device)
-        _call("gdn_scan_fwd", ctypes.byref(p), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(Bm), _ptr(Cm), _ptr(skip),
-              _ptr(z), _ptr(dt_bias), _ptr(cu_seqlens), _ptr(initial_state), _ptr(y), _ptr(fin), _ptr(ws),
-              ws.numel(), _stream_arg(s))
-    return y, fin
+    _fit((("initial_state", initial_state, (S, D, N), f32),))
+    index = _place(x, (("dt", dt), ("Bm", Bm), ("Cm", Cm), ("z", z)),
+                   (("A_log", A_log), ("skip", skip), ("dt_bias", dt_bias), ("cu_seqlens", cu_seqlens),
+                    ("initial_state", initial_state)))
+    ws_bytes = _lib().gdn_scan_fwd_workspace_size(p, int(cu_seqlens is not None))
+
+    def body(s):
+        empty = _torch().empty
+        y = empty((B, T, D), dtype=x.dtype, device=x.device)
+        fin = empty((S, D, N), dtype=f32, device=x.device) if output_final_state else None
+        ws, ws_ptr, ws_size = _workspace(ws_bytes, index)
+        _call("gdn_scan_fwd", p, x.data_ptr(), dt.data_ptr(), A_log.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), _p(skip),
+              _p(z), _p(dt_bias), _p(cu_seqlens), _p(initial_state), y.data_ptr(), _p(fin), ws_ptr, ws_size, s)
+        return y, fin
+    return _on(index, stream, (x, dt, A_log, Bm, Cm, skip, z, dt_bias, cu_seqlens, initial_state), body)
 
 
 def scan_bwd(x, dt, A_log, Bm, Cm, d_y, d_final_state=None, skip=None, z=None, dt_bias=None, cu_seqlens=None,
@@ -397,36 +447,57 @@ def scan_bwd(x, dt, A_log, Bm, Cm, d_y, d_final_state=None, skip=None, z=None, d
     """Gradients of scan_fwd through gdn_scan_bwd: dict of dx, ddt, dBm, dCm (and dz with
     z) in x's dtype, dA_log, dskip, ddt_bias and dh0 in fp32.  x and z may both be their
     checkpoints (Packed8)."""
-    torch = _torch()
-    f32 = torch.float32
+    f32 = _torch().float32
     xd, xs, dtype = _maybe_packed("x", x)
     zd, zs, z_dtype = (None, None, None) if z is None else _maybe_packed("z", z)
     if z is not None and (xs is None) != (zs is None):
         raise ValueError("x and z must both be checkpoints, or neither")
     p, B, T, D, G, N, S = _scan_sizes(xd, dtype, dt, A_log, Bm, Cm, skip, zd, z_dtype, dt_bias, cu_seqlens)
-    _check_tensor("d_y", d_y, (B, T, D), dtype)
-    _check_tensor("d_final_state", d_final_state, (S, D, N), f32, required=False)
-    _check_tensor("initial_state", initial_state, (S, D, N), f32, required=False)
-    device = xd.device
-    _scan_place(xd, dt, Bm, Cm, zd, [("A_log", A_log), ("skip", skip), ("dt_bias", dt_bias),
-                                     ("cu_seqlens", cu_seqlens), ("initial_state", initial_state), ("d_y", d_y),
-                                     ("d_final_state", d_final_state), ("x.scales", xs), ("z.scales", zs)])
-    ws_bytes = int(_binding.load_library().gdn_scan_bwd_workspace_size(ctypes.byref(p), int(cu_seqlens is not None)))
-    with _on(device, stream, (xd, xs, dt, A_log, Bm, Cm, d_y, d_final_state, skip, zd, zs, dt_bias, cu_seqlens,
-                              initial_state)) as s:
-        new = lambda shape, dt_: torch.empty(shape, dtype=dt_, device=device)  # noqa: E731
+    _need(d_y=d_y)
+    _fit((("d_y", d_y, (B, T, D), dtype), ("d_final_state", d_final_state, (S, D, N), f32),
+          ("initial_state", initial_state, (S, D, N), f32)))
+    index = _place(xd, (("dt", dt), ("Bm", Bm), ("Cm", Cm), ("z", zd)),
+                   (("A_log", A_log), ("skip", skip), ("dt_bias", dt_bias), ("cu_seqlens", cu_seqlens),
+                    ("initial_state", initial_state), ("d_y", d_y), ("d_final_state", d_final_state),
+                    ("x.scales", xs), ("z.scales", zs)))
+    ws_bytes = _lib().gdn_scan_bwd_workspace_size(p, int(cu_seqlens is not None))
+
+    def body(s):
+        empty, device = _torch().empty, xd.device
+        new = lambda shape, dt_: empty(shape, dtype=dt_, device=device)  # noqa: E731
         g = dict(dx=new((B, T, D), dtype), ddt=new((B, T, D), dtype), dA_log=new((D, N), f32),
                  dBm=new((B, T, G, N), dtype), dCm=new((B, T, G, N), dtype), dskip=new((D,), f32),
                  ddt_bias=new((D,), f32), dh0=new((S, D, N), f32))
         if z is not None:
             g["dz"] = new((B, T, D), dtype)
-        ws = _workspace(ws_bytes, device)
-        _call("gdn_scan_bwd", ctypes.byref(p), _ptr(xd), _ptr(xs), _ptr(dt), _ptr(A_log), _ptr(Bm), _ptr(Cm),
-              _ptr(skip), _ptr(zd), _ptr(zs), _ptr(dt_bias), _ptr(cu_seqlens), _ptr(initial_state), _ptr(d_y),
-              _ptr(d_final_state), _ptr(g["dx"]), _ptr(g["ddt"]), _ptr(g["dA_log"]), _ptr(g["dBm"]),
-              _ptr(g["dCm"]), _ptr(g["dskip"]), _ptr(g.get("dz")), _ptr(g["ddt_bias"]), _ptr(g["dh0"]), _ptr(ws),
-              ws.numel(), _stream_arg(s))
-    return g
+        ws, ws_ptr, ws_size = _workspace(ws_bytes, index)
+        _call("gdn_scan_bwd", p, xd.data_ptr(), _p(xs), dt.data_ptr(), A_log.data_ptr(), Bm.data_ptr(), Cm.data_ptr(),
+              _p(skip), _p(zd), _p(zs), _p(dt_bias), _p(cu_seqlens), _p(initial_state), d_y.data_ptr(),
+              _p(d_final_state), g["dx"].data_ptr(), g["ddt"].data_ptr(), g["dA_log"].data_ptr(), g["dBm"].data_ptr(),
+              g["dCm"].data_ptr(), g["dskip"].data_ptr(), _p(g.get("dz")), g["ddt_bias"].data_ptr(),
+              g["dh0"].data_ptr(), ws_ptr, ws_size, s)
+        return g
+    return _on(index, stream, (xd, xs, dt, A_log, Bm, Cm, d_y, d_final_state, skip, zd, zs, dt_bias, cu_seqlens,
+                               initial_state), body)
+
+
+def _scan_decode_args(x, dt, A_log, Bm, Cm, state, skip, z, dt_bias, new_state, out):
+    f32 = _torch().float32
+    p, B, T, D, G, N, _ = _scan_sizes(x, x.dtype, dt, A_log, Bm, Cm, skip, z, None if z is None else z.dtype,
+                                      dt_bias, None)
+    _need(state=state)
+    _fit((("state", state, (B, D, N), f32), ("new_state", new_state, (B, D, N), f32), ("out", out, (B, T, D), x.dtype)))
+    index = _place(x, (("dt", dt), ("Bm", Bm), ("Cm", Cm), ("z", z)),
+                   (("A_log", A_log), ("skip", skip), ("dt_bias", dt_bias), ("state", state), ("new_state", new_state),
+                    ("out", out)))
+
+    def args(s):
+        y = _torch().empty((B, T, D), dtype=x.dtype, device=x.device) if out is None else out
+        new = state if new_state is None else new_state
+        _lib()
+        return (p, x.data_ptr(), dt.data_ptr(), A_log.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), _p(skip), _p(z),
+                _p(dt_bias), state.data_ptr(), new.data_ptr(), y.data_ptr(), s), y
+    return index, args
 
 
 def scan_decode_launcher(x, dt, A_log, Bm, Cm, state, skip=None, z=None, dt_bias=None, new_state=None, out=None,
@@ -434,31 +505,23 @@ def scan_decode_launcher(x, dt, A_log, Bm, Cm, state, skip=None, z=None, dt_bias
     """Check and marshal gdn_scan_decode's arguments once; returns (launch, y), where
     launch() enqueues the scan of x's T tokens after `state` [B,D,N], writing the state
     after them to new_state (default: `state` itself)."""
-    torch = _torch()
-    p, B, T, D, G, N, _ = _scan_sizes(x, x.dtype, dt, A_log, Bm, Cm, skip, z, None if z is None else z.dtype,
-                                      dt_bias, None)
-    _check_tensor("state", state, (B, D, N), torch.float32)
-    _check_tensor("new_state", new_state, (B, D, N), torch.float32, required=False)
-    _check_tensor("out", out, (B, T, D), x.dtype, required=False)
-    _scan_place(x, dt, Bm, Cm, z, [("A_log", A_log), ("skip", skip), ("dt_bias", dt_bias), ("state", state),
-                                   ("new_state", new_state), ("out", out)])
-    new = state if new_state is None else new_state
-    with _on(x.device, stream, (x, dt, A_log, Bm, Cm, skip, z, dt_bias, state, new_state, out)) as s:
-        if out is None:
-            out = torch.empty((B, T, D), dtype=x.dtype, device=x.device)
-    args = (ctypes.byref(p), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(Bm), _ptr(Cm), _ptr(skip), _ptr(z), _ptr(dt_bias),
-            _ptr(state), _ptr(new), _ptr(out), _stream_arg(s))
-    return _launcher("gdn_scan_decode", x.device, args,
-                     (p, s, x, dt, A_log, Bm, Cm, skip, z, dt_bias, state, new, out)), out
+    index, args = _scan_decode_args(x, dt, A_log, Bm, Cm, state, skip, z, dt_bias, new_state, out)
+    keep = (x, dt, A_log, Bm, Cm, state, skip, z, dt_bias, new_state, out, stream)
+    args, y = _on(index, stream, keep[:-1], args)
+    return _launcher("gdn_scan_decode", index, args, keep + (y,)), y
 
 
 def scan_decode(x, dt, A_log, Bm, Cm, state, skip=None, z=None, dt_bias=None, new_state=None, out=None,
                 stream=None):
     """T tokens (1: a decode step) of each of B sequences through gdn_scan_decode: returns
     y [B,T,D]; the state after them goes to new_state, or updates `state` in place."""
-    launch, out = scan_decode_launcher(x, dt, A_log, Bm, Cm, state, skip, z, dt_bias, new_state, out, stream)
-    launch()
-    return out
+    index, args = _scan_decode_args(x, dt, A_log, Bm, Cm, state, skip, z, dt_bias, new_state, out)
+
+    def body(s):
+        a, y = args(s)
+        _call("gdn_scan_decode", *a)
+        return y
+    return _on(index, stream, (x, dt, A_log, Bm, Cm, state, skip, z, dt_bias, new_state, out), body)
 
 
 # ---------------------------------------------------------------------------
