@@ -25,18 +25,28 @@ struct ConvGeo {
 
 __device__ __forceinline__ float conv_act(float s, bool silu) { return silu ? s * fast_sigmoid(s) : s; }
 
-// Row of the sequence's inputs at place p (p < 0: the initial state), as fp32.
+// The inputs at place q of sequence n (q < 0: rows of the initial state, or zeros),
+// behind one load whatever the place, so that loads of several rows are in flight
+// together.  x from a checkpoint: the initial state is read on its own.
 template <typename E, int W, int VEC>
-__device__ __forceinline__ void conv_before(const ConvGeo& g, const Src& x, const E* h0, int n,
-                                            int64_t start, int64_t p, int c, float (&v)[VEC]) {
-  if (p >= 0) {
-    raw_unpack<E, VEC>(raw_load<E, VEC>(x, start + p, c, g.nblk), x.scales != nullptr, v);
-  } else if (h0) {
-    vec_load<E, VEC>(h0 + ((int64_t)n * (W - 1) + (W - 1 + p)) * g.C + c, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = 0.f;
+__device__ __forceinline__ RawVec<E, VEC> conv_row(const ConvGeo& g, const Src& x, const E* h0, int n,
+                                                   int start, int q, int c) {
+  if (x.scales) {
+    if (q >= 0) return raw_load<E, VEC>(x, start + q, c, g.nblk);
+    RawVec<E, VEC> r = {};
+    if (h0) r = raw_load<E, VEC>(Src{h0, nullptr, g.C}, (int64_t)n * (W - 1) + (W - 1 + q), c, 0);
+    return r;
   }
+  const E* p = static_cast<const E*>(x.p) + (int64_t)(start + max(q, 0)) * x.ld;
+  const bool before = q < 0;
+  if (before && h0) p = h0 + ((int64_t)n * (W - 1) + (W - 1 + q)) * g.C;
+  RawVec<E, VEC> r = raw_load<E, VEC>(Src{p, nullptr, 0}, 0, c, 0);
+  if (before && !h0) r = {};
+  return r;
+}
+template <typename E, int W, int VEC>
+__device__ __forceinline__ void conv_value(const RawVec<E, VEC>& r, bool packed, int q, float (&v)[VEC]) {
+  raw_unpack<E, VEC>(r, packed && q >= 0, v);
 }
 
 template <int W, int VEC>
@@ -53,49 +63,63 @@ __device__ __forceinline__ void conv_params(const float* weight, const float* bi
 constexpr int kConvGroup = 8;  // tokens whose loads are in flight together
 
 // Work items: (tile, vector of channels), then (sequence, state row, vector) for
-// the final state.  Consecutive lanes take consecutive vectors of a row.
+// the final state.  Consecutive lanes take consecutive vectors of a row.  The rows of a
+// tile's first group are sent for before the weights: a lane's life is little more than
+// its loads' latency.
 template <typename E, int W, int VEC>
 __global__ __launch_bounds__(256) void gdn_conv_fwd_kernel(ConvGeo g, Src x,
                                                            const float* __restrict__ weight,
                                                            const float* __restrict__ bias,
                                                            const E* __restrict__ h0,
                                                            E* __restrict__ y, E* __restrict__ fin) {
-  const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t unit = item / g.cvn;
+  const uint32_t item = blockIdx.x * 256u + threadIdx.x;  // below 2^32, see the host
+  const uint32_t unit = item / (uint32_t)g.cvn;
   const int c = (int)(item - unit * g.cvn) * VEC;
-  const int64_t tiles = (int64_t)g.ntiles * (g.cu ? 1 : g.B);
+  const uint32_t tiles = (uint32_t)g.ntiles * (g.cu ? 1 : g.B);
   if (unit >= tiles) {
-    const int64_t r = unit - tiles;
-    if (!fin || r >= (int64_t)g.N * (W - 1)) return;
-    const int n = (int)(r / (W - 1)), row = (int)(r - (int64_t)n * (W - 1));
-    const int64_t start = g.cu ? seq_offset(g.cu, n, g.T) : (int64_t)n * g.T;
-    const int64_t end = g.cu ? seq_offset(g.cu, n + 1, g.T) : start + g.T;
-    const int64_t len = end > start ? end - start : 0;
+    const uint32_t r = unit - tiles;
+    if (!fin || r >= (uint64_t)g.N * (W - 1)) return;
+    const int n = r / (W - 1), row = r - n * (W - 1);
+    const int start = g.cu ? seq_offset(g.cu, n, g.T) : n * g.T;
+    const int end = g.cu ? seq_offset(g.cu, n + 1, g.T) : start + g.T;
+    const int len = max(end - start, 0);
     float v[VEC];
-    conv_before<E, W, VEC>(g, x, h0, n, start, len - (W - 1) + row, c, v);
-    vec_store<E, VEC>(fin + r * g.C + c, v);
+    // (a row of the initial state where there are no tokens at all)
+    if (len == 0 && !h0)
+      for (int i = 0; i < VEC; ++i) v[i] = 0.f;
+    else conv_value<E, W, VEC>(conv_row<E, W, VEC>(g, x, h0, n, start, len - (W - 1) + row, c), false, 0, v);
+    vec_store<E, VEC>(fin + (int64_t)r * g.C + c, v);
     return;
   }
-  float w[VEC][W], b[VEC];
-  conv_params<W, VEC>(weight, bias, c, w, b);
   const bool silu = g.silu;
   Run<false> run;
   run.init(g.cu, g.T, g.N, (int)unit, g.ntiles, g.tile);
-  for (; !run.done(); run.next()) {
-    float win[W - 1][VEC];
+  RawVec<E, VEC> old[W - 1], raw[kConvGroup];
+  auto first = [&]() {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
-      conv_before<E, W, VEC>(g, x, h0, run.n, run.start, run.ta - run.start - (W - 1) + j, c, win[j]);
-    for (int t = run.ta; t < run.tb; t += kConvGroup) {
-      RawVec<E, VEC> raw[kConvGroup];
+      old[j] = conv_row<E, W, VEC>(g, x, h0, run.n, run.start, run.ta - run.start - (W - 1) + j, c);
 #pragma unroll
-      for (int k = 0; k < kConvGroup; ++k)
-        raw[k] = raw_load<E, VEC>(x, min(t + k, run.tb - 1), c, g.nblk);
+    for (int k = 0; k < kConvGroup; ++k) raw[k] = raw_load<E, VEC>(x, min(run.ta + k, run.tb - 1), c, 0);
+  };
+  if (run.done()) return;
+  first();
+  float w[VEC][W], b[VEC];
+  conv_params<W, VEC>(weight, bias, c, w, b);
+  for (;;) {
+    float win[W - 1][VEC];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) conv_value<E, W, VEC>(old[j], false, 0, win[j]);
+    for (int t = run.ta; t < run.tb; t += kConvGroup) {
+      if (t > run.ta) {
+#pragma unroll
+        for (int k = 0; k < kConvGroup; ++k) raw[k] = raw_load<E, VEC>(x, min(t + k, run.tb - 1), c, 0);
+      }
 #pragma unroll
       for (int k = 0; k < kConvGroup; ++k) {
         if (t + k >= run.tb) break;
         float cur[VEC], out[VEC];
-        raw_unpack<E, VEC>(raw[k], x.scales != nullptr, cur);
+        raw_unpack<E, VEC>(raw[k], false, cur);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           float s = b[i];
@@ -113,6 +137,9 @@ __global__ __launch_bounds__(256) void gdn_conv_fwd_kernel(ConvGeo g, Src x,
         }
       }
     }
+    run.next();
+    if (run.done()) return;
+    first();
   }
 }
 
@@ -170,38 +197,120 @@ __global__ __launch_bounds__(256) void gdn_conv_decode_kernel(ConvGeo g, Src x,
 // workgroup that own the same channels add theirs through LDS, and each workgroup
 // writes one row of partial sums, added up in a fixed order by the sums kernel.
 
-template <int W>
+// dy times the activation's slope at s.
 __device__ __forceinline__ float conv_dact(float s, float dy, bool silu) {
-  if (!silu) return dy;
-  const float sg = fast_sigmoid(s);
-  // d/ds s sg = sg + s sg (1 - sg); 1 - sg formed as sigmoid(-s) keeps it exact
-  // where sg rounds to 1
-  return dy * fmaf(s * sg, fast_sigmoid(-s), sg);
+  return silu ? dy * silu_slope(s, fast_sigmoid(s)) : dy;
 }
 
-// Workgroup: cl lanes (a power of two) of neighbouring vectors times 256 / cl tiles.
-// Block id = (group of tiles, channel group of cl vectors), the latter fastest.
-// partial [tile groups][W + 1][C]: dweight's W rows, then dbias.
+// d_initial of one (sequence, vector): the first W-1 outputs' p once more.
 template <typename E, int W, int VEC>
-__global__ __launch_bounds__(256) void gdn_conv_bwd_kernel(ConvGeo g, Src x,
-                                                           const float* __restrict__ weight,
-                                                           const float* __restrict__ bias,
-                                                           const E* __restrict__ h0,
-                                                           const E* __restrict__ d_y,
-                                                           const E* __restrict__ d_fin,
-                                                           E* __restrict__ dx,
-                                                           float* __restrict__ partial, int cl,
-                                                           int cgroups) {
-  __shared__ float sm[256 * VEC];
-  const int tl = 256 / cl, lc = threadIdx.x & (cl - 1), lt = threadIdx.x / cl;
+__device__ __forceinline__ void conv_bwd_state(const ConvGeo& g, const Src& x, const float* weight,
+                                               const float* bias, const E* h0, const E* d_y,
+                                               const E* d_fin, E* dh0, int n, int c) {
+  const int start = g.cu ? seq_offset(g.cu, n, g.T) : n * g.T;
+  const int end = g.cu ? seq_offset(g.cu, n + 1, g.T) : start + g.T;
+  const int len = max(end - start, 0);
+  const bool packed = x.scales != nullptr;
+  float out[W - 1][VEC];
+#pragma unroll
+  for (int r = 0; r < W - 1; ++r) {
+    const int kept = r - len;  // the final row that holds row r, if any
+    if (d_fin && kept >= 0) vec_load<E, VEC>(d_fin + ((int64_t)n * (W - 1) + kept) * g.C + c, out[r]);
+    else
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) out[r][i] = 0.f;
+  }
+  if (len > 0) {
+    RawVec<E, VEC> raw[2 * (W - 1)], rd[W - 1];  // places -(W-1) .. W-2, held to the last
+#pragma unroll
+    for (int j = 0; j < 2 * (W - 1); ++j)
+      raw[j] = conv_row<E, W, VEC>(g, x, h0, n, start, min(j - (W - 1), len - 1), c);
+#pragma unroll
+    for (int q = 0; q < W - 1; ++q) rd[q] = raw_load<E, VEC>(Src{d_y, nullptr, g.C}, start + min(q, len - 1), c, 0);
+    float w[VEC][W], b[VEC], line[2 * (W - 1)][VEC];
+    conv_params<W, VEC>(weight, bias, c, w, b);
+#pragma unroll
+    for (int j = 0; j < 2 * (W - 1); ++j) conv_value<E, W, VEC>(raw[j], packed, j - (W - 1), line[j]);
+#pragma unroll
+    for (int q = 0; q < W - 1; ++q) {
+      if (q >= len) break;
+      float d[VEC];
+      raw_unpack<E, VEC>(rd[q], false, d);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        float s = b[i];
+#pragma unroll
+        for (int j = 0; j < W; ++j) s = fmaf(w[i][j], line[q + j][i], s);
+        const float p = conv_dact(s, d[i], g.silu);
+#pragma unroll
+        for (int r = q; r < W - 1; ++r) out[r][i] = fmaf(w[i][r - q], p, out[r][i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < W - 1; ++r) vec_store<E, VEC>(dh0 + ((int64_t)n * (W - 1) + r) * g.C + c, out[r]);
+}
+
+// U tokens of one vector of channels as loaded, so that the loads are all in flight
+// before the first is converted.
+template <typename E, int VEC, int U, bool CK> struct VecVals {
+  RawVec<E, VEC> v[U];
+  // tokens t .. t + U - 1, those from `end` on held to the last before it
+  __device__ __forceinline__ void fetch(const Src& src, int t, int end, uint32_t off, uint32_t soff, int nblk) {
+    if (t + U <= end) walk(src, t, off, soff, nblk, [](int) { return true; });
+    else walk(src, t, off, soff, nblk, [&](int k) { return t + k + 1 < end; });
+  }
+  template <typename F>
+  __device__ __forceinline__ void walk(const Src& src, int t, uint32_t off, uint32_t soff, int nblk, F&& more) {
+    const int64_t step = src.ld * (CK ? 1 : (int)sizeof(E));
+    Global<const char> p = (Global<const char>)src.p + t * step;
+    Global<const uint8_t> q = (Global<const uint8_t>)src.scales + (CK ? (int64_t)t * nblk : 0);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      v[k] = raw_load_at<E, VEC, CK>(p, q, off, soff);
+      p = stepped<const char>(p, more(k) ? step : 0);
+      if constexpr (CK) q = stepped<const uint8_t>(q, more(k) ? nblk : 0);
+    }
+  }
+};
+
+constexpr int kConvTiles = 4;  // tiles per workgroup, a wave each
+
+// A wave owns 64 neighbouring vectors of channels (its last lanes beyond C hold the last
+// vector once more: they store the same values again and their sums are not used) and a
+// tile.  Block id = (group of tiles, channel group), the latter fastest; blocks behind
+// those form d_initial.  partial [tile groups][W + 1][C]: dweight's W rows, then dbias.
+//
+// Bound by memory, and by how much of it is in flight.  B=4, T=8192, C=2048, W=4 bf16
+// (403 MB, 79 us at a copy's 5.1 TB/s): 105 us with tiles of 29 or 61 tokens, 133 with 13,
+// 120 with 125.  The loads of U tokens are sent for ahead of the U being computed; without
+// that the same kernel took 144 us, and with eight channels per lane (234 registers) 112.
+// Tiles are uniform over a wave, so the row pointers are scalar and the middle of a tile
+// has no branches: with stores under a lane's condition, every wait for loads is also one
+// for the stores before them (154 us).
+template <typename E, int W, int VEC, bool CK>
+__global__ __launch_bounds__(64 * kConvTiles, 2) void gdn_conv_bwd_kernel(
+    ConvGeo g, Src x, const float* __restrict__ weight, const float* __restrict__ bias,
+    const E* __restrict__ h0, const E* __restrict__ d_y, const E* __restrict__ d_fin, E* __restrict__ dx,
+    E* __restrict__ dh0, float* __restrict__ partial, int cgroups, int main_blocks) {
+  constexpr int U = sizeof(E) == 2 ? kConvGroup : kConvGroup / 2;
+  __shared__ float sm[64 * kConvTiles * VEC];
+  if ((int)blockIdx.x >= main_blocks) {
+    const uint32_t item = (blockIdx.x - main_blocks) * (64u * kConvTiles) + threadIdx.x;
+    const uint32_t n = item / (uint32_t)g.cvn;
+    if (n < (uint32_t)g.N)
+      conv_bwd_state<E, W, VEC>(g, x, weight, bias, h0, d_y, d_fin, dh0, (int)n, (int)(item - n * g.cvn) * VEC);
+    return;
+  }
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tg = blockIdx.x / cgroups, cg = blockIdx.x - tg * cgroups;
-  const int v = cg * cl + lc;
-  const bool on = v < g.cvn;
-  const int c = (on ? v : 0) * VEC;
-  const int64_t tiles = (int64_t)g.ntiles * (g.cu ? 1 : g.B);
-  const int64_t tile = (int64_t)tg * tl + lt;
-  const bool silu = g.silu, packed = x.scales != nullptr;
+  const int c = min(cg * 64 + lane, g.cvn - 1) * VEC;
+  const int tiles = g.ntiles * (g.cu ? 1 : g.B);
+  const int tile = tg * kConvTiles + wave;
+  const bool silu = g.silu;
   const Src dys{d_y, nullptr, g.C};
+  const uint32_t off = lane_offset(c * (uint32_t)sizeof(E)), xoff = CK ? lane_offset(c) : off;
+  const uint32_t soff = CK ? lane_offset((uint32_t)c >> 5) : 0;
 
   float dw[W][VEC], db[VEC];
 #pragma unroll
@@ -210,77 +319,95 @@ __global__ __launch_bounds__(256) void gdn_conv_bwd_kernel(ConvGeo g, Src x,
 #pragma unroll
     for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
   }
-  if (on && tile < tiles) {
-    float w[VEC][W], b[VEC];
-    conv_params<W, VEC>(weight, bias, c, w, b);
-    Run<false> run;
-    run.init(g.cu, g.T, g.N, (int)tile, g.ntiles, g.tile);
+  if (tile < tiles) {
     if (g.cu) {  // rows behind the last sequence get a zero gradient
-      const int64_t last = seq_offset(g.cu, g.N, g.T);
+      const int last = uniform<true>(seq_offset(g.cu, g.N, g.T));
       const float zero[VEC] = {};
-      for (int64_t t = max((int64_t)tile * g.tile, last); t < min((int64_t)(tile + 1) * g.tile, (int64_t)g.T); ++t)
-        vec_store<E, VEC>(dx + t * g.C + c, zero);
+      for (int t = max(tile * g.tile, last); t < min((tile + 1) * g.tile, g.T); ++t)
+        vec_store<E, VEC>(dx + (int64_t)t * g.C + c, zero);
     }
+    Run<true> run;
+    run.init(g.cu, g.T, g.N, tile, g.ntiles, g.tile);
+    float w[VEC][W], b[VEC];
+    if (!run.done()) conv_params<W, VEC>(weight, bias, c, w, b);
     for (; !run.done(); run.next()) {
-      float win[W - 1][VEC], p[W][VEC];  // p[i]: p of the token i before the current one
+      const int lim = run.tb + (W - 1);  // tokens at or beyond the sequence's end have p = 0
+      const int stop = min(lim, run.end);
+      RawVec<E, VEC> old[W - 1];
+      VecVals<E, VEC, U, CK> rx;
+      VecVals<E, VEC, U, false> rd;
 #pragma unroll
       for (int j = 0; j < W - 1; ++j)
-        conv_before<E, W, VEC>(g, x, h0, run.n, run.start, run.ta - run.start - (W - 1) + j, c, win[j]);
+        old[j] = conv_row<E, W, VEC>(g, x, h0, run.n, run.start, run.ta - run.start - (W - 1) + j, c);
+      rx.fetch(x, run.ta, stop, xoff, soff, g.nblk);
+      rd.fetch(dys, run.ta, stop, off, 0, 0);
+      float win[W - 1][VEC], p[W][VEC];  // p[i]: p of the token i before the current one
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) conv_value<E, W, VEC>(old[j], CK, run.ta - run.start - (W - 1) + j, win[j]);
 #pragma unroll
       for (int j = 0; j < W; ++j)
 #pragma unroll
         for (int i = 0; i < VEC; ++i) p[j][i] = 0.f;
-      const int lim = run.tb + (W - 1);  // tokens at or beyond the sequence's end have p = 0
-      const int stop = min(lim, run.end);
-      for (int t = run.ta; t < lim; t += kConvGroup / 2) {
-        RawVec<E, VEC> rx[kConvGroup / 2], rd[kConvGroup / 2];
+      // one token; `edge`: one of the tile's first or last, whose conditions it checks
+      auto token = [&](int u, const RawVec<E, VEC>& rawx, const RawVec<E, VEC>& rawd, bool edge) {
+        float cur[VEC], d[VEC];
+        raw_unpack<E, VEC>(rawx, CK, cur);
+        raw_unpack<E, VEC>(rawd, false, d);
+        const bool live = !edge || u < stop;
 #pragma unroll
-        for (int k = 0; k < kConvGroup / 2; ++k) {
-          const int q = min(t + k, stop - 1);
-          rx[k] = raw_load<E, VEC>(x, q, c, g.nblk);
-          rd[k] = raw_load<E, VEC>(dys, q, c, 0);
+        for (int i = 0; i < VEC; ++i) {
+#pragma unroll
+          for (int j = W - 1; j > 0; --j) p[j][i] = p[j - 1][i];
+          float s = b[i];
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j) s = fmaf(w[i][j], win[j][i], s);
+          s = fmaf(w[i][W - 1], cur[i], s);
+          p[0][i] = live ? conv_dact(s, d[i], silu) : 0.f;
         }
-#pragma unroll
-        for (int k = 0; k < kConvGroup / 2; ++k) {
-          const int u = t + k;
-          if (u >= lim) break;
-          float cur[VEC], d[VEC];
-          raw_unpack<E, VEC>(rx[k], packed, cur);
-          raw_unpack<E, VEC>(rd[k], false, d);
-          const bool live = u < stop, own = u < run.tb;
+        if (!edge || u < run.tb) {  // a token of this tile's own
 #pragma unroll
           for (int i = 0; i < VEC; ++i) {
+            db[i] += p[0][i];
 #pragma unroll
-            for (int j = W - 1; j > 0; --j) p[j][i] = p[j - 1][i];
-            float s = b[i];
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) s = fmaf(w[i][j], win[j][i], s);
-            s = fmaf(w[i][W - 1], cur[i], s);
-            p[0][i] = live ? conv_dact<W>(s, d[i], silu) : 0.f;
-            if (own) {
-              db[i] += p[0][i];
-#pragma unroll
-              for (int j = 0; j < W - 1; ++j) dw[j][i] = fmaf(p[0][i], win[j][i], dw[j][i]);
-              dw[W - 1][i] = fmaf(p[0][i], cur[i], dw[W - 1][i]);
-            }
-#pragma unroll
-            for (int j = 0; j < W - 2; ++j) win[j][i] = win[j + 1][i];
-            win[W - 2][i] = cur[i];
+            for (int j = 0; j < W - 1; ++j) dw[j][i] = fmaf(p[0][i], win[j][i], dw[j][i]);
+            dw[W - 1][i] = fmaf(p[0][i], cur[i], dw[W - 1][i]);
           }
-          const int o = u - (W - 1);  // its later outputs are all known now
-          if (o >= run.ta) {
-            float out[VEC];
-            const int row = o - run.end + (W - 1);  // >= 0: held in the final state
-            if (d_fin && row >= 0) vec_load<E, VEC>(d_fin + ((int64_t)run.n * (W - 1) + row) * g.C + c, out);
-            else
+        }
 #pragma unroll
-              for (int i = 0; i < VEC; ++i) out[i] = 0.f;
+        for (int i = 0; i < VEC; ++i) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i)
+          for (int j = 0; j < W - 2; ++j) win[j][i] = win[j + 1][i];
+          win[W - 2][i] = cur[i];
+        }
+        const int o = u - (W - 1);  // its later outputs are all known now
+        if (!edge || o >= run.ta) {
+          float out[VEC];
+          const int row = o - run.end + (W - 1);  // >= 0: held in the final state
+          if (edge && d_fin && row >= 0) vec_load<E, VEC>(d_fin + ((int64_t)run.n * (W - 1) + row) * g.C + c, out);
+          else
 #pragma unroll
-              for (int j = 0; j < W; ++j) out[i] = fmaf(w[i][j], p[j][i], out[i]);
-            vec_store<E, VEC, true>(dx + (int64_t)o * g.C + c, out);
-          }
+            for (int i = 0; i < VEC; ++i) out[i] = 0.f;
+#pragma unroll
+          for (int i = 0; i < VEC; ++i)
+#pragma unroll
+            for (int j = 0; j < W; ++j) out[i] = fmaf(w[i][j], p[j][i], out[i]);
+          vec_store<E, VEC>(reinterpret_cast<E*>(reinterpret_cast<char*>(dx + (int64_t)o * g.C) + off), out);
+        }
+        __builtin_amdgcn_sched_barrier(0);  // token by token: interleaved they take all registers
+      };
+      for (int t = run.ta; t < lim; t += U) {
+        const VecVals<E, VEC, U, CK> cx = rx;
+        const VecVals<E, VEC, U, false> cd = rd;
+        const int next = min(t + U, stop - 1);
+        rx.fetch(x, next, stop, xoff, soff, g.nblk);
+        rd.fetch(dys, next, stop, off, 0, 0);
+        if (t >= run.ta + W - 1 && t + U <= run.tb) {
+#pragma unroll
+          for (int k = 0; k < U; ++k) token(t + k, cx.v[k], cd.v[k], false);
+        } else {
+#pragma unroll
+          for (int k = 0; k < U; ++k)
+            if (t + k < lim) token(t + k, cx.v[k], cd.v[k], true);
         }
       }
     }
@@ -290,82 +417,39 @@ __global__ __launch_bounds__(256) void gdn_conv_bwd_kernel(ConvGeo g, Src x,
   for (int k = 0; k <= W; ++k) {
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) sm[i * 256 + threadIdx.x] = k < W ? dw[k < W ? k : 0][i] : db[i];
+    for (int i = 0; i < VEC; ++i) sm[(wave * VEC + i) * 64 + lane] = k < W ? dw[k < W ? k : 0][i] : db[i];
     __syncthreads();
-    for (int e = threadIdx.x; e < cl * VEC; e += 256) {
-      const int i = e / cl, l = e - i * cl;
+    for (int e = threadIdx.x; e < 64 * VEC; e += 64 * kConvTiles) {
+      const int i = e / 64, l = e - i * 64;
       float s = 0.f;
-      for (int q = 0; q < tl; ++q) s += sm[i * 256 + q * cl + l];
-      const int ch = (cg * cl + l) * VEC + i;
+#pragma unroll
+      for (int q = 0; q < kConvTiles; ++q) s += sm[(q * VEC + i) * 64 + l];
+      const int ch = (cg * 64 + l) * VEC + i;
       if (ch < g.C) partial[((int64_t)tg * (W + 1) + k) * g.C + ch] = s;
     }
   }
 }
 
-// d_initial, one lane per (sequence, vector): the first W-1 outputs' p once more.
-template <typename E, int W, int VEC>
-__global__ __launch_bounds__(256) void gdn_conv_bwd_state_kernel(
-    ConvGeo g, Src x, const float* __restrict__ weight, const float* __restrict__ bias,
-    const E* __restrict__ h0, const E* __restrict__ d_y, const E* __restrict__ d_fin,
-    E* __restrict__ dh0) {
-  const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t n = item / g.cvn;
-  if (n >= g.N) return;
-  const int c = (int)(item - n * g.cvn) * VEC;
-  const int64_t start = g.cu ? seq_offset(g.cu, (int)n, g.T) : n * g.T;
-  const int64_t end = g.cu ? seq_offset(g.cu, (int)n + 1, g.T) : start + g.T;
-  const int64_t len = end > start ? end - start : 0;
-  float w[VEC][W], b[VEC], line[2 * (W - 1)][VEC], out[W - 1][VEC];
-  conv_params<W, VEC>(weight, bias, c, w, b);
-#pragma unroll
-  for (int j = 0; j < 2 * (W - 1); ++j) {  // places -(W-1) .. W-2
-    const int64_t q = j - (W - 1);
-    conv_before<E, W, VEC>(g, x, h0, (int)n, start, len > 0 ? min(q, len - 1) : min(q, (int64_t)-1), c, line[j]);
-  }
-#pragma unroll
-  for (int r = 0; r < W - 1; ++r) {
-    const int64_t kept = r - len;  // the final row that holds row r, if any
-    if (d_fin && kept >= 0) vec_load<E, VEC>(d_fin + (n * (W - 1) + kept) * g.C + c, out[r]);
-    else
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) out[r][i] = 0.f;
-  }
-#pragma unroll
-  for (int q = 0; q < W - 1; ++q) {
-    if (q >= len) break;
-    float d[VEC];
-    vec_load<E, VEC>(d_y + (start + q) * g.C + c, d);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      float s = b[i];
-#pragma unroll
-      for (int j = 0; j < W; ++j) s = fmaf(w[i][j], line[q + j][i], s);
-      const float p = conv_dact<W>(s, d[i], g.silu);
-#pragma unroll
-      for (int r = q; r < W - 1; ++r) out[r][i] = fmaf(w[i][r - q], p, out[r][i]);
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < W - 1; ++r) vec_store<E, VEC>(dh0 + (n * (W - 1) + r) * g.C + c, out[r]);
-}
-
 // dweight [C][W] and dbias [C] from the partial rows: a workgroup adds 64
-// neighbouring values, four lanes of rows each.
+// neighbouring values, 16 lanes of rows each.
 template <int W>
-__global__ __launch_bounds__(256) void gdn_conv_bwd_sums_kernel(const float* __restrict__ partial,
-                                                                int rows, int C,
-                                                                float* __restrict__ dweight,
-                                                                float* __restrict__ dbias) {
-  __shared__ float sm[256];
+__global__ __launch_bounds__(1024) void gdn_conv_bwd_sums_kernel(const float* __restrict__ partial,
+                                                                 int rows, int C,
+                                                                 float* __restrict__ dweight,
+                                                                 float* __restrict__ dbias) {
+  __shared__ float sm[1024];
   const int64_t e = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63), n = (int64_t)(W + 1) * C;
   const int q = threadIdx.x >> 6;
   float s = 0.f;
-  if (e < n)
-    for (int r = q; r < rows; r += 4) s += partial[r * n + e];
+  if (e < n) {
+#pragma unroll 8
+    for (int r = q; r < rows; r += 16) s += partial[r * n + e];
+  }
   sm[threadIdx.x] = s;
   __syncthreads();
   if (q || e >= n) return;
-  s = (sm[threadIdx.x] + sm[64 + threadIdx.x]) + (sm[128 + threadIdx.x] + sm[192 + threadIdx.x]);
+#pragma unroll
+  for (int i = 1; i < 16; ++i) s += sm[64 * i + threadIdx.x];
   const int k = (int)(e / C), c = (int)(e - (int64_t)k * C);
   if (k < W) dweight[(int64_t)c * W + k] = s;
   else if (dbias) dbias[c] = s;

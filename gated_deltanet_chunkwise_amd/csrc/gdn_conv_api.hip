@@ -10,17 +10,9 @@ struct ConvPlan {
   gdn::ConvGeo geo;
   int64_t ld;     // elements between x's rows
   size_t esz;
-  int vec;        // channels per lane: 16 bytes' worth, or 1
-  int cl;         // backward: neighbouring vectors per workgroup
   int64_t rows;   // backward: rows of partial sums
   size_t total;   // backward workspace bytes
 };
-
-int pow2_at_least(int v) {
-  int p = 1;
-  while (p < v) p <<= 1;
-  return p;
-}
 
 // Sizes only.
 gdn_status_t conv_sizes(const gdn_conv_params_t* p, bool packed, ConvPlan* out) {
@@ -40,44 +32,42 @@ gdn_status_t conv_sizes(const gdn_conv_params_t* p, bool packed, ConvPlan* out) 
   g.silu = p->activation;
   g.nblk = (int)ceil_div(p->C, gdn::kPackBlock);
   if ((int64_t)g.N * 3 * p->C > ((int64_t)1 << 38)) return GDN_ERR_UNSUPPORTED;  // grid range
-  // 16-byte vectors if the channels divide into them; the smaller tile of the two
-  // paths below bounds the workspace, so it does not depend on pointers
-  const int wide = (int)(16 / pl.esz);
-  pl.vec = p->C % wide == 0 ? wide : 1;
   *out = pl;
   return GDN_OK;
 }
 
-// The backward pass's tiles: each lane's tile as long as leaves about 8 waves per
+constexpr int kBwdVec = 4;
+
+// The backward pass's tiles: each lane's tile as long as leaves about 16 waves per
 // CU (256 CUs are taken for granted, so that the workspace is the same on every
 // device), 16 tokens at least (its W-1 tokens of overlap are then at most a fifth)
 // and 256 at most.
 void conv_bwd_tiles(const gdn_conv_params_t* p, bool packed, int vec, ConvPlan* pl) {
   gdn::ConvGeo& g = pl->geo;
-  pl->vec = vec;
   g.cvn = p->C / vec;
   const int64_t ntok = (int64_t)p->B * p->T;
-  int64_t tile = ntok * g.cvn / (256 * 8 * 64);
-  tile = std::min<int64_t>(std::max<int64_t>(tile, 16), 256);
+  int64_t tile = ntok * g.cvn / (256 * 16 * 64);
+  // whole groups of loads for the tile and the W-1 tokens after it
+  tile = std::min<int64_t>(std::max<int64_t>(tile / gdn::kConvGroup, 2), 32) * gdn::kConvGroup - (p->W - 1);
   g.tile = (int)tile;
   g.ntiles = (int)std::max<int64_t>(ceil_div(p->T, tile), 1);
-  pl->cl = std::min(64, pow2_at_least(g.cvn));
   const int64_t tiles = (int64_t)g.ntiles * (packed ? 1 : p->B);
-  pl->rows = ceil_div(tiles, 256 / pl->cl);
+  pl->rows = ceil_div(tiles, gdn::kConvTiles);
   pl->total = align_up((size_t)pl->rows * (p->W + 1) * p->C * 4);
 }
 
 size_t conv_ws(const gdn_conv_params_t* p, bool packed, ConvPlan pl) {
-  conv_bwd_tiles(p, packed, pl.vec, &pl);
-  size_t total = pl.total;
   conv_bwd_tiles(p, packed, 1, &pl);  // what misaligned pointers would take
+  const size_t total = pl.total;
+  if (p->C % kBwdVec == 0) conv_bwd_tiles(p, packed, kBwdVec, &pl);
   return std::max(total, pl.total);
 }
 
-bool vec_ok(const ConvPlan& pl, std::initializer_list<const void*> rows) {
-  if (pl.vec == 1 || pl.ld % pl.vec) return false;
+// Whether rows of C elements from these addresses split into vectors of `vec` elements.
+bool vec_ok(const ConvPlan& pl, int vec, std::initializer_list<const void*> rows) {
+  if (pl.geo.C % vec || pl.ld % vec) return false;
   for (const void* q : rows)
-    if (!aligned(q, 16)) return false;
+    if (!aligned(q, vec * pl.esz)) return false;
   return true;
 }
 
@@ -96,7 +86,7 @@ gdn_status_t conv_fwd_run(ConvPlan pl, const void* x, const float* w, const floa
   const int64_t units = (int64_t)g.ntiles * (g.cu ? 1 : g.B) + (fin ? (int64_t)g.N * (W - 1) : 0);
   const int64_t blocks = ceil_div(units * g.cvn, 256);
   if (blocks == 0) return GDN_OK;
-  if (blocks > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  if (blocks > (1 << 24)) return GDN_ERR_UNSUPPORTED;  // 32-bit work items
   return launch(gdn::gdn_conv_fwd_kernel<E, W, VEC>, dim3((unsigned)blocks), dim3(256), s, g,
                 gdn::Src{x, nullptr, pl.ld}, w, b, static_cast<const E*>(h0), static_cast<E*>(y),
                 static_cast<E*>(fin)) == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
@@ -134,21 +124,22 @@ gdn_status_t conv_bwd_run(const ConvPlan& pl, const ConvBwdArgs& a, void* ws, hi
     if (e != hipSuccess && err == hipSuccess) err = e;
   };
   const bool tokens = (int64_t)g.B * g.T > 0;
-  const int cgroups = (int)ceil_div(g.cvn, pl.cl);
-  if (tokens)
-    ok(launch(gdn::gdn_conv_bwd_kernel<E, W, VEC>, dim3((unsigned)(pl.rows * cgroups)), dim3(256), s, g, x, a.w, a.b, static_cast<const E*>(a.h0), static_cast<const E*>(a.dy),
-              static_cast<const E*>(a.dfin), static_cast<E*>(a.dx), partial, pl.cl, cgroups));
-  if (a.dh0 && g.N > 0)
-    ok(launch(gdn::gdn_conv_bwd_state_kernel<E, W, VEC>, dim3((unsigned)ceil_div((int64_t)g.N * g.cvn, 256)),
-              dim3(256), s, g, x, a.w, a.b, static_cast<const E*>(a.h0), static_cast<const E*>(a.dy),
-              static_cast<const E*>(a.dfin), static_cast<E*>(a.dh0)));
+  const int cgroups = (int)ceil_div(g.cvn, 64);
+  const int64_t main_blocks = tokens ? pl.rows * cgroups : 0;
+  const int64_t states = a.dh0 ? ceil_div((int64_t)g.N * g.cvn, 256) : 0;
+  if (main_blocks + states > INT32_MAX || states > (1 << 24)) return GDN_ERR_UNSUPPORTED;
+  if (main_blocks + states > 0)
+    ok(launch(a.scales ? gdn::gdn_conv_bwd_kernel<E, W, VEC, true> : gdn::gdn_conv_bwd_kernel<E, W, VEC, false>,
+              dim3((unsigned)(main_blocks + states)), dim3(64 * gdn::kConvTiles), s, g, x, a.w, a.b,
+              static_cast<const E*>(a.h0), static_cast<const E*>(a.dy), static_cast<const E*>(a.dfin),
+              static_cast<E*>(a.dx), static_cast<E*>(a.dh0), partial, cgroups, (int)main_blocks));
   ok(launch(gdn::gdn_conv_bwd_sums_kernel<W>, dim3((unsigned)ceil_div((int64_t)(W + 1) * g.C, 64)),
-            dim3(256), s, partial, tokens ? (int)pl.rows : 0, g.C, a.dw, a.db));
+            dim3(1024), s, partial, tokens ? (int)pl.rows : 0, g.C, a.dw, a.db));
   return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
-// F<E, W, VEC>::run for the plan's type, width and vector length.
-template <template <typename, int, int> class F, typename... A>
+// F<E, W, VEC>::run for the call's type and width; VEC = V16 for bf16, 4 for fp32, or 1.
+template <template <typename, int, int> class F, int V16, typename... A>
 gdn_status_t conv_dispatch(const gdn_conv_params_t* p, bool vec, A&&... a) {
   auto width = [&](auto e, auto v) {
     using E = decltype(e);
@@ -159,7 +150,7 @@ gdn_status_t conv_dispatch(const gdn_conv_params_t* p, bool vec, A&&... a) {
   };
   using One = std::integral_constant<int, 1>;
   if (p->dtype == GDN_BF16)
-    return vec ? width(gdn::bf16{}, std::integral_constant<int, 8>{}) : width(gdn::bf16{}, One{});
+    return vec ? width(gdn::bf16{}, std::integral_constant<int, V16>{}) : width(gdn::bf16{}, One{});
   return vec ? width(0.f, std::integral_constant<int, 4>{}) : width(0.f, One{});
 }
 template <typename E, int W, int VEC> struct FwdRun {
@@ -247,7 +238,7 @@ gdn_status_t gdn_conv_fwd(const gdn_conv_params_t* p, const void* x, const float
       !aligned(final_state, pl.esz) || !aligned(weight, 4) || !aligned(bias, 4) || !aligned(cu_seqlens, 8))
     return GDN_ERR_ALIGN;
   pl.geo.cu = cu_seqlens;
-  return conv_dispatch<FwdRun>(p, vec_ok(pl, {x, y, initial_state, final_state}), pl, x, weight, bias,
+  return conv_dispatch<FwdRun, 8>(p, vec_ok(pl, (int)(16 / pl.esz), {x, y, initial_state, final_state}), pl, x, weight, bias,
                                initial_state, y, final_state, static_cast<hipStream_t>(stream));
 }
 
@@ -266,10 +257,10 @@ gdn_status_t gdn_conv_decode(const gdn_conv_params_t* p, const void* x, const fl
   if (p->B == 0 || (p->T == 0 && state == new_state)) return GDN_OK;
   if (p->T == 0) {  // no weights to read: the state passes through
     pl.geo.cu = nullptr;
-    return conv_dispatch<FwdRun>(p, vec_ok(pl, {state, new_state}), pl, x, weight, bias, state, y,
+    return conv_dispatch<FwdRun, 8>(p, vec_ok(pl, (int)(16 / pl.esz), {state, new_state}), pl, x, weight, bias, state, y,
                                  new_state, static_cast<hipStream_t>(stream));
   }
-  return conv_dispatch<DecodeRun>(p, vec_ok(pl, {x, y, state, new_state}), pl, x, weight, bias, state,
+  return conv_dispatch<DecodeRun, 8>(p, vec_ok(pl, (int)(16 / pl.esz), {x, y, state, new_state}), pl, x, weight, bias, state,
                                   new_state, y, static_cast<hipStream_t>(stream));
 }
 
@@ -300,14 +291,13 @@ gdn_status_t gdn_conv_bwd(const gdn_conv_params_t* p, const void* x, const uint8
       !aligned(dweight, 4) || !aligned(dbias, 4) || !aligned(cu_seqlens, 8) || !aligned(workspace, kWsAlign))
     return GDN_ERR_ALIGN;
   if (workspace_bytes < need) return GDN_ERR_WORKSPACE;
-  const bool vec = vec_ok(pl, {x_scales ? nullptr : x, d_y, dx, initial_state, d_final_state, d_initial_state}) &&
-                   aligned(x, 8);
-  conv_bwd_tiles(p, packed, vec ? pl.vec : 1, &pl);
-  if (pl.rows * ceil_div(pl.geo.cvn, pl.cl) > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  const bool vec = vec_ok(pl, kBwdVec, {x_scales ? nullptr : x, d_y, dx, initial_state, d_final_state, d_initial_state}) &&
+                   aligned(x, kBwdVec);
+  conv_bwd_tiles(p, packed, vec ? kBwdVec : 1, &pl);
   pl.geo.cu = cu_seqlens;
   const ConvBwdArgs a{x, x_scales, weight, bias, initial_state, d_y, d_final_state,
                       dx, dweight, dbias, d_initial_state};
-  return conv_dispatch<BwdRun>(p, vec, pl, a, workspace, static_cast<hipStream_t>(stream));
+  return conv_dispatch<BwdRun, kBwdVec>(p, vec, pl, a, workspace, static_cast<hipStream_t>(stream));
 }
 
 gdn_status_t gdn_pack8(const void* x, gdn_dtype_t dtype, int64_t rows, int32_t C, int64_t x_stride,

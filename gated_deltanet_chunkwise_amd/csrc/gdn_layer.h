@@ -11,6 +11,22 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // A pointer into global memory with its address space spelled out.
 template <typename E> using Global = __attribute__((address_space(1))) E*;
 
+// A lane's offset, in a form that the compiler adds to a uniform pointer within the load
+// itself (it would otherwise form 64-bit sums in vector registers).
+__device__ __forceinline__ uint32_t lane_offset(uint32_t bytes) {
+  asm("" : "+v"(bytes));
+  return bytes;
+}
+
+// p + n, in a form that the compiler does not fold into other sums: the walks below step
+// their row pointers token by token, and without this it keeps every multiple of every
+// stride in scalar registers, which then spill.
+template <typename T> __device__ __forceinline__ Global<T> stepped(Global<T> p, int64_t n) {
+  p += n;
+  asm("" : "+s"(p));
+  return p;
+}
+
 constexpr int kPackBlock = 32;  // channels that share one checkpoint scale
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -32,6 +48,10 @@ __device__ __forceinline__ float softplus_flat(float x) {
   return x > 20.f ? x : u == 1.f ? y : r;
 }
 
+// d/dx x sigmoid(x) = s (1 + x (1 - s)), s = sigmoid(x).  1 - s is off by at most 2^-24,
+// which x (1 - s) + 1 loses only |x| 2^-24 to.
+__device__ __forceinline__ float silu_slope(float x, float s) { return s * fmaf(x, 1.f - s, 1.f); }
+
 // The checkpoint scale of a stored byte b: 2^(b - 127), and NaN for 255 (a block
 // that held an infinity or a NaN).
 __device__ __forceinline__ float pack_scale(uint32_t b) {
@@ -49,39 +69,52 @@ struct Src {
 // VEC consecutive channels of one row, as loaded (not yet converted), so that
 // loads can be issued well before their use.
 template <typename E, int VEC> struct RawVec;
-template <> struct RawVec<bf16, 8> { u32x4 w; };
-template <> struct RawVec<float, 4> { u32x4 w; };
+template <> struct RawVec<bf16, 8> { u32x4 w; uint32_t s; };
+template <> struct RawVec<bf16, 4> { u32x2 w; uint32_t s; };
+template <> struct RawVec<float, 4> { u32x4 w; uint32_t s; };
 template <typename E> struct RawVec<E, 1> { uint32_t w, s; };
 
 template <typename E, int VEC>
 __device__ __forceinline__ RawVec<E, VEC> raw_load(const Src& s, int64_t row, int c, int nblk) {
-  RawVec<E, VEC> r;
-  if constexpr (VEC == 1) {
-    if (s.scales) {
-      r.w = static_cast<const uint8_t*>(s.p)[row * s.ld + c];
-      r.s = s.scales[row * nblk + (c >> 5)];
+  RawVec<E, VEC> r = {};
+  if (s.scales) {  // VEC divides 32: one scale for the vector
+    const uint8_t* q = static_cast<const uint8_t*>(s.p) + row * s.ld + c;
+    if constexpr (VEC == 1) {
+      r.w = *q;
+    } else if constexpr (VEC == 8) {
+      const u32x2 d = *reinterpret_cast<const u32x2*>(q);
+      r.w[0] = d.x;
+      r.w[1] = d.y;
     } else {
-      const E* q = static_cast<const E*>(s.p) + row * s.ld + c;
-      if constexpr (sizeof(E) == 2) r.w = *reinterpret_cast<const uint16_t*>(q);
-      else r.w = *reinterpret_cast<const uint32_t*>(q);
-      r.s = 0;
+      r.w[0] = *reinterpret_cast<const uint32_t*>(q);
     }
+    r.s = s.scales[row * nblk + (c >> 5)];
   } else {
-    if (s.scales) {  // VEC divides 32: one scale for the vector
-      const uint8_t* q = static_cast<const uint8_t*>(s.p) + row * s.ld + c;
-      if constexpr (VEC == 8) {
-        const u32x2 d = *reinterpret_cast<const u32x2*>(q);
-        r.w.x = d.x;
-        r.w.y = d.y;
-      } else {
-        r.w.x = *reinterpret_cast<const uint32_t*>(q);
-        r.w.y = 0;
-      }
-      r.w.z = s.scales[row * nblk + (c >> 5)];
-      r.w.w = 0;
+    const E* q = static_cast<const E*>(s.p) + row * s.ld + c;
+    if constexpr (VEC == 1 && sizeof(E) == 2) r.w = *reinterpret_cast<const uint16_t*>(q);
+    else r.w = *reinterpret_cast<const decltype(r.w)*>(q);
+  }
+  return r;
+}
+
+// The same at a wave-uniform row and a lane's offset in bytes (in a checkpoint: the same
+// of its code; `soff` that of its scale).
+template <typename E, int VEC, bool CK>
+__device__ __forceinline__ RawVec<E, VEC> raw_load_at(Global<const char> row, Global<const uint8_t> srow,
+                                                      uint32_t off, uint32_t soff) {
+  RawVec<E, VEC> r = {};
+  Global<const char> q = row + off;
+  if constexpr (!CK) {
+    if constexpr (VEC == 1 && sizeof(E) == 2) r.w = *(Global<const uint16_t>)q;
+    else r.w = *(Global<const decltype(r.w)>)q;
+  } else {
+    if constexpr (VEC == 1) {
+      r.w = *(Global<const uint8_t>)q;
     } else {
-      r.w = *reinterpret_cast<const u32x4*>(static_cast<const E*>(s.p) + row * s.ld + c);
+      static_assert(VEC == 4, "");
+      r.w[0] = *(Global<const uint32_t>)q;
     }
+    r.s = srow[soff];
   }
   return r;
 }
@@ -89,20 +122,19 @@ __device__ __forceinline__ RawVec<E, VEC> raw_load(const Src& s, int64_t row, in
 // The raw vector as fp32; `packed` as the load's (s.scales != nullptr).
 template <typename E, int VEC>
 __device__ __forceinline__ void raw_unpack(const RawVec<E, VEC>& r, bool packed, float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    if (packed) v[0] = (float)(int8_t)r.w * pack_scale(r.s);
-    else v[0] = sizeof(E) == 2 ? __uint_as_float(r.w << 16) : __uint_as_float(r.w);
+  if (packed) {
+    const float sc = pack_scale(r.s);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      if constexpr (VEC == 1) v[0] = (float)(int8_t)r.w * sc;
+      else v[i] = (float)(int8_t)(r.w[i >> 2] >> (8 * (i & 3))) * sc;
+    }
   } else {
-    if (packed) {
-      const float sc = pack_scale(r.w.z);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) v[i] = (float)(int8_t)(r.w[i >> 2] >> (8 * (i & 3))) * sc;
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        if constexpr (sizeof(E) == 2) v[i] = (i & 1) ? bf16_hi(r.w[i >> 1]) : bf16_lo(r.w[i >> 1]);
-        else v[i] = __uint_as_float(r.w[i]);
-      }
+    for (int i = 0; i < VEC; ++i) {
+      if constexpr (VEC == 1) v[0] = __uint_as_float(sizeof(E) == 2 ? r.w << 16 : r.w);
+      else if constexpr (sizeof(E) == 2) v[i] = (i & 1) ? bf16_hi(r.w[i >> 1]) : bf16_lo(r.w[i >> 1]);
+      else v[i] = __uint_as_float(r.w[i]);
     }
   }
 }
@@ -122,6 +154,10 @@ template <typename E, int VEC, bool NT = false>
 __device__ __forceinline__ void vec_store(E* p, const float (&v)[VEC]) {
   if constexpr (VEC == 1) {
     *p = (E)v[0];
+  } else if constexpr (sizeof(E) == 2 && VEC == 4) {
+    const bf16x4 w = to_bf16x4(f32x4{v[0], v[1], v[2], v[3]});
+    if constexpr (NT) __builtin_nontemporal_store(w, reinterpret_cast<bf16x4*>(p));
+    else *reinterpret_cast<bf16x4*>(p) = w;
   } else if constexpr (sizeof(E) == 2) {
     const f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
     const bf16x4 a = to_bf16x4(lo), b = to_bf16x4(hi);

@@ -85,22 +85,6 @@ template <typename E> __device__ __forceinline__ uint32_t load1(const E* row, ui
 template <typename E> __device__ __forceinline__ void store1(Global<E> row, uint32_t off, float v) {
   *(Global<E>)((Global<char>)row + off) = (E)v;
 }
-// A lane's offset, in a form that the compiler adds to a uniform pointer within the load
-// itself (it would otherwise form 64-bit sums in vector registers).
-__device__ __forceinline__ uint32_t lane_offset(uint32_t bytes) {
-  asm("" : "+v"(bytes));
-  return bytes;
-}
-
-// p + n, in a form that the compiler does not fold into other sums: the walks below step
-// their row pointers token by token, and without this it keeps every multiple of every
-// stride in scalar registers, which then spill.
-template <typename T> __device__ __forceinline__ Global<T> stepped(Global<T> p, int64_t n) {
-  p += n;
-  asm("" : "+s"(p));
-  return p;
-}
-
 // Waits for the scalar loads in flight, and lets nothing later move before the wait.
 // Scalar loads return out of order, so the compiler's own wait for one row would, placed
 // at its first use, also wait for the next row's loads issued meanwhile.
@@ -243,6 +227,16 @@ __global__ __launch_bounds__(64 * kScanMaxWaves) void gdn_scan_kernel(
   if (!SPLIT && !w.valid) return;
   float A2[NS], h[NS];
   scan_rates<NS, WHOLE>(A_log, g, w.d, w.n0, A2);
+  if (SPLIT && !w.valid) {  // no channels: only the workgroup's barriers
+    if constexpr (!ENDS) {
+      Run<true> run;
+      for (run.init(g.cu, g.T, g.S, w.tile, g.ntiles, g.len); !run.done(); run.next()) {
+        const int n = run.tb - run.ta;
+        for (int i = 0; i < n % U + n / U; ++i) __syncthreads();
+      }
+    }
+    return;
+  }
   const float bias = dt_bias ? dt_bias[w.d] : 0.f, sk = skip ? skip[w.d] : 0.f;
   const uint32_t off = lane_offset(w.d * (uint32_t)sizeof(E));
   const bool gate = !ENDS && z.p != nullptr;
@@ -299,9 +293,11 @@ __global__ __launch_bounds__(64 * kScanMaxWaves) void gdn_scan_kernel(
       }
       return acc0 + acc1;
     };
+    // Lanes without a channel of their own hold the last channel's once more and store the
+    // same value to the same place: a store under a condition would make every later wait
+    // for a load wait for the stores as well.
     auto finish = [&](float acc, float xv, float gv, Global<E> row) {
-      const float o = fmaf(sk, xv, acc) * gv;
-      if (w.on) store1<E>(row, off, o);
+      store1<E>(row, off, fmaf(sk, xv, acc) * gv);
     };
     // SPLIT: the waves' parts of a group's outputs are added through LDS, each wave
     // finishing every nw-th token.  The other buffer is written next, and the barrier

@@ -123,9 +123,6 @@ __device__ __forceinline__ float softplus_both(float x, float& slope) {
   return x > 20.f ? x : u == 1.f ? y : r;
 }
 
-// silu'(z) = s + z s (1 - s), s = sigmoid(z); 1 - s as sigmoid(-z).
-__device__ __forceinline__ float dsilu(float z, float s) { return fmaf(z * s, fast_sigmoid(-z), s); }
-
 // (1).  states, rev [tile][np][D]; sums, rsums [tile][D] (-1: nothing passes through).
 // R needs no walk backwards: with P_t = a_1 .. a_t it is sum_t P_t Cm_t r_t.
 template <typename E, typename BE, int NS, bool WHOLE, bool CK>
@@ -272,7 +269,14 @@ __global__ __launch_bounds__(64 * NW * scan_bwd_units(NW), 2) void gdn_scan_bwd_
   }
   ScanPlace w;
   w.init<NS>(g, blockIdx.x);
-  if (NW == 1 && !w.valid) return;
+  if (!w.valid) {  // no channels: only the workgroup's barriers
+    if constexpr (NW > 1) {
+      Run<true> run;
+      for (run.init(g.cu, g.T, g.S, w.tile, g.ntiles, g.len); !run.done(); run.next())
+        for (int s = 0; s < 2 * ((run.tb - run.ta + SUB - 1) / SUB); ++s) __syncthreads();
+    }
+    return;
+  }
   auto& part = part_[NW > 1 ? w.unit : 0];
   const int kept = w.unit * NW + w.wave;
   // lane offsets: of E, of a checkpoint's codes and scales
@@ -296,12 +300,12 @@ __global__ __launch_bounds__(64 * NW * scan_bwd_units(NW), 2) void gdn_scan_bwd_
   if (g.cu) {  // rows behind the last sequence
     const int last = max(uniform<true>(seq_offset(g.cu, g.S, g.T)), w.tile * g.len);
     for (int t = last; t < min((w.tile + 1) * g.len, g.T); ++t) {
-      if (w.on && w.wave == 0) {
+      if (w.wave == 0) {
         store1<E>((Global<E>)dx + (int64_t)t * g.D, off, 0.f);
         store1<E>((Global<E>)ddt + (int64_t)t * g.D, off, 0.f);
         if (gate) store1<E>((Global<E>)dz + (int64_t)t * g.D, off, 0.f);
       }
-      if (w.valid && w.lane % kRep == 0) store1<float>(pb + (int64_t)t * 2 * g.np, pboff, 0.f);
+      store1<float>(pb + (int64_t)t * 2 * g.np, pboff, 0.f);
     }
   }
 
@@ -312,9 +316,6 @@ __global__ __launch_bounds__(64 * NW * scan_bwd_units(NW), 2) void gdn_scan_bwd_
     else state_load<NS, WHOLE>(h0, g, run.n, w.d, w.n0, h);
     if (run.tb == run.end) state_load<NS, WHOLE>(d_fin, g, run.n, w.d, w.n0, l);
     else tile_state_load<NS>(rev, g, w, l);
-#pragma unroll
-    for (int j = 0; j < NS; ++j) l[j] = w.on ? l[j] : 0.f;  // lanes without a channel add nothing
-
     // groups of SUB tokens, the last one maybe shorter (its rows held to the run's last)
     const int nsub = (run.tb - run.ta + SUB - 1) / SUB;
     TokenVals<E, SUB, CK> rx, rz = {};
@@ -367,16 +368,16 @@ __global__ __launch_bounds__(64 * NW * scan_bwd_units(NW), 2) void gdn_scan_bwd_
       float xv[SUB], dl[SUB], sig[SUB], r[SUB], rz2[SUB], hp[SUB][NS];
 #pragma unroll
       for (int k = 0; k < SUB; ++k) {
-        xv[k] = w.on ? rx[k] : 0.f;
+        xv[k] = rx[k];
         dl[k] = softplus_both(rd[k] + bias, sig[k]);
-        r[k] = w.on ? ry[k] : 0.f;
+        r[k] = ry[k];
         rz2[k] = 0.f;
       }
       if (gate) {
 #pragma unroll
         for (int k = 0; k < SUB; ++k) {
           const float zv = rz[k], sg = fast_sigmoid(zv);
-          rz2[k] = r[k] * dsilu(zv, sg);
+          rz2[k] = r[k] * silu_slope(zv, sg);
           r[k] *= zv * sg;
         }
       }
@@ -419,6 +420,9 @@ __global__ __launch_bounds__(64 * NW * scan_bwd_units(NW), 2) void gdn_scan_bwd_
         b.load(br);
         c.load(cr);
         const float u = dl[k] * xv[k];
+        // lanes without a channel of their own hold the last channel's once more; to the
+        // sums over channels they add nothing
+        const float um = w.on ? u : 0.f, rm = w.on ? r[k] : 0.f;
         float a[NS], bc[2 * NS], sy = 0.f, sb = 0.f, sq = 0.f;
 #pragma unroll
         for (int j = 0; j < NS; ++j) a[j] = fast_exp2(dl[k] * A2[j]);
@@ -433,12 +437,11 @@ __global__ __launch_bounds__(64 * NW * scan_bwd_units(NW), 2) void gdn_scan_bwd_
           const float q = lam * ah;
           sq = fmaf(q, A2[j], sq);
           dA[j] = fmaf(q, dl[k], dA[j]);
-          bc[j] = lam * u;
-          bc[NS + j] = ht * r[k];
+          bc[j] = lam * um;
+          bc[NS + j] = ht * rm;
           l[j] = a[j] * lam;
         }
-        const float tot = wave_sums<2 * NS>(bc);
-        if (w.valid && w.lane % kRep == 0) store1<float>(pr, pboff, tot);
+        store1<float>(pr, pboff, wave_sums<2 * NS>(bc));  // kRep lanes the same value
         pr = stepped<float>(pr, -2 * g.np);
         if (NW == 1 || k % NW == w.wave) {
           own[k / NW][0] = sy;
@@ -467,11 +470,9 @@ __global__ __launch_bounds__(64 * NW * scan_bwd_units(NW), 2) void gdn_scan_bwd_
         }
         const int64_t o = (int64_t)(t + k) * g.D;
         const float dr = fmaf(sb, xv[k], sq * 0.693147180559945309f) * sig[k];
-        if (w.on) {
-          if (gate) store1<E>((Global<E>)dz + o, off, rz2[k] * fmaf(sk, xv[k], sy));
-          store1<E>((Global<E>)dx + o, off, fmaf(dl[k], sb, sk * r[k]));
-          store1<E>((Global<E>)ddt + o, off, dr);
-        }
+        if (gate) store1<E>((Global<E>)dz + o, off, rz2[k] * fmaf(sk, xv[k], sy));
+        store1<E>((Global<E>)dx + o, off, fmaf(dl[k], sb, sk * r[k]));
+        store1<E>((Global<E>)ddt + o, off, dr);
         dskip = fmaf(r[k], xv[k], dskip);
         dbias += dr;
       }
