@@ -1,24 +1,30 @@
 // gdn_scan_api.hip -- entry points of the selective scan's forward pass and decode
 // step: validation, tiles and launches.  See include/gdn.h.
 #include "gdn_scan_host.h"
-#include <cstdlib>
 
 namespace {
 
-// Tokens per tile: as many as leave about 16 waves per CU (256 CUs taken for granted, so
-// that sizes alone decide), 16 at least; one tile per sequence where its waves alone come
-// to a quarter of that.
-// TODO measured
-constexpr int kTileWaves = 256 * 16, kLeastTile = 16;
+// Tokens per tile.  256 CUs are taken for granted, so that sizes alone decide and the
+// workspace is the same on every device.  Measured on MI355X, N = 16 bf16, us per call:
+//   one tile per sequence, which forms the states once, from a wave per SIMD on (1024;
+//   packed sequences are one row and are always cut): T=512, D=4096, B=16 (1024 waves)
+//   209 against 227 in tiles of 64; B=12 (768) 199 against 175; B=64, T=128, D=2048 (2048)
+//   73 against 137;
+//   else tiles for about 8192 waves, of 32 tokens at least: B=2, T=2048, D=2048 (64 waves
+//   a tile) 80 with 32 tokens, 84 with 64, 114 with 128, 87 with 16; T=32768 packed (32
+//   waves) 494 with 128, 497 with 64, 520 with 256, 559 with 32 (the join's chain grows);
+//   16 tokens where 32 leave less than 2048 waves: B=3, T=777, D=1002, G=2 fp32 (48 waves)
+//   48 against 55.
+constexpr int kOneTileWaves = 1024, kTileWaves = 8192, kTile = 32, kShortTile = 16;
 
 int scan_fwd_len(const ScanPlan& pl) {
-  if (getenv("TILE")) return atoi(getenv("TILE"));
   const gdn::ScanGeo& g = pl.geo;
   const int64_t waves = (int64_t)g.cgroups * g.nw * (pl.packed ? 1 : g.B);  // of one tile per row
-  if (g.T <= kLeastTile || (!pl.packed && waves * 4 >= kTileWaves)) return std::max(g.T, 1);
+  if (g.T <= kTile || (!pl.packed && waves >= kOneTileWaves)) return std::max(g.T, 1);
+  if (waves * ceil_div(g.T, kTile) < kOneTileWaves * 2) return kShortTile;
   const int64_t tiles = std::max<int64_t>(kTileWaves / waves, 1);
   const int64_t len = ceil_div(ceil_div(g.T, tiles), gdn::kScanGroup) * gdn::kScanGroup;
-  return (int)std::max<int64_t>(len, kLeastTile);
+  return (int)std::max<int64_t>(len, kTile);
 }
 
 gdn_status_t fwd_sizes(const gdn_scan_params_t* p, bool packed, ScanPlan* pl) {

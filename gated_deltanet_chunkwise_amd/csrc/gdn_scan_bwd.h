@@ -28,11 +28,10 @@ namespace gdn {
 
 constexpr int kScanBwdStates = 8;  // states per lane
 constexpr int kScanBwdSub = 8;     // tokens per group
-// Tokens per tile.  The states that a tile keeps take 32 bytes of LDS per token and lane:
-// 64 tokens leave room for 8 waves per CU with up to two waves per workgroup (256
-// registers allow no more), 32 with more waves.
+// Tokens per tile.  B=2, T=2048, D=2048, N=16 bf16: 262 us of kernels with 32, 263 with 64,
+// 281 with 16 (more tiles to join); B=2, T=1024, D=1024: 101 against 144 with 64.
+constexpr int kScanBwdTile = 32;
 constexpr int scan_bwd_units(int waves) { return waves >= 4 ? 1 : 4 / waves; }  // per workgroup
-constexpr int scan_bwd_tile(int waves) { return waves > 2 ? 32 : 64; }
 
 // U tokens' values of one channel as loaded, so that the loads are all in flight before
 // the first is converted.  CK: from a checkpoint, code and scale.
@@ -258,7 +257,7 @@ __global__ __launch_bounds__(64 * NW * scan_bwd_units(NW), 2) void gdn_scan_bwd_
     E* __restrict__ dx, E* __restrict__ ddt, E* __restrict__ dz, float* __restrict__ pbc,
     float* __restrict__ psum, float* __restrict__ dh0) {
   constexpr int UPW = scan_bwd_units(NW);
-  __shared__ float hs[scan_bwd_tile(NW) / SUB][UPW * NW][NS][64];
+  __shared__ float hs[kScanBwdTile / SUB][UPW * NW][NS][64];
   __shared__ float part_[NW > 1 ? UPW : 1][NW > 1 ? SUB : 1][NW > 1 ? NW - 1 : 1][3][NW > 1 ? 64 : 1];
   const ScanGeo& g = bg.g;
   const int64_t ntok = (int64_t)g.B * g.T;
@@ -365,7 +364,7 @@ __global__ __launch_bounds__(64 * NW * scan_bwd_units(NW), 2) void gdn_scan_bwd_
     for (int s = nsub - 1; s >= 0; --s) {
       const int t = run.ta + s * SUB, cnt = min(SUB, run.tb - t);
       // per token: x, D, softplus', r = dy silu(z), dy silu'(z)
-      float xv[SUB], dl[SUB], sig[SUB], r[SUB], rz2[SUB], hp[SUB][NS];
+      float xv[SUB], dl[SUB], sig[SUB], r[SUB], rz2[SUB], hp[SUB + 1][NS];
 #pragma unroll
       for (int k = 0; k < SUB; ++k) {
         xv[k] = rx[k];
@@ -386,12 +385,18 @@ __global__ __launch_bounds__(64 * NW * scan_bwd_units(NW), 2) void gdn_scan_bwd_
       b.load(br);
 #pragma unroll
       for (int j = 0; j < NS; ++j) hp[0][j] = hs[s][kept][j][w.lane];
+      // hp[k]: the state before token k; the last is the next group's first, where there is one
+      const bool last = s == nsub - 1;
+      if (!last) {
 #pragma unroll
-      for (int k = 0; k + 1 < SUB; ++k) {
-        if (k + 1 >= cnt) break;
+        for (int j = 0; j < NS; ++j) hp[SUB][j] = hs[s + 1][kept][j][w.lane];
+      }
+#pragma unroll
+      for (int k = 0; k < SUB; ++k) {
+        if (k + 1 >= cnt + (last ? 1 : 0)) break;
         scalar_loads_done();
         const ScalarRow<BE, NS> bt = b;
-        br = stepped<const BE>(br, g.ldb);
+        if (k + 1 < cnt) br = stepped<const BE>(br, g.ldb);
         b.load(br);
         const float u = dl[k] * xv[k];
         float a[NS];
@@ -401,7 +406,7 @@ __global__ __launch_bounds__(64 * NW * scan_bwd_units(NW), 2) void gdn_scan_bwd_
 #pragma unroll
         for (int j = 0; j < NS; ++j) hp[k + 1][j] = fmaf(a[j], hp[k][j], bt[j] * u);
       }
-      float own[SUB / NW][3];  // sums over the states of the tokens this wave finishes
+      float own[(SUB + NW - 1) / NW][3];  // sums over the states of the tokens this wave finishes
       br = bp + (int64_t)(t + cnt - 1) * g.ldb;
       Global<const BE> cr = cp + (int64_t)(t + cnt - 1) * g.ldc;
       Global<float> pr = pb + (int64_t)(t + cnt - 1) * 2 * g.np;
@@ -419,27 +424,25 @@ __global__ __launch_bounds__(64 * NW * scan_bwd_units(NW), 2) void gdn_scan_bwd_
         }
         b.load(br);
         c.load(cr);
-        const float u = dl[k] * xv[k];
         // lanes without a channel of their own hold the last channel's once more; to the
         // sums over channels they add nothing
-        const float um = w.on ? u : 0.f, rm = w.on ? r[k] : 0.f;
+        const float um = w.on ? dl[k] * xv[k] : 0.f, rm = w.on ? r[k] : 0.f;
         float a[NS], bc[2 * NS], sy = 0.f, sb = 0.f, sq = 0.f;
 #pragma unroll
         for (int j = 0; j < NS; ++j) a[j] = fast_exp2(dl[k] * A2[j]);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
-          const float ah = a[j] * hp[k][j];
-          const float ht = fmaf(bt[j], u, ah);
+          const float ht = hp[k + 1][j];
           const float lam = fmaf(ct[j], r[k], l[j]);
           sy = fmaf(ct[j], ht, sy);
           sb = fmaf(bt[j], lam, sb);
-          const float q = lam * ah;
+          l[j] = a[j] * lam;
+          const float q = l[j] * hp[k][j];
           sq = fmaf(q, A2[j], sq);
           dA[j] = fmaf(q, dl[k], dA[j]);
           bc[j] = lam * um;
           bc[NS + j] = ht * rm;
-          l[j] = a[j] * lam;
         }
         store1<float>(pr, pboff, wave_sums<2 * NS>(bc));  // kRep lanes the same value
         pr = stepped<float>(pr, -2 * g.np);

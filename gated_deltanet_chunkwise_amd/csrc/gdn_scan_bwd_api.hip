@@ -33,7 +33,7 @@ gdn_status_t bwd_sizes(const gdn_scan_params_t* p, bool packed, ScanPlan* pl) {
   int nw = 1;
   while (nw * gdn::kScanBwdStates < p->N) nw *= 2;
   scan_waves(&pl->geo, gdn::kScanBwdStates, nw);
-  scan_tiles(pl, gdn::scan_bwd_tile(pl->geo.nw));
+  scan_tiles(pl, gdn::kScanBwdTile);
   return GDN_OK;
 }
 
