@@ -338,3 +338,168 @@ def test_automatic_segments_layout():
     assert gdn.check(P(seg_chunks=-2), ptrs(), 1 << 40) == ESHAPE
     # an explicit length is reported as given (no device query needed)
     assert gdn.seg_chunks(P(seg_chunks=5)) == 5 and gdn.seg_chunks(P()) == 0
+
+
+# ---- the layer operators (convolution, scan, checkpoints) --------------------------
+
+def CP(**kw):
+    from gated_deltanet_chunkwise_amd._layers import ConvParams
+    d = dict(B=2, T=20, C=64, W=4, num_seqs=0, dtype=gdn.GDN_BF16, activation=1, x_stride=0)
+    d.update(kw)
+    return ConvParams(*(d[n] for n, _ in ConvParams._fields_))
+
+
+def SP(**kw):
+    from gated_deltanet_chunkwise_amd._layers import ScanParams
+    d = dict(B=2, T=20, D=64, G=2, N=16, num_seqs=0, dtype=gdn.GDN_BF16, x_stride=0, dt_stride=0,
+             z_stride=0, b_stride=0, c_stride=0)
+    d.update(kw)
+    return ScanParams(*(d[n] for n, _ in ScanParams._fields_))
+
+
+def addresses(names, given):
+    """Fake, aligned, never-dereferenced addresses by name; `given` replaces some."""
+    base = {n: 0x100000 * (i + 1) for i, n in enumerate(names)}
+    for n in ("cu", "x_scales", "z_scales"):
+        if n in base:
+            base[n] = None
+    base.update(given)
+    return [base[n] for n in names]
+
+
+def conv_fwd(p, **given):
+    names = ("x", "weight", "bias", "cu", "h0", "y", "fin")
+    return gdn.load_library().gdn_conv_fwd(p and ctypes.byref(p), *addresses(names, given), None)
+
+
+def conv_decode(p, **given):
+    names = ("x", "weight", "bias", "state", "new", "y")
+    return gdn.load_library().gdn_conv_decode(p and ctypes.byref(p), *addresses(names, given), None)
+
+
+def conv_bwd(p, ws_bytes=1 << 40, **given):
+    names = ("x", "x_scales", "weight", "bias", "cu", "h0", "d_y", "d_fin", "dx", "dw", "db", "dh0", "ws")
+    return gdn.load_library().gdn_conv_bwd(p and ctypes.byref(p), *addresses(names, given), ws_bytes, None)
+
+
+def scan_fwd(p, ws_bytes=1 << 40, **given):
+    names = ("x", "dt", "A_log", "Bm", "Cm", "skip", "z", "dt_bias", "cu", "h0", "y", "fin", "ws")
+    return gdn.load_library().gdn_scan_fwd(p and ctypes.byref(p), *addresses(names, given), ws_bytes, None)
+
+
+def scan_decode(p, **given):
+    names = ("x", "dt", "A_log", "Bm", "Cm", "skip", "z", "dt_bias", "state", "new", "y")
+    return gdn.load_library().gdn_scan_decode(p and ctypes.byref(p), *addresses(names, given), None)
+
+
+def scan_bwd(p, ws_bytes=1 << 40, **given):
+    names = ("x", "x_scales", "dt", "A_log", "Bm", "Cm", "skip", "z", "z_scales", "dt_bias", "cu", "h0", "d_y",
+             "d_fin", "dx", "ddt", "dA_log", "dBm", "dCm", "dskip", "dz", "ddt_bias", "dh0", "ws")
+    return gdn.load_library().gdn_scan_bwd(p and ctypes.byref(p), *addresses(names, given), ws_bytes, None)
+
+
+CONV_BAD = [(dict(dtype=7), EDTYPE), (dict(dtype=gdn.GDN_F16), EDTYPE), (dict(C=0), ESHAPE), (dict(W=0), ESHAPE),
+            (dict(W=1), EUNSUP), (dict(W=5), EUNSUP), (dict(activation=2), ESHAPE), (dict(B=-1), ESHAPE),
+            (dict(T=-1), ESHAPE), (dict(x_stride=63), ESHAPE), (dict(x_stride=-64), ESHAPE),
+            (dict(B=1 << 16, T=1 << 15), EUNSUP), (dict(B=2, T=(1 << 30) - 100), EUNSUP)]
+
+
+@pytest.mark.parametrize("kw,status", CONV_BAD)
+def test_conv_refuses_sizes(kw, status):
+    p = CP(**kw)
+    assert conv_fwd(p) == status and conv_bwd(p) == status and conv_decode(p) == status
+    assert gdn.load_library().gdn_conv_bwd_workspace_size(ctypes.byref(p), 0) == 0
+
+
+SCAN_BAD = [(dict(dtype=7), EDTYPE), (dict(dtype=gdn.GDN_F16), EDTYPE), (dict(D=0), ESHAPE), (dict(G=0), ESHAPE),
+            (dict(N=0), ESHAPE), (dict(G=3), ESHAPE), (dict(N=65), EUNSUP), (dict(B=-1), ESHAPE),
+            (dict(x_stride=63), ESHAPE), (dict(dt_stride=1), ESHAPE), (dict(z_stride=-1), ESHAPE),
+            (dict(b_stride=31), ESHAPE), (dict(c_stride=31), ESHAPE), (dict(B=65536, T=1), EUNSUP),
+            (dict(B=2, T=(1 << 30) - 100), EUNSUP), (dict(D=1 << 26, G=1), EUNSUP)]
+
+
+@pytest.mark.parametrize("kw,status", SCAN_BAD)
+def test_scan_refuses_sizes(kw, status):
+    p = SP(**kw)
+    assert scan_fwd(p) == status and scan_bwd(p) == status and scan_decode(p) == status
+    for f in ("gdn_scan_fwd_workspace_size", "gdn_scan_bwd_workspace_size"):
+        assert getattr(gdn.load_library(), f)(ctypes.byref(p), 0) == 0
+
+
+@pytest.mark.parametrize("call,P_", [(conv_fwd, CP), (conv_bwd, CP), (scan_fwd, SP), (scan_bwd, SP)])
+def test_layer_packed_rules(call, P_):
+    cu = 0x9000000
+    assert call(P_(B=2, num_seqs=3), cu=cu) == ESHAPE      # one row of tokens
+    assert call(P_(B=1, num_seqs=-1), cu=cu) == ESHAPE
+    assert call(P_(B=1, num_seqs=0), cu=cu) == ESHAPE      # tokens of no sequence
+    assert call(P_(B=1, num_seqs=2), cu=cu + 4) == EALIGN
+    assert call(None) == ENULL
+
+
+@pytest.mark.parametrize("call,P_", [(conv_decode, CP), (scan_decode, SP)])
+def test_layer_decode_is_for_sequences_of_one_length(call, P_):
+    assert call(P_(B=1, num_seqs=2)) == ESHAPE
+    assert call(None) == ENULL
+
+
+@pytest.mark.parametrize("call,P_,required,optional", [
+    (conv_fwd, CP, "x weight y", "bias h0 fin"),
+    (conv_decode, CP, "x weight y state new", "bias"),
+    (conv_bwd, CP, "x weight d_y dx dw ws", "bias h0 d_fin db dh0"),
+    (scan_fwd, SP, "x dt A_log Bm Cm y", "skip z dt_bias h0 fin"),
+    (scan_decode, SP, "x dt A_log Bm Cm y state new", "skip z dt_bias"),
+    (scan_bwd, SP, "x dt A_log Bm Cm d_y dx ddt dA_log dBm dCm dz ws", "skip dt_bias h0 d_fin dskip ddt_bias dh0")])
+def test_layer_pointers(call, P_, required, optional):
+    for n in required.split():
+        assert call(P_(), **{n: None}) == ENULL, n
+    for n in required.split() + optional.split():
+        assert call(P_(), **{n: 0x100001}) == EALIGN, n
+    # what may be missing is not asked for: a later check answers
+    later = dict(x=0x100001)
+    for n in optional.split():
+        assert call(P_(), **{n: None}, **later) == EALIGN, n
+
+
+def test_layer_workspaces():
+    lib = gdn.load_library()
+    need = lib.gdn_conv_bwd_workspace_size(ctypes.byref(CP()), 0)
+    assert need > 0 and conv_bwd(CP(), ws_bytes=need - 1) == EWS
+    p = SP(T=500)
+    for size, call in ((lib.gdn_scan_fwd_workspace_size, scan_fwd), (lib.gdn_scan_bwd_workspace_size, scan_bwd)):
+        need = size(ctypes.byref(p), 0)
+        assert need > 0 and need % 256 == 0 and call(p, ws_bytes=need - 1) == EWS
+        assert call(p, ws=0x100080) == EALIGN and call(p, ws=None) == ENULL
+        assert size(None, 0) == 0
+    # a short call with whole rows of Bm and Cm forms nothing in between
+    assert lib.gdn_scan_fwd_workspace_size(ctypes.byref(SP(T=1, dtype=gdn.GDN_F32)), 0) >= 0
+
+
+def test_checkpoints_are_dense():
+    assert conv_bwd(CP(x_stride=128), x_scales=0x9000000) == ESHAPE
+    assert scan_bwd(SP(x_stride=128), x_scales=0x9000000, z_scales=0x9100000) == ESHAPE
+    assert scan_bwd(SP(z_stride=128), x_scales=0x9000000, z_scales=0x9100000) == ESHAPE
+    assert scan_bwd(SP(), x_scales=0x9000000) == ESHAPE    # one of x and z alone
+    assert scan_bwd(SP(), z_scales=0x9000000) == ESHAPE
+
+
+def test_pack8_validation():
+    lib = gdn.load_library()
+    A, B_, C_ = 0x100000, 0x200000, 0x300000
+    pack = lambda x=A, dt=gdn.GDN_BF16, rows=4, C=64, ld=0, codes=B_, scales=C_: lib.gdn_pack8(  # noqa: E731
+        x, dt, rows, C, ld, codes, scales, None)
+    unpack = lambda codes=A, scales=B_, rows=4, C=64, y=C_, dt=gdn.GDN_BF16: lib.gdn_unpack8(  # noqa: E731
+        codes, scales, rows, C, y, dt, None)
+    for f in (pack, unpack):
+        assert f(dt=gdn.GDN_F16) == EDTYPE and f(dt=9) == EDTYPE
+        assert f(rows=-1) == ESHAPE and f(C=0) == ESHAPE and f(rows=1 << 60) == ESHAPE
+        assert f(codes=None) == ENULL and f(scales=None) == ENULL
+        assert f(rows=0) == OK
+    assert pack(ld=63) == ESHAPE and pack(x=None) == ENULL and pack(x=A + 1) == EALIGN
+    assert pack(x=A + 2, dt=gdn.GDN_F32) == EALIGN
+    assert unpack(y=None) == ENULL and unpack(y=C_ + 1) == EALIGN
+
+
+def test_layer_calls_with_nothing_to_do_enqueue_nothing():
+    assert conv_decode(CP(B=0)) == OK and scan_decode(SP(B=0)) == OK
+    assert conv_decode(CP(T=0), new=0x400000) == OK        # `new` is `state` (the fourth address)
+    assert conv_fwd(CP(T=0), fin=None) == OK and scan_fwd(SP(T=0), fin=None) == OK

@@ -1,0 +1,297 @@
+"""The layer operators as a layer uses them together: the convolution of a projection's
+slices before the gated delta rule and before the selective scan, a prompt and then single
+tokens, training steps with and without 8-bit checkpoints; guard bands around everything
+they write; calls at once on two streams; replays of captured decode steps."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import gated_deltanet_chunkwise_amd as gdn
+import layer_oracle as lo
+import oracle
+from gpu_helpers import f64
+from gated_deltanet_chunkwise_amd._layers import ConvParams, ScanParams
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+# ---- convolution, then gated delta rule -------------------------------------------
+
+B, T, H, HV, K, V, W = 2, 70, 1, 2, 64, 64, 4
+CQ, CK, CV = H * K, H * K, HV * V
+C = CQ + CK + CV
+
+
+def layer_inputs(seed=1, B=B, T=T):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    # the projection is small so that k, after the convolution, keeps the rule stable
+    return dict(proj=r(B, T, C) * 0.3, weight=r(C, W) * 0.5, bias=r(C) * 0.1, g_raw=r(B, T, HV),
+                beta=torch.sigmoid(r(B, T, HV)), A_log=r(HV).abs(), dt_bias=r(HV) * 0.1,
+                c0=r(B, W - 1, C) * 0.3, h0=r(B, HV, K, V) * 0.1), dict(
+                    d_o=r(B, T, HV, V), d_fin=r(B, HV, K, V) * 0.1)
+
+
+def qkv(y):
+    b, t = y.shape[:2]
+    return (y[..., :CQ].reshape(b, t, H, K).contiguous(), y[..., CQ:CQ + CK].reshape(b, t, H, K).contiguous(),
+            y[..., CQ + CK:].reshape(b, t, HV, V).contiguous())
+
+
+def oracle_layer(d):
+    r = lo.double(d)
+    y, c1 = lo.conv(r["proj"], r["weight"], r["bias"], None, r["c0"])
+    q, k, v = (t.numpy() for t in qkv(y))
+    o, fin = oracle.fwd(q, k, v, *(r[n].numpy() for n in ("g_raw", "beta", "A_log", "dt_bias")), h0=r["h0"].numpy())
+    return (q, k, v), o, fin, c1
+
+
+def close(x, ref, what, tol):
+    ref = np.asarray(ref, np.float64)
+    x = f64(x) if torch.is_tensor(x) else np.asarray(x)
+    rel = np.linalg.norm(x - ref) / np.linalg.norm(ref)
+    print("  %-10s rel_l2=%.2e" % (what, rel), flush=True)
+    assert np.isfinite(x).all() and rel <= tol, (what, rel)
+
+
+def test_gated_delta_rule_layer_trains():
+    d, seeds = layer_inputs()
+    (q, k, v), o_ref, fin_ref, _ = oracle_layer(d)
+    r = lo.double(d)
+    gr = oracle.bwd(q, k, v, *(r[n].numpy() for n in ("g_raw", "beta", "A_log", "dt_bias")),
+                    seeds["d_o"].double().numpy(), seeds["d_fin"].double().numpy(), h0=r["h0"].numpy())
+    d_y = torch.cat([torch.from_numpy(np.asarray(gr[n])).reshape(B, T, -1) for n in ("dq", "dk", "dv")], -1)
+    ref = lo.gradients(lambda **a: lo.conv(a["x"], a["weight"], a["bias"], None, a["h0"]),
+                       dict(x=r["proj"], weight=r["weight"], bias=r["bias"], h0=r["c0"]), (d_y, None))
+    leaf = {n: t.cuda().requires_grad_() for n, t in d.items()}
+    y, _ = gdn.causal_conv(leaf["proj"], leaf["weight"], leaf["bias"], initial_state=leaf["c0"])
+    o, fin = gdn.gated_delta_rule(*qkv(y), leaf["g_raw"], leaf["beta"], leaf["A_log"], leaf["dt_bias"],
+                                  initial_state=leaf["h0"])
+    # the rule's own bounds for fp32 (tests of gdn_fwd and gdn_bwd), which the
+    # convolution's few roundings do not change
+    close(o, o_ref, "o", 1e-4)
+    close(fin, fin_ref, "final", 1e-4)
+    ((o * seeds["d_o"].cuda()).sum() + (fin * seeds["d_fin"].cuda()).sum()).backward()
+    for n, g in (("proj", ref["x"]), ("weight", ref["weight"]), ("bias", ref["bias"]), ("c0", ref["h0"]),
+                 ("g_raw", gr["dg_raw"]), ("beta", gr["dbeta"]), ("h0", gr["dh0"])):
+        close(leaf[n].grad, g, "d" + n, 1e-3)
+
+
+def test_gated_delta_rule_layer_trains_from_checkpoints():
+    """Every operator's gradients are those at its own checkpoint, given the gradient of
+    what follows: composed by hand, call by call."""
+    d, seeds = layer_inputs(2)
+    g = lo.cuda(d)
+    leaf = {n: t.clone().requires_grad_() for n, t in g.items()}
+    y, _ = gdn.causal_conv(leaf["proj"], leaf["weight"], leaf["bias"], initial_state=leaf["c0"], checkpoint_bits=8)
+    o, fin = gdn.gated_delta_rule(*qkv(y), leaf["g_raw"], leaf["beta"], leaf["A_log"], leaf["dt_bias"],
+                                  initial_state=leaf["h0"], checkpoint_bits=8)
+    ((o * seeds["d_o"].cuda()).sum() + (fin * seeds["d_fin"].cuda()).sum()).backward()
+    y2, _ = gdn.conv_fwd(g["proj"], g["weight"], g["bias"], initial_state=g["c0"])
+    assert torch.equal(y, y2)
+    at = [gdn.unpack8(gdn.pack8(t)) for t in qkv(y2)]
+    gr = gdn.bwd(*at, g["g_raw"], g["beta"], g["A_log"], g["dt_bias"], seeds["d_o"].cuda(), seeds["d_fin"].cuda(),
+                 initial_state=g["h0"])
+    d_y = torch.cat([gr[n].reshape(B, T, -1) for n in ("dq", "dk", "dv")], -1)
+    gc = gdn.conv_bwd(gdn.pack8(g["proj"]), g["weight"], g["bias"], d_y, initial_state=g["c0"])
+    for n, v in (("proj", gc["dx"]), ("weight", gc["dweight"]), ("bias", gc["dbias"]), ("c0", gc["dh0"]),
+                 ("g_raw", gr["dg_raw"]), ("h0", gr["dh0"])):
+        close(leaf[n].grad, f64(v), "d" + n, 1e-3)  # gdn_bwd's LDS atomics change low bits
+
+
+def test_gated_delta_rule_layer_answers():
+    """A prompt of 66 tokens, then four single tokens, against the whole."""
+    d, _ = layer_inputs(3)
+    _, o_ref, fin_ref, c_ref = oracle_layer(d)
+    g = lo.cuda(d)
+    cut = lambda n, a, b: g[n][:, a:b].contiguous()  # noqa: E731
+    y, conv_state = gdn.conv_fwd(cut("proj", 0, 66), g["weight"], g["bias"], initial_state=g["c0"])
+    o, state = gdn.fwd(*qkv(y), cut("g_raw", 0, 66), cut("beta", 0, 66), g["A_log"], g["dt_bias"], initial_state=g["h0"])
+    outs = [o]
+    for t in range(66, 70):
+        y = gdn.conv_decode(g["proj"][:, t:t + 1], g["weight"], conv_state, g["bias"])
+        outs.append(gdn.decode(*qkv(y), cut("g_raw", t, t + 1), cut("beta", t, t + 1), g["A_log"], state, g["dt_bias"]))
+    close(torch.cat(outs, 1), o_ref, "o", 1e-4)
+    close(state, fin_ref, "state", 1e-4)
+    assert np.array_equal(f64(conv_state), c_ref.numpy())
+
+
+# ---- convolution, then selective scan ----------------------------------------------
+
+D, N = 70, 16
+
+
+def scan_layer(seed, S, T, dtype=F32):
+    d, _ = lo.scan_inputs(1, T, D, N, 1, dtype, seed, S)
+    c, _ = lo.conv_inputs(1, T, D, W, dtype, seed + 1, S)
+    return dict(d, proj=c["x"], weight=c["weight"], bias=c["bias"], c0=c["h0"])
+
+
+def scan_args(d):
+    return dict(dt=d["dt"], A_log=d["A_log"], Bm=d["Bm"], Cm=d["Cm"], skip=d["skip"], z=d["z"], dt_bias=d["dt_bias"])
+
+
+def test_scan_layer_trains_on_packed_sequences():
+    lengths = [40, 0, 1, 75]
+    cu, T_ = lo.offsets(lengths), sum(lengths)
+    d = scan_layer(4, len(lengths), T_)
+    seed = torch.randn(1, T_, D, generator=torch.Generator().manual_seed(5))
+
+    def plain(proj, weight, bias, c0, h0, **a):
+        y, _ = lo.conv(proj, weight, bias, cu, c0)
+        return lo.scan(x=y, cu=cu, h0=h0, **a)
+    names = ("proj", "weight", "bias", "c0", "h0", "dt", "A_log", "Bm", "Cm", "skip", "z", "dt_bias")
+    r = lo.double(d)
+    y_ref, _ = plain(**{n: r[n] for n in names})
+    ref = lo.gradients(plain, {n: r[n] for n in names}, (seed.double(), None))
+    leaf = {n: d[n].cuda().requires_grad_() for n in names}
+    c, _ = gdn.causal_conv(leaf["proj"], leaf["weight"], leaf["bias"], cu.cuda(), leaf["c0"])
+    y, _ = gdn.selective_scan(c, **scan_args(leaf), cu_seqlens=cu.cuda(), initial_state=leaf["h0"])
+    lo.close(y, y_ref, T_, "y")
+    (y * seed.cuda()).sum().backward()
+    for n in names:
+        lo.close(leaf[n].grad, ref[n], 2 * T_, "d" + n)
+
+
+def test_scan_layer_answers_from_a_captured_step():
+    """A prompt, then single tokens from one captured graph with its states in place: each
+    replay continues where the last one ended."""
+    T_ = 70
+    d = scan_layer(6, 1, T_ + 5)
+    r = lo.double(d)
+    c_ref, _ = lo.conv(r["proj"], r["weight"], r["bias"], None, r["c0"])
+    y_ref, fin_ref = lo.scan(x=c_ref, h0=r["h0"], **scan_args(r))
+    g = lo.cuda(d)
+    y, cs = gdn.conv_fwd(g["proj"][:, :T_], g["weight"], g["bias"], initial_state=g["c0"])
+    y, hs = gdn.scan_fwd(y, *(g[n][:, :T_] if n != "A_log" else g[n] for n in ("dt", "A_log", "Bm", "Cm")), g["skip"],
+                         g["z"][:, :T_], g["dt_bias"], initial_state=g["h0"])
+    lo.close(y, y_ref[:, :T_], T_, "prompt")
+    token = {n: g[n][:, T_:T_ + 1].clone() for n in ("proj", "dt", "Bm", "Cm", "z")}
+    keep = [cs.clone(), hs.clone()]
+
+    def step():
+        c = gdn.conv_decode(token["proj"], g["weight"], cs, g["bias"])
+        return gdn.scan_decode(c, token["dt"], g["A_log"], token["Bm"], token["Cm"], hs, g["skip"], token["z"], g["dt_bias"])
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    cs.copy_(keep[0])
+    hs.copy_(keep[1])
+    got = []
+    for t in range(T_, T_ + 5):
+        for n in token:
+            token[n].copy_(g[n][:, t:t + 1])
+        graph.replay()
+        torch.cuda.synchronize()
+        got.append(out.clone())
+    lo.close(torch.cat(got, 1), y_ref[:, T_:], T_ + 5, "tokens")
+    lo.close(hs, fin_ref, T_ + 5, "state")
+
+
+# ---- guard bands -------------------------------------------------------------------
+
+class Banded:
+    """Tensors inside larger allocations, 4 KB of a fixed byte on both sides."""
+
+    def __init__(self):
+        self.all = []
+
+    def __call__(self, shape, dtype, shift=0):
+        n = int(np.prod(shape)) * torch.empty((), dtype=dtype).element_size()
+        buf = torch.full((n + 8192 + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+        self.all.append((buf, 4096 + shift, n))
+        return buf[4096 + shift:4096 + shift + n].view(dtype).view(shape)
+
+    def untouched(self):
+        torch.cuda.synchronize()
+        return all(bool((b[:a] == 0xA5).all()) and bool((b[a + n:] == 0xA5).all()) for b, a, n in self.all)
+
+
+def P(t):
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def run(name, *args):
+    s = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert getattr(gdn.load_library(), name)(*args, s) == 0
+
+
+@pytest.mark.parametrize("dtype,T,D,N,lengths,shift", [
+    (BF16, 70, 64, 16, None, 0), (BF16, 70, 66, 13, None, 2), (F32, 33, 70, 40, [5, 0, 28], 4),
+    (BF16, 300, 130, 8, [64, 65, 0, 1, 100], 0)])
+def test_nothing_is_written_outside_the_outputs(dtype, T, D, N, lengths, shift):
+    code = gdn.GDN_BF16 if dtype == BF16 else gdn.GDN_F32
+    new = Banded()
+    cu = None if lengths is None else lo.offsets(lengths).cuda()
+    S = 1 if cu is None else len(lengths)
+    out = lambda *s, dtype=dtype: new(s, dtype, shift if dtype != F32 else (4 if shift else 0))  # noqa: E731
+    d, s = lo.conv_inputs(1, T, D, 4, dtype, 7, S)
+    g, s = lo.cuda(d), lo.cuda(s)
+    p = ConvParams(1, T, D, 4, 0 if cu is None else S, code, 1, 0)
+    y, fin = out(1, T, D), out(S, 3, D)
+    run("gdn_conv_fwd", ctypes.byref(p), P(g["x"]), P(g["weight"]), P(g["bias"]), P(cu), P(g["h0"]), P(y), P(fin))
+    nb = gdn.load_library().gdn_conv_bwd_workspace_size(ctypes.byref(p), int(cu is not None))
+    ws = new((nb,), torch.uint8)
+    dx, dw, db, dh0 = out(1, T, D), out(D, 4, dtype=F32), out(D, dtype=F32), out(S, 3, D)
+    run("gdn_conv_bwd", ctypes.byref(p), P(g["x"]), None, P(g["weight"]), P(g["bias"]), P(cu), P(g["h0"]), P(s["d_y"]),
+        P(s["d_fin"]), P(dx), P(dw), P(db), P(dh0), P(ws), nb)
+    st, y1 = out(S, 3, D), out(S, 1, D)
+    x1 = g["h0"][:, 0].contiguous()
+    q = ConvParams(S, 1, D, 4, 0, code, 1, 0)
+    run("gdn_conv_decode", ctypes.byref(q), P(x1), P(g["weight"]), P(g["bias"]), P(g["h0"]), P(st), P(y1))
+    codes, scales, back = new((T, D), torch.int8, shift), new((T, (D + 31) // 32), torch.uint8, shift), out(T, D)
+    run("gdn_pack8", P(g["x"]), code, T, D, 0, P(codes), P(scales))
+    run("gdn_unpack8", P(codes), P(scales), T, D, P(back), code)
+
+    d, s = lo.scan_inputs(1, T, D, N, 1, dtype, 8, S)
+    g, s = lo.cuda(d), lo.cuda(s)
+    p = ScanParams(1, T, D, 1, N, 0 if cu is None else S, code, 0, 0, 0, 0, 0)
+    y, fin = out(1, T, D), out(S, D, N, dtype=F32)
+    nb = gdn.load_library().gdn_scan_fwd_workspace_size(ctypes.byref(p), int(cu is not None))
+    ws = new((nb,), torch.uint8)
+    ins = [P(g[n]) for n in ("x", "dt", "A_log", "Bm", "Cm", "skip", "z", "dt_bias")] + [P(cu), P(g["h0"])]
+    run("gdn_scan_fwd", ctypes.byref(p), *ins, P(y), P(fin), P(ws), nb)
+    nb = gdn.load_library().gdn_scan_bwd_workspace_size(ctypes.byref(p), int(cu is not None))
+    ws = new((nb,), torch.uint8)
+    o = dict(dx=out(1, T, D), ddt=out(1, T, D), dA=out(D, N, dtype=F32), dB=out(1, T, 1, N), dC=out(1, T, 1, N),
+             dskip=out(D, dtype=F32), dz=out(1, T, D), dbias=out(D, dtype=F32), dh0=out(S, D, N, dtype=F32))
+    run("gdn_scan_bwd", ctypes.byref(p), ins[0], None, *ins[1:7], None, *ins[7:], P(s["d_y"]), P(s["d_fin"]),
+        *(P(t) for t in o.values()), P(ws), nb)
+    q = ScanParams(S, 1, D, 1, N, 0, code, 0, 0, 0, 0, 0)
+    h1, y1 = out(S, D, N, dtype=F32), out(S, 1, D)
+    keep = [g[n][:, :1].expand(S, *g[n][:, :1].shape[1:]).contiguous() for n in ("x", "dt", "Bm", "Cm", "z")]
+    x1, dt1, b1, c1, z1 = (P(t) for t in keep)
+    run("gdn_scan_decode", ctypes.byref(q), x1, dt1, P(g["A_log"]), b1, c1, P(g["skip"]), z1, P(g["dt_bias"]), P(g["h0"]),
+        P(h1), P(y1))
+    assert new.untouched()
+
+
+# ---- calls at once ------------------------------------------------------------------
+
+def test_two_calls_at_once():
+    """Backward passes of different problems on two streams, each with its own workspace,
+    started without waiting for one another, against the same calls one after the other."""
+    cases = []
+    for seed, T_ in ((9, 500), (10, 333)):
+        d, s = lo.scan_inputs(2, T_, 128, 16, 1, BF16, seed)
+        c, cs = lo.conv_inputs(2, T_, 128, 4, BF16, seed)
+        cases.append((lo.cuda(d), lo.cuda(s), lo.cuda(c), lo.cuda(cs)))
+
+    def work(case, stream):
+        g, s, c, cs = case
+        a = gdn.scan_bwd(g["x"], g["dt"], g["A_log"], g["Bm"], g["Cm"], s["d_y"], s["d_fin"], g["skip"], g["z"],
+                         g["dt_bias"], initial_state=g["h0"], stream=stream)
+        b = gdn.conv_bwd(c["x"], c["weight"], c["bias"], cs["d_y"], cs["d_fin"], initial_state=c["h0"], stream=stream)
+        return [*a.values(), *b.values(), *gdn.pack8(g["x"], stream=stream)[:2]]
+    ref = [work(c, None) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = [work(c, s) for c, s in zip(cases, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for x, y in zip(got, ref) for a, b in zip(x, y))
