@@ -149,25 +149,19 @@ __device__ __forceinline__ void vec_load(const E* p, float (&v)[VEC]) {
     raw_unpack<E, VEC>(raw_load<E, VEC>(s, 0, 0, 0), false, v);
   }
 }
-// NT: streamed past the caches (nobody reads it soon).
-template <typename E, int VEC, bool NT = false>
+template <typename E, int VEC>
 __device__ __forceinline__ void vec_store(E* p, const float (&v)[VEC]) {
   if constexpr (VEC == 1) {
     *p = (E)v[0];
   } else if constexpr (sizeof(E) == 2 && VEC == 4) {
     const bf16x4 w = to_bf16x4(f32x4{v[0], v[1], v[2], v[3]});
-    if constexpr (NT) __builtin_nontemporal_store(w, reinterpret_cast<bf16x4*>(p));
-    else *reinterpret_cast<bf16x4*>(p) = w;
+    *reinterpret_cast<bf16x4*>(p) = w;
   } else if constexpr (sizeof(E) == 2) {
     const f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
     const bf16x4 a = to_bf16x4(lo), b = to_bf16x4(hi);
-    const bf16x8 w = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-    if constexpr (NT) __builtin_nontemporal_store(w, reinterpret_cast<bf16x8*>(p));
-    else *reinterpret_cast<bf16x8*>(p) = w;
+    *reinterpret_cast<bf16x8*>(p) = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   } else {
-    const f32x4 w = {v[0], v[1], v[2], v[3]};
-    if constexpr (NT) __builtin_nontemporal_store(w, reinterpret_cast<f32x4*>(p));
-    else *reinterpret_cast<f32x4*>(p) = w;
+    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
   }
 }
 
@@ -225,6 +219,8 @@ template <bool UNIFORM> struct Run {
     if (cu && ta < t1) {
       ++n;
       fit();
+      // the identity for well-formed offsets: only a tile's first run continues a sequence
+      start = max(start, ta);
     }
   }
   // The sequence that holds token ta, from n on: skips empty ones; behind the last

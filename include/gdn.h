@@ -501,7 +501,7 @@ gdn_status_t gdn_conv_bwd(const gdn_conv_params_t *p, const void *x, const uint8
  * All arithmetic is fp32; y is rounded once.  Long sequences are cut into tiles of
  * tokens that run side by side (three kernels); where the channels alone fill the
  * device, one kernel runs each sequence through.  The cut is chosen from the sizes
- * and the current device's compute units.  dtype, alignment, limits and errors as for
+ * alone.  dtype, alignment, limits and errors as for
  * gdn_conv_fwd; GDN_ERR_UNSUPPORTED for N > 64.  Outputs must not overlap inputs or
  * each other (gdn_scan_decode: new_state may be state).  Enqueued on `stream`;
  * nothing is allocated. */
@@ -560,7 +560,7 @@ gdn_status_t gdn_scan_bwd(const gdn_scan_params_t *p, const void *x, const uint8
  * shorter): a scale s = 2^(b-127), stored as the byte b, the least power of two with
  * max|x| <= 127 s (b between 1 and 248), and one signed code per channel, x / s rounded
  * to the nearest integer, ties to even, within [-127, 127].  The checkpoint stands for
- * code * s, at most max|x| / 127 from x.  A block that holds an infinity or a NaN gets
+ * code * s, at most max|x| / 127 from x (2^-127 where that is more).  A block that holds an infinity or a NaN gets
  * b = 255, which stands for NaN.
  *   x        rows of C channels, x_stride elements apart (0: C), dtype (GDN_F32, GDN_BF16)
  *   codes    [rows][C] int8;  scales [rows][ceil(C/32)] uint8

@@ -271,6 +271,30 @@ def test_nothing_is_written_outside_the_outputs(dtype, T, D, N, lengths, shift):
     assert new.untouched()
 
 
+@pytest.mark.parametrize("T", [12, 100])
+def test_ill_formed_offsets_stay_inside_the_buffers(T):
+    """A sequence that begins before the one ahead of it ends: what its tokens give is
+    undefined, but nothing outside the outputs is written, no tile's state is read that was
+    never formed, and the sequence ahead keeps its result."""
+    D, N, cu = 64, 16, torch.tensor([0, 5, 3, T], dtype=torch.int64)
+    d, s = lo.scan_inputs(1, T, D, N, 1, F32, 11, 3)
+    c, cs = lo.conv_inputs(1, T, D, 4, F32, 12, 3)
+    g, gc = lo.cuda(d), lo.cuda(c)
+    a = [g[n] for n in ("x", "dt", "A_log", "Bm", "Cm")]
+    kw = dict(skip=g["skip"], z=g["z"], dt_bias=g["dt_bias"], cu_seqlens=cu.cuda(), initial_state=g["h0"])
+    y, fin = gdn.scan_fwd(*a, **kw)
+    back = gdn.scan_bwd(*a, s["d_y"].cuda(), s["d_fin"].cuda(), **kw)
+    yc, _ = gdn.conv_fwd(gc["x"], gc["weight"], gc["bias"], cu.cuda(), gc["h0"])
+    gdn.conv_bwd(gc["x"], gc["weight"], gc["bias"], cs["d_y"].cuda(), cs["d_fin"].cuda(), cu.cuda(), gc["h0"])
+    torch.cuda.synchronize()
+    ref, _ = lo.scan(cu=torch.tensor([0, 5, T, T]), **{n: v.double() for n, v in d.items()})
+    refc, _ = lo.conv(c["x"].double(), c["weight"].double(), c["bias"].double(), torch.tensor([0, 5, T, T]),
+                      c["h0"].double())
+    lo.close(y[:, :5], ref[:, :5], 5, "y")
+    lo.close(yc[:, :5], refc[:, :5], 5, "conv y")
+    assert all(t.isfinite().all() for t in (fin[0], back["dx"][:, :5]))
+
+
 # ---- calls at once ------------------------------------------------------------------
 
 def test_two_calls_at_once():
