@@ -57,10 +57,10 @@ template <typename BE, int NS> struct ScalarRow {
 
 // Brings the rows of Bm and Cm of 64 tokens from `t` on (those before `end`) into the L2,
 // a lane per token, by loading a value of each.  The scalar loads that follow token by
-// token wait for one row at a time: from memory that is 1 to 2 us for every cache line of
-// two rows (the backward pass's first kernel: 73 us for 64 tokens, however few waves), from
-// the L2 it is hidden behind the token before.  The values are of no use: land() takes them,
-// late enough that nothing waits for them.
+// token wait for one row at a time, a longer wait from memory than from the L2, which the
+// token before hides.  Measured in tiles of 64 tokens, us of kernels: B=3, T=777, D=1002,
+// G=2, N=13 fp32 38 -> 30; T=32768 packed, D=2048, N=16 bf16, the first kernel 273 -> 259.
+// The values are of no use: land() takes them, late enough that nothing waits for them.
 struct RowAhead {
   uint32_t b = 0, c = 0;
   template <typename BE>
@@ -213,7 +213,7 @@ __global__ __launch_bounds__(64 * kScanMaxWaves) void gdn_scan_kernel(
   constexpr int U = kScanGroup;
   // [buffer][unit * nw + wave]
   __shared__ float part[SPLIT && !ENDS ? 2 : 1][SPLIT && !ENDS ? kScanMaxWaves : 1][U][SPLIT && !ENDS ? 64 : 1];
-  
+
   const int tiles = g.ntiles * (g.cu ? 1 : g.B);
   const uint32_t main_blocks = (uint32_t)tiles * g.cgb;
   if constexpr (ENDS) {
@@ -405,39 +405,46 @@ __global__ __launch_bounds__(64 * kScanMaxWaves) void gdn_scan_kernel(
   }
 }
 
-// (2): states [row of the batch][tile][np][D] from end states to start states, in
-// place; one lane per (row, state, channel).  BACK: from the last tile to the first, from
-// what each tile adds to the state gradient before it to the gradient of its end state
-// (the backward pass's).  A chain of a few operations per tile: what it takes is the
-// latency of its loads, so U tiles are sent for ahead of the U being joined, and before
-// anything else.
-template <bool BACK>
-__global__ __launch_bounds__(256) void gdn_scan_join_kernel(ScanGeo g, const float* __restrict__ A_log,
-                                                            const float* __restrict__ h0,
-                                                            float* __restrict__ states,
-                                                            const float* __restrict__ sums) {
+// (2): end states [row of the batch][tile][np][D] to start states, in place; one lane per
+// (row, state, channel).  Back: from the last tile to the first, from what each tile adds
+// to the state gradient before it to the gradient of its end state (the backward pass's;
+// blocks with z = 1).  A chain of a few operations per tile: what it takes is the latency
+// of its loads, so U tiles are sent for ahead of the U being joined, and before anything
+// else.  B=2, T=2048, D=2048, N=16, 64 tiles: 9.5 us for one chain, 13.7 for both (67 MB,
+// 4.9 TB/s; 19 in two launches).
+struct JoinArgs {
+  float* states;
+  const float* sums;
+  const float* h0;
+};
+static __global__ __launch_bounds__(256) void gdn_scan_join_kernel(ScanGeo g, const float* __restrict__ A_log,
+                                                                   JoinArgs fore, JoinArgs aft) {
   constexpr int U = 16;
   const uint32_t per = (uint32_t)g.np * g.D;  // checked on the host: below 2^31
   const uint32_t r = blockIdx.x * 256u + threadIdx.x;
   if (r >= per) return;
+  const bool back = blockIdx.z;
+  const JoinArgs& j = back ? aft : fore;
   const int row = blockIdx.y, last = g.ntiles - 1;
   const uint32_t n = r / g.D, d = r - n * g.D;
-  float* p = states + (int64_t)row * g.ntiles * per;
-  const float* s = sums + (int64_t)row * g.ntiles * g.D;
+  // the chain's first tile, and the steps to the next
+  const int64_t first = (int64_t)row * g.ntiles + (back ? last : 0);
+  float* p = j.states + first * per;
+  const float* s = j.sums + first * g.D;
+  const int64_t pstep = back ? -(int64_t)per : per, sstep = back ? -(int64_t)g.D : g.D;
   float e[U], sm[U];
   auto fetch = [&](int t) {
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const int q = min(t + k, last);
-      const int64_t at = BACK ? last - q : q;
-      e[k] = (p + at * per)[r];
-      sm[k] = (s + at * g.D)[d];
+      const int64_t q = min(t + k, last);
+      e[k] = (p + q * pstep)[r];
+      sm[k] = (s + q * sstep)[d];
     }
   };
   fetch(0);
   const int64_t sd = (int64_t)d * g.N + min(n, (uint32_t)g.N - 1);
   const bool in = n < (uint32_t)g.N;
-  float H = !BACK && !g.cu && h0 ? h0[(int64_t)row * g.D * g.N + sd] : 0.f;
+  float H = !g.cu && j.h0 ? j.h0[(int64_t)row * g.D * g.N + sd] : 0.f;
   H = in ? H : 0.f;
   const float A2 = in ? scan_rate(A_log[sd]) : 0.f;
   for (int t = 0; t <= last; t += U) {
@@ -451,7 +458,7 @@ __global__ __launch_bounds__(256) void gdn_scan_join_kernel(ScanGeo g, const flo
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       if (t + k > last) break;
-      (p + (int64_t)(BACK ? last - (t + k) : t + k) * per)[r] = out[k];
+      (p + (t + k) * pstep)[r] = out[k];
     }
   }
 }
@@ -476,64 +483,72 @@ __global__ __launch_bounds__(256) void gdn_scan_rows_kernel(const E* __restrict_
 
 // Decode: nl = a power of two of lanes per channel, four states each (nl >= N / 4),
 // 64 / nl channels per wave, T tokens one after the other.  The state's read and
-// write bound it (8 N bytes per channel); `vec`: rows of the state are 16-byte
-// aligned multiples of four.
-template <typename E>
+// write bound it (8 N bytes per channel).  VEC: N is a multiple of four, and a lane's four
+// values of the states, of A_log, Bm and Cm are one aligned load each.  Bound by how many
+// loads a lane needs for its 32 bytes of state: one token each of B=256, D=4096, N=16 bf16
+// (143 MB) 32 us = 4.4 TB/s, 49 us without VEC; B=64, D=2048 6.6 against 8.3 (N=13: 8.6).
+template <typename E, bool VEC>
 __global__ __launch_bounds__(256) void gdn_scan_decode_kernel(
     ScanGeo g, Src x, const E* __restrict__ dt, Src z, const float* __restrict__ A_log,
     const E* __restrict__ Bm, const E* __restrict__ Cm, const float* __restrict__ skip,
     const float* __restrict__ dt_bias, const float* state_in, float* state_out, E* __restrict__ y,
-    int nl, int vec) {
+    int nl) {
   const int64_t item = ((int64_t)blockIdx.x * 256 + threadIdx.x) / nl;
-  const int part = threadIdx.x & (nl - 1), n0 = 4 * part;
+  const int part = threadIdx.x & (nl - 1);
   const bool on = item < (int64_t)g.B * g.D;  // lanes without a channel stay for the sums
   const int64_t it = on ? item : 0;
   const int64_t b = it / g.D;
   const int d = (int)(it - b * g.D), gi = d / g.DG;
+  // the lane's states, of which it has `cnt` (VEC: four or none; with none it reads the
+  // row's first ones, and its rates and rows count as 0)
+  const int cnt = max(min(g.N - 4 * part, 4), 0), n0 = cnt ? 4 * part : 0;
+  auto four = [&](const auto* p, float (&v)[4]) {
+    using P = std::remove_cv_t<std::remove_pointer_t<decltype(p)>>;
+    if constexpr (VEC) {
+      vec_load<P, 4>(p, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = (float)p[max(min(j, cnt - 1), 0)];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = j < cnt ? v[j] : 0.f;
+  };
   float A2[4], h[4];
-  const float* hp = state_in + it * g.N + n0;
-  if (vec && n0 < g.N) {
-    const f32x4 v = *reinterpret_cast<const f32x4*>(hp);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = v[j];
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = n0 + j < g.N ? hp[j] : 0.f;
-  }
-  scan_rates<4, false>(A_log, g, d, n0, A2);
+  four(state_in + it * g.N + n0, h);
+  four(A_log + (int64_t)d * g.N + n0, A2);
   const float bias = dt_bias ? dt_bias[d] : 0.f, sk = skip ? skip[d] : 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) A2[j] = scan_rate(A2[j]);
   for (int t = 0; t < g.T; ++t) {
     const int64_t tok = b * g.T + t;
     const float xv = (float)static_cast<const E*>(x.p)[tok * x.ld + d];
-    const float dl = gate_softplus((float)dt[tok * g.lddt + d] + bias);
-    const float u = dl * xv;
-    const E* bp = Bm + tok * g.ldb + (int64_t)gi * g.N + n0;
-    const E* cp = Cm + tok * g.ldc + (int64_t)gi * g.N + n0;
+    const float dv = (float)dt[tok * g.lddt + d];
+    float zv = 0.f, bv[4], cv[4];
+    if (z.p) zv = (float)static_cast<const E*>(z.p)[tok * z.ld + d];
+    four(Bm + tok * g.ldb + (int64_t)gi * g.N + n0, bv);
+    four(Cm + tok * g.ldc + (int64_t)gi * g.N + n0, cv);
+    const float dl = gate_softplus(dv + bias), u = dl * xv;
     float acc = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const bool in = n0 + j < g.N;
-      h[j] = fmaf(fast_exp2(dl * A2[j]), h[j], in ? (float)bp[j] * u : 0.f);
-      if (in) acc = fmaf((float)cp[j], h[j], acc);
+      h[j] = fmaf(fast_exp2(dl * A2[j]), h[j], j < cnt ? bv[j] * u : 0.f);
+      if (j < cnt) acc = fmaf(cv[j], h[j], acc);
     }
     for (int o = nl >> 1; o; o >>= 1) acc += __shfl_xor(acc, o, 64);
     if (on && part == 0) {
       float v = fmaf(sk, xv, acc);
-      if (z.p) {
-        const float zv = (float)static_cast<const E*>(z.p)[tok * z.ld + d];
-        v *= zv * fast_sigmoid(zv);
-      }
+      if (z.p) v *= zv * fast_sigmoid(zv);
       y[tok * g.D + d] = (E)v;
     }
   }
   if (!on) return;
   float* op = state_out + it * g.N + n0;
-  if (vec && n0 < g.N) {
-    *reinterpret_cast<f32x4*>(op) = f32x4{h[0], h[1], h[2], h[3]};
+  if constexpr (VEC) {
+    if (cnt) vec_store<float, 4>(op, h);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (n0 + j < g.N) op[j] = h[j];
+      if (j < cnt) op[j] = h[j];
   }
 }
 

@@ -111,7 +111,8 @@ gdn_status_t scan_fwd_run(ScanPlan pl, const FwdArgs& a, void* ws, hipStream_t s
     if (g.ntiles > 1) {
       ok(launch(gdn::gdn_scan_kernel<E, BE, NS, WHOLE, SPLIT, true>, dim3((unsigned)main_blocks), block, s, g, x, dt, z,
                 a.A_log, b, c, a.skip, a.dt_bias, a.h0, states, sums, y, a.fin));
-      ok(launch(gdn::gdn_scan_join_kernel<false>, scan_join_grid(g), dim3(256), s, g, a.A_log, a.h0, states, sums));
+      ok(launch(gdn::gdn_scan_join_kernel, scan_join_grid(g, 1), dim3(256), s, g, a.A_log, gdn::JoinArgs{states, sums, a.h0},
+                gdn::JoinArgs{}));
     }
     ok(launch(gdn::gdn_scan_kernel<E, BE, NS, WHOLE, SPLIT, false>, dim3((unsigned)(main_blocks + empties)), block, s, g, x,
               dt, z, a.A_log, b, c, a.skip, a.dt_bias, a.h0, states, sums, y, a.fin));
@@ -170,15 +171,18 @@ gdn_status_t gdn_scan_decode(const gdn_scan_params_t* p, const void* x, const vo
   const gdn::ScanGeo& g = pl.geo;
   int nl = 1;
   while (nl * 4 < g.N) nl <<= 1;
-  const int vec = g.N % 4 == 0 && aligned(state, 16) && aligned(new_state, 16);
+  const size_t four = 4 * pl.esz;
+  const bool vec = g.N % 4 == 0 && aligned(state, 16) && aligned(new_state, 16) && aligned(A_log, 16) &&
+                   aligned(Bm, four) && aligned(Cm, four) && g.ldb % 4 == 0 && g.ldc % 4 == 0;
   const int64_t blocks = ceil_div((int64_t)g.B * g.D * nl, 256);
   if (blocks > INT32_MAX) return GDN_ERR_UNSUPPORTED;
   auto go = [&](auto e) {
     using E = decltype(e);
-    return launch(gdn::gdn_scan_decode_kernel<E>, dim3((unsigned)blocks), dim3(256),
+    return launch(vec ? gdn::gdn_scan_decode_kernel<E, true> : gdn::gdn_scan_decode_kernel<E, false>,
+                  dim3((unsigned)blocks), dim3(256),
                   static_cast<hipStream_t>(stream), g, gdn::Src{x, nullptr, pl.ldx}, static_cast<const E*>(dt),
                   gdn::Src{z, nullptr, pl.ldz}, A_log, static_cast<const E*>(Bm), static_cast<const E*>(Cm),
-                  skip, dt_bias, state, new_state, static_cast<E*>(y), nl, vec);
+                  skip, dt_bias, state, new_state, static_cast<E*>(y), nl);
   };
   return (p->dtype == GDN_BF16 ? go(gdn::bf16{}) : go(0.f)) == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }

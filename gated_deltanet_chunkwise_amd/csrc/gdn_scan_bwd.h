@@ -123,7 +123,9 @@ __device__ __forceinline__ float softplus_both(float x, float& slope) {
 }
 
 // (1).  states, rev [tile][np][D]; sums, rsums [tile][D] (-1: nothing passes through).
-// R needs no walk backwards: with P_t = a_1 .. a_t it is sum_t P_t Cm_t r_t.
+// R needs no walk backwards: with P_t = a_1 .. a_t it is sum_t P_t Cm_t r_t.  VALU-bound;
+// B=2, T=2048, D=2048, N=16 bf16: 47 us with four tokens' loads in flight (126 registers, so
+// the launch's four waves per SIMD run side by side), 52 with eight (154 registers).
 template <typename E, typename BE, int NS, bool WHOLE, bool CK>
 __global__ __launch_bounds__(64 * kScanMaxWaves) void gdn_scan_bwd_ends_kernel(
     ScanBwdGeo bg, Src x, const E* __restrict__ dt, Src z, const float* __restrict__ A_log,
@@ -131,7 +133,7 @@ __global__ __launch_bounds__(64 * kScanMaxWaves) void gdn_scan_bwd_ends_kernel(
     const float* __restrict__ h0, const E* __restrict__ d_y, const float* __restrict__ d_fin,
     float* __restrict__ states, float* __restrict__ rev, float* __restrict__ sums,
     float* __restrict__ rsums) {
-  constexpr int U = kScanGroup;
+  constexpr int U = kScanGroup / 2;
   const ScanGeo& g = bg.g;
   ScanPlace w;
   w.init<NS>(g, blockIdx.x);

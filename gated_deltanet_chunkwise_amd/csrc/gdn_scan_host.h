@@ -65,8 +65,8 @@ inline int64_t scan_all_tiles(const ScanPlan& pl) {
   return (int64_t)pl.geo.ntiles * (pl.packed ? 1 : pl.geo.B);
 }
 
-inline dim3 scan_join_grid(const gdn::ScanGeo& g) {
-  return dim3((unsigned)ceil_div((int64_t)g.np * g.D, 256), g.cu ? 1 : g.B);
+inline dim3 scan_join_grid(const gdn::ScanGeo& g, int chains) {
+  return dim3((unsigned)ceil_div((int64_t)g.np * g.D, 256), g.cu ? 1 : g.B, chains);
 }
 
 // Whether Bm and Cm can be read in place: whole rows of np states at 4-byte aligned
