@@ -9,6 +9,11 @@
 // tile of tokens with the W-1 previous inputs in registers, so each input is read
 // once per tile (W-1 rows more at a tile's start, which its neighbour has just
 // brought into the L2).  All sums are fp32; y is rounded once.
+//
+// Forward, W=4 bf16, x at its rows' own stride: B=4, T=8192, C=2048 (268 MB) 54 us, a
+// copy's 5 TB/s; B=2, T=2048 (34 MB) 13.3, B=1, T=300 6.4: there the latency of a lane's
+// loads and of the launch.  Rows that do not split into 16-byte vectors take a channel per
+// lane: B=4, T=4096, C=2047 33 us against 31 with C=2048.
 #pragma once
 #include "gdn_layer.h"
 
@@ -281,10 +286,13 @@ constexpr int kConvTiles = 4;  // tiles per workgroup, a wave each
 // tile.  Block id = (group of tiles, channel group), the latter fastest; blocks behind
 // those form d_initial.  partial [tile groups][W + 1][C]: dweight's W rows, then dbias.
 //
-// Bound by memory, and by how much of it is in flight.  B=4, T=8192, C=2048, W=4 bf16
-// (403 MB, 79 us at a copy's 5.1 TB/s): 105 us with tiles of 29 or 61 tokens, 133 with 13,
-// 120 with 125.  The loads of U tokens are sent for ahead of the U being computed; without
-// that the same kernel took 144 us, and with eight channels per lane (234 registers) 112.
+// Bound by memory, and by how much of it is in flight: the loads of U tokens are sent for
+// ahead of the U being computed (144 us without that, 105 with, four channels per lane at
+// the first size below).  B=4, T=8192, C=2048, W=4 bf16 (403 MB, 79 us at a copy's 5.1 TB/s):
+// 96 us.  Channels per lane, us, before the tiles were held to 80 tokens: there one 112, two
+// 109, four 114; B=4, T=4096 57, 56, 64; B=2, T=2048 21, 23, 28; fp32 T=8192 one 184, four
+// 189.  Hence two of bf16 and one of fp32; U = 4 in fp32 (128 us against 141 with 8 where
+// x and d_y were one tensor).
 // Tiles are uniform over a wave, so the row pointers are scalar and the middle of a tile
 // has no branches: with stores under a lane's condition, every wait for loads is also one
 // for the stores before them (154 us).

@@ -36,19 +36,22 @@ gdn_status_t conv_sizes(const gdn_conv_params_t* p, bool packed, ConvPlan* out) 
   return GDN_OK;
 }
 
-constexpr int kBwdVec = 4;
+// Channels per lane in the backward pass: two of bf16, one of fp32 (see its kernel).
+int bwd_vec(const ConvPlan& pl) { return pl.esz == 2 ? 2 : 1; }
 
-// The backward pass's tiles: each lane's tile as long as leaves about 16 waves per
+// The backward pass's tiles: each lane's tile as long as leaves about 12 waves per
 // CU (256 CUs are taken for granted, so that the workspace is the same on every
 // device), 16 tokens at least (its W-1 tokens of overlap are then at most a fifth)
-// and 256 at most.
+// and 80 at most, the overlap included.  us, W=4: at most 80 and 256 tokens: B=4, T=8192,
+// C=2048 bf16 96 and 108, C=2044 119 and 130; 12, 16 and 24 waves: B=1, T=32768, C=512 bf16
+// 32, 34 and 40, B=2, T=4096, C=1000 fp32 30, 33 and 36.
 void conv_bwd_tiles(const gdn_conv_params_t* p, bool packed, int vec, ConvPlan* pl) {
   gdn::ConvGeo& g = pl->geo;
   g.cvn = p->C / vec;
   const int64_t ntok = (int64_t)p->B * p->T;
-  int64_t tile = ntok * g.cvn / (256 * 16 * 64);
+  int64_t tile = ntok * g.cvn / (256 * 12 * 64);
   // whole groups of loads for the tile and the W-1 tokens after it
-  tile = std::min<int64_t>(std::max<int64_t>(tile / gdn::kConvGroup, 2), 32) * gdn::kConvGroup - (p->W - 1);
+  tile = std::min<int64_t>(std::max<int64_t>(tile / gdn::kConvGroup, 2), 10) * gdn::kConvGroup - (p->W - 1);
   g.tile = (int)tile;
   g.ntiles = (int)std::max<int64_t>(ceil_div(p->T, tile), 1);
   const int64_t tiles = (int64_t)g.ntiles * (packed ? 1 : p->B);
@@ -59,7 +62,7 @@ void conv_bwd_tiles(const gdn_conv_params_t* p, bool packed, int vec, ConvPlan* 
 size_t conv_ws(const gdn_conv_params_t* p, bool packed, ConvPlan pl) {
   conv_bwd_tiles(p, packed, 1, &pl);  // what misaligned pointers would take
   const size_t total = pl.total;
-  if (p->C % kBwdVec == 0) conv_bwd_tiles(p, packed, kBwdVec, &pl);
+  if (p->C % bwd_vec(pl) == 0) conv_bwd_tiles(p, packed, bwd_vec(pl), &pl);
   return std::max(total, pl.total);
 }
 
@@ -138,8 +141,8 @@ gdn_status_t conv_bwd_run(const ConvPlan& pl, const ConvBwdArgs& a, void* ws, hi
   return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
-// F<E, W, VEC>::run for the call's type and width; VEC = V16 for bf16, 4 for fp32, or 1.
-template <template <typename, int, int> class F, int V16, typename... A>
+// F<E, W, VEC>::run for the call's type and width; VEC = V16 for bf16, V32 for fp32, or 1.
+template <template <typename, int, int> class F, int V16, int V32, typename... A>
 gdn_status_t conv_dispatch(const gdn_conv_params_t* p, bool vec, A&&... a) {
   auto width = [&](auto e, auto v) {
     using E = decltype(e);
@@ -151,7 +154,7 @@ gdn_status_t conv_dispatch(const gdn_conv_params_t* p, bool vec, A&&... a) {
   using One = std::integral_constant<int, 1>;
   if (p->dtype == GDN_BF16)
     return vec ? width(gdn::bf16{}, std::integral_constant<int, V16>{}) : width(gdn::bf16{}, One{});
-  return vec ? width(0.f, std::integral_constant<int, 4>{}) : width(0.f, One{});
+  return vec ? width(0.f, std::integral_constant<int, V32>{}) : width(0.f, One{});
 }
 template <typename E, int W, int VEC> struct FwdRun {
   template <typename... A> static gdn_status_t run(A&&... a) { return conv_fwd_run<E, W, VEC>(a...); }
@@ -176,8 +179,7 @@ gdn_status_t pack_run(const void* xv, int64_t ld, int64_t rows, int C, int8_t* c
   const E* x = static_cast<const E*>(xv);
   const int nblk = (int)ceil_div(C, gdn::kPackBlock);
   const int64_t cap = (int64_t)device_cus() * 16;  // workgroups beyond that loop
-  const bool vec = C % 8 == 0 && ld % (16 / (int)sizeof(E)) == 0 && aligned(x, 16) && aligned(codes, 8);
-  if (!vec) {
+  if (C < 8) {
     const int64_t blocks = std::min(ceil_div(rows * nblk, 8), cap);
     return launch(gdn::gdn_pack8_scalar_kernel<E>, dim3((unsigned)blocks), dim3(256), s, x, ld, codes,
                   scales, rows, C, nblk) == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
@@ -187,7 +189,7 @@ gdn_status_t pack_run(const void* xv, int64_t ld, int64_t rows, int C, int8_t* c
   for (int64_t r = 0; r < rows; r += most) {
     const int64_t n = std::min(most, rows - r);
     const int64_t blocks = std::min(ceil_div(n * vpr, 256 * gdn::kPackUnroll), cap);
-    if (launch(gdn::gdn_pack8_vec_kernel<E>, dim3((unsigned)blocks), dim3(256), s, x + r * ld, ld,
+    if (launch(C % 8 ? gdn::gdn_pack8_vec_kernel<E, true> : gdn::gdn_pack8_vec_kernel<E, false>, dim3((unsigned)blocks), dim3(256), s, x + r * ld, ld,
                codes + r * C, scales + r * nblk, (uint32_t)n, C, (uint32_t)vpr) != hipSuccess)
       return GDN_ERR_LAUNCH;
   }
@@ -200,17 +202,17 @@ gdn_status_t unpack_run(const int8_t* codes, const uint8_t* scales, int64_t rows
   E* y = static_cast<E*>(yv);
   const int nblk = (int)ceil_div(C, gdn::kPackBlock);
   const int64_t cap = (int64_t)device_cus() * 16;
-  if (C % 8 != 0 || !aligned(y, 16) || !aligned(codes, 8)) {
+  if (C < 8) {
     const int64_t blocks = std::min(ceil_div(rows * C, 256), 2 * cap);
     return launch(gdn::gdn_unpack8_scalar_kernel<E>, dim3((unsigned)blocks), dim3(256), s, codes, scales,
                   y, rows * C, C, nblk) == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
   }
-  const int64_t vpr = C / 8, most = std::max<int64_t>(((int64_t)1 << 30) / vpr, 1);
+  const int64_t vpr = ceil_div(C, 8), most = std::max<int64_t>(((int64_t)1 << 30) / vpr, 1);
   for (int64_t r = 0; r < rows; r += most) {
     const int64_t n = std::min(most, rows - r);
     const int64_t blocks = std::min(ceil_div(n * vpr, 256 * gdn::kPackUnroll), cap);
-    if (launch(gdn::gdn_unpack8_vec_kernel<E>, dim3((unsigned)blocks), dim3(256), s, codes + r * C,
-               scales + r * nblk, y + r * C, (uint32_t)n, (uint32_t)vpr, (uint32_t)nblk) != hipSuccess)
+    if (launch(C % 8 ? gdn::gdn_unpack8_vec_kernel<E, true> : gdn::gdn_unpack8_vec_kernel<E, false>, dim3((unsigned)blocks), dim3(256), s, codes + r * C,
+               scales + r * nblk, y + r * C, (uint32_t)n, C, (uint32_t)vpr, (uint32_t)nblk) != hipSuccess)
       return GDN_ERR_LAUNCH;
   }
   return GDN_OK;
@@ -238,7 +240,7 @@ gdn_status_t gdn_conv_fwd(const gdn_conv_params_t* p, const void* x, const float
       !aligned(final_state, pl.esz) || !aligned(weight, 4) || !aligned(bias, 4) || !aligned(cu_seqlens, 8))
     return GDN_ERR_ALIGN;
   pl.geo.cu = cu_seqlens;
-  return conv_dispatch<FwdRun, 8>(p, vec_ok(pl, (int)(16 / pl.esz), {x, y, initial_state, final_state}), pl, x, weight, bias,
+  return conv_dispatch<FwdRun, 8, 4>(p, vec_ok(pl, (int)(16 / pl.esz), {x, y, initial_state, final_state}), pl, x, weight, bias,
                                initial_state, y, final_state, static_cast<hipStream_t>(stream));
 }
 
@@ -257,10 +259,10 @@ gdn_status_t gdn_conv_decode(const gdn_conv_params_t* p, const void* x, const fl
   if (p->B == 0 || (p->T == 0 && state == new_state)) return GDN_OK;
   if (p->T == 0) {  // no weights to read: the state passes through
     pl.geo.cu = nullptr;
-    return conv_dispatch<FwdRun, 8>(p, vec_ok(pl, (int)(16 / pl.esz), {state, new_state}), pl, x, weight, bias, state, y,
+    return conv_dispatch<FwdRun, 8, 4>(p, vec_ok(pl, (int)(16 / pl.esz), {state, new_state}), pl, x, weight, bias, state, y,
                                  new_state, static_cast<hipStream_t>(stream));
   }
-  return conv_dispatch<DecodeRun, 8>(p, vec_ok(pl, (int)(16 / pl.esz), {x, y, state, new_state}), pl, x, weight, bias, state,
+  return conv_dispatch<DecodeRun, 8, 4>(p, vec_ok(pl, (int)(16 / pl.esz), {x, y, state, new_state}), pl, x, weight, bias, state,
                                   new_state, y, static_cast<hipStream_t>(stream));
 }
 
@@ -291,13 +293,14 @@ gdn_status_t gdn_conv_bwd(const gdn_conv_params_t* p, const void* x, const uint8
       !aligned(dweight, 4) || !aligned(dbias, 4) || !aligned(cu_seqlens, 8) || !aligned(workspace, kWsAlign))
     return GDN_ERR_ALIGN;
   if (workspace_bytes < need) return GDN_ERR_WORKSPACE;
-  const bool vec = vec_ok(pl, kBwdVec, {x_scales ? nullptr : x, d_y, dx, initial_state, d_final_state, d_initial_state}) &&
-                   aligned(x, kBwdVec);
-  conv_bwd_tiles(p, packed, vec ? kBwdVec : 1, &pl);
+  const int v = bwd_vec(pl);
+  const bool vec = vec_ok(pl, v, {x_scales ? nullptr : x, d_y, dx, initial_state, d_final_state, d_initial_state}) &&
+                   aligned(x, v);
+  conv_bwd_tiles(p, packed, vec ? v : 1, &pl);
   pl.geo.cu = cu_seqlens;
   const ConvBwdArgs a{x, x_scales, weight, bias, initial_state, d_y, d_final_state,
                       dx, dweight, dbias, d_initial_state};
-  return conv_dispatch<BwdRun, kBwdVec>(p, vec, pl, a, workspace, static_cast<hipStream_t>(stream));
+  return conv_dispatch<BwdRun, 2, 1>(p, vec, pl, a, workspace, static_cast<hipStream_t>(stream));
 }
 
 gdn_status_t gdn_pack8(const void* x, gdn_dtype_t dtype, int64_t rows, int32_t C, int64_t x_stride,

@@ -7,6 +7,7 @@ namespace gdn {
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // A pointer into global memory with its address space spelled out.
 template <typename E> using Global = __attribute__((address_space(1))) E*;
@@ -66,11 +67,12 @@ struct Src {
   int64_t ld;  // elements between rows (codes: C)
 };
 
-// VEC consecutive channels of one row, as loaded (not yet converted), so that
-// loads can be issued well before their use.
+// VEC consecutive channels of one row, as loaded (not yet converted), so that loads can
+// be issued well before their use; two at most from a checkpoint.
 template <typename E, int VEC> struct RawVec;
 template <> struct RawVec<bf16, 8> { u32x4 w; uint32_t s; };
 template <> struct RawVec<bf16, 4> { u32x2 w; uint32_t s; };
+template <> struct RawVec<bf16, 2> { uint32_t w, s; };
 template <> struct RawVec<float, 4> { u32x4 w; uint32_t s; };
 template <typename E> struct RawVec<E, 1> { uint32_t w, s; };
 
@@ -79,15 +81,8 @@ __device__ __forceinline__ RawVec<E, VEC> raw_load(const Src& s, int64_t row, in
   RawVec<E, VEC> r = {};
   if (s.scales) {  // VEC divides 32: one scale for the vector
     const uint8_t* q = static_cast<const uint8_t*>(s.p) + row * s.ld + c;
-    if constexpr (VEC == 1) {
-      r.w = *q;
-    } else if constexpr (VEC == 8) {
-      const u32x2 d = *reinterpret_cast<const u32x2*>(q);
-      r.w[0] = d.x;
-      r.w[1] = d.y;
-    } else {
-      r.w[0] = *reinterpret_cast<const uint32_t*>(q);
-    }
+    if constexpr (VEC == 1) r.w = *q;
+    else if constexpr (VEC == 2) r.w = *reinterpret_cast<const uint16_t*>(q);
     r.s = s.scales[row * nblk + (c >> 5)];
   } else {
     const E* q = static_cast<const E*>(s.p) + row * s.ld + c;
@@ -108,12 +103,9 @@ __device__ __forceinline__ RawVec<E, VEC> raw_load_at(Global<const char> row, Gl
     if constexpr (VEC == 1 && sizeof(E) == 2) r.w = *(Global<const uint16_t>)q;
     else r.w = *(Global<const decltype(r.w)>)q;
   } else {
-    if constexpr (VEC == 1) {
-      r.w = *(Global<const uint8_t>)q;
-    } else {
-      static_assert(VEC == 4, "");
-      r.w[0] = *(Global<const uint32_t>)q;
-    }
+    static_assert(VEC <= 2, "");
+    if constexpr (VEC == 1) r.w = *(Global<const uint8_t>)q;
+    else r.w = *(Global<const uint16_t>)q;
     r.s = srow[soff];
   }
   return r;
@@ -122,20 +114,20 @@ __device__ __forceinline__ RawVec<E, VEC> raw_load_at(Global<const char> row, Gl
 // The raw vector as fp32; `packed` as the load's (s.scales != nullptr).
 template <typename E, int VEC>
 __device__ __forceinline__ void raw_unpack(const RawVec<E, VEC>& r, bool packed, float (&v)[VEC]) {
-  if (packed) {
-    const float sc = pack_scale(r.s);
+  if constexpr (VEC <= 2) {
+    if (packed) {
+      const float sc = pack_scale(r.s);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      if constexpr (VEC == 1) v[0] = (float)(int8_t)r.w * sc;
-      else v[i] = (float)(int8_t)(r.w[i >> 2] >> (8 * (i & 3))) * sc;
+      for (int i = 0; i < VEC; ++i) v[i] = (float)(int8_t)(r.w >> (8 * i)) * sc;
+      return;
     }
-  } else {
+  }
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      if constexpr (VEC == 1) v[0] = __uint_as_float(sizeof(E) == 2 ? r.w << 16 : r.w);
-      else if constexpr (sizeof(E) == 2) v[i] = (i & 1) ? bf16_hi(r.w[i >> 1]) : bf16_lo(r.w[i >> 1]);
-      else v[i] = __uint_as_float(r.w[i]);
-    }
+  for (int i = 0; i < VEC; ++i) {
+    if constexpr (VEC == 1) v[0] = __uint_as_float(sizeof(E) == 2 ? r.w << 16 : r.w);
+    else if constexpr (VEC == 2) v[i] = i ? bf16_hi(r.w) : bf16_lo(r.w);
+    else if constexpr (sizeof(E) == 2) v[i] = (i & 1) ? bf16_hi(r.w[i >> 1]) : bf16_lo(r.w[i >> 1]);
+    else v[i] = __uint_as_float(r.w[i]);
   }
 }
 
@@ -153,6 +145,8 @@ template <typename E, int VEC>
 __device__ __forceinline__ void vec_store(E* p, const float (&v)[VEC]) {
   if constexpr (VEC == 1) {
     *p = (E)v[0];
+  } else if constexpr (VEC == 2) {
+    *reinterpret_cast<bf16x2*>(p) = bf16x2{(bf16)v[0], (bf16)v[1]};
   } else if constexpr (sizeof(E) == 2 && VEC == 4) {
     const bf16x4 w = to_bf16x4(f32x4{v[0], v[1], v[2], v[3]});
     *reinterpret_cast<bf16x4*>(p) = w;

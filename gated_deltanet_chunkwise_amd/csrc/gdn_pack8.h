@@ -13,8 +13,20 @@
 //
 // Copy-bound: e + 1 + 1/32 bytes per element each way.  Eight channels per lane,
 // so a lane's load is 16 bytes of bf16 (32 of fp32) and its codes 8; four lanes
-// share a block and agree on its maximum by two lane exchanges.
+// share a block and agree on its maximum by two lane exchanges.  Rows whose length
+// is no multiple of eight, and addresses that are no multiple of a lane's bytes,
+// take the same kernels: gfx950's vector loads and stores need no alignment beyond
+// the element's.  A row's last lane then has fewer than eight channels; it loads
+// eight (the memory behind them is the next row's; the last row's lane takes them
+// one by one) and stores its own in pieces of 4, 2 and 1 (TAIL; where no row has such
+// a lane the test for it is left out, which is worth a tenth in small calls).
+//
+// Measured, us: 32768 rows of 2048 bf16 (207 MB) pack 37, unpack 32 (a copy of
+// that size, part of it in the caches, 8 TB/s: 26); 262144 rows 392 and 352 (from memory,
+// 4.1 and 4.6 TB/s); 65536 of 1001 38 and 34, where a lane per channel took 135 and 73.
 #pragma once
+#include <type_traits>
+
 #include "gdn_layer.h"
 
 namespace gdn {
@@ -34,10 +46,43 @@ __device__ __forceinline__ int pack_code(float x, uint32_t b) {
   return (int)fminf(fmaxf(q, -127.f), 127.f);
 }
 
-// Vectors of 8 channels: C % 8 == 0, ld % 8 == 0, 16-byte aligned x.  Lane groups
-// of four per block; `vpr` = 4 * ceil(C / 32) vector places per row, those at or
-// beyond C / 8 hold nothing.  rows * vpr < 2^31.
-template <typename E>
+typedef uint32_t u32x4_e2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_e4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x2_e1 __attribute__((ext_vector_type(2), aligned(1)));
+
+// Eight channels of E as loaded from an address aligned to the element; `n` < 8: of those
+// only n, one by one, the others 0.
+template <typename E> struct Oct {
+  uint32_t w[2 * sizeof(E)];
+  __device__ __forceinline__ void load(const E* p) {
+    using V = std::conditional_t<sizeof(E) == 2, u32x4_e2, u32x4_e4>;
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(E) / 2; ++k) {
+      const u32x4 q = reinterpret_cast<const V*>(p)[k];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[4 * k + i] = q[i];
+    }
+  }
+  __device__ __forceinline__ void load(const E* p, int n) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if constexpr (sizeof(E) == 4) {
+        w[k] = k < n ? reinterpret_cast<const uint32_t*>(p)[k] : 0u;
+      } else {
+        const uint32_t v = k < n ? reinterpret_cast<const uint16_t*>(p)[k] : 0u;
+        w[k >> 1] = (k & 1) ? w[k >> 1] | v << 16 : v;
+      }
+    }
+  }
+  __device__ __forceinline__ float operator[](int k) const {
+    if constexpr (sizeof(E) == 2) return (k & 1) ? bf16_hi(w[k >> 1]) : bf16_lo(w[k >> 1]);
+    else return __uint_as_float(w[k]);
+  }
+};
+
+// Any C >= 8.  Lane groups of four per block; `vpr` = 4 * ceil(C / 32) places of eight
+// channels per row, those at or beyond C hold nothing.  rows * vpr < 2^31.
+template <typename E, bool TAIL>
 __global__ __launch_bounds__(256) void gdn_pack8_vec_kernel(const E* __restrict__ x, int64_t ld,
                                                             int8_t* __restrict__ codes,
                                                             uint8_t* __restrict__ scales,
@@ -45,9 +90,9 @@ __global__ __launch_bounds__(256) void gdn_pack8_vec_kernel(const E* __restrict_
   const uint32_t total = rows * vpr, step = gridDim.x * 256u;
   const uint32_t nblk = vpr >> 2;
   for (uint32_t i0 = blockIdx.x * 256u + threadIdx.x; i0 < total; i0 += step * kPackUnroll) {
-    u32x4 w[kPackUnroll][sizeof(E) / 2];
+    Oct<E> w[kPackUnroll];
     uint32_t row[kPackUnroll], v[kPackUnroll];
-    bool in[kPackUnroll];
+    int cnt[kPackUnroll];  // channels of the lane's own
 #pragma unroll
     for (int u = 0; u < kPackUnroll; ++u) {
       const uint32_t i = i0 + u * step;
@@ -55,22 +100,21 @@ __global__ __launch_bounds__(256) void gdn_pack8_vec_kernel(const E* __restrict_
       const bool any = i < total && i >= i0;
       row[u] = any ? i / vpr : 0;
       v[u] = any ? i - row[u] * vpr : 0;
-      in[u] = any && (int)(v[u] * 8) < C;
-      const u32x4* q = reinterpret_cast<const u32x4*>(x + (int64_t)row[u] * ld + v[u] * 8);
-#pragma unroll
-      for (int k = 0; k < (int)sizeof(E) / 2; ++k) w[u][k] = in[u] ? q[k] : u32x4{0, 0, 0, 0};
+      cnt[u] = any ? min(max(C - (int)(v[u] * 8), 0), 8) : 0;
+      if (!TAIL) cnt[u] = cnt[u] ? 8 : 0;
+      const E* q = x + (int64_t)row[u] * ld + (cnt[u] ? v[u] * 8 : 0);  // (without channels: the row's first)
+      if (TAIL && (cnt[u] & 7) && row[u] == rows - 1) w[u].load(q, cnt[u]);
+      else w[u].load(q);
     }
 #pragma unroll
     for (int u = 0; u < kPackUnroll; ++u) {
       float f[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if constexpr (sizeof(E) == 2) f[k] = (k & 1) ? bf16_hi(w[u][0][k >> 1]) : bf16_lo(w[u][0][k >> 1]);
-        else f[k] = __uint_as_float(w[u][k >> 2][k & 3]);
-      }
       uint32_t m = 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(f[k]) & 0x7fffffffu);
+      for (int k = 0; k < 8; ++k) {
+        f[k] = k < cnt[u] ? w[u][k] : 0.f;
+        m = max(m, __float_as_uint(f[k]) & 0x7fffffffu);
+      }
       // lanes xor 1, then xor 2 (quad permutations)
       m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xf, 0xf, true));
       m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xf, 0xf, true));
@@ -78,15 +122,30 @@ __global__ __launch_bounds__(256) void gdn_pack8_vec_kernel(const E* __restrict_
       u32x2 c = {0, 0};
 #pragma unroll
       for (int k = 0; k < 8; ++k) c[k >> 2] |= ((uint32_t)pack_code(f[k], b) & 255u) << (8 * (k & 3));
-      if (in[u]) {
-        *reinterpret_cast<u32x2*>(codes + (int64_t)row[u] * C + v[u] * 8) = c;
-        if ((v[u] & 3) == 0) scales[(int64_t)row[u] * nblk + (v[u] >> 2)] = (uint8_t)b;
+      uint8_t* q = reinterpret_cast<uint8_t*>(codes) + (int64_t)row[u] * C + v[u] * 8;
+      if (cnt[u] == 8) {
+        *reinterpret_cast<u32x2_e1*>(q) = c;
+      } else if (TAIL && cnt[u]) {
+        uint32_t d = c.x;
+        if (cnt[u] & 4) {
+          __builtin_memcpy(q, &d, 4);
+          d = c.y;
+          q += 4;
+        }
+        if (cnt[u] & 2) {
+          const uint16_t h = (uint16_t)d;
+          __builtin_memcpy(q, &h, 2);
+          d >>= 16;
+          q += 2;
+        }
+        if (cnt[u] & 1) *q = (uint8_t)d;
       }
+      if (cnt[u] && (v[u] & 3) == 0) scales[(int64_t)row[u] * nblk + (v[u] >> 2)] = (uint8_t)b;
     }
   }
 }
 
-// Any C, stride and alignment: 32 lanes per block, one channel each.
+// Rows of fewer than eight channels: 32 lanes per block, one channel each.
 template <typename E>
 __global__ __launch_bounds__(256) void gdn_pack8_scalar_kernel(const E* __restrict__ x, int64_t ld,
                                                                int8_t* __restrict__ codes,
@@ -107,41 +166,71 @@ __global__ __launch_bounds__(256) void gdn_pack8_scalar_kernel(const E* __restri
   }
 }
 
-// The values a checkpoint stands for, rows contiguous.  Vectors of 8 channels:
-// C % 8 == 0, 16-byte aligned y, 8-byte aligned codes; rows * C / 8 < 2^31.
-template <typename E>
+// The values a checkpoint stands for, rows contiguous.  Any C >= 8: `vpr` = ceil(C / 8)
+// places of eight channels per row; rows * vpr < 2^31.
+template <typename E, bool TAIL>
 __global__ __launch_bounds__(256) void gdn_unpack8_vec_kernel(const int8_t* __restrict__ codes,
                                                               const uint8_t* __restrict__ scales,
-                                                              E* __restrict__ y, uint32_t rows,
+                                                              E* __restrict__ y, uint32_t rows, int C,
                                                               uint32_t vpr, uint32_t nblk) {
   const uint32_t total = rows * vpr, step = gridDim.x * 256u;
   for (uint32_t i0 = blockIdx.x * 256u + threadIdx.x; i0 < total; i0 += step * kPackUnroll) {
     u32x2 c[kPackUnroll];
     uint32_t b[kPackUnroll];
+    int64_t at[kPackUnroll];
+    int cnt[kPackUnroll];
 #pragma unroll
     for (int u = 0; u < kPackUnroll; ++u) {
       const uint32_t i = i0 + u * step;
       const bool any = i < total && i >= i0;
-      const uint32_t j = any ? i : i0;
-      const uint32_t row = j / vpr;
-      c[u] = reinterpret_cast<const u32x2*>(codes)[j];
-      b[u] = scales[(int64_t)row * nblk + ((j - row * vpr) >> 2)];
+      const uint32_t j = any ? i : i0, row = j / vpr, v = j - row * vpr;
+      const int own = TAIL ? min(C - (int)(v * 8), 8) : 8;
+      cnt[u] = any ? own : 0;
+      at[u] = (int64_t)row * C + v * 8;
+      const uint8_t* q = reinterpret_cast<const uint8_t*>(codes) + at[u];
+      if (TAIL && own < 8 && row == rows - 1) {
+        c[u] = {0, 0};
+#pragma unroll
+        for (int k = 0; k < 7; ++k)
+          if (k < own) c[u][k >> 2] |= (uint32_t)q[k] << (8 * (k & 3));
+      } else {
+        c[u] = *reinterpret_cast<const u32x2_e1*>(q);
+      }
+      b[u] = scales[(int64_t)row * nblk + (v >> 2)];
     }
 #pragma unroll
     for (int u = 0; u < kPackUnroll; ++u) {
-      const uint32_t i = i0 + u * step;
-      if (!(i < total && i >= i0)) continue;
+      if (!cnt[u]) continue;
       const float s = pack_scale(b[u]);
       float f[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) f[k] = (float)(int8_t)(c[u][k >> 2] >> (8 * (k & 3))) * s;
-      E* q = y + (int64_t)i * 8;
-      if constexpr (sizeof(E) == 2) {
-        vec_store<E, 8>(q, f);
-      } else {
-        reinterpret_cast<f32x4*>(q)[0] = f32x4{f[0], f[1], f[2], f[3]};
-        reinterpret_cast<f32x4*>(q)[1] = f32x4{f[4], f[5], f[6], f[7]};
+      E* q = y + at[u];
+      typedef E E4 __attribute__((ext_vector_type(4), aligned(sizeof(E))));
+      typedef E E2 __attribute__((ext_vector_type(2), aligned(sizeof(E))));
+      if (!TAIL || cnt[u] == 8) {
+        if constexpr (sizeof(E) == 2) {
+          typedef E E8 __attribute__((ext_vector_type(8), aligned(2)));
+          *reinterpret_cast<E8*>(q) = E8{(E)f[0], (E)f[1], (E)f[2], (E)f[3], (E)f[4], (E)f[5], (E)f[6], (E)f[7]};
+        } else {
+          reinterpret_cast<E4*>(q)[0] = E4{f[0], f[1], f[2], f[3]};
+          reinterpret_cast<E4*>(q)[1] = E4{f[4], f[5], f[6], f[7]};
+        }
+        continue;
       }
+      if (cnt[u] & 4) {
+        *reinterpret_cast<E4*>(q) = E4{(E)f[0], (E)f[1], (E)f[2], (E)f[3]};
+        f[0] = f[4];
+        f[1] = f[5];
+        f[2] = f[6];
+        q += 4;
+      }
+      if (cnt[u] & 2) {
+        *reinterpret_cast<E2*>(q) = E2{(E)f[0], (E)f[1]};
+        f[0] = f[2];
+        q += 2;
+      }
+      if (cnt[u] & 1) *q = (E)f[0];
     }
   }
 }

@@ -35,6 +35,26 @@ def test_codes_and_scales(rows, C, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("C", [8, 9, 10, 12, 15, 23, 31, 39, 63, 65, 1001])
+def test_rows_that_end_inside_a_lane(C, dtype):
+    for rows in (1, 2, 300):
+        check(values(rows, C, dtype, rows + C).cuda())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_any_address(dtype):
+    """Rows, codes and scales at addresses that only their elements are aligned to."""
+    wide = values(9, 101, dtype, 3).cuda()
+    x = wide[:, 1:42]
+    p = gdn.pack8(x)
+    q = gdn.pack8(x.contiguous())
+    assert torch.equal(p.codes, q.codes) and torch.equal(p.scales, q.scales)
+    odd = torch.empty(9 * 41 + 1, dtype=torch.int8, device="cuda")[1:].view(9, 41).copy_(p.codes)
+    out = torch.empty(9 * 41 + 1, dtype=dtype, device="cuda")[1:].view(9, 41)
+    assert torch.equal(gdn.unpack8(gdn.Packed8(odd, p.scales, dtype), out=out), gdn.unpack8(q))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_where_the_scale_changes(dtype):
     # the block's maximum at and next to 127 s, ties between two codes, zeros
     x = torch.zeros(8, 32)
