@@ -21,9 +21,11 @@
 // one by one) and stores its own in pieces of 4, 2 and 1 (TAIL; where no row has such
 // a lane the test for it is left out, which is worth a tenth in small calls).
 //
-// Measured, us: 32768 rows of 2048 bf16 (207 MB) pack 37, unpack 32 (a copy of
-// that size, part of it in the caches, 8 TB/s: 26); 262144 rows 392 and 352 (from memory,
-// 4.1 and 4.6 TB/s); 65536 of 1001 38 and 34, where a lane per channel took 135 and 73.
+// Measured, us: 32768 rows of 2048 bf16 (207 MB) pack 34, unpack 32 (a copy of that
+// size, part of it in the caches, 8 TB/s: 26); 262144 rows 381 and 353 (from memory, 4.3
+// and 4.6 TB/s); 65536 of 1001 35 and 34, where a lane per channel took 135 and 73.  Next
+// to memory it is the VALU: 18 operations per channel in pack, with clamps, conversions and
+// shifts of their own for each code, were 37 us at the first size.
 #pragma once
 #include <type_traits>
 
@@ -40,10 +42,19 @@ __device__ __forceinline__ uint32_t pack_byte(uint32_t m) {
   const int b = (int)(m >> 23) - 6 + ((m & 0x7fffffu) > 0x7e0000u ? 1 : 0);
   return (uint32_t)min(max(b, 1), 248);
 }
-__device__ __forceinline__ int pack_code(float x, uint32_t b) {
-  if (b == 255u) return 0;
-  const float q = rintf(x * __uint_as_float((254u - b) << 23));
-  return (int)fminf(fmaxf(q, -127.f), 127.f);
+// 1 / scale (0 for a block of NaN: its codes are taken as 0).
+__device__ __forceinline__ float pack_inverse(uint32_t b) { return b == 255u ? 0.f : __uint_as_float((254u - b) << 23); }
+// A code in the low byte (what is above it is of no use).  x / s is at most 127, and just
+// below 128 where the scale is at its upper end: held to 127, then 1.5 * 2^23 added, which
+// rounds to the nearest integer, ties to even, and leaves it in the low bits, in two's
+// complement.
+__device__ __forceinline__ uint32_t pack_code(float x, float inverse) {
+  return __float_as_uint(__builtin_amdgcn_fmed3f(x * inverse, -127.f, 127.f) + 12582912.f);
+}
+// Four codes' low bytes in a word: byte selectors 0..3 take from the second operand, 4..7
+// from the first, 12 gives 0.
+__device__ __forceinline__ uint32_t pack_word(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0c0c0400u), __builtin_amdgcn_perm(b, a, 0x0c0c0400u), 0x05040100u);
 }
 
 typedef uint32_t u32x4_e2 __attribute__((ext_vector_type(4), aligned(2)));
@@ -108,20 +119,24 @@ __global__ __launch_bounds__(256) void gdn_pack8_vec_kernel(const E* __restrict_
     }
 #pragma unroll
     for (int u = 0; u < kPackUnroll; ++u) {
-      float f[8];
       uint32_t m = 0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        f[k] = k < cnt[u] ? w[u][k] : 0.f;
-        m = max(m, __float_as_uint(f[k]) & 0x7fffffffu);
+        const uint32_t e = __float_as_uint(w[u][k]) & 0x7fffffffu;
+        m = max(m, !TAIL || k < cnt[u] ? e : 0u);
       }
+      if (!TAIL) m = cnt[u] ? m : 0u;
       // lanes xor 1, then xor 2 (quad permutations)
       m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xf, 0xf, true));
       m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xf, 0xf, true));
       const uint32_t b = pack_byte(m);
-      u32x2 c = {0, 0};
+      const float inverse = pack_inverse(b);
+      u32x2 c;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) c[k >> 2] |= ((uint32_t)pack_code(f[k], b) & 255u) << (8 * (k & 3));
+      for (int k = 0; k < 2; ++k)
+        c[k] = pack_word(pack_code(w[u][4 * k], inverse), pack_code(w[u][4 * k + 1], inverse),
+                         pack_code(w[u][4 * k + 2], inverse), pack_code(w[u][4 * k + 3], inverse));
+      if (b == 255u) c = {0, 0};
       uint8_t* q = reinterpret_cast<uint8_t*>(codes) + (int64_t)row[u] * C + v[u] * 8;
       if (cnt[u] == 8) {
         *reinterpret_cast<u32x2_e1*>(q) = c;
@@ -161,7 +176,7 @@ __global__ __launch_bounds__(256) void gdn_pack8_scalar_kernel(const E* __restri
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 32));
     const uint32_t b = pack_byte(m);
-    if (c < C) codes[row * C + c] = (int8_t)pack_code(f, b);
+    if (c < C) codes[row * C + c] = b == 255u ? (int8_t)0 : (int8_t)pack_code(f, pack_inverse(b));
     if (l == 0) scales[i] = (uint8_t)b;
   }
 }
