@@ -14,9 +14,15 @@
 // what its own tokens send to the state before it (R = sum_t (a_1 .. a_t) Cm_t r_t);
 // (2) both joined over the tiles, forwards for the states and backwards for their
 // gradients; (3) every tile on its own: forwards once, the state before every group of
-// SUB tokens kept in LDS; then, from the last group to the first, forwards again with
-// the group's states in registers and backwards through them; (4) sums over waves and
-// tiles.  VALU-bound like the forward pass, with about three times its operations.
+// SUB tokens kept in LDS; then, from the last group to the first, forwards again within
+// the group, its states in registers, and backwards through them; (4) sums over waves and
+// tiles.  VALU-bound like the forward pass: B=2, T=2048, D=2048, N=16 bf16, us: (1) 47,
+// (2) 14, (3) 182 with its vector units busy for 72 % of them, (4) 9; the bytes alone
+// would be 23.
+//
+// Eight states per lane and eight tokens per group: (3) then takes 245 registers, two
+// waves per SIMD, which 45 KB of LDS per workgroup allow as well.  Held to three waves per
+// SIMD the registers spill; with groups of four tokens it took 199 us.
 //
 // dBm and dCm need sums over channels, that is over lanes: 2 NS values of a token are
 // added over 64 lanes by halving (in each step a lane keeps half of its values and
