@@ -5,15 +5,17 @@
 // its initial state [W-1][C] (oldest first) or are 0.  The final state holds the
 // sequence's last W-1 inputs.
 //
-// Copy-bound: a lane owns VEC neighbouring channels (16 bytes) and walks down a
-// tile of tokens with the W-1 previous inputs in registers, so each input is read
-// once per tile (W-1 rows more at a tile's start, which its neighbour has just
-// brought into the L2).  All sums are fp32; y is rounded once.
+// Copy-bound: a lane owns VEC neighbouring channels and walks down a tile of tokens
+// with the W-1 previous inputs in registers, so each input is read once per tile (W-1
+// rows more at a tile's start, which its neighbour has just brought into the L2).  All
+// sums are fp32; y is rounded once.
 //
-// Forward, W=4 bf16, x at its rows' own stride: B=4, T=8192, C=2048 (268 MB) 54 us, a
-// copy's 5 TB/s; B=2, T=2048 (34 MB) 13.3, B=1, T=300 6.4: there the latency of a lane's
-// loads and of the launch.  Rows that do not split into 16-byte vectors take a channel per
-// lane: B=4, T=4096, C=2047 33 us against 31 with C=2048.
+// Channels per lane, forward, W=4, us from memory (with the number of waves per CU that
+// suits each): B=4, T=8192, C=2048 bf16 (268 MB) one 69, two 51 (5.2 TB/s, a copy's), four 53,
+// eight 55; B=2, T=2048 13.0, 11.1, 11.5, 15.0; B=1, T=300 4.1, 4.3, 4.8, 6.7: fewer bytes per
+// load, but more waves and fewer registers.  fp32 T=8192 one 111, four 109; T=5003, C=1000 one
+// 10.0, four 11.0, packed in seven sequences with W=3 14.3 and 10.9.  Hence two of bf16 and
+// four of fp32.
 #pragma once
 #include "gdn_layer.h"
 
@@ -69,8 +71,8 @@ constexpr int kConvGroup = 8;  // tokens whose loads are in flight together
 
 // Work items: (tile, vector of channels), then (sequence, state row, vector) for
 // the final state.  Consecutive lanes take consecutive vectors of a row.  The rows of a
-// tile's first group are sent for before the weights: a lane's life is little more than
-// its loads' latency.
+// tile's first group are sent for before the weights, and before the search for the
+// sequence that they are in: a lane's life is little more than its loads' latency.
 template <typename E, int W, int VEC>
 __global__ __launch_bounds__(256) void gdn_conv_fwd_kernel(ConvGeo g, Src x,
                                                            const float* __restrict__ weight,
@@ -98,17 +100,28 @@ __global__ __launch_bounds__(256) void gdn_conv_fwd_kernel(ConvGeo g, Src x,
   }
   const bool silu = g.silu;
   Run<false> run;
-  run.init(g.cu, g.T, g.N, (int)unit, g.ntiles, g.tile);
+  run.place(g.cu, g.T, g.N, (int)unit, g.ntiles, g.tile);
+  const int ta = run.ta;
   RawVec<E, VEC> old[W - 1], raw[kConvGroup];
-  auto first = [&]() {
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) old[j] = raw_load<E, VEC>(x, max(ta - (W - 1) + j, 0), c, 0);
+#pragma unroll
+  for (int k = 0; k < kConvGroup; ++k) raw[k] = raw_load<E, VEC>(x, min(ta + k, run.t1 - 1), c, 0);
+  // the inputs before a run: those already on their way, unless its sequence has just begun
+  auto before = [&]() {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
       old[j] = conv_row<E, W, VEC>(g, x, h0, run.n, run.start, run.ta - run.start - (W - 1) + j, c);
+  };
+  auto first = [&]() {
+    before();
 #pragma unroll
     for (int k = 0; k < kConvGroup; ++k) raw[k] = raw_load<E, VEC>(x, min(run.ta + k, run.tb - 1), c, 0);
   };
+  run.locate();
   if (run.done()) return;
-  first();
+  if (run.ta != ta) first();  // only with ill-formed offsets
+  else if (run.ta - run.start < W - 1) before();
   float w[VEC][W], b[VEC];
   conv_params<W, VEC>(weight, bias, c, w, b);
   for (;;) {
@@ -150,7 +163,9 @@ __global__ __launch_bounds__(256) void gdn_conv_fwd_kernel(ConvGeo g, Src x,
 
 // T tokens of each of B sequences after its state [B][W-1][C], which is written
 // back (state_out may be state_in: a lane reads its channels' rows before it
-// writes them, and no other lane touches them).
+// writes them, and no other lane touches them).  One token, W=4, us with two channels of
+// bf16 per lane and with eight: B=64, C=2048 2.6 and 4.0 (the latency of one lane's loads),
+// B=256, C=8192 7.2 (29 MB, in the caches) and 14.7.
 template <typename E, int W, int VEC>
 __global__ __launch_bounds__(256) void gdn_conv_decode_kernel(ConvGeo g, Src x,
                                                               const float* __restrict__ weight,

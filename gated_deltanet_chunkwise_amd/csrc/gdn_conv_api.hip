@@ -36,8 +36,10 @@ gdn_status_t conv_sizes(const gdn_conv_params_t* p, bool packed, ConvPlan* out) 
   return GDN_OK;
 }
 
-// Channels per lane in the backward pass: two of bf16, one of fp32 (see its kernel).
-int bwd_vec(const ConvPlan& pl) { return pl.esz == 2 ? 2 : 1; }
+// Channels per lane where rows and addresses allow: two of bf16; of fp32 four forward, one
+// in the decode step and backward (see the kernels).
+constexpr int kFwd32 = 4;
+int conv_vec(const ConvPlan& pl, int fp32 = 1) { return pl.esz == 2 ? 2 : fp32; }
 
 // The backward pass's tiles: each lane's tile as long as leaves about 12 waves per
 // CU (256 CUs are taken for granted, so that the workspace is the same on every
@@ -62,7 +64,7 @@ void conv_bwd_tiles(const gdn_conv_params_t* p, bool packed, int vec, ConvPlan* 
 size_t conv_ws(const gdn_conv_params_t* p, bool packed, ConvPlan pl) {
   conv_bwd_tiles(p, packed, 1, &pl);  // what misaligned pointers would take
   const size_t total = pl.total;
-  if (p->C % bwd_vec(pl) == 0) conv_bwd_tiles(p, packed, bwd_vec(pl), &pl);
+  if (p->C % conv_vec(pl) == 0) conv_bwd_tiles(p, packed, conv_vec(pl), &pl);
   return std::max(total, pl.total);
 }
 
@@ -79,10 +81,11 @@ gdn_status_t conv_fwd_run(ConvPlan pl, const void* x, const float* w, const floa
                           const void* h0, void* y, void* fin, hipStream_t s) {
   gdn::ConvGeo& g = pl.geo;
   g.cvn = g.C / VEC;
-  // Tokens per lane: as long as leaves about 8 waves per CU, at least one group of
-  // loads, at most 64.
+  // Tokens per lane: as long as leaves about 16 waves per CU, at least one group of
+  // loads, at most 64.  8, 16 and 32 waves, us, bf16: B=1, T=2000, C=8192 20, 16, 17; T=32768,
+  // C=512 19, 17, 16; B=4, T=4096, C=2044 31, 32, 31.
   const int64_t ntok = (int64_t)g.B * g.T;
-  const int64_t lanes = (int64_t)device_cus() * 8 * 64;
+  const int64_t lanes = (int64_t)device_cus() * 16 * 64;
   const int64_t tile = ntok * g.cvn / std::max<int64_t>(lanes, 1) / gdn::kConvGroup * gdn::kConvGroup;
   g.tile = (int)std::min<int64_t>(std::max<int64_t>(tile, gdn::kConvGroup), 64);
   g.ntiles = (int)ceil_div(g.T, g.tile);
@@ -141,8 +144,8 @@ gdn_status_t conv_bwd_run(const ConvPlan& pl, const ConvBwdArgs& a, void* ws, hi
   return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
-// F<E, W, VEC>::run for the call's type and width; VEC = V16 for bf16, V32 for fp32, or 1.
-template <template <typename, int, int> class F, int V16, int V32, typename... A>
+// F<E, W, VEC>::run for the call's type and width; `vec`: VEC = conv_vec(.., V32), else 1.
+template <template <typename, int, int> class F, int V32, typename... A>
 gdn_status_t conv_dispatch(const gdn_conv_params_t* p, bool vec, A&&... a) {
   auto width = [&](auto e, auto v) {
     using E = decltype(e);
@@ -152,9 +155,8 @@ gdn_status_t conv_dispatch(const gdn_conv_params_t* p, bool vec, A&&... a) {
     return F<E, 4, V>::run(a...);
   };
   using One = std::integral_constant<int, 1>;
-  if (p->dtype == GDN_BF16)
-    return vec ? width(gdn::bf16{}, std::integral_constant<int, V16>{}) : width(gdn::bf16{}, One{});
-  return vec ? width(0.f, std::integral_constant<int, V32>{}) : width(0.f, One{});
+  if (p->dtype != GDN_BF16) return vec ? width(0.f, std::integral_constant<int, V32>{}) : width(0.f, One{});
+  return vec ? width(gdn::bf16{}, std::integral_constant<int, 2>{}) : width(gdn::bf16{}, One{});
 }
 template <typename E, int W, int VEC> struct FwdRun {
   template <typename... A> static gdn_status_t run(A&&... a) { return conv_fwd_run<E, W, VEC>(a...); }
@@ -240,7 +242,7 @@ gdn_status_t gdn_conv_fwd(const gdn_conv_params_t* p, const void* x, const float
       !aligned(final_state, pl.esz) || !aligned(weight, 4) || !aligned(bias, 4) || !aligned(cu_seqlens, 8))
     return GDN_ERR_ALIGN;
   pl.geo.cu = cu_seqlens;
-  return conv_dispatch<FwdRun, 8, 4>(p, vec_ok(pl, (int)(16 / pl.esz), {x, y, initial_state, final_state}), pl, x, weight, bias,
+  return conv_dispatch<FwdRun, kFwd32>(p, vec_ok(pl, conv_vec(pl, kFwd32), {x, y, initial_state, final_state}), pl, x, weight, bias,
                                initial_state, y, final_state, static_cast<hipStream_t>(stream));
 }
 
@@ -259,10 +261,10 @@ gdn_status_t gdn_conv_decode(const gdn_conv_params_t* p, const void* x, const fl
   if (p->B == 0 || (p->T == 0 && state == new_state)) return GDN_OK;
   if (p->T == 0) {  // no weights to read: the state passes through
     pl.geo.cu = nullptr;
-    return conv_dispatch<FwdRun, 8, 4>(p, vec_ok(pl, (int)(16 / pl.esz), {state, new_state}), pl, x, weight, bias, state, y,
+    return conv_dispatch<FwdRun, kFwd32>(p, vec_ok(pl, conv_vec(pl, kFwd32), {state, new_state}), pl, x, weight, bias, state, y,
                                  new_state, static_cast<hipStream_t>(stream));
   }
-  return conv_dispatch<DecodeRun, 8, 4>(p, vec_ok(pl, (int)(16 / pl.esz), {x, y, state, new_state}), pl, x, weight, bias, state,
+  return conv_dispatch<DecodeRun, 1>(p, vec_ok(pl, conv_vec(pl), {x, y, state, new_state}), pl, x, weight, bias, state,
                                   new_state, y, static_cast<hipStream_t>(stream));
 }
 
@@ -293,14 +295,14 @@ gdn_status_t gdn_conv_bwd(const gdn_conv_params_t* p, const void* x, const uint8
       !aligned(dweight, 4) || !aligned(dbias, 4) || !aligned(cu_seqlens, 8) || !aligned(workspace, kWsAlign))
     return GDN_ERR_ALIGN;
   if (workspace_bytes < need) return GDN_ERR_WORKSPACE;
-  const int v = bwd_vec(pl);
+  const int v = conv_vec(pl);
   const bool vec = vec_ok(pl, v, {x_scales ? nullptr : x, d_y, dx, initial_state, d_final_state, d_initial_state}) &&
                    aligned(x, v);
   conv_bwd_tiles(p, packed, vec ? v : 1, &pl);
   pl.geo.cu = cu_seqlens;
   const ConvBwdArgs a{x, x_scales, weight, bias, initial_state, d_y, d_final_state,
                       dx, dweight, dbias, d_initial_state};
-  return conv_dispatch<BwdRun, 2, 1>(p, vec, pl, a, workspace, static_cast<hipStream_t>(stream));
+  return conv_dispatch<BwdRun, 1>(p, vec, pl, a, workspace, static_cast<hipStream_t>(stream));
 }
 
 gdn_status_t gdn_pack8(const void* x, gdn_dtype_t dtype, int64_t rows, int32_t C, int64_t x_stride,

@@ -70,7 +70,6 @@ struct Src {
 // VEC consecutive channels of one row, as loaded (not yet converted), so that loads can
 // be issued well before their use; two at most from a checkpoint.
 template <typename E, int VEC> struct RawVec;
-template <> struct RawVec<bf16, 8> { u32x4 w; uint32_t s; };
 template <> struct RawVec<bf16, 4> { u32x2 w; uint32_t s; };
 template <> struct RawVec<bf16, 2> { uint32_t w, s; };
 template <> struct RawVec<float, 4> { u32x4 w; uint32_t s; };
@@ -150,10 +149,6 @@ __device__ __forceinline__ void vec_store(E* p, const float (&v)[VEC]) {
   } else if constexpr (sizeof(E) == 2 && VEC == 4) {
     const bf16x4 w = to_bf16x4(f32x4{v[0], v[1], v[2], v[3]});
     *reinterpret_cast<bf16x4*>(p) = w;
-  } else if constexpr (sizeof(E) == 2) {
-    const f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
-    const bf16x4 a = to_bf16x4(lo), b = to_bf16x4(hi);
-    *reinterpret_cast<bf16x8*>(p) = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   } else {
     *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
   }
@@ -191,14 +186,17 @@ template <bool UNIFORM> struct Run {
   const int64_t* cu;
 
   __device__ __forceinline__ void init(const int64_t* cu_, int T_, int N_, int tile, int ntiles, int len) {
+    place(cu_, T_, N_, tile, ntiles, len);
+    locate();
+  }
+  // The tile's tokens [ta, t1), which need no offset; then its first run.
+  __device__ __forceinline__ void place(const int64_t* cu_, int T_, int N_, int tile, int ntiles, int len) {
     cu = cu_;
     T = T_;
     N = N_;
     if (cu) {
       ta = tile * len;
       t1 = min(ta + len, T);
-      n = uniform<UNIFORM>(seq_of_token(cu, N, T, ta));
-      fit();
     } else {
       n = tile / ntiles;
       start = n * T;
@@ -206,6 +204,11 @@ template <bool UNIFORM> struct Run {
       ta = start + (tile - n * ntiles) * len;
       t1 = tb = min(ta + len, end);
     }
+  }
+  __device__ __forceinline__ void locate() {
+    if (!cu) return;
+    n = uniform<UNIFORM>(seq_of_token(cu, N, T, ta));
+    fit();
   }
   __device__ __forceinline__ bool done() const { return ta >= t1; }
   __device__ __forceinline__ void next() {

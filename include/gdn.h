@@ -438,8 +438,8 @@ gdn_status_t gdn_kda_gate(const void *g, gdn_dtype_t g_dtype, const float *A_log
  *   initial_state, final_state  [N][W-1][C], dtype, oldest row first, or NULL
  *   y            [B][T][C] contiguous, dtype, written
  * Sums are fp32, rounded once.  dtype: GDN_F32 or GDN_BF16.  Alignment: element
- * size (rows of 16-byte aligned, 16-byte divisible vectors are faster); cu_seqlens
- * 8; workspace 256.  B * T below 2^31 - 4096.  Errors as for gdn_fwd, all checked
+ * size (rows that split into four bytes of bf16 or sixteen of fp32 are faster);
+ * cu_seqlens 8; workspace 256.  B * T below 2^31 - 4096.  Errors as for gdn_fwd, all checked
  * before anything is enqueued; GDN_ERR_UNSUPPORTED for another W.  Outputs must not
  * overlap inputs or each other (gdn_conv_decode: new_state may be state).
  * Enqueued on `stream`; nothing is allocated. */
