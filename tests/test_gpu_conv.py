@@ -71,6 +71,15 @@ def test_backward(case):
     assert all(torch.equal(got[k], again[k]) for k in got), "the same call gives the same bits"
 
 
+@pytest.mark.parametrize("case", [
+    (1, 2600, 4096, 4, BF16, True, [1000, 0, 3, 1590], True, True),
+    (2, 800, 4099, 3, F32, True, None, True, True)], ids=["packed", "odd"])
+def test_tiles_of_several_groups(case):
+    """Enough channels that a lane's tile is longer than one group of loads, in both passes."""
+    test_forward(case)
+    test_backward(case)
+
+
 def test_rows_behind_the_last_sequence_stay():
     d, seeds, cu, act, used = make(CASES[10])
     g, s = lo.cuda(d), lo.cuda(seeds)
