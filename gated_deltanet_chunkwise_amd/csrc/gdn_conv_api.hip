@@ -92,7 +92,7 @@ gdn_status_t conv_fwd_run(ConvPlan pl, const void* x, const float* w, const floa
   const int64_t units = (int64_t)g.ntiles * (g.cu ? 1 : g.B) + (fin ? (int64_t)g.N * (W - 1) : 0);
   const int64_t blocks = ceil_div(units * g.cvn, 256);
   if (blocks == 0) return GDN_OK;
-  if (blocks > (1 << 24)) return GDN_ERR_UNSUPPORTED;  // 32-bit work items
+  if (!grid_fits(blocks, 256)) return GDN_ERR_UNSUPPORTED;  // (the kernel's work items are 32 bits as well)
   return launch(gdn::gdn_conv_fwd_kernel<E, W, VEC>, dim3((unsigned)blocks), dim3(256), s, g,
                 gdn::Src{x, nullptr, pl.ld}, w, b, static_cast<const E*>(h0), static_cast<E*>(y),
                 static_cast<E*>(fin)) == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
@@ -104,7 +104,7 @@ gdn_status_t conv_decode_run(ConvPlan pl, const void* x, const float* w, const f
   gdn::ConvGeo& g = pl.geo;
   g.cvn = g.C / VEC;
   const int64_t blocks = ceil_div((int64_t)g.B * g.cvn, 256);
-  if (blocks > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  if (!grid_fits(blocks, 256)) return GDN_ERR_UNSUPPORTED;
   return launch(gdn::gdn_conv_decode_kernel<E, W, VEC>, dim3((unsigned)blocks), dim3(256), s, g,
                 gdn::Src{x, nullptr, pl.ld}, w, b, static_cast<const E*>(in), static_cast<E*>(out),
                 static_cast<E*>(y)) == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
@@ -133,14 +133,14 @@ gdn_status_t conv_bwd_run(const ConvPlan& pl, const ConvBwdArgs& a, void* ws, hi
   const int cgroups = (int)ceil_div(g.cvn, 64);
   const int64_t main_blocks = tokens ? pl.rows * cgroups : 0;
   const int64_t states = a.dh0 ? ceil_div((int64_t)g.N * g.cvn, 256) : 0;
-  if (main_blocks + states > INT32_MAX || states > (1 << 24)) return GDN_ERR_UNSUPPORTED;
+  const int64_t sums = ceil_div((int64_t)(W + 1) * g.C, 64);
+  if (!grid_fits(main_blocks + states, 64 * gdn::kConvTiles) || !grid_fits(sums, 1024)) return GDN_ERR_UNSUPPORTED;
   if (main_blocks + states > 0)
     ok(launch(a.scales ? gdn::gdn_conv_bwd_kernel<E, W, VEC, true> : gdn::gdn_conv_bwd_kernel<E, W, VEC, false>,
               dim3((unsigned)(main_blocks + states)), dim3(64 * gdn::kConvTiles), s, g, x, a.w, a.b,
               static_cast<const E*>(a.h0), static_cast<const E*>(a.dy), static_cast<const E*>(a.dfin),
               static_cast<E*>(a.dx), static_cast<E*>(a.dh0), partial, cgroups, (int)main_blocks));
-  ok(launch(gdn::gdn_conv_bwd_sums_kernel<W>, dim3((unsigned)ceil_div((int64_t)(W + 1) * g.C, 64)),
-            dim3(1024), s, partial, tokens ? (int)pl.rows : 0, g.C, a.dw, a.db));
+  ok(launch(gdn::gdn_conv_bwd_sums_kernel<W>, dim3((unsigned)sums), dim3(1024), s, partial, tokens ? (int)pl.rows : 0, g.C, a.dw, a.db));
   return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 

@@ -49,6 +49,10 @@ hipError_t launch(void (*kern)(KArgs...), dim3 grid, dim3 block, hipStream_t s, 
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Whether a grid of that many workgroups can be launched: HIP takes less than 2^32 threads
+// per dimension.  Asked for every launch of a call before the first one.
+inline bool grid_fits(int64_t blocks, int64_t threads) { return blocks <= (int64_t)UINT32_MAX / threads; }
+
 // Sequence and token counts of a batch: B sequences of T tokens, or (packed) N
 // sequences in one row of T tokens.  The rules are gdn_fwd's.
 inline gdn_status_t check_batch(int32_t B, int32_t T, int32_t num_seqs, bool packed) {

@@ -76,6 +76,9 @@ struct FwdArgs {
 
 gdn_status_t scan_fwd_run(ScanPlan pl, const FwdArgs& a, void* ws, hipStream_t s) {
   gdn::ScanGeo& g = pl.geo;
+  const int64_t main_blocks = pl.tok > 0 ? scan_all_tiles(pl) * g.cgb : 0;
+  const int64_t empties = (g.cu || g.T == 0) && a.fin ? g.S : 0;
+  if (!grid_fits(main_blocks + empties, 64 * g.nw * g.upw)) return GDN_ERR_UNSUPPORTED;
   const FwdSpace sp = fwd_space(pl);
   char* w = static_cast<char*>(ws);
   float* states = reinterpret_cast<float*>(w + sp.states);
@@ -93,9 +96,6 @@ gdn_status_t scan_fwd_run(ScanPlan pl, const FwdArgs& a, void* ws, hipStream_t s
     Bm = Bw;
     Cm = Cw;
   }
-  const int64_t main_blocks = pl.tok > 0 ? scan_all_tiles(pl) * g.cgb : 0;
-  const int64_t empties = (g.cu || g.T == 0) && a.fin ? g.S : 0;
-  if (main_blocks + empties > INT32_MAX) return GDN_ERR_UNSUPPORTED;
   if (pl.tok == 0) g.ntiles = 0;  // no tile blocks: the first block is the first sequence's
   if (main_blocks + empties == 0) return GDN_OK;
   gdn_status_t st = scan_dispatch(pl, direct, [&](auto e, auto be, auto ns, auto whole, auto split) {
@@ -175,7 +175,7 @@ gdn_status_t gdn_scan_decode(const gdn_scan_params_t* p, const void* x, const vo
   const bool vec = g.N % 4 == 0 && aligned(state, 16) && aligned(new_state, 16) && aligned(A_log, 16) &&
                    aligned(Bm, four) && aligned(Cm, four) && g.ldb % 4 == 0 && g.ldc % 4 == 0;
   const int64_t blocks = ceil_div((int64_t)g.B * g.D * nl, 256);
-  if (blocks > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  if (!grid_fits(blocks, 256)) return GDN_ERR_UNSUPPORTED;
   auto go = [&](auto e) {
     using E = decltype(e);
     return launch(vec ? gdn::gdn_scan_decode_kernel<E, true> : gdn::gdn_scan_decode_kernel<E, false>,

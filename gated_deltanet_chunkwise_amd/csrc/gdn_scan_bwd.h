@@ -497,8 +497,8 @@ __global__ __launch_bounds__(64 * NW * scan_bwd_units(NW), 2) void gdn_scan_bwd_
   store1<float>(ps + g.D, w.d * 4u, dbias);
 }
 
-// (4).  Blocks below `row_blocks`: dBm and dCm, a lane per value, summed over the group's
-// channel waves.  The others: dA_log, dskip and ddt_bias, summed over the tiles, 64
+// (4).  Blocks below `row_blocks`: dBm and dCm, a value at a time per lane, summed over the
+// group's channel waves.  The others: dA_log, dskip and ddt_bias, summed over the tiles, 64
 // neighbouring values per workgroup, four lanes of tiles each; np rows of D values for
 // dA_log, then two rows.
 template <typename E>
@@ -509,20 +509,20 @@ __global__ __launch_bounds__(256) void gdn_scan_bwd_sums_kernel(
     float* __restrict__ ddt_bias) {
   __shared__ float sm[256];
   if (blockIdx.x < row_blocks) {
-    const int64_t per = (int64_t)g.B * g.T * 2 * g.np;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int gi = (int)(i / per);
-    if (gi >= g.G) return;
-    const int64_t r = i - gi * per;
-    const uint32_t w2 = 2 * g.np;
-    const int64_t t = r / w2;
-    const int m = (int)(r - t * w2), c = m >= g.np, n = m - c * g.np;
-    if (n >= g.N) return;
-    const float* p = pbc + (int64_t)gi * g.wpg * per + r;
-    float s = 0.f;
+    const int64_t per = (int64_t)g.B * g.T * 2 * g.np, total = per * g.G;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)row_blocks * 256) {
+      const int gi = (int)(i / per);
+      const int64_t r = i - gi * per;
+      const uint32_t w2 = 2 * g.np;
+      const int64_t t = r / w2;
+      const int m = (int)(r - t * w2), c = m >= g.np, n = m - c * g.np;
+      if (n >= g.N) continue;
+      const float* p = pbc + (int64_t)gi * g.wpg * per + r;
+      float s = 0.f;
 #pragma unroll 8
-    for (int k = 0; k < g.wpg; ++k) s += p[k * per];
-    (c ? dCm : dBm)[(t * g.G + gi) * g.N + n] = (E)s;
+      for (int k = 0; k < g.wpg; ++k) s += p[k * per];
+      (c ? dCm : dBm)[(t * g.G + gi) * g.N + n] = (E)s;
+    }
     return;
   }
   const int64_t e = (int64_t)(blockIdx.x - row_blocks) * 64 + (threadIdx.x & 63), per = (int64_t)g.np * g.D;

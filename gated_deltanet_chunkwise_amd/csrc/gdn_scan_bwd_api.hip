@@ -71,9 +71,12 @@ gdn_status_t scan_bwd_run(ScanPlan pl, const BwdArgs& a, void* ws, hipStream_t s
   const int64_t tiles = pl.tok > 0 ? scan_all_tiles(pl) : 0;
   const int64_t main_blocks = tiles * g.cgb;
   const int64_t empties = (g.cu || g.T == 0) && a.dh0 ? g.S : 0;
-  const int64_t row_blocks = pl.tok > 0 ? ceil_div(pl.tok * g.G * 2 * g.np, 256) : 0;
+  // rows of dBm and dCm: workgroups beyond that loop
+  const int64_t row_blocks = std::min<int64_t>(pl.tok > 0 ? ceil_div(pl.tok * g.G * 2 * g.np, 256) : 0, 1 << 16);
   const int64_t param_blocks = ceil_div((int64_t)(g.np + 2) * g.D, 64);
-  if (main_blocks + empties > INT32_MAX || row_blocks + param_blocks > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  // (the first kernel has no more threads than the main one)
+  if (!grid_fits(main_blocks + empties, 64 * g.nw * g.upw) || !grid_fits(row_blocks + param_blocks, 256))
+    return GDN_ERR_UNSUPPORTED;
   if (!direct && pl.tok > 0) {
     float *Bw = F(sp.rows), *Cw = F(sp.rows + scan_rows_bytes(pl));
     ok(pl.esz == 2 ? scan_copy_rows<gdn::bf16>(&pl, Bm, Cm, Bw, Cw, s) : scan_copy_rows<float>(&pl, Bm, Cm, Bw, Cw, s));

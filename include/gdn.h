@@ -440,7 +440,8 @@ gdn_status_t gdn_kda_gate(const void *g, gdn_dtype_t g_dtype, const float *A_log
  * Sums are fp32, rounded once.  dtype: GDN_F32 or GDN_BF16.  Alignment: element
  * size (rows that split into four bytes of bf16 or sixteen of fp32 are faster);
  * cu_seqlens 8; workspace 256.  B * T below 2^31 - 4096.  Errors as for gdn_fwd, all checked
- * before anything is enqueued; GDN_ERR_UNSUPPORTED for another W.  Outputs must not
+ * before anything is enqueued; GDN_ERR_UNSUPPORTED for another W, and for sizes that would
+ * take 2^32 threads or more in one launch.  Outputs must not
  * overlap inputs or each other (gdn_conv_decode: new_state may be state).
  * Enqueued on `stream`; nothing is allocated. */
 typedef struct {
@@ -502,7 +503,7 @@ gdn_status_t gdn_conv_bwd(const gdn_conv_params_t *p, const void *x, const uint8
  * tokens that run side by side (three kernels); where the channels alone fill the
  * device, one kernel runs each sequence through.  The cut is chosen from the sizes
  * alone.  dtype, alignment, limits and errors as for
- * gdn_conv_fwd; GDN_ERR_UNSUPPORTED for N > 64.  Outputs must not overlap inputs or
+ * gdn_conv_fwd; GDN_ERR_UNSUPPORTED for N > 64 and for B > 65535.  Outputs must not overlap inputs or
  * each other (gdn_scan_decode: new_state may be state).  Enqueued on `stream`;
  * nothing is allocated. */
 typedef struct {

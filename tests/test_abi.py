@@ -503,3 +503,29 @@ def test_layer_calls_with_nothing_to_do_enqueue_nothing():
     assert conv_decode(CP(B=0)) == OK and scan_decode(SP(B=0)) == OK
     assert conv_decode(CP(T=0), new=0x400000) == OK        # `new` is `state` (the fourth address)
     assert conv_fwd(CP(T=0), fin=None) == OK and scan_fwd(SP(T=0), fin=None) == OK
+
+
+# A launch holds less than 2^32 threads per dimension of its grid; sizes beyond that are
+# refused before the first of a call's kernels is enqueued (without a GPU a call that gets
+# as far as enqueuing answers GDN_ERR_LAUNCH).
+GRID = [
+    (conv_decode, CP(B=1 << 20, T=1, C=(1 << 13) + 1)),              # a lane per sequence and channel
+    (lambda p: conv_fwd(p, x=0x100004), CP(B=1 << 22, T=1, C=256, dtype=gdn.GDN_F32)),  # exactly 2^32
+    (conv_bwd, CP(B=1, T=20, C=1 << 26)),                            # the sums over tiles
+    (conv_bwd, CP(B=1 << 23, T=0, C=513)),                           # initial states
+    (scan_decode, SP(B=1 << 15, T=1, D=1 << 16, N=8)),
+    (scan_fwd, SP(B=65535, T=1, D=1 << 17, G=1 << 17, N=1)),         # a wave per sequence and group
+    (lambda p: scan_bwd(p, ws_bytes=1 << 50), SP(B=65535, T=1, D=1 << 17, G=1 << 17, N=1)),
+    (scan_bwd, SP(B=1, T=20, D=1 << 24, G=1, N=64)),                 # the sums over tiles
+]
+
+
+@pytest.mark.parametrize("call,p", GRID)
+def test_layer_launches_beyond_the_grid(call, p):
+    assert call(p) == EUNSUP
+
+
+@pytest.mark.parametrize("call", [scan_fwd, scan_bwd])
+def test_empty_sequences_beyond_the_grid(call):
+    # a workgroup copies each empty sequence's state
+    assert call(SP(B=1, T=0, num_seqs=1 << 25), cu=0x9000000) == EUNSUP

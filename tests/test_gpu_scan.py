@@ -100,6 +100,11 @@ def test_many_channels_run_in_one_pass():
     lo.close(fin, fin_ref, 150, "final state")
 
 
+def test_more_rows_of_bm_and_cm_than_one_grid_sums():
+    # 2100 * 64 groups * 2 * 64 states: beyond 2^24 values the sums' workgroups loop
+    check_backward((1, 2100, 64, 64, 64, F32, None, ALL))
+
+
 def test_extreme_decays_and_time_steps():
     """States that vanish within a token (A D of about -400, also across whole tiles), that
     never decay (A about -1e-9), and D beyond softplus's threshold and below 1e-9."""
