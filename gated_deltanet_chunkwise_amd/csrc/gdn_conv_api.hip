@@ -31,7 +31,8 @@ gdn_status_t conv_sizes(const gdn_conv_params_t* p, bool packed, ConvPlan* out) 
   g.N = packed ? p->num_seqs : p->B;
   g.silu = p->activation;
   g.nblk = (int)ceil_div(p->C, gdn::kPackBlock);
-  if ((int64_t)g.N * 3 * p->C > ((int64_t)1 << 38)) return GDN_ERR_UNSUPPORTED;  // grid range
+  // beyond any grid, and near where three rows of states per sequence pass 64 bits
+  if ((int64_t)g.N * p->C > ((int64_t)1 << 38) / 3) return GDN_ERR_UNSUPPORTED;
   *out = pl;
   return GDN_OK;
 }

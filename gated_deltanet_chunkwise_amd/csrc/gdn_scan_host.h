@@ -24,6 +24,8 @@ inline gdn_status_t scan_sizes(const gdn_scan_params_t* p, bool packed, ScanPlan
   const int64_t bn = (int64_t)p->G * p->N;
   // 32-bit indices of a row of states; rows of the batch in a grid's second dimension
   if (bn > INT32_MAX || (int64_t)p->D * 64 > INT32_MAX || p->B > 65535) return GDN_ERR_UNSUPPORTED;
+  // beyond any memory; workspaces take up to about 1 KB per token and channel, counted in 64 bits
+  if ((int64_t)p->B * p->T > ((int64_t)1 << 48) / p->D) return GDN_ERR_UNSUPPORTED;
   auto bad = [](int64_t ld, int64_t least) { return ld != 0 && ld < least; };
   if (bad(p->x_stride, p->D) || bad(p->dt_stride, p->D) || bad(p->z_stride, p->D) ||
       bad(p->b_stride, bn) || bad(p->c_stride, bn))

@@ -529,3 +529,21 @@ def test_layer_launches_beyond_the_grid(call, p):
 def test_empty_sequences_beyond_the_grid(call):
     # a workgroup copies each empty sequence's state
     assert call(SP(B=1, T=0, num_seqs=1 << 25), cu=0x9000000) == EUNSUP
+
+
+# Sizes whose products pass 64 bits (or that no memory holds) are refused, and their
+# workspaces asked for as 0: a size that wrapped round would let the call through.
+@pytest.mark.parametrize("call,p,cu", [
+    (conv_fwd, CP(B=(1 << 31) - 1, T=0, C=(1 << 31) - 1), None),     # B 3 C
+    (conv_decode, CP(B=(1 << 31) - 1, T=0, C=(1 << 31) - 1), None),
+    (conv_fwd, CP(B=1, T=0, C=(1 << 31) - 1, num_seqs=(1 << 31) - 1), 0x9000000),
+    (conv_bwd, CP(B=(1 << 31) - 1, T=0, C=(1 << 31) - 1), None)])
+def test_conv_sizes_beyond_64_bits(call, p, cu):
+    assert (call(p, cu=cu) if cu else call(p)) == EUNSUP
+
+
+def test_scan_sizes_beyond_64_bits():
+    p = SP(B=1, T=(1 << 31) - 5000, D=1 << 24, G=1 << 24, N=63)
+    assert scan_fwd(p) == EUNSUP and scan_bwd(p) == EUNSUP and scan_decode(p) == EUNSUP
+    for f in ("gdn_scan_fwd_workspace_size", "gdn_scan_bwd_workspace_size"):
+        assert getattr(gdn.load_library(), f)(ctypes.byref(p), 0) == 0
