@@ -19,6 +19,7 @@ Packed8 = collections.namedtuple("Packed8", ("codes", "scales", "dtype"))
 Packed8.__doc__ = """A checkpoint of an activation [..., C] (pack8): codes [..., C] int8, scales
 [..., ceil(C / 32)] uint8, and the activation's dtype."""
 
+GDN_ZERO_REST = 0x100  # include/gdn.h: rows of y behind the last sequence are set to 0
 _ACTIVATIONS = {None: 0, "silu": 1}
 PACK_BLOCK = 32  # channels per checkpoint scale
 
@@ -294,8 +295,9 @@ def _conv_sizes(data, dtype, weight, bias, cu_seqlens, activation):
     if activation not in _ACTIVATIONS:
         raise ValueError("activation must be None or 'silu', got %r" % (activation,))
     N = _sequences(cu_seqlens, B)
-    p = ConvParams(B, T, C, W, 0 if cu_seqlens is None else N, _dtype_code(dtype), _ACTIVATIONS[activation],
-                   _row_stride("x", data))
+    code = _dtype_code(dtype)
+    p = ConvParams(B, T, C, W, *((0, code) if cu_seqlens is None else (N, code | GDN_ZERO_REST)),
+                   _ACTIVATIONS[activation], _row_stride("x", data))
     return ctypes.byref(p), B, T, C, W, N
 
 
@@ -304,7 +306,8 @@ def conv_fwd(x, weight, bias=None, cu_seqlens=None, initial_state=None, activati
     """Short causal depthwise convolution through gdn_conv_fwd: x [B,T,C] (bf16 or fp32),
     weight [C,W] fp32 with W in 2..4, bias [C] fp32 or None, initial_state [N,W-1,C] in
     x's dtype or None, activation "silu" or None.  Returns (y [B,T,C], final_state
-    [N,W-1,C] or None)."""
+    [N,W-1,C] or None); rows of y behind the last sequence (where cu_seqlens end before
+    T) are 0."""
     p, B, T, C, W, N = _conv_sizes(x, x.dtype, weight, bias, cu_seqlens, activation)
     _fit((("initial_state", initial_state, (N, W - 1, C), x.dtype),))
     index = _place(x, (), (("weight", weight), ("bias", bias), ("cu_seqlens", cu_seqlens),
@@ -425,7 +428,8 @@ def _scan_sizes(x, dtype, dt, A_log, Bm, Cm, skip, z, z_dtype, dt_bias, cu_seqle
             raise TypeError("z must be %s, got %s" % (dtype, z_dtype))
         z_ld = _row_stride("z", z)
     S = _sequences(cu_seqlens, B)
-    p = ScanParams(B, T, D, G, N, 0 if cu_seqlens is None else S, _dtype_code(dtype), _row_stride("x", x),
+    code = _dtype_code(dtype)
+    p = ScanParams(B, T, D, G, N, *((0, code) if cu_seqlens is None else (S, code | GDN_ZERO_REST)), _row_stride("x", x),
                    _row_stride("dt", dt), z_ld, _row_stride("Bm", Bm), _row_stride("Cm", Cm))
     return ctypes.byref(p), B, T, D, G, N, S
 
@@ -435,7 +439,8 @@ def scan_fwd(x, dt, A_log, Bm, Cm, skip=None, z=None, dt_bias=None, cu_seqlens=N
     """Selective state space scan through gdn_scan_fwd: x, dt, z [B,T,D] and Bm, Cm
     [B,T,G,N] in bf16 or fp32, A_log [D,N], skip and dt_bias [D] fp32, initial_state
     [sequences,D,N] fp32; skip, z, dt_bias and initial_state may be None.  Returns
-    (y [B,T,D], final_state [sequences,D,N] fp32 or None)."""
+    (y [B,T,D], final_state [sequences,D,N] fp32 or None); rows of y behind the last
+    sequence are 0, as conv_fwd's."""
     f32 = _torch().float32
     p, B, T, D, G, N, S = _scan_sizes(x, x.dtype, dt, A_log, Bm, Cm, skip, z, None if z is None else z.dtype,
                                       dt_bias, cu_seqlens)

@@ -27,6 +27,7 @@ struct ConvGeo {
   int nblk;          // checkpoint scales per row
   int tile, ntiles;  // tokens per tile; tiles per row of the batch
   int silu;
+  int zero;          // forward: y's rows behind the last sequence are set to 0
   const int64_t* cu;  // packed offsets or nullptr
 };
 
@@ -118,8 +119,13 @@ __global__ __launch_bounds__(256) void gdn_conv_fwd_kernel(ConvGeo g, Src x,
 #pragma unroll
     for (int k = 0; k < kConvGroup; ++k) raw[k] = raw_load<E, VEC>(x, min(run.ta + k, run.tb - 1), c, 0);
   };
+  auto leave = [&]() {
+    if (!g.zero) return;
+    const float none[VEC] = {};
+    for (int t = run.rest; t < run.t1; ++t) vec_store<E, VEC>(y + (int64_t)t * g.C + c, none);
+  };
   run.locate();
-  if (run.done()) return;
+  if (run.done()) return leave();
   if (run.ta != ta) first();  // only with ill-formed offsets
   else if (run.ta - run.start < W - 1) before();
   float w[VEC][W], b[VEC];
@@ -156,7 +162,7 @@ __global__ __launch_bounds__(256) void gdn_conv_fwd_kernel(ConvGeo g, Src x,
       }
     }
     run.next();
-    if (run.done()) return;
+    if (run.done()) return leave();
     first();
   }
 }

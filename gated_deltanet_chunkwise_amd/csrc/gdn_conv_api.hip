@@ -17,7 +17,8 @@ struct ConvPlan {
 // Sizes only.
 gdn_status_t conv_sizes(const gdn_conv_params_t* p, bool packed, ConvPlan* out) {
   if (!p) return GDN_ERR_NULL;
-  if (p->dtype != GDN_F32 && p->dtype != GDN_BF16) return GDN_ERR_DTYPE;
+  const int32_t dtype = p->dtype & ~GDN_ZERO_REST;
+  if (dtype != GDN_F32 && dtype != GDN_BF16) return GDN_ERR_DTYPE;
   if (p->C <= 0 || p->W <= 0 || (p->activation != 0 && p->activation != 1)) return GDN_ERR_SHAPE;
   gdn_status_t st = check_batch(p->B, p->T, p->num_seqs, packed);
   if (st != GDN_OK) return st;
@@ -25,11 +26,12 @@ gdn_status_t conv_sizes(const gdn_conv_params_t* p, bool packed, ConvPlan* out) 
   if (p->x_stride != 0 && p->x_stride < p->C) return GDN_ERR_SHAPE;
   ConvPlan pl{};
   pl.ld = p->x_stride ? p->x_stride : p->C;
-  pl.esz = p->dtype == GDN_BF16 ? 2 : 4;
+  pl.esz = dtype == GDN_BF16 ? 2 : 4;
   gdn::ConvGeo& g = pl.geo;
   g.B = p->B; g.T = p->T; g.C = p->C;
   g.N = packed ? p->num_seqs : p->B;
   g.silu = p->activation;
+  g.zero = packed && (p->dtype & GDN_ZERO_REST);
   g.nblk = (int)ceil_div(p->C, gdn::kPackBlock);
   // beyond any grid, and near where three rows of states per sequence pass 64 bits
   if ((int64_t)g.N * p->C > ((int64_t)1 << 38) / 3) return GDN_ERR_UNSUPPORTED;
@@ -147,16 +149,16 @@ gdn_status_t conv_bwd_run(const ConvPlan& pl, const ConvBwdArgs& a, void* ws, hi
 
 // F<E, W, VEC>::run for the call's type and width; `vec`: VEC = conv_vec(.., V32), else 1.
 template <template <typename, int, int> class F, int V32, typename... A>
-gdn_status_t conv_dispatch(const gdn_conv_params_t* p, bool vec, A&&... a) {
+gdn_status_t conv_dispatch(const ConvPlan& pl, int W, bool vec, A&&... a) {
   auto width = [&](auto e, auto v) {
     using E = decltype(e);
     constexpr int V = decltype(v)::value;
-    if (p->W == 2) return F<E, 2, V>::run(a...);
-    if (p->W == 3) return F<E, 3, V>::run(a...);
-    return F<E, 4, V>::run(a...);
+    if (W == 2) return F<E, 2, V>::run(pl, a...);
+    if (W == 3) return F<E, 3, V>::run(pl, a...);
+    return F<E, 4, V>::run(pl, a...);
   };
   using One = std::integral_constant<int, 1>;
-  if (p->dtype != GDN_BF16) return vec ? width(0.f, std::integral_constant<int, V32>{}) : width(0.f, One{});
+  if (pl.esz == 4) return vec ? width(0.f, std::integral_constant<int, V32>{}) : width(0.f, One{});
   return vec ? width(gdn::bf16{}, std::integral_constant<int, 2>{}) : width(gdn::bf16{}, One{});
 }
 template <typename E, int W, int VEC> struct FwdRun {
@@ -243,8 +245,8 @@ gdn_status_t gdn_conv_fwd(const gdn_conv_params_t* p, const void* x, const float
       !aligned(final_state, pl.esz) || !aligned(weight, 4) || !aligned(bias, 4) || !aligned(cu_seqlens, 8))
     return GDN_ERR_ALIGN;
   pl.geo.cu = cu_seqlens;
-  return conv_dispatch<FwdRun, kFwd32>(p, vec_ok(pl, conv_vec(pl, kFwd32), {x, y, initial_state, final_state}), pl, x, weight, bias,
-                               initial_state, y, final_state, static_cast<hipStream_t>(stream));
+  return conv_dispatch<FwdRun, kFwd32>(pl, p->W, vec_ok(pl, conv_vec(pl, kFwd32), {x, y, initial_state, final_state}), x, weight,
+                                       bias, initial_state, y, final_state, static_cast<hipStream_t>(stream));
 }
 
 gdn_status_t gdn_conv_decode(const gdn_conv_params_t* p, const void* x, const float* weight,
@@ -262,11 +264,11 @@ gdn_status_t gdn_conv_decode(const gdn_conv_params_t* p, const void* x, const fl
   if (p->B == 0 || (p->T == 0 && state == new_state)) return GDN_OK;
   if (p->T == 0) {  // no weights to read: the state passes through
     pl.geo.cu = nullptr;
-    return conv_dispatch<FwdRun, kFwd32>(p, vec_ok(pl, conv_vec(pl, kFwd32), {state, new_state}), pl, x, weight, bias, state, y,
-                                 new_state, static_cast<hipStream_t>(stream));
+    return conv_dispatch<FwdRun, kFwd32>(pl, p->W, vec_ok(pl, conv_vec(pl, kFwd32), {state, new_state}), x, weight, bias, state,
+                                         y, new_state, static_cast<hipStream_t>(stream));
   }
-  return conv_dispatch<DecodeRun, 1>(p, vec_ok(pl, conv_vec(pl), {x, y, state, new_state}), pl, x, weight, bias, state,
-                                  new_state, y, static_cast<hipStream_t>(stream));
+  return conv_dispatch<DecodeRun, 1>(pl, p->W, vec_ok(pl, conv_vec(pl), {x, y, state, new_state}), x, weight, bias, state,
+                                     new_state, y, static_cast<hipStream_t>(stream));
 }
 
 size_t gdn_conv_bwd_workspace_size(const gdn_conv_params_t* p, int packed) {
@@ -303,7 +305,7 @@ gdn_status_t gdn_conv_bwd(const gdn_conv_params_t* p, const void* x, const uint8
   pl.geo.cu = cu_seqlens;
   const ConvBwdArgs a{x, x_scales, weight, bias, initial_state, d_y, d_final_state,
                       dx, dweight, dbias, d_initial_state};
-  return conv_dispatch<BwdRun, 1>(p, vec, pl, a, workspace, static_cast<hipStream_t>(stream));
+  return conv_dispatch<BwdRun, 1>(pl, p->W, vec, a, workspace, static_cast<hipStream_t>(stream));
 }
 
 gdn_status_t gdn_pack8(const void* x, gdn_dtype_t dtype, int64_t rows, int32_t C, int64_t x_stride,

@@ -183,6 +183,7 @@ template <bool UNIFORM> __device__ __forceinline__ int uniform(int v) {
 // wave walk the same tile.
 template <bool UNIFORM> struct Run {
   int n, N, T, start, end, ta, tb, t1;
+  int rest;  // once done: the tile's first token behind the last sequence, or t1
   const int64_t* cu;
 
   __device__ __forceinline__ void init(const int64_t* cu_, int T_, int N_, int tile, int ntiles, int len) {
@@ -196,13 +197,13 @@ template <bool UNIFORM> struct Run {
     N = N_;
     if (cu) {
       ta = tile * len;
-      t1 = min(ta + len, T);
+      t1 = rest = min(ta + len, T);
     } else {
       n = tile / ntiles;
       start = n * T;
       end = start + T;
       ta = start + (tile - n * ntiles) * len;
-      t1 = tb = min(ta + len, end);
+      t1 = rest = tb = min(ta + len, end);
     }
   }
   __device__ __forceinline__ void locate() {
@@ -232,6 +233,7 @@ template <bool UNIFORM> struct Run {
         return;
       }
     }
+    rest = ta;
     ta = tb = t1;
   }
 };

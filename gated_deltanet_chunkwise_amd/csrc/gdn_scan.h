@@ -32,6 +32,7 @@ struct ScanGeo {
   int len, ntiles;       // tokens per tile; tiles per row of the batch
   int nw, np;            // waves per 64 channels; nw * NS
   int upw, cgb;          // units of nw waves per workgroup, workgroups for all channels
+  int zero;              // forward: y's rows behind the last sequence are set to 0
   const int64_t* cu;
   int64_t lddt;
   int64_t ldb, ldc;      // elements between rows of Bm and Cm, and between groups
@@ -401,7 +402,10 @@ __global__ __launch_bounds__(64 * kScanMaxWaves) void gdn_scan_kernel(
     if constexpr (!ENDS)
       if (fin && w.on && run.tb == run.end) state_store<NS, WHOLE>(fin, g, run.n, w.d, w.n0, h);
   }
-  if constexpr (ENDS) {
+  if constexpr (!ENDS) {
+    if (g.zero && w.wave == 0)
+      for (int t = run.rest; t < run.t1; ++t) store1<E>((Global<E>)y + (int64_t)t * g.D, off, 0.f);
+  } else {
     if (!w.on) return;
     tile_state_store<NS>(states, g, w, h);
     if (w.wave == 0) sums[(int64_t)w.tile * g.D + w.d] = sum;

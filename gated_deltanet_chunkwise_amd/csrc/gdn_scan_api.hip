@@ -184,7 +184,7 @@ gdn_status_t gdn_scan_decode(const gdn_scan_params_t* p, const void* x, const vo
                   gdn::Src{z, nullptr, pl.ldz}, A_log, static_cast<const E*>(Bm), static_cast<const E*>(Cm),
                   skip, dt_bias, state, new_state, static_cast<E*>(y), nl);
   };
-  return (p->dtype == GDN_BF16 ? go(gdn::bf16{}) : go(0.f)) == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+  return (pl.esz == 2 ? go(gdn::bf16{}) : go(0.f)) == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
 }  // extern "C"

@@ -16,7 +16,8 @@ struct ScanPlan {
 // Sizes only.
 inline gdn_status_t scan_sizes(const gdn_scan_params_t* p, bool packed, ScanPlan* out) {
   if (!p) return GDN_ERR_NULL;
-  if (p->dtype != GDN_F32 && p->dtype != GDN_BF16) return GDN_ERR_DTYPE;
+  const int32_t dtype = p->dtype & ~GDN_ZERO_REST;
+  if (dtype != GDN_F32 && dtype != GDN_BF16) return GDN_ERR_DTYPE;
   if (p->D <= 0 || p->G <= 0 || p->N <= 0 || p->D % p->G) return GDN_ERR_SHAPE;
   gdn_status_t st = check_batch(p->B, p->T, p->num_seqs, packed);
   if (st != GDN_OK) return st;
@@ -32,7 +33,7 @@ inline gdn_status_t scan_sizes(const gdn_scan_params_t* p, bool packed, ScanPlan
     return GDN_ERR_SHAPE;
   ScanPlan pl{};
   pl.packed = packed;
-  pl.esz = p->dtype == GDN_BF16 ? 2 : 4;
+  pl.esz = dtype == GDN_BF16 ? 2 : 4;
   pl.tok = (int64_t)p->B * p->T;
   pl.ldx = p->x_stride ? p->x_stride : p->D;
   pl.ldz = p->z_stride ? p->z_stride : p->D;
@@ -40,6 +41,7 @@ inline gdn_status_t scan_sizes(const gdn_scan_params_t* p, bool packed, ScanPlan
   g.B = p->B; g.T = p->T; g.D = p->D; g.G = p->G; g.N = p->N;
   g.S = packed ? p->num_seqs : p->B;
   g.DG = p->D / p->G;
+  g.zero = packed && (p->dtype & GDN_ZERO_REST);
   g.wpg = (int)ceil_div(g.DG, 64);
   g.cgroups = g.G * g.wpg;
   g.lddt = p->dt_stride ? p->dt_stride : p->D;

@@ -434,7 +434,8 @@ gdn_status_t gdn_kda_gate(const void *g, gdn_dtype_t g_dtype, const float *A_log
  *   weight       [C][W] fp32; bias [C] fp32 or NULL (0)
  *   cu_seqlens   [N+1] int64 or NULL, as for gdn_fwd, except that it may end before T:
  *                rows of y behind the last sequence are left as they were, rows of dx
- *                are set to 0
+ *                are set to 0.  With GDN_ZERO_REST added to dtype rows of y are set to 0
+ *                there as well
  *   initial_state, final_state  [N][W-1][C], dtype, oldest row first, or NULL
  *   y            [B][T][C] contiguous, dtype, written
  * Sums are fp32, rounded once.  dtype: GDN_F32 or GDN_BF16.  Alignment: element
@@ -444,6 +445,8 @@ gdn_status_t gdn_kda_gate(const void *g, gdn_dtype_t g_dtype, const float *A_log
  * take 2^32 threads or more in one launch.  Outputs must not
  * overlap inputs or each other (gdn_conv_decode: new_state may be state).
  * Enqueued on `stream`; nothing is allocated. */
+#define GDN_ZERO_REST 0x100 /* added to a params' dtype; of no effect but on y's rows */
+
 typedef struct {
   int32_t B, T, C, W;
   int32_t num_seqs;   /* N with cu_seqlens; ignored (N = B) without */

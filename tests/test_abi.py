@@ -547,3 +547,12 @@ def test_scan_sizes_beyond_64_bits():
     assert scan_fwd(p) == EUNSUP and scan_bwd(p) == EUNSUP and scan_decode(p) == EUNSUP
     for f in ("gdn_scan_fwd_workspace_size", "gdn_scan_bwd_workspace_size"):
         assert getattr(gdn.load_library(), f)(ctypes.byref(p), 0) == 0
+
+
+@pytest.mark.parametrize("call,P_", [(conv_fwd, CP), (conv_bwd, CP), (conv_decode, CP), (scan_fwd, SP), (scan_bwd, SP),
+                                     (scan_decode, SP)])
+def test_zero_rest_is_a_bit_of_the_dtype(call, P_):
+    for code in (gdn.GDN_F32, gdn.GDN_BF16):
+        assert call(P_(dtype=code | 0x100), x=0x100001) == EALIGN  # a later check answers
+    for code in (gdn.GDN_F16 | 0x100, 7 | 0x100, gdn.GDN_BF16 | 0x200):
+        assert call(P_(dtype=code)) == EDTYPE

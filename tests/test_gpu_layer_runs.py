@@ -319,3 +319,30 @@ def test_two_calls_at_once():
         got = [work(c, s) for c, s in zip(cases, streams)]
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for x, y in zip(got, ref) for a, b in zip(x, y))
+
+
+# ---- offsets that end before the batch does --------------------------------------------
+
+@pytest.mark.parametrize("dtype,T,D,N,lengths", [
+    (BF16, 50, 64, 16, [20, 13]), (F32, 50, 66, 40, [20, 13, 0]), (BF16, 300, 330, 20, [0, 130, 1]), (F32, 90, 24, 8, [0, 0]),
+    (BF16, 700, 1056, 16, [63])])
+def test_rows_behind_the_last_sequence_are_zero(dtype, T, D, N, lengths):
+    """What the operators return there does not depend on what the memory held, so that a
+    loss may mask those rows by a product."""
+    d, _ = lo.scan_inputs(1, T, D, N, 1, dtype, 15, len(lengths))
+    c, _ = lo.conv_inputs(1, T, D, 4, dtype, 16, len(lengths))
+    cu, used = lo.offsets(lengths), sum(lengths)
+    g, gc, gcu = lo.cuda(d), lo.cuda(c), cu.cuda()
+    o = dict(skip=g["skip"], z=g["z"], dt_bias=g["dt_bias"], cu_seqlens=gcu, initial_state=g["h0"])
+    y_ref, _ = lo.scan(cu=cu, **lo.double(d))
+    c_ref, _ = lo.conv(cu=cu, **lo.double(c))
+    for call, ref, steps in (
+            (lambda: gdn.conv_fwd(gc["x"], gc["weight"], gc["bias"], gcu, gc["h0"]), c_ref, 4),
+            (lambda: gdn.causal_conv(gc["x"], gc["weight"], gc["bias"], gcu, gc["h0"]), c_ref, 4),
+            (lambda: gdn.scan_fwd(g["x"], g["dt"], g["A_log"], g["Bm"], g["Cm"], **o), y_ref, T),
+            (lambda: gdn.selective_scan(g["x"], g["dt"], g["A_log"], g["Bm"], g["Cm"], **o), y_ref, T)):
+        junk = torch.full_like(g["x"], float("nan"))
+        del junk  # its memory is the next to be given out for a tensor of this size
+        y, _ = call()
+        assert (y[0, used:] == 0).all()
+        lo.close(y, ref, steps, "y")
