@@ -628,10 +628,10 @@ def gated_delta_rule(q, k, v, g_raw, beta, A_log, dt_bias=None, cu_seqlens=None,
     as for fwd(): contiguous GPU tensors of the documented shapes and dtypes.
     checkpoint_bits=8 keeps q, k and v for the backward pass as 8-bit checkpoints (pack8):
     the gradients are then those at the values the checkpoints stand for."""
-    from ._layers import check_bits
-    check_bits(checkpoint_bits)
+    from ._layers import kept_bits
+    bits = kept_bits(checkpoint_bits, q, k, v, g_raw, beta, A_log, dt_bias, initial_state)
     return _gated_delta_rule_fn().apply(q, k, v, g_raw, beta, A_log, dt_bias, cu_seqlens,
-                                        initial_state, scale, checkpoint_bits)
+                                        initial_state, scale, bits)
 
 
 def bwd(q, k, v, g_raw, beta, A_log, dt_bias, d_o, d_final_state=None, cu_seqlens=None,

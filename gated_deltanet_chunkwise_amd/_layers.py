@@ -545,9 +545,15 @@ def scan_decode(x, dt, A_log, Bm, Cm, state, skip=None, z=None, dt_bias=None, ne
 # ---------------------------------------------------------------------------
 # differentiable forms
 
-def check_bits(bits):
+def kept_bits(bits, *inputs):
+    """checkpoint_bits, checked; None where no backward pass can follow, so that nothing is
+    packed for one (a Function's forward cannot tell: gradients are off within it)."""
     if bits not in (None, 8):
         raise ValueError("checkpoint_bits must be None or 8, got %r" % (bits,))
+    if bits is None:
+        return None
+    follows = _torch().is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs)
+    return bits if follows else None
 
 
 def keep(t, bits):
@@ -604,8 +610,8 @@ def causal_conv(x, weight, bias=None, cu_seqlens=None, initial_state=None, activ
     x, weight, bias and initial_state through gdn_conv_bwd.  checkpoint_bits=8 keeps x
     for the backward pass as an 8-bit checkpoint: the gradients are then those at the
     values it stands for."""
-    check_bits(checkpoint_bits)
-    return _conv_function().apply(x, weight, bias, cu_seqlens, initial_state, activation, checkpoint_bits)
+    bits = kept_bits(checkpoint_bits, x, weight, bias, initial_state)
+    return _conv_function().apply(x, weight, bias, cu_seqlens, initial_state, activation, bits)
 
 
 def _scan_function():
@@ -647,6 +653,5 @@ def selective_scan(x, dt, A_log, Bm, Cm, skip=None, z=None, dt_bias=None, cu_seq
     forms the states again.  checkpoint_bits=8 keeps x and z as 8-bit checkpoints (dt, of
     which the decays depend exponentially, and the small Bm and Cm stay as they are): the
     gradients are then those at the values the checkpoints stand for."""
-    check_bits(checkpoint_bits)
-    return _scan_function().apply(x, dt, A_log, Bm, Cm, skip, z, dt_bias, cu_seqlens, initial_state,
-                                  checkpoint_bits)
+    bits = kept_bits(checkpoint_bits, x, dt, A_log, Bm, Cm, skip, z, dt_bias, initial_state)
+    return _scan_function().apply(x, dt, A_log, Bm, Cm, skip, z, dt_bias, cu_seqlens, initial_state, bits)

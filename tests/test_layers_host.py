@@ -162,6 +162,31 @@ def test_rows_that_are_not_evenly_spaced(t):
         _layers._row_stride("t", t)
 
 
+@pytest.mark.parametrize("grad", [True, False])
+@pytest.mark.parametrize("wanted", ["nothing", "a weight", "x"])
+def test_checkpoints_are_formed_only_for_a_backward_pass(monkeypatch, grad, wanted):
+    packs = []
+    monkeypatch.setattr(_layers, "pack8", lambda t: packs.append(t.shape) or packed(*t.shape, dtype=t.dtype))
+    monkeypatch.setattr(_layers, "conv_fwd", lambda x, *a: (x.clone(), x.clone()))
+    monkeypatch.setattr(_layers, "scan_fwd", lambda x, *a: (x.clone(), x.clone()))
+    monkeypatch.setattr(_binding, "fwd", lambda q, k, v, *a, **kw: (v.clone(), v.clone()))
+    d, c = scan_case(), conv_case()
+    d["A_log"].requires_grad_(wanted == "a weight")
+    c["weight"].requires_grad_(wanted == "a weight")
+    for t in (d["x"], c["x"]):
+        t.requires_grad_(wanted == "x")
+    q = torch.zeros(1, 5, 2, 64, requires_grad=wanted == "x")
+    w = torch.zeros(2, requires_grad=wanted == "a weight")
+    g = torch.zeros(1, 5, 2)
+    with torch.set_grad_enabled(grad):
+        outs = (gdn.causal_conv(c["x"], c["weight"], checkpoint_bits=8),
+                gdn.selective_scan(d["x"], d["dt"], d["A_log"], d["Bm"], d["Cm"], z=d["z"], checkpoint_bits=8),
+                gdn.gated_delta_rule(q, q, q, g, g, w, checkpoint_bits=8))
+    follows = grad and wanted != "nothing"
+    assert all(t.requires_grad == follows for o in outs for t in o)
+    assert len(packs) == (6 if follows else 0)  # x; x and z; q, k and v
+
+
 # ---- the forms the GPU tests compare with ----------------------------------------
 
 @pytest.mark.parametrize("lengths", [None, [0, 4, 1, 0, 5]])
