@@ -98,10 +98,9 @@ def _fit(specs):
             _check_tensor(name, t, shape, dtype)
 
 
-def _need(**tensors):
-    for name, t in tensors.items():
-        if t is None:
-            raise ValueError("%s is required" % name)
+def _need(name, t):
+    if t is None:
+        raise ValueError("%s is required" % name)
 
 
 def _place(x, rows, dense):
@@ -174,6 +173,19 @@ def _call(name, *args):
 
 def _p(t):
     return None if t is None else t.data_ptr()
+
+
+_WRITTEN = None
+
+
+def _written(tensors):
+    """Tells autograd that the call has written to these tensors of the caller's (a tuple),
+    as torch's in-place operations do: a backward pass that saved one of them then refuses it."""
+    global _WRITTEN
+    if _WRITTEN is None:
+        torch = _torch()
+        _WRITTEN = getattr(torch._C, "_increment_version", torch.autograd.graph.increment_version)
+    _WRITTEN(tensors)
 
 
 _LIKE = None
@@ -268,6 +280,8 @@ def unpack8(packed, out=None, stream=None):
         C = codes.shape[-1]
         _lib()
         _call("gdn_unpack8", codes.data_ptr(), scales.data_ptr(), codes.numel() // C, C, y.data_ptr(), code, s)
+        if out is not None:
+            _written((out,))
         return y
     return _on(index, stream, (codes, scales, out), body)
 
@@ -330,7 +344,7 @@ def conv_bwd(x, weight, bias, d_y, d_final_state=None, cu_seqlens=None, initial_
     in x's dtype, dweight [C,W] and dbias [C] fp32.  x may be its checkpoint (Packed8)."""
     data, scales, dtype = _maybe_packed("x", x)
     p, B, T, C, W, N = _conv_sizes(data, dtype, weight, bias, cu_seqlens, activation)
-    _need(d_y=d_y)
+    _need("d_y", d_y)
     _fit((("d_y", d_y, (B, T, C), dtype), ("d_final_state", d_final_state, (N, W - 1, C), dtype),
           ("initial_state", initial_state, (N, W - 1, C), dtype)))
     index = _place(data, (), (("weight", weight), ("bias", bias), ("cu_seqlens", cu_seqlens),
@@ -354,7 +368,7 @@ def conv_bwd(x, weight, bias, d_y, d_final_state=None, cu_seqlens=None, initial_
 
 def _conv_decode_args(x, weight, state, bias, activation, new_state, out):
     p, B, T, C, W, _ = _conv_sizes(x, x.dtype, weight, bias, None, activation)
-    _need(state=state)
+    _need("state", state)
     shape = (B, W - 1, C)
     _fit((("state", state, shape, x.dtype), ("new_state", new_state, shape, x.dtype), ("out", out, (B, T, C), x.dtype)))
     index = _place(x, (), (("weight", weight), ("bias", bias), ("state", state), ("new_state", new_state), ("out", out)))
@@ -363,7 +377,8 @@ def _conv_decode_args(x, weight, state, bias, activation, new_state, out):
         y = _like(x) if out is None else out
         new = state if new_state is None else new_state
         _lib()
-        return (p, x.data_ptr(), weight.data_ptr(), _p(bias), state.data_ptr(), new.data_ptr(), y.data_ptr(), s), y
+        return ((p, x.data_ptr(), weight.data_ptr(), _p(bias), state.data_ptr(), new.data_ptr(), y.data_ptr(), s), y,
+                (new,) if out is None else (new, out))
     return index, args
 
 
@@ -373,11 +388,11 @@ def conv_decode_launcher(x, weight, state, bias=None, activation="silu", new_sta
     the state after them to new_state (default: `state` itself)."""
     index, args = _conv_decode_args(x, weight, state, bias, activation, new_state, out)
     keep = (x, weight, state, bias, new_state, out, stream)
-    args, y = _on(index, stream, keep[:-1], args)
-    return _launcher("gdn_conv_decode", index, args, keep + (y,)), y
+    args, y, written = _on(index, stream, keep[:-1], args)
+    return _launcher("gdn_conv_decode", index, args, keep + (y,), written), y
 
 
-def _launcher(name, index, args, keep):
+def _launcher(name, index, args, keep, written):
     torch = _torch()
     fn = getattr(_lib(), name)
 
@@ -390,6 +405,7 @@ def _launcher(name, index, args, keep):
                 st = fn(*args)
         if st:
             raise GdnError(st, name)
+        _written(written)
     return launch
 
 
@@ -399,8 +415,9 @@ def conv_decode(x, weight, state, bias=None, activation="silu", new_state=None, 
     index, args = _conv_decode_args(x, weight, state, bias, activation, new_state, out)
 
     def body(s):
-        a, y = args(s)
+        a, y, written = args(s)
         _call("gdn_conv_decode", *a)
+        _written(written)
         return y
     return _on(index, stream, (x, weight, state, bias, new_state, out), body)
 
@@ -472,7 +489,7 @@ def scan_bwd(x, dt, A_log, Bm, Cm, d_y, d_final_state=None, skip=None, z=None, d
     if z is not None and (xs is None) != (zs is None):
         raise ValueError("x and z must both be checkpoints, or neither")
     p, B, T, D, G, N, S = _scan_sizes(xd, dtype, dt, A_log, Bm, Cm, skip, zd, z_dtype, dt_bias, cu_seqlens)
-    _need(d_y=d_y)
+    _need("d_y", d_y)
     _fit((("d_y", d_y, (B, T, D), dtype), ("d_final_state", d_final_state, (S, D, N), f32),
           ("initial_state", initial_state, (S, D, N), f32)))
     index = _place(xd, (("dt", dt), ("Bm", Bm), ("Cm", Cm), ("z", zd)),
@@ -503,7 +520,7 @@ def _scan_decode_args(x, dt, A_log, Bm, Cm, state, skip, z, dt_bias, new_state, 
     f32 = _torch().float32
     p, B, T, D, G, N, _ = _scan_sizes(x, x.dtype, dt, A_log, Bm, Cm, skip, z, None if z is None else z.dtype,
                                       dt_bias, None)
-    _need(state=state)
+    _need("state", state)
     _fit((("state", state, (B, D, N), f32), ("new_state", new_state, (B, D, N), f32), ("out", out, (B, T, D), x.dtype)))
     index = _place(x, (("dt", dt), ("Bm", Bm), ("Cm", Cm), ("z", z)),
                    (("A_log", A_log), ("skip", skip), ("dt_bias", dt_bias), ("state", state), ("new_state", new_state),
@@ -514,7 +531,8 @@ def _scan_decode_args(x, dt, A_log, Bm, Cm, state, skip, z, dt_bias, new_state, 
         new = state if new_state is None else new_state
         _lib()
         return (p, x.data_ptr(), dt.data_ptr(), A_log.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), _p(skip), _p(z),
-                _p(dt_bias), state.data_ptr(), new.data_ptr(), y.data_ptr(), s), y
+                _p(dt_bias), state.data_ptr(), new.data_ptr(), y.data_ptr(), s), y, (
+                    (new,) if out is None else (new, out))
     return index, args
 
 
@@ -525,8 +543,8 @@ def scan_decode_launcher(x, dt, A_log, Bm, Cm, state, skip=None, z=None, dt_bias
     after them to new_state (default: `state` itself)."""
     index, args = _scan_decode_args(x, dt, A_log, Bm, Cm, state, skip, z, dt_bias, new_state, out)
     keep = (x, dt, A_log, Bm, Cm, state, skip, z, dt_bias, new_state, out, stream)
-    args, y = _on(index, stream, keep[:-1], args)
-    return _launcher("gdn_scan_decode", index, args, keep + (y,)), y
+    args, y, written = _on(index, stream, keep[:-1], args)
+    return _launcher("gdn_scan_decode", index, args, keep + (y,), written), y
 
 
 def scan_decode(x, dt, A_log, Bm, Cm, state, skip=None, z=None, dt_bias=None, new_state=None, out=None,
@@ -536,8 +554,9 @@ def scan_decode(x, dt, A_log, Bm, Cm, state, skip=None, z=None, dt_bias=None, ne
     index, args = _scan_decode_args(x, dt, A_log, Bm, Cm, state, skip, z, dt_bias, new_state, out)
 
     def body(s):
-        a, y = args(s)
+        a, y, written = args(s)
         _call("gdn_scan_decode", *a)
+        _written(written)
         return y
     return _on(index, stream, (x, dt, A_log, Bm, Cm, state, skip, z, dt_bias, new_state, out), body)
 

@@ -346,3 +346,38 @@ def test_rows_behind_the_last_sequence_are_zero(dtype, T, D, N, lengths):
         y, _ = call()
         assert (y[0, used:] == 0).all()
         lo.close(y, ref, steps, "y")
+
+
+# ---- states updated in place ---------------------------------------------------------
+
+@pytest.mark.parametrize("launcher", [False, True])
+def test_a_state_updated_in_place_is_not_taken_for_the_saved_one(launcher):
+    """A backward pass that needs the initial state refuses one that a decode step has
+    overwritten, as torch's own in-place operations have it."""
+    d, _ = lo.scan_inputs(2, 9, 64, 16, 1, F32, 17)
+    c, _ = lo.conv_inputs(2, 9, 64, 4, F32, 18)
+    g, gc = lo.cuda(d), lo.cuda(c)
+    w, a = gc["weight"].requires_grad_(), g["A_log"].requires_grad_()
+    for state, out, step in (
+            (gc["h0"], lambda s: gdn.causal_conv(gc["x"], w, initial_state=s),
+             lambda f, s, **k: f(gc["x"][:, :1], gc["weight"].detach(), s, **k)),
+            (g["h0"], lambda s: gdn.selective_scan(g["x"], g["dt"], a, g["Bm"], g["Cm"], initial_state=s),
+             lambda f, s, **k: f(*(g[n][:, :1] for n in ("x", "dt")), a.detach(), *(g[n][:, :1] for n in ("Bm", "Cm")), s, **k))):
+        conv = state is gc["h0"]
+
+        def decode(s, **k):
+            if launcher:
+                step(gdn.conv_decode_launcher if conv else gdn.scan_decode_launcher, s, **k)[0]()
+            else:
+                step(gdn.conv_decode if conv else gdn.scan_decode, s, **k)
+        y, _ = out(state)
+        decode(state, new_state=torch.empty_like(state))  # elsewhere: nothing that is saved changes
+        y.sum().backward()
+        y, _ = out(state)
+        decode(state)
+        with pytest.raises(RuntimeError, match="inplace"):
+            y.sum().backward()
+        y, _ = out(state)
+        decode(state.clone(), new_state=state)
+        with pytest.raises(RuntimeError, match="inplace"):
+            y.sum().backward()
