@@ -385,7 +385,9 @@ def _conv_decode_args(x, weight, state, bias, activation, new_state, out):
 def conv_decode_launcher(x, weight, state, bias=None, activation="silu", new_state=None, out=None, stream=None):
     """Check and marshal gdn_conv_decode's arguments once; returns (launch, y), where
     launch() enqueues the convolution of x's T tokens after `state` [B,W-1,C], writing
-    the state after them to new_state (default: `state` itself)."""
+    the state after them to new_state (default: `state` itself).  Every launch() goes to
+    `stream`, or to the stream that was current when the launcher was made, whichever is
+    current later: a launcher for a graph is made on the stream that captures it."""
     index, args = _conv_decode_args(x, weight, state, bias, activation, new_state, out)
     keep = (x, weight, state, bias, new_state, out, stream)
     args, y, written = _on(index, stream, keep[:-1], args)
@@ -540,7 +542,8 @@ def scan_decode_launcher(x, dt, A_log, Bm, Cm, state, skip=None, z=None, dt_bias
                          stream=None):
     """Check and marshal gdn_scan_decode's arguments once; returns (launch, y), where
     launch() enqueues the scan of x's T tokens after `state` [B,D,N], writing the state
-    after them to new_state (default: `state` itself)."""
+    after them to new_state (default: `state` itself).  The stream is as for
+    conv_decode_launcher."""
     index, args = _scan_decode_args(x, dt, A_log, Bm, Cm, state, skip, z, dt_bias, new_state, out)
     keep = (x, dt, A_log, Bm, Cm, state, skip, z, dt_bias, new_state, out, stream)
     args, y, written = _on(index, stream, keep[:-1], args)

@@ -381,3 +381,71 @@ def test_a_state_updated_in_place_is_not_taken_for_the_saved_one(launcher):
         decode(state.clone(), new_state=state)
         with pytest.raises(RuntimeError, match="inplace"):
             y.sum().backward()
+
+
+# ---- decode launchers ------------------------------------------------------------------
+
+def decode_step(kind, dtype, Bn, T_, seed):
+    """(call on a state and its options, the same through the launcher, the state's inputs,
+    the token tensors)."""
+    if kind == "conv":
+        d, _ = lo.conv_inputs(Bn, T_, 72, 4, dtype, seed)
+        g = lo.cuda(d)
+        call = lambda f, state, **k: f(g["x"], g["weight"], state, g["bias"], **k)  # noqa: E731
+        return call, gdn.conv_decode, gdn.conv_decode_launcher, g["h0"], g["x"]
+    d, _ = lo.scan_inputs(Bn, T_, 66, 13, 1, dtype, seed)
+    g = lo.cuda(d)
+    call = lambda f, state, **k: f(g["x"], g["dt"], g["A_log"], g["Bm"], g["Cm"], state, g["skip"], g["z"],  # noqa: E731
+                                   g["dt_bias"], **k)
+    return call, gdn.scan_decode, gdn.scan_decode_launcher, g["h0"], g["x"]
+
+
+@pytest.mark.parametrize("kind", ["conv", "scan"])
+@pytest.mark.parametrize("dtype,Bn,T_", [(BF16, 3, 1), (F32, 2, 2)])
+def test_launchers(kind, dtype, Bn, T_):
+    """Repeated launches in place, into other tensors, and on a stream of its own, against
+    the plain calls bit for bit."""
+    call, plain, launcher, h0, x = decode_step(kind, dtype, Bn, T_, 19)
+    ref, state = h0.clone(), h0.clone()
+    launch, y = call(launcher, state)
+    for i in range(3):
+        launch()
+        assert torch.equal(y, call(plain, ref)) and torch.equal(state, ref), i
+        x.mul_(-0.5)  # the launcher reads the tensors as they are
+    new, out = torch.empty_like(h0), torch.empty_like(x)
+    launch, y = call(launcher, h0, new_state=new, out=out)
+    assert y is out
+    for i in range(2):  # the same result again: `state` is not written
+        new.fill_(float("nan"))
+        launch()
+        ref.copy_(h0)
+        assert torch.equal(out, call(plain, ref)) and torch.equal(new, ref), i
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    launch, y = call(launcher, h0, new_state=new, stream=side)
+    launch()
+    side.synchronize()
+    assert torch.equal(y, call(plain, ref.copy_(h0))) and torch.equal(new, ref)
+
+
+@pytest.mark.parametrize("kind", ["conv", "scan"])
+def test_a_captured_launcher_replays(kind):
+    call, plain, launcher, h0, x = decode_step(kind, BF16, 2, 1, 20)
+    cap = torch.cuda.Stream()
+    cap.wait_stream(torch.cuda.current_stream())
+    state, ref = h0.clone(), h0.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(cap):
+        launch, y = call(launcher, state)
+        launch()
+    cap.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=cap):
+        launch()
+    state.copy_(h0)
+    for i in range(4):
+        x.mul_(-0.5)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, call(plain, ref)) and torch.equal(state, ref), i
