@@ -449,3 +449,60 @@ def test_a_captured_launcher_replays(kind):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, call(plain, ref)) and torch.equal(state, ref), i
+
+
+# ---- ill-formed offsets, every value ----------------------------------------------------
+
+@pytest.mark.parametrize("T", [12, 29, 100, 333])
+@pytest.mark.parametrize("dtype,D,N", [(F32, 64, 16), (BF16, 66, 40)])
+def test_a_sequence_that_begins_too_early_starts_where_the_one_ahead_ended(T, dtype, D, N):
+    """Offsets [0, 5, 3, T] are taken as [0, 5), nothing, [5, T) from the third state: all
+    the scan computes, and the convolution but for the last sequence's d_initial, as for
+    those; nothing outside the outputs and the workspace is written, and what the
+    workspace held (NaN) is not read."""
+    bad, good = torch.tensor([0, 5, 3, T], dtype=torch.int64), torch.tensor([0, 5, 5, T], dtype=torch.int64)
+    code, lib, new = (gdn.GDN_BF16 if dtype == BF16 else gdn.GDN_F32), gdn.load_library(), Banded()
+    out = lambda *s, dtype=dtype: new(s, dtype)  # noqa: E731
+
+    def space(size, p):
+        nb = size(ctypes.byref(p), 1)
+        return new((nb,), torch.uint8).fill_(0xFF), nb
+    cu = bad.cuda()
+    d, seeds = lo.scan_inputs(1, T, D, N, 1, dtype, 11, 3)
+    g, s = lo.cuda(d), lo.cuda(seeds)
+    r = lo.double(d)
+    p = ScanParams(1, T, D, 1, N, 3, code, 0, 0, 0, 0, 0)
+    y, fin = out(1, T, D), out(3, D, N, dtype=F32)
+    ws, nb = space(lib.gdn_scan_fwd_workspace_size, p)
+    ins = [P(g[n]) for n in ("x", "dt", "A_log", "Bm", "Cm", "skip", "z", "dt_bias")] + [P(cu), P(g["h0"])]
+    run("gdn_scan_fwd", ctypes.byref(p), *ins, P(y), P(fin), P(ws), nb)
+    y_ref, fin_ref = lo.scan(cu=good, **r)
+    lo.close(y, y_ref, T, "y")
+    lo.close(fin, fin_ref, T, "final")
+    ws, nb = space(lib.gdn_scan_bwd_workspace_size, p)
+    o = dict(x=out(1, T, D), dt=out(1, T, D), A_log=out(D, N, dtype=F32), Bm=out(1, T, 1, N), Cm=out(1, T, 1, N),
+             skip=out(D, dtype=F32), z=out(1, T, D), dt_bias=out(D, dtype=F32), h0=out(3, D, N, dtype=F32))
+    run("gdn_scan_bwd", ctypes.byref(p), ins[0], None, *ins[1:7], None, *ins[7:], P(s["d_y"]), P(s["d_fin"]),
+        *(P(t) for t in o.values()), P(ws), nb)
+    ref = lo.gradients(lambda **k: lo.scan(cu=good, **k), r, [t.double() for t in seeds.values()])
+    for n, t in o.items():
+        lo.close(t, ref[n], 2 * T + D, "d" + n)
+
+    c, cs = lo.conv_inputs(1, T, D, 4, dtype, 12, 3)
+    g, s, r = lo.cuda(c), lo.cuda(cs), lo.double(c)
+    p = ConvParams(1, T, D, 4, 3, code, 1, 0)
+    y, fin = out(1, T, D), out(3, 3, D)
+    run("gdn_conv_fwd", ctypes.byref(p), P(g["x"]), P(g["weight"]), P(g["bias"]), P(cu), P(g["h0"]), P(y), P(fin))
+    y_ref, fin_ref = lo.conv(cu=good, **r)
+    lo.close(y, y_ref, 4, "conv y")
+    assert torch.equal(fin.cpu().double(), fin_ref)
+    ws, nb = space(lib.gdn_conv_bwd_workspace_size, p)
+    o = dict(x=out(1, T, D), weight=out(D, 4, dtype=F32), bias=out(D, dtype=F32), h0=out(3, 3, D))
+    run("gdn_conv_bwd", ctypes.byref(p), P(g["x"]), None, P(g["weight"]), P(g["bias"]), P(cu), P(g["h0"]), P(s["d_y"]),
+        P(s["d_fin"]), *(P(t) for t in o.values()), P(ws), nb)
+    ref = lo.gradients(lambda **k: lo.conv(cu=good, **k), r, [t.double() for t in cs.values()])
+    for n, t in o.items():
+        if n == "h0":
+            t, ref[n] = t[:2], ref[n][:2]
+        lo.close(t, ref[n], T, "conv d" + n)
+    assert new.untouched()
