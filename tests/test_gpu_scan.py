@@ -105,6 +105,43 @@ def test_more_rows_of_bm_and_cm_than_one_grid_sums():
     check_backward((1, 2100, 64, 64, 64, F32, None, ALL))
 
 
+def forward_workspace(case, length):
+    """gdn_scan_fwd_workspace_size() of a case cut into tiles of `length` tokens."""
+    B, T, D, N, G = case[:5]
+    up = lambda b: -(-b // 256) * 256  # noqa: E731
+    np_ = 8 if N <= 8 else 16 * -(-N // 16)
+    tiles = -(-T // length) * (1 if case[6] is not None else B)
+    return up(up(tiles * np_ * D * 4) + tiles * D * 4) + 2 * up(B * T * G * np_ * 4)
+
+
+@pytest.mark.parametrize("case,length", [
+    ((2, 1030, 2048, 16, 1, BF16, None, ALL), 32),
+    ((1, 18500, 2048, 16, 1, BF16, [9000, 0, 77, 9423], ALL), 80),          # rows sent for twice per tile
+    ((1, 17001, 2040, 13, 1, F32, [1, 16900, 100], dict(ALL, gate=False)), 72),
+    ((1, 2201, 4096, 32, 1, F32, [2100, 101], ALL), 40),                     # two waves per channel, five groups
+    ((2, 901, 4100, 40, 2, BF16, None, ALL), 48),                            # three waves, six groups
+    ((1, 9000, 4096, 20, 2, BF16, [5000, 3900], ALL), 144)], ids=lambda v: str(v) if isinstance(v, int) else "%dx%dx%d-n%d" % v[:4])
+def test_long_tiles(case, length):
+    """The tiles of large problems, checked on 64 channels of each group (channels do not
+    see each other); the workspace tells their length."""
+    from gated_deltanet_chunkwise_amd._layers import ScanParams
+    B, T, D, N, G, dtype, lengths, _ = case
+    p = ScanParams(B, T, D, G, N, 0 if lengths is None else len(lengths), 0 if dtype == F32 else 1, 0, 0, 0, 0, 0)
+    nb = gdn.load_library().gdn_scan_fwd_workspace_size(ctypes.byref(p), int(lengths is not None))
+    assert nb == forward_workspace(case, length), "another tile length than this case is for"
+    d, _, cu, used = make(case)
+    pick = torch.cat([torch.randperm(D // G, generator=torch.Generator().manual_seed(g))[:64].sort()[0] + g * (D // G)
+                      for g in range(G)])
+    part = {k: v if v is None or k in ("Bm", "Cm") else v[pick] if k in ("A_log", "skip", "dt_bias") else
+            v[:, pick] if k == "h0" else v[..., pick] for k, v in d.items()}
+    y_ref, fin_ref = lo.scan(cu=cu, **lo.double(part))
+    y, fin = fwd(lo.cuda(d), cu)
+    steps = T if lengths is None else max(lengths)
+    lo.close(y[..., pick.cuda()].view(-1, len(pick))[:used], y_ref.view(-1, len(pick))[:used], steps, "y")
+    lo.close(fin[:, pick.cuda()], fin_ref, steps, "final state")
+    assert y.isfinite().all() and fin.isfinite().all()
+
+
 def test_extreme_decays_and_time_steps():
     """States that vanish within a token (A D of about -400, also across whole tiles), that
     never decay (A about -1e-9), and D beyond softplus's threshold and below 1e-9."""
@@ -210,6 +247,29 @@ def test_backward_from_checkpoints(dtype, D):
     a = bwd(g, s, None, px, pz)
     b = bwd(dict(g, x=gdn.unpack8(px), z=gdn.unpack8(pz)), s, None)
     assert all(torch.equal(a[k], b[k]) for k in a), "the checkpoints' values, read in place"
+
+
+@pytest.mark.parametrize("case", [
+    (1, 300, 70, 16, 1, BF16, [1, 0, 63, 64, 2, 130, 0, 40], ALL),
+    (1, 200, 66, 33, 1, F32, [0, 120, 50], ALL),            # ends before T
+    (2, 90, 130, 64, 2, BF16, None, ALL),
+    (1, 150, 64, 20, 1, F32, [150], dict(ALL, gate=False))], ids=["packed", "n33", "n64", "n20"])
+def test_backward_from_checkpoints_packed_and_with_many_states(case):
+    d, seeds, cu, used = make(case, 12)
+    g, s = lo.cuda(d), lo.cuda(seeds)
+    px = gdn.pack8(g["x"])
+    pz = None if g["z"] is None else gdn.pack8(g["z"])
+    at = dict(g, x=gdn.unpack8(px), z=None if pz is None else gdn.unpack8(pz))
+    a, b = bwd(g, s, cu, px, pz), bwd(at, s, cu)
+    assert a.keys() == b.keys() and all(torch.equal(a[k], b[k]) for k in a)
+    live = (torch.arange(case[1]) < used)[:, None] | torch.tensor(cu is None)
+    ref = lo.gradients(lambda **k: lo.scan(cu=cu, **k), lo.double({k: None if v is None else v.cpu() for k, v in at.items()}),
+                       (torch.where(live, seeds["d_y"].double(), 0.0), seeds["d_fin"].double()))
+    n = case[0] * case[1]
+    for k, name in (("dx", "x"), ("ddt", "dt"), ("dBm", "Bm"), ("dCm", "Cm"), ("dz", "z"), ("dA_log", "A_log"),
+                    ("dskip", "skip"), ("ddt_bias", "dt_bias"), ("dh0", "h0")):
+        if d[name] is not None:
+            lo.close(a[k], ref[name], 2 * n + case[2], k)
 
 
 @pytest.mark.parametrize("bits", [None, 8])
