@@ -180,6 +180,22 @@ def test_backward_from_a_checkpoint(dtype, C):
     assert all(torch.equal(a[k], b[k]) for k in a), "the checkpoint's values, read in place"
 
 
+@pytest.mark.parametrize("case", [CASES[7], CASES[8], CASES[9], CASES[10], (1, 2600, 4096, 4, BF16, True, [1000, 0, 3, 1590], True, True)],
+                         ids=["short", "fp32", "odd", "ends-early", "several-groups"])
+def test_backward_from_a_packed_checkpoint(case):
+    d, seeds, cu, act, used = make(case, 11)
+    g, s = lo.cuda(d), lo.cuda(seeds)
+    p = gdn.pack8(g["x"])
+    at = gdn.unpack8(p)
+    a, b = (gdn.conv_bwd(x, g["weight"], g["bias"], s["d_y"], s["d_fin"], cu.cuda(), g["h0"], act) for x in (p, at))
+    assert all(torch.equal(a[k], b[k]) for k in a)
+    live = (torch.arange(case[1]) < used)[:, None]
+    ref = lo.gradients(lambda **k: lo.conv(cu=cu, silu=act is not None, **k), dict(lo.double(d), x=at.cpu().double()),
+                       (torch.where(live, seeds["d_y"].double(), 0.0), seeds["d_fin"].double()))
+    lo.close(a["dx"], ref["x"], case[3], "dx")
+    lo.close(a["dweight"], ref["weight"], case[1], "dweight")
+
+
 @pytest.mark.parametrize("bits", [None, 8])
 def test_autograd(bits):
     d, seeds = lo.conv_inputs(2, 50, 64, 4, F32, 8)
