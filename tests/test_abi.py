@@ -556,3 +556,17 @@ def test_zero_rest_is_a_bit_of_the_dtype(call, P_):
         assert call(P_(dtype=code | 0x100), x=0x100001) == EALIGN  # a later check answers
     for code in (gdn.GDN_F16 | 0x100, 7 | 0x100, gdn.GDN_BF16 | 0x200):
         assert call(P_(dtype=code)) == EDTYPE
+
+
+def test_layer_workspace_sizes():
+    """What the forward scan's workspace holds: nothing of tiles where a row is one tile (32
+    tokens or fewer), the two fp32 copies of Bm and Cm (for calls that cannot read them in
+    place) always; nothing without tokens."""
+    size = lambda **kw: gdn.load_library().gdn_scan_fwd_workspace_size(ctypes.byref(SP(**kw)), 0)  # noqa: E731
+    up = lambda b: -(-b // 256) * 256  # noqa: E731
+    for T in (1, 20, 32):
+        for N, np_ in ((16, 16), (5, 8), (33, 48)):
+            assert size(T=T, N=N) == 2 * up(2 * T * 2 * np_ * 4)
+    tiles = 2 * 3  # of 16 tokens
+    assert size(T=33) == up(up(tiles * 16 * 64 * 4) + tiles * 64 * 4) + 2 * up(2 * 33 * 2 * 16 * 4)
+    assert size(T=0) == 0 and size(B=0) == 0
