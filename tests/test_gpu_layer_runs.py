@@ -506,3 +506,43 @@ def test_a_sequence_that_begins_too_early_starts_where_the_one_ahead_ended(T, dt
             t, ref[n] = t[:2], ref[n][:2]
         lo.close(t, ref[n], T, "conv d" + n)
     assert new.untouched()
+
+
+# ---- a captured training step ------------------------------------------------------------
+
+@pytest.mark.parametrize("bits", [None, 8])
+def test_a_captured_training_step_replays(bits):
+    """Convolution, scan and their gradients in one graph (gradients returned, not
+    accumulated, so that nothing of an earlier eager step is part of it), its workspaces
+    and checkpoints in the graph's own memory; replays against the eager step."""
+    T_ = 70
+    d = lo.cuda(scan_layer(21, 2, T_))
+    cu = lo.offsets([50, 13]).cuda()
+    seed = torch.randn(1, T_, D, generator=torch.Generator().manual_seed(22)).cuda()
+    names = ("proj", "weight", "bias", "c0", "h0", "dt", "A_log", "Bm", "Cm", "skip", "z", "dt_bias")
+
+    def step():
+        leaf = {n: d[n].detach().requires_grad_() for n in names}
+        c, _ = gdn.causal_conv(leaf["proj"], leaf["weight"], leaf["bias"], cu, leaf["c0"], checkpoint_bits=bits)
+        y, fin = gdn.selective_scan(c, **scan_args(leaf), cu_seqlens=cu, initial_state=leaf["h0"], checkpoint_bits=bits)
+        return [y.detach(), fin.detach(), *torch.autograd.grad((y, fin), [leaf[n] for n in names], (seed, fin.detach()))]
+    cap = torch.cuda.Stream()
+    cap.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(cap):
+        step()
+    cap.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=cap):
+        outs = step()
+    for i in range(3):
+        for n in ("proj", "dt", "z"):
+            d[n].copy_(torch.randn(d[n].shape, generator=torch.Generator().manual_seed(30 + i)))
+        for o in outs:
+            o.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        replayed = [o.clone() for o in outs]
+        eager = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(replayed, eager)), i

@@ -161,6 +161,37 @@ def test_extreme_decays_and_time_steps():
         lo.close(got[k], ref[name], 400, k)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("low", [-float("inf"), "lowest"])
+def test_tokens_masked_by_their_time_step(dtype, low):
+    """dt of minus infinity, or the type's lowest value: D = 0, so the token leaves the state
+    as it was and takes no gradient of its own; whole tiles of them among others."""
+    d, seeds = lo.scan_inputs(1, 130, 64, 16, 1, dtype, 13)
+    low = torch.finfo(dtype).min if low == "lowest" else low
+    mask = torch.zeros(130, dtype=torch.bool)
+    mask[[0, 5, 129]] = True
+    mask[40:100] = True
+    d["dt"][0, mask] = low
+    r = lo.double(d)
+    y_ref, fin_ref = lo.scan(**r)
+    g, s = lo.cuda(d), lo.cuda(seeds)
+    y, fin = fwd(g, None)
+    lo.close(y, y_ref, 130, "y")
+    lo.close(fin, fin_ref, 130, "final state")
+    # (the oracle's own slope at minus infinity is not a number: its inputs at -1000 give the same D)
+    at = dict(r, dt=r["dt"].clamp(min=-1000.0))
+    ref = lo.gradients(lo.scan, at, (seeds["d_y"].double(), seeds["d_fin"].double()))
+    got = bwd(g, s, None)
+    assert (got["ddt"][0, mask.cuda()] == 0).all()
+    for k, name in (("dx", "x"), ("ddt", "dt"), ("dBm", "Bm"), ("dCm", "Cm"), ("dz", "z"), ("dA_log", "A_log"),
+                    ("dskip", "skip"), ("ddt_bias", "dt_bias"), ("dh0", "h0")):
+        lo.close(got[k], ref[name], 2 * 130 + 64, k)
+    state = g["h0"].clone()
+    y1 = gdn.scan_decode(g["x"], g["dt"], g["A_log"], g["Bm"], g["Cm"], state, g["skip"], g["z"], g["dt_bias"])
+    lo.close(y1, y_ref, 130, "decode y")
+    lo.close(state, fin_ref, 130, "decode state")
+
+
 def test_rows_behind_the_last_sequence_stay():
     d, seeds, cu, used = make(CASES[15])
     g, s = lo.cuda(d), lo.cuda(seeds)
