@@ -277,29 +277,6 @@ __device__ __forceinline__ void conv_bwd_state(const ConvGeo& g, const Src& x, c
   for (int r = 0; r < W - 1; ++r) vec_store<E, VEC>(dh0 + ((int64_t)n * (W - 1) + r) * g.C + c, out[r]);
 }
 
-// U tokens of one vector of channels as loaded, so that the loads are all in flight
-// before the first is converted.
-template <typename E, int VEC, int U, bool CK> struct VecVals {
-  RawVec<E, VEC> v[U];
-  // tokens t .. t + U - 1, those from `end` on held to the last before it
-  __device__ __forceinline__ void fetch(const Src& src, int t, int end, uint32_t off, uint32_t soff, int nblk) {
-    if (t + U <= end) walk(src, t, off, soff, nblk, [](int) { return true; });
-    else walk(src, t, off, soff, nblk, [&](int k) { return t + k + 1 < end; });
-  }
-  template <typename F>
-  __device__ __forceinline__ void walk(const Src& src, int t, uint32_t off, uint32_t soff, int nblk, F&& more) {
-    const int64_t step = src.ld * (CK ? 1 : (int)sizeof(E));
-    Global<const char> p = (Global<const char>)src.p + t * step;
-    Global<const uint8_t> q = (Global<const uint8_t>)src.scales + (CK ? (int64_t)t * nblk : 0);
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      v[k] = raw_load_at<E, VEC, CK>(p, q, off, soff);
-      p = stepped<const char>(p, more(k) ? step : 0);
-      if constexpr (CK) q = stepped<const uint8_t>(q, more(k) ? nblk : 0);
-    }
-  }
-};
-
 constexpr int kConvTiles = 4;  // tiles per workgroup, a wave each
 
 // A wave owns 64 neighbouring vectors of channels (its last lanes beyond C hold the last
@@ -363,8 +340,8 @@ __global__ __launch_bounds__(64 * kConvTiles, 2) void gdn_conv_bwd_kernel(
       const int lim = run.tb + (W - 1);  // tokens at or beyond the sequence's end have p = 0
       const int stop = min(lim, run.end);
       RawVec<E, VEC> old[W - 1];
-      VecVals<E, VEC, U, CK> rx;
-      VecVals<E, VEC, U, false> rd;
+      TokenVals<E, VEC, U, CK> rx;
+      TokenVals<E, VEC, U, false> rd;
 #pragma unroll
       for (int j = 0; j < W - 1; ++j)
         old[j] = conv_row<E, W, VEC>(g, x, h0, run.n, run.start, run.ta - run.start - (W - 1) + j, c);
@@ -425,8 +402,8 @@ __global__ __launch_bounds__(64 * kConvTiles, 2) void gdn_conv_bwd_kernel(
         __builtin_amdgcn_sched_barrier(0);  // token by token: interleaved they take all registers
       };
       for (int t = run.ta; t < lim; t += U) {
-        const VecVals<E, VEC, U, CK> cx = rx;
-        const VecVals<E, VEC, U, false> cd = rd;
+        const TokenVals<E, VEC, U, CK> cx = rx;
+        const TokenVals<E, VEC, U, false> cd = rd;
         const int next = min(t + U, stop - 1);
         rx.fetch(x, next, stop, xoff, soff, g.nblk);
         rd.fetch(dys, next, stop, off, 0, 0);

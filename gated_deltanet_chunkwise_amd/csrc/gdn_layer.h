@@ -146,13 +146,41 @@ __device__ __forceinline__ void vec_store(E* p, const float (&v)[VEC]) {
     *p = (E)v[0];
   } else if constexpr (VEC == 2) {
     *reinterpret_cast<bf16x2*>(p) = bf16x2{(bf16)v[0], (bf16)v[1]};
-  } else if constexpr (sizeof(E) == 2 && VEC == 4) {
-    const bf16x4 w = to_bf16x4(f32x4{v[0], v[1], v[2], v[3]});
-    *reinterpret_cast<bf16x4*>(p) = w;
   } else {
+    static_assert(sizeof(E) == 4, "");
     *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
   }
 }
+
+// U tokens of one vector of channels as loaded, so that the loads are all in flight
+// before the first is converted.  CK: from a checkpoint, codes and scale.
+template <typename E, int VEC, int U, bool CK> struct TokenVals {
+  RawVec<E, VEC> v[U];
+  // tokens t .. t + U - 1, those from `end` on held to the last before it; `off`: the
+  // lane's offset in bytes, `soff` that of its scale
+  __device__ __forceinline__ void fetch(const Src& src, int t, int end, uint32_t off, uint32_t soff, int nblk) {
+    if (t + U <= end) walk(src, t, off, soff, nblk, [](int) { return true; });
+    else walk(src, t, off, soff, nblk, [&](int k) { return t + k + 1 < end; });
+  }
+  template <typename F>
+  __device__ __forceinline__ void walk(const Src& src, int t, uint32_t off, uint32_t soff, int nblk, F&& more) {
+    const int64_t step = src.ld * (CK ? 1 : (int)sizeof(E));
+    Global<const char> p = (Global<const char>)src.p + t * step;
+    Global<const uint8_t> q = (Global<const uint8_t>)src.scales + (CK ? (int64_t)t * nblk : 0);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      v[k] = raw_load_at<E, VEC, CK>(p, q, off, soff);
+      p = stepped<const char>(p, more(k) ? step : 0);
+      if constexpr (CK) q = stepped<const uint8_t>(q, more(k) ? nblk : 0);
+    }
+  }
+  __device__ __forceinline__ float operator[](int k) const {
+    static_assert(VEC == 1, "");
+    float f[1];
+    raw_unpack<E, 1>(v[k], CK, f);
+    return f[0];
+  }
+};
 
 // Packed sequences.  Offsets are read clamped to [0, T], so that ill-formed ones
 // never lead outside the buffers.

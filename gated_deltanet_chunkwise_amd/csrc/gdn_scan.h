@@ -83,9 +83,6 @@ template <typename E> __device__ __forceinline__ uint32_t load1(Global<const E> 
   if constexpr (sizeof(E) == 2) return *(Global<const uint16_t>)p;
   else return *(Global<const uint32_t>)p;
 }
-template <typename E> __device__ __forceinline__ uint32_t load1(const E* row, uint32_t off) {
-  return load1<E>((Global<const E>)row, off);
-}
 template <typename E> __device__ __forceinline__ void store1(Global<E> row, uint32_t off, float v) {
   *(Global<E>)((Global<char>)row + off) = (E)v;
 }
@@ -422,7 +419,6 @@ __global__ __launch_bounds__(64 * kScanMaxWaves) void gdn_scan_kernel(
 struct JoinArgs {
   float* states;
   const float* sums;
-  const float* h0;
 };
 static __global__ __launch_bounds__(256) void gdn_scan_join_kernel(ScanGeo g, const float* __restrict__ A_log,
                                                                    JoinArgs fore, JoinArgs aft) {
@@ -451,8 +447,9 @@ static __global__ __launch_bounds__(256) void gdn_scan_join_kernel(ScanGeo g, co
   fetch(0);
   const int64_t sd = (int64_t)d * g.N + min(n, (uint32_t)g.N - 1);
   const bool in = n < (uint32_t)g.N;
-  float H = !g.cu && j.h0 ? j.h0[(int64_t)row * g.D * g.N + sd] : 0.f;
-  H = in ? H : 0.f;
+  // a row's first tile starts its sequence, from a state that the tile reads itself; behind
+  // its last tile there is nothing
+  float H = 0.f;
   const float A2 = in ? scan_rate(A_log[sd]) : 0.f;
   for (int t = 0; t <= last; t += U) {
     float out[U];

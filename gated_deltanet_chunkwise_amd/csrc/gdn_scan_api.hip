@@ -111,7 +111,7 @@ gdn_status_t scan_fwd_run(ScanPlan pl, const FwdArgs& a, void* ws, hipStream_t s
     if (g.ntiles > 1) {
       ok(launch(gdn::gdn_scan_kernel<E, BE, NS, WHOLE, SPLIT, true>, dim3((unsigned)main_blocks), block, s, g, x, dt, z,
                 a.A_log, b, c, a.skip, a.dt_bias, a.h0, states, sums, y, a.fin));
-      ok(launch(gdn::gdn_scan_join_kernel, scan_join_grid(g, 1), dim3(256), s, g, a.A_log, gdn::JoinArgs{states, sums, a.h0},
+      ok(launch(gdn::gdn_scan_join_kernel, scan_join_grid(g, 1), dim3(256), s, g, a.A_log, gdn::JoinArgs{states, sums},
                 gdn::JoinArgs{}));
     }
     ok(launch(gdn::gdn_scan_kernel<E, BE, NS, WHOLE, SPLIT, false>, dim3((unsigned)(main_blocks + empties)), block, s, g, x,

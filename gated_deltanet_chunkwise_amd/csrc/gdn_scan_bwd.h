@@ -39,47 +39,9 @@ constexpr int kScanBwdSub = 8;     // tokens per group
 constexpr int kScanBwdTile = 32;
 constexpr int scan_bwd_units(int waves) { return waves >= 4 ? 1 : 4 / waves; }  // per workgroup
 
-// U tokens' values of one channel as loaded, so that the loads are all in flight before
-// the first is converted.  CK: from a checkpoint, code and scale.
-template <typename E, int U, bool CK> struct TokenVals {
-  uint32_t w[U], s[CK ? U : 1];
-  // tokens t .. t + U - 1, those from `end` on held to the last before it; `off`: the
-  // lane's offset in bytes (CK: d and d / 32)
-  __device__ __forceinline__ void fetch(const Src& src, int t, int end, uint32_t off, uint32_t soff, int nblk) {
-    if (t + U <= end) walk(src, t, off, soff, nblk, [](int) { return true; });
-    else walk(src, t, off, soff, nblk, [&](int k) { return t + k + 1 < end; });
-  }
-  template <typename F>
-  __device__ __forceinline__ void walk(const Src& src, int t, uint32_t off, uint32_t soff, int nblk, F&& more) {
-    if constexpr (CK) {
-      Global<const uint8_t> p = (Global<const uint8_t>)src.p + (int64_t)t * src.ld;
-      Global<const uint8_t> q = (Global<const uint8_t>)src.scales + (int64_t)t * nblk;
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        w[k] = p[off];
-        s[k] = q[soff];
-        p = stepped<const uint8_t>(p, more(k) ? src.ld : 0);
-        q = stepped<const uint8_t>(q, more(k) ? nblk : 0);
-      }
-    } else {
-      Global<const E> p = (Global<const E>)src.p + (int64_t)t * src.ld;
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        w[k] = load1<E>(p, off);
-        p = stepped<const E>(p, more(k) ? src.ld : 0);
-      }
-    }
-  }
-  __device__ __forceinline__ float operator[](int k) const {
-    if constexpr (CK) return (float)(int8_t)w[k] * pack_scale(s[k]);
-    else return value1<E>(w[k]);
-  }
-};
-
-// Sums over the wave's 64 lanes of V values each (V = 16 or 32): returns the sum of
-// value lane / (64 / V).
-template <int V> __device__ __forceinline__ float wave_sums(float (&v)[V]) {
-  static_assert(V == 16 || V == 32, "");
+// Sums over the wave's 64 lanes of 16 values each: returns the sum of value lane / 4.
+__device__ __forceinline__ float wave_sums(float (&v)[16]) {
+  constexpr int V = 16;
   // lanes 32 apart: the lower half keeps the values below V / 2
 #pragma unroll
   for (int i = 0; i < V / 2; ++i) {
@@ -109,8 +71,7 @@ template <int V> __device__ __forceinline__ float wave_sums(float (&v)[V]) {
   for (int i = 0; i < V / 8; ++i) half(i, i + V / 8, 8, Ror8{});
 #pragma unroll
   for (int i = 0; i < V / 16; ++i) half(i, i + V / 16, 4, Mirror{});
-  if constexpr (V == 32) half(0, 1, 2, Xor2{});
-  else v[0] += dpp(v[0], Xor2{});
+  v[0] += dpp(v[0], Xor2{});
   return v[0] + dpp(v[0], Xor1{});
 }
 
@@ -167,8 +128,8 @@ __global__ __launch_bounds__(64 * kScanMaxWaves) void gdn_scan_bwd_ends_kernel(
     float pass = 0.f;
     Global<const BE> br = (Global<const BE>)Bm + run.ta * g.ldb + (int64_t)w.gi * g.bgs + w.n0;
     Global<const BE> cr = (Global<const BE>)Cm + run.ta * g.ldc + (int64_t)w.gi * g.cgs + w.n0;
-    TokenVals<E, U, CK> rx, rz = {};
-    TokenVals<E, U, false> rd, ry = {};
+    TokenVals<E, 1, U, CK> rx, rz = {};
+    TokenVals<E, 1, U, false> rd, ry = {};
     auto fetch = [&](int t) {
       rx.fetch(x, t, run.tb, xoff, soff, bg.nblk);
       rd.fetch(Src{dt, nullptr, g.lddt}, t, run.tb, off, 0, 0);
@@ -177,7 +138,8 @@ __global__ __launch_bounds__(64 * kScanMaxWaves) void gdn_scan_bwd_ends_kernel(
         if (z.p) rz.fetch(z, t, run.tb, xoff, soff, bg.nblk);
       }
     };
-    RowAhead ahead;  // a tile is 64 tokens at most
+    RowAhead ahead;
+    static_assert(kScanBwdTile <= 64, "one round of rows sent for ahead");
     ahead.send<BE>((Global<const BE>)Bm + (int64_t)w.gi * g.bgs + w.n0, (Global<const BE>)Cm + (int64_t)w.gi * g.cgs + w.n0,
                    g.ldb, g.ldc, run.ta, run.tb);
     ScalarRow<BE, NS> b, c;
@@ -325,8 +287,8 @@ __global__ __launch_bounds__(64 * NW * scan_bwd_units(NW), 2) void gdn_scan_bwd_
     else tile_state_load<NS>(rev, g, w, l);
     // groups of SUB tokens, the last one maybe shorter (its rows held to the run's last)
     const int nsub = (run.tb - run.ta + SUB - 1) / SUB;
-    TokenVals<E, SUB, CK> rx, rz = {};
-    TokenVals<E, SUB, false> rd, ry;
+    TokenVals<E, 1, SUB, CK> rx, rz = {};
+    TokenVals<E, 1, SUB, false> rd, ry;
     auto fetch = [&](int t, bool all) {
       rx.fetch(x, t, run.tb, xoff, soff, bg.nblk);
       rd.fetch(Src{dt, nullptr, g.lddt}, t, run.tb, off, 0, 0);
@@ -452,7 +414,7 @@ __global__ __launch_bounds__(64 * NW * scan_bwd_units(NW), 2) void gdn_scan_bwd_
           bc[j] = lam * um;
           bc[NS + j] = ht * rm;
         }
-        store1<float>(pr, pboff, wave_sums<2 * NS>(bc));  // kRep lanes the same value
+        store1<float>(pr, pboff, wave_sums(bc));  // kRep lanes the same value
         pr = stepped<float>(pr, -2 * g.np);
         if (NW == 1 || k % NW == w.wave) {
           own[k / NW][0] = sy;

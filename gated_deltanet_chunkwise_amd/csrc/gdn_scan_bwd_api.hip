@@ -107,7 +107,7 @@ gdn_status_t scan_bwd_run(ScanPlan pl, const BwdArgs& a, void* ws, hipStream_t s
       if constexpr (NW == 1) ends(std::integral_constant<int, 8>{});
       else ends(std::integral_constant<int, 16>{});
       ok(launch(gdn::gdn_scan_join_kernel, scan_join_grid(g, 2), dim3(256), s, g, a.A_log,
-                gdn::JoinArgs{F(sp.states), F(sp.sums), a.h0}, gdn::JoinArgs{F(sp.rev), F(sp.rsums), nullptr}));
+                gdn::JoinArgs{F(sp.states), F(sp.sums)}, gdn::JoinArgs{F(sp.rev), F(sp.rsums)}));
     }
     if (main_blocks + empties > 0)
       ok(launch(gdn::gdn_scan_bwd_kernel<E, BE, NS, WHOLE, NW, gdn::kScanBwdSub, CK>, dim3((unsigned)(main_blocks + empties)),
