@@ -15,7 +15,8 @@
 // eight 55; B=2, T=2048 13.0, 11.1, 11.5, 15.0; B=1, T=300 4.1, 4.3, 4.8, 6.7: fewer bytes per
 // load, but more waves and fewer registers.  fp32 T=8192 one 111, four 109; T=5003, C=1000 one
 // 10.0, four 11.0, packed in seven sequences with W=3 14.3 and 10.9.  Hence two of bf16 and
-// four of fp32.
+// four of fp32; an odd number of channels goes one by one (us a call, bf16 T=8192: C=2048 49,
+// C=2047 66; backward 96 and 137).
 #pragma once
 #include "gdn_layer.h"
 
@@ -171,7 +172,9 @@ __global__ __launch_bounds__(256) void gdn_conv_fwd_kernel(ConvGeo g, Src x,
 // back (state_out may be state_in: a lane reads its channels' rows before it
 // writes them, and no other lane touches them).  One token, W=4, us with two channels of
 // bf16 per lane and with eight: B=64, C=2048 2.6 and 4.0 (the latency of one lane's loads),
-// B=256, C=8192 7.2 (29 MB, in the caches) and 14.7.
+// B=256, C=8192 7.2 (29 MB, in the caches) and 14.7.  fp32, us a call, with one channel per
+// lane and with four: B=64, C=2048 10.1 and 10.1 (the host), B=256, C=8192 11.8 and 12.8,
+// B=2048, C=8192 91 and 110.
 template <typename E, int W, int VEC>
 __global__ __launch_bounds__(256) void gdn_conv_decode_kernel(ConvGeo g, Src x,
                                                               const float* __restrict__ weight,

@@ -21,11 +21,13 @@
 // one by one) and stores its own in pieces of 4, 2 and 1 (TAIL; where no row has such
 // a lane the test for it is left out, which is worth a tenth in small calls).
 //
-// Measured, us: 32768 rows of 2048 bf16 (207 MB) pack 34, unpack 32 (a copy of that
-// size, part of it in the caches, 8 TB/s: 26); 262144 rows 381 and 353 (from memory, 4.3
-// and 4.6 TB/s); 65536 of 1001 35 and 34, where a lane per channel took 135 and 73.  Next
-// to memory it is the VALU: 18 operations per channel in pack, with clamps, conversions and
-// shifts of their own for each code, were 37 us at the first size.
+// Measured, us: 32768 rows of 2048 bf16 (207 MB) pack 34, unpack 32 where the same rows
+// come again and are in part in the caches (a copy there, 8 TB/s: 26), 40 and 38 with two
+// sets in turn; 262144 rows 383 and 354 (from memory, 4.2 and 4.6 TB/s); 65536 of 1001 34
+// and 34, where a lane per channel took 135 and 73.  Next to memory it is the VALU: 18
+// operations per channel in pack, with clamps, conversions and shifts of their own for each
+// code, were 37 us at the first size.  fp32, the same two sizes of 2048 channels: pack 62 (65
+// in turn) and 578, unpack 95 and 735 (4.7 and 3.7 TB/s).
 #pragma once
 #include <type_traits>
 

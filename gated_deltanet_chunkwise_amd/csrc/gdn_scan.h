@@ -6,14 +6,18 @@
 // A wave owns 64 channels of one group, a lane one channel with NS of its states in
 // registers; Bm and Cm of a token are the same for all its lanes and come through
 // scalar loads into scalar registers.  With more than NS states the workgroup has
-// ceil(N / NS) waves for the same channels, which add their parts of y through LDS (D=1024, N=32: 82 us
-// a call, D=2048, N=16: 78; eight states per lane where there are no more: N=8 54).
+// ceil(N / NS) waves for the same channels, which add their parts of y through LDS; eight
+// states per lane where there are no more.  B=2, T=2048, D=2048 bf16, us a call: N=8 50,
+// N=16 72, N=32 129.  Other N run as the next of those (N=9 to 13 90, the copies of Bm and
+// Cm included, N=17 to 20 159), and a group of fewer than 64 channels leaves lanes without
+// one (N=16 in groups of 32 channels 118, of 16 206).
 //
 // Per token, channel and state the recurrence takes one v_exp_f32 and four other
 // VALU operations (D A, D x B, the state's and y's multiply-adds), measured at 8.8 and 4.6
 // cycles of a SIMD each, so at N = 16 it is bound by the VALU and not by the 8 bytes of x,
-// dt, z and y.  B=2, T=2048, D=2048, N=16 bf16: the main kernel 36 us, its vector units
-// busy for 82 % of them; the tiles' end states 32 us (74 %); the bytes alone would be 13.
+// dt, z and y.  B=2, T=2048, D=2048, N=16 bf16: the main kernel 34 us, its vector units
+// busy for 86 % of them; the tiles' end states 31 us (78 %); the bytes alone would be 8
+// from the caches, 13 from memory.
 //
 // Few channels leave most of the device idle, so the tokens are cut into tiles that
 // run side by side: (1) each tile's end state from a zero start, and its sum of D,
@@ -414,8 +418,8 @@ __global__ __launch_bounds__(64 * kScanMaxWaves) void gdn_scan_kernel(
 // to the state gradient before it to the gradient of its end state (the backward pass's;
 // blocks with z = 1).  A chain of a few operations per tile: what it takes is the latency
 // of its loads, so U tiles are sent for ahead of the U being joined, and before anything
-// else.  B=2, T=2048, D=2048, N=16, 64 tiles: 9.5 us for one chain, 13.7 for both (67 MB,
-// 4.9 TB/s; 19 in two launches).
+// else.  B=2, T=2048, D=2048, N=16, 64 tiles: 9.2 us for one chain, 13.3 for both (67 MB,
+// 5.0 TB/s; 19 in two launches).
 struct JoinArgs {
   float* states;
   const float* sums;
@@ -491,6 +495,8 @@ __global__ __launch_bounds__(256) void gdn_scan_rows_kernel(const E* __restrict_
 // values of the states, of A_log, Bm and Cm are one aligned load each.  Bound by how many
 // loads a lane needs for its 32 bytes of state: one token each of B=256, D=4096, N=16 bf16
 // (143 MB) 32 us = 4.4 TB/s, 49 us without VEC; B=64, D=2048 6.6 against 8.3 (N=13: 8.6).
+// The fp32 state is nearly all of it in either type: calls with two sets of inputs in turn
+// take 36 us in bf16 and 37 in fp32 at the first size.
 template <typename E, bool VEC>
 __global__ __launch_bounds__(256) void gdn_scan_decode_kernel(
     ScanGeo g, Src x, const E* __restrict__ dt, Src z, const float* __restrict__ A_log,

@@ -8,13 +8,13 @@ namespace {
 // workspace is the same on every device.  Measured on MI355X, N = 16 bf16, us per call:
 //   one tile per sequence, which forms the states once, from a wave per SIMD on (1024;
 //   packed sequences are one row and are always cut): T=512, D=4096, B=16 (1024 waves)
-//   209 against 227 in tiles of 64; B=12 (768) 199 against 175; B=64, T=128, D=2048 (2048)
-//   73 against 137;
+//   197 against 228 in tiles; B=12 (768) 196 either way; B=64, T=128, D=2048 (2048) 72
+//   against 137;
 //   else tiles for about 8192 waves, of 32 tokens at least: B=2, T=2048, D=2048 (64 waves
-//   a tile) 80 with 32 tokens, 84 with 64, 114 with 128, 87 with 16; T=32768 packed (32
-//   waves) 494 with 128, 497 with 64, 520 with 256, 559 with 32 (the join's chain grows);
+//   a tile) 72 with 32 tokens, 76 with 64, 78 with 128, 78 with 16; T=32768 packed (32
+//   waves) 428 with 128, 438 with 64, 441 with 256, 483 with 32 (the join's chain grows);
 //   16 tokens where 32 leave less than 2048 waves: B=3, T=777, D=1002, G=2 fp32 (48 waves)
-//   48 against 55.
+//   50 against 53 with 32, and 53 with 8.
 constexpr int kOneTileWaves = 1024, kTileWaves = 8192, kTile = 32, kShortTile = 16;
 
 int scan_fwd_len(const ScanPlan& pl) {

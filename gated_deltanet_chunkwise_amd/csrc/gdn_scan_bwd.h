@@ -16,13 +16,15 @@
 // gradients; (3) every tile on its own: forwards once, the state before every group of
 // SUB tokens kept in LDS; then, from the last group to the first, forwards again within
 // the group, its states in registers, and backwards through them; (4) sums over waves and
-// tiles.  VALU-bound like the forward pass: B=2, T=2048, D=2048, N=16 bf16, us: (1) 47,
-// (2) 14, (3) 182 with its vector units busy for 72 % of them, (4) 9; the bytes alone
-// would be 23.
+// tiles.  VALU-bound like the forward pass: B=2, T=2048, D=2048, N=16 bf16, us: (1) 43,
+// (2) 13, (3) 167 with its vector units busy for 78 % of them, (4) 9; the bytes alone
+// would be 15 from the caches, 23 from memory.  Calls there, us: bf16 231 (fp32 248), N=8
+// 129, N=32 439, N=64 916; other N run as the next of those (N=13 249, N=17 463, N=33 963).
 //
-// Eight states per lane and eight tokens per group: (3) then takes 245 registers, two
-// waves per SIMD, which 45 KB of LDS per workgroup allow as well.  Held to three waves per
-// SIMD the registers spill; with groups of four tokens it took 199 us.
+// Eight states per lane and eight tokens per group: (3) then takes 241 registers, two
+// waves per SIMD, which 45 KB of LDS per workgroup allow as well (from checkpoints 256 and
+// up to 36 bytes of scratch per lane).  Held to three waves per SIMD the registers spill;
+// groups of four tokens took a tenth more.
 //
 // dBm and dCm need sums over channels, that is over lanes: 2 NS values of a token are
 // added over 64 lanes by halving (in each step a lane keeps half of its values and
@@ -34,8 +36,8 @@ namespace gdn {
 
 constexpr int kScanBwdStates = 8;  // states per lane
 constexpr int kScanBwdSub = 8;     // tokens per group
-// Tokens per tile.  B=2, T=2048, D=2048, N=16 bf16: 262 us of kernels with 32, 263 with 64,
-// 281 with 16 (more tiles to join); B=2, T=1024, D=1024: 101 against 144 with 64.
+// Tokens per tile.  B=2, T=2048, D=2048, N=16 bf16, us a call: 231 with 32, 238 with 64, 249
+// with 16 (more tiles to join); B=2, T=1024, D=1024: 81 with 32 and 16, 115 with 64.
 constexpr int kScanBwdTile = 32;
 constexpr int scan_bwd_units(int waves) { return waves >= 4 ? 1 : 4 / waves; }  // per workgroup
 
@@ -91,8 +93,8 @@ __device__ __forceinline__ float softplus_both(float x, float& slope) {
 
 // (1).  states, rev [tile][np][D]; sums, rsums [tile][D] (-1: nothing passes through).
 // R needs no walk backwards: with P_t = a_1 .. a_t it is sum_t P_t Cm_t r_t.  VALU-bound;
-// B=2, T=2048, D=2048, N=16 bf16: 47 us with four tokens' loads in flight (126 registers, so
-// the launch's four waves per SIMD run side by side), 52 with eight (154 registers).
+// B=2, T=2048, D=2048, N=16 bf16: 43 us with four tokens' loads in flight (122 registers, so
+// the launch's four waves per SIMD run side by side); a tenth more with eight (154 registers).
 template <typename E, typename BE, int NS, bool WHOLE, bool CK>
 __global__ __launch_bounds__(64 * kScanMaxWaves) void gdn_scan_bwd_ends_kernel(
     ScanBwdGeo bg, Src x, const E* __restrict__ dt, Src z, const float* __restrict__ A_log,

@@ -442,9 +442,8 @@ gdn_status_t gdn_kda_gate(const void *g, gdn_dtype_t g_dtype, const float *A_log
  * size (rows that split into four bytes of bf16 or sixteen of fp32 are faster);
  * cu_seqlens 8; workspace 256.  B * T below 2^31 - 4096.  Errors as for gdn_fwd, all checked
  * before anything is enqueued; GDN_ERR_UNSUPPORTED for another W, and for sizes that would
- * take 2^32 threads or more in one launch.  Outputs must not
- * overlap inputs or each other (gdn_conv_decode: new_state may be state).
- * Enqueued on `stream`; nothing is allocated. */
+ * take 2^32 threads or more in one launch.  Outputs must not overlap inputs or each other
+ * (gdn_conv_decode: new_state may be state).  Enqueued on `stream`; nothing is allocated. */
 #define GDN_ZERO_REST 0x100 /* added to a params' dtype; of no effect but on y's rows */
 
 typedef struct {
@@ -505,9 +504,11 @@ gdn_status_t gdn_conv_bwd(const gdn_conv_params_t *p, const void *x, const uint8
  * All arithmetic is fp32; y is rounded once.  Long sequences are cut into tiles of
  * tokens that run side by side (three kernels); where the channels alone fill the
  * device, one kernel runs each sequence through.  The cut is chosen from the sizes
- * alone.  dtype, alignment, limits and errors as for
- * gdn_conv_fwd; GDN_ERR_UNSUPPORTED for N > 64 and for B > 65535.  Outputs must not overlap inputs or
- * each other (gdn_scan_decode: new_state may be state).  Enqueued on `stream`;
+ * alone.  dt of minus infinity, or so low that D is 0, leaves a state as it was.  An
+ * infinity or NaN among the inputs reaches what depends on it, as infinity or NaN (which
+ * of the two is left open), and nothing else.  dtype, alignment, limits and errors as for
+ * gdn_conv_fwd; GDN_ERR_UNSUPPORTED for N > 64 and for B > 65535.  Outputs must not overlap
+ * inputs or each other (gdn_scan_decode: new_state may be state).  Enqueued on `stream`;
  * nothing is allocated. */
 typedef struct {
   int32_t B, T, D, G, N;
