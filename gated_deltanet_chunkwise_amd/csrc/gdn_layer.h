@@ -249,10 +249,10 @@ template <bool UNIFORM> struct Run {
       start = max(start, ta);
     }
   }
-  // The sequence that holds token ta, from n on: skips empty ones; behind the last
-  // sequence the walk ends.
+  // The sequence that holds token ta, from n on: past empty ones by a search (offsets padded
+  // to a fixed count hold thousands of them); behind the last sequence the walk ends.
   __device__ __forceinline__ void fit() {
-    for (; n < N; ++n) {
+    for (; n < N; n = max(n + 1, uniform<UNIFORM>(seq_of_token(cu, N, T, ta)))) {
       start = uniform<UNIFORM>(seq_offset(cu, n, T));
       end = uniform<UNIFORM>(seq_offset(cu, n + 1, T));
       if (end > ta) {

@@ -546,3 +546,32 @@ def test_a_captured_training_step_replays(bits):
         eager = step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(replayed, eager)), i
+
+
+# ---- padded offsets ----------------------------------------------------------------------
+
+def test_thousands_of_empty_sequences():
+    """Offsets padded to a fixed count, and a run of empty sequences inside a tile: both
+    passes as without the empty ones, whose states pass through."""
+    lengths = [37, 0, 1] + [0] * 5000 + [70, 2] + [0] * 3000 + [25] + [0] * 7000
+    real = [i for i, n in enumerate(lengths) if n]
+    T_, C_, N_, S = 150, 40, 5, len(lengths)  # 15 tokens behind the last sequence
+    cu, few = lo.offsets(lengths).cuda(), lo.offsets([lengths[i] for i in real]).cuda()
+    d, s = lo.scan_inputs(1, T_, C_, N_, 1, F32, 23, S)
+    c, cs = lo.conv_inputs(1, T_, C_, 4, F32, 24, S)
+    d, s, c, cs = (lo.cuda(t) for t in (d, s, c, cs))
+    a, o = [d[n] for n in ("x", "dt", "A_log", "Bm", "Cm")], dict(skip=d["skip"], z=d["z"], dt_bias=d["dt_bias"])
+
+    def passes(cu, at):
+        h0, c0, df, cf = (t[at].contiguous() for t in (d["h0"], c["h0"], s["d_fin"], cs["d_fin"]))
+        y, fin = gdn.scan_fwd(*a, **o, cu_seqlens=cu, initial_state=h0)
+        g = gdn.scan_bwd(*a, s["d_y"], df, **o, cu_seqlens=cu, initial_state=h0)
+        cy, cfin = gdn.conv_fwd(c["x"], c["weight"], c["bias"], cu, c0)
+        cg = gdn.conv_bwd(c["x"], c["weight"], c["bias"], cs["d_y"], cf, cu, c0)
+        return ([y, cy] + [v for k, v in [*g.items(), *cg.items()] if k != "dh0"], [fin, cfin, g["dh0"], cg["dh0"]])
+    tokens, states = passes(cu, slice(None))
+    ref_tokens, ref_states = passes(few, real)
+    assert all(torch.equal(x, y) for x, y in zip(tokens, ref_tokens))
+    empty = [i for i in range(S) if i not in real]
+    for got, ref, through in zip(states, ref_states, (d["h0"], c["h0"], s["d_fin"], cs["d_fin"])):
+        assert torch.equal(got[real], ref) and torch.equal(got[empty], through[empty])
