@@ -225,13 +225,13 @@ template <bool UNIFORM> struct Run {
     N = N_;
     if (cu) {
       ta = tile * len;
-      t1 = rest = min(ta + len, T);
+      t1 = rest = ta + min(len, T - ta);  // (ta + len may pass 2^31)
     } else {
       n = tile / ntiles;
       start = n * T;
       end = start + T;
       ta = start + (tile - n * ntiles) * len;
-      t1 = rest = tb = min(ta + len, end);
+      t1 = rest = tb = ta + min(len, end - ta);
     }
   }
   __device__ __forceinline__ void locate() {
