@@ -255,7 +255,7 @@ template <bool UNIFORM> struct Run {
     for (; n < N; n = max(n + 1, uniform<UNIFORM>(seq_of_token(cu, N, T, ta)))) {
       start = uniform<UNIFORM>(seq_offset(cu, n, T));
       end = uniform<UNIFORM>(seq_offset(cu, n + 1, T));
-      if (end > ta) {
+      if (end > ta && end > start) {
         if (start > ta) ta = min(start, t1);  // only for ill-formed offsets
         tb = min(end, t1);
         return;

@@ -1,7 +1,7 @@
 """The walk over packed sequences that the convolution's and the scan's kernels share (Run in
 csrc/gdn_layer.h), compiled for the CPU: every token of a tile in one run of the sequence
-that holds it, for well-formed offsets, padded ones, and token counts near
-2^31."""
+that holds it, for well-formed offsets, padded and ill-formed ones, and token
+counts near 2^31."""
 import ctypes
 import os
 import random
@@ -83,6 +83,23 @@ def test_well_formed_offsets(lib):
                 else:
                     want.append([n, cu[n], t, t + 1, cu[n + 1]])
         assert runs == [tuple(w) for w in want], (cu, T, length)
+
+
+def test_ill_formed_offsets(lib):
+    """Whatever the offsets: runs lie in their tile one after the other, within a sequence's
+    bounds, and only a tile's first run continues one that began before it."""
+    rng = random.Random(2)
+    for _ in range(2000):
+        N, T = rng.choice([1, 2, 3, 9]), rng.choice([1, 5, 33, 150])
+        cu = [rng.choice([rng.randint(-5, T + 5), rng.randint(0, T), -2 ** 62, 2 ** 62]) for _ in range(N + 1)]
+        length = rng.choice([8, 13, 32])
+        for i, (runs, rest, t1) in enumerate(tiles(lib, cu, T, N, length)):
+            at = i * length
+            for k, (n, start, ta, tb, end) in enumerate(runs):
+                assert 0 <= n < N and at <= ta < tb <= t1 and 0 <= start <= ta and tb <= end <= T
+                assert k == 0 or start == ta
+                at = tb
+            assert i * length <= rest <= t1 <= T
 
 
 @pytest.mark.parametrize("packed", [False, True])
