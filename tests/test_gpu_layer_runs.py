@@ -575,3 +575,71 @@ def test_thousands_of_empty_sequences():
     empty = [i for i in range(S) if i not in real]
     for got, ref, through in zip(states, ref_states, (d["h0"], c["h0"], s["d_fin"], cs["d_fin"])):
         assert torch.equal(got[real], ref) and torch.equal(got[empty], through[empty])
+
+
+# ---- sizes at both ends ------------------------------------------------------------------
+
+def test_tensors_beyond_32_bit_offsets():
+    """1.1 million tokens of 2048 channels: 2.25e9 elements, 4.5 GB a tensor, and workspaces
+    of more than 4 GB.  The last sequence against the same tokens on their own."""
+    T_, D_, N_, n = 1100000, 2048, 16, 300
+    gen = torch.Generator(device="cuda").manual_seed(25)
+    r = lambda *s, dtype=BF16: torch.randn(*s, generator=gen, device="cuda", dtype=dtype)  # noqa: E731
+    x, dt, z, d_y = (r(1, T_, D_) for _ in range(4))
+    Bm, Cm, h0, c0 = r(1, T_, 1, N_), r(1, T_, 1, N_), r(2, D_, N_, dtype=F32), r(2, 3, D_)
+    w, bias, skip, dt_bias = r(D_, 4, dtype=F32), r(D_, dtype=F32), r(D_, dtype=F32), r(D_, dtype=F32) - 3
+    A_log = torch.log(torch.arange(1, N_ + 1, device="cuda").float()).expand(D_, N_).contiguous()
+    cu = torch.tensor([0, T_ - n, T_], device="cuda")
+    end = lambda t: t[:, -n:].contiguous()  # noqa: E731
+
+    y, fin = gdn.conv_fwd(x, w, bias, cu, c0)
+    y1, fin1 = gdn.conv_fwd(end(x), w, bias, initial_state=c0[1:])
+    assert torch.equal(end(y), y1) and torch.equal(fin[1:], fin1)
+    del y
+    g = gdn.conv_bwd(x, w, bias, d_y, None, cu, c0)
+    g1 = gdn.conv_bwd(end(x), w, bias, end(d_y), initial_state=c0[1:])
+    assert torch.equal(end(g["dx"]), g1["dx"]) and torch.equal(g["dh0"][1:], g1["dh0"])
+    del g
+    o = dict(skip=skip, dt_bias=dt_bias)
+    y, fin = gdn.scan_fwd(x, dt, A_log, Bm, Cm, z=z, **o, cu_seqlens=cu, initial_state=h0)
+    last = [end(x), end(dt), A_log, end(Bm), end(Cm)]
+    y1, fin1 = gdn.scan_fwd(*last, z=end(z), **o, initial_state=h0[1:])
+    lo.close(end(y), y1.cpu().double(), n, "y")
+    lo.close(fin[1:], fin1.cpu().double(), n, "final state")
+    assert y.isfinite().all()
+    del y
+    g = gdn.scan_bwd(x, dt, A_log, Bm, Cm, d_y, z=z, **o, cu_seqlens=cu, initial_state=h0)
+    g1 = gdn.scan_bwd(*last, end(d_y), z=end(z), **o, initial_state=h0[1:])
+    for k in ("dx", "ddt", "dz", "dBm", "dCm"):
+        lo.close(end(g[k]), g1[k].cpu().double(), 2 * n + D_, k)
+    lo.close(g["dh0"][1:], g1["dh0"].cpu().double(), 2 * n, "dh0")
+    del g, x, dt, z, d_y
+    rows = torch.randn(T_, D_, generator=gen, device="cuda", dtype=BF16)
+    p = gdn.pack8(rows)
+    p1 = gdn.pack8(rows[-n:])
+    assert torch.equal(p.codes[-n:], p1.codes) and torch.equal(p.scales[-n:], p1.scales)
+    assert torch.equal(gdn.unpack8(p)[-n:], gdn.unpack8(p1))
+    del rows, p
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_no_sequences_at_all(packed):
+    """B = 0, or offsets [0]: empty outputs, and parameters' gradients of 0."""
+    B_, T_ = (1, 0) if packed else (0, 7)
+    d, s = lo.scan_inputs(B_, T_, 40, 5, 1, F32, 26, 0)
+    c, cs = lo.conv_inputs(B_, T_, 40, 4, F32, 27, 0)
+    d, s, c, cs = (lo.cuda(t) for t in (d, s, c, cs))
+    cu = torch.zeros(1, dtype=torch.int64, device="cuda") if packed else None
+    a, o = [d[n] for n in ("x", "dt", "A_log", "Bm", "Cm")], dict(skip=d["skip"], z=d["z"], dt_bias=d["dt_bias"], cu_seqlens=cu)
+    y, fin = gdn.scan_fwd(*a, **o, initial_state=d["h0"])
+    g = gdn.scan_bwd(*a, s["d_y"], s["d_fin"], **o, initial_state=d["h0"])
+    cy, cfin = gdn.conv_fwd(c["x"], c["weight"], c["bias"], cu, c["h0"])
+    cg = gdn.conv_bwd(c["x"], c["weight"], c["bias"], cs["d_y"], cs["d_fin"], cu, c["h0"])
+    assert y.shape == (B_, T_, 40) == cy.shape and fin.shape == (0, 40, 5) and cfin.shape == (0, 3, 40)
+    torch.cuda.synchronize()
+    for t in (g["dA_log"], g["dskip"], g["ddt_bias"], cg["dweight"], cg["dbias"]):
+        assert t.numel() and (t == 0).all()
+    if not packed:
+        gdn.conv_decode(c["x"][:, :1], c["weight"], c["h0"], c["bias"])
+        gdn.scan_decode(*(d[n][:, :1] for n in ("x", "dt")), d["A_log"], *(d[n][:, :1] for n in ("Bm", "Cm")), d["h0"])
