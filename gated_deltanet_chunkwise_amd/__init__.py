@@ -58,8 +58,16 @@ from ._layers import (  # noqa: F401
     selective_scan,
     unpack8,
 )
+from ._linattn import (  # noqa: F401
+    linear_attention,
+    linear_attn_bwd,
+    linear_attn_decode,
+    linear_attn_decode_launcher,
+    linear_attn_fwd,
+)
 
 __all__ = [
+    "linear_attention", "linear_attn_bwd", "linear_attn_decode", "linear_attn_decode_launcher", "linear_attn_fwd",
     "Packed8", "causal_conv", "conv_bwd", "conv_decode", "conv_decode_launcher", "conv_fwd", "pack8", "scan_bwd",
     "scan_decode", "scan_decode_launcher", "scan_fwd", "selective_scan", "unpack8",
     "BWD_NUM_STAGES", "BWD_STAGES", "GdnBackward", "bwd",

@@ -559,6 +559,72 @@ gdn_status_t gdn_scan_bwd(const gdn_scan_params_t *p, const void *x, const uint8
                           float *d_initial_state, void *workspace, size_t workspace_bytes,
                           void *stream);
 
+/* ---- Linear attention with a decay for each head ----------------------------------
+ * The recurrence of the gated delta rule without its correction and with one fixed decay
+ * per value head, a = exp(log_decay[hv]):
+ *     H_t = a H_{t-1} + k_t v_t^T,    o_t = scale * H_t^T q_t
+ * with H the [K][V] fp32 state of each (sequence, value head); value head hv reads query
+ * and key head hv / (HV/H).  Evaluated in chunks of 64 tokens on the matrix cores.
+ *   p             sizes; K and V 64 or 128, HV % H == 0; num_seqs with cu_seqlens (then B = 1)
+ *   q, k          [B][T] rows of H*K values, q_stride, k_stride elements apart (0: H*K), dtype
+ *   v             [B][T] rows of HV*V values, v_stride elements apart (0: HV*V), dtype: slices
+ *                 of a wider projection are read in place
+ *   log_decay     [HV] fp32, a constant of the model (it takes no gradient): 0 keeps
+ *                 everything, minus infinity nothing but the token itself.  Above 0 the state
+ *                 grows, as the formula says
+ *   cu_seqlens    [num_seqs+1] int64 or NULL, as for gdn_conv_fwd
+ *   initial_state, final_state  [sequences][HV][K][V] fp32 or NULL
+ *   o             [B][T][HV][V] contiguous, dtype, written
+ *   workspace     gdn_linattn_fwd_workspace_size() bytes
+ * dtype: GDN_F32 or GDN_BF16.  bf16: products of bf16 operands summed in fp32; a chunk's
+ * weighted products q.k, and the state where it meets q, are rounded to bf16; the states
+ * themselves are held and returned to fp32's precision.  An infinity or NaN in q reaches
+ * its own row of o (and in the gradients what depends on it); one in k or v reaches every
+ * row of its sequence and head from the start of its chunk on.
+ * Alignment: rows (pointers and strides) and states 16 bytes, log_decay 4, cu_seqlens 8,
+ * workspace 256.  B * T below 2^31 - 4096.  Errors as for gdn_fwd, all checked before
+ * anything is enqueued; GDN_ERR_UNSUPPORTED for another K or V, and for sizes that would take
+ * 2^32 threads or more in one launch.  Outputs must not overlap inputs or each other
+ * (gdn_linattn_decode: new_state may be state).  The same call gives the same bits.
+ * Enqueued on `stream`; nothing is allocated. */
+typedef struct {
+  int32_t B, T, H, HV, K, V;
+  int32_t num_seqs; /* sequences with cu_seqlens; ignored (B) without */
+  int32_t dtype;    /* gdn_dtype_t of q, k, v and o; GDN_ZERO_REST may be added */
+  float scale;
+  int64_t q_stride, k_stride, v_stride; /* elements between rows, 0 = dense */
+} gdn_linattn_params_t;
+
+size_t gdn_linattn_fwd_workspace_size(const gdn_linattn_params_t *p, int packed);
+
+gdn_status_t gdn_linattn_fwd(const gdn_linattn_params_t *p, const void *q, const void *k,
+                             const void *v, const float *log_decay, const int64_t *cu_seqlens,
+                             const float *initial_state, void *o, float *final_state,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/* T tokens (1: a decode step) of each of B sequences after `state` [B][HV][K][V] fp32, token
+ * by token in fp32; the state after them is written to new_state, which may be `state` (in
+ * place) and must not overlap it otherwise.  num_seqs = 0. */
+gdn_status_t gdn_linattn_decode(const gdn_linattn_params_t *p, const void *q, const void *k,
+                                const void *v, const float *log_decay, const float *state,
+                                float *new_state, void *o, void *stream);
+
+/* Gradients for L = sum <d_o, o> + <d_final_state, final_state>; the states are formed again.
+ *   d_o           [B][T][HV][V] contiguous, dtype; d_final_state [sequences][HV][K][V] fp32 or
+ *                 NULL (0)
+ *   dq, dk        [B][T][H][K] (sums over the value heads that read each key head), dv
+ *                 [B][T][HV][V]: dtype, written (rows behind the last sequence: 0)
+ *   d_initial_state  [sequences][HV][K][V] fp32, written, or NULL
+ *   workspace     gdn_linattn_bwd_workspace_size() bytes */
+size_t gdn_linattn_bwd_workspace_size(const gdn_linattn_params_t *p, int packed);
+
+gdn_status_t gdn_linattn_bwd(const gdn_linattn_params_t *p, const void *q, const void *k,
+                             const void *v, const float *log_decay, const int64_t *cu_seqlens,
+                             const float *initial_state, const void *d_o,
+                             const float *d_final_state, void *dq, void *dk, void *dv,
+                             float *d_initial_state, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
 /* ---- Activation checkpoints in 8 bits --------------------------------------------
  * What a training step keeps of an activation until its backward pass, in 1 + 1/32
  * bytes per element.  Each row of C channels is held in blocks of 32 (the last may be
