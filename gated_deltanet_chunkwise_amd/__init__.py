@@ -65,8 +65,17 @@ from ._linattn import (  # noqa: F401
     linear_attn_decode_launcher,
     linear_attn_fwd,
 )
+from ._norms import (  # noqa: F401
+    gated_norm,
+    gated_norm_bwd,
+    gated_norm_fwd,
+    residual_norm,
+    residual_norm_bwd,
+    residual_norm_fwd,
+)
 
 __all__ = [
+    "gated_norm", "gated_norm_bwd", "gated_norm_fwd", "residual_norm", "residual_norm_bwd", "residual_norm_fwd",
     "linear_attention", "linear_attn_bwd", "linear_attn_decode", "linear_attn_decode_launcher", "linear_attn_fwd",
     "Packed8", "causal_conv", "conv_bwd", "conv_decode", "conv_decode_launcher", "conv_fwd", "pack8", "scan_bwd",
     "scan_decode", "scan_decode_launcher", "scan_fwd", "selective_scan", "unpack8",

@@ -22,7 +22,9 @@ SYMBOLS = ("gdn_fwd_workspace_size", "gdn_fwd_workspace_layout", "gdn_fwd_check"
            "gdn_scan_fwd_workspace_size", "gdn_scan_fwd", "gdn_scan_decode",
            "gdn_scan_bwd_workspace_size", "gdn_scan_bwd", "gdn_pack8", "gdn_unpack8",
            "gdn_linattn_fwd_workspace_size", "gdn_linattn_fwd", "gdn_linattn_decode",
-           "gdn_linattn_bwd_workspace_size", "gdn_linattn_bwd")
+           "gdn_linattn_bwd_workspace_size", "gdn_linattn_bwd",
+           "gdn_gated_norm_fwd", "gdn_gated_norm_bwd_workspace_size", "gdn_gated_norm_bwd",
+           "gdn_residual_norm_fwd", "gdn_residual_norm_bwd_workspace_size", "gdn_residual_norm_bwd")
 GDN_SEG_AUTO = -1  # include/gdn.h: seg_chunks chosen per call
 GDN_SCRATCH_BYTES = 64 << 20  # include/gdn.h: the static workspace of gdn_fwd_noalloc
 NUM_STAGES = 4
@@ -115,9 +117,9 @@ def _declare(lib):
     lib.gdn_fwd_noalloc.argtypes = [P] + [vp] * 11 + [fp]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_status_string.argtypes = [ctypes.c_int]
-    from . import _layers, _linattn
-    _layers.declare(lib)
-    _linattn.declare(lib)
+    from . import _layers, _linattn, _norms
+    for part in (_layers, _linattn, _norms):
+        part.declare(lib)
     return lib
 
 

@@ -13,10 +13,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgdn.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("gdn_api.hip", "gdn_conv_api.hip", "gdn_scan_api.hip", "gdn_scan_bwd_api.hip",
-                                           "gdn_linattn_api.hip")]
+                                           "gdn_linattn_api.hip", "gdn_norm_api.hip")]
 HEADERS = [os.path.join(CSRC, f) for f in
            ("gdn_common.h", "gdn_kernels.h", "gdn_kda.h", "gdn_decode.h", "gdn_bwd.h", "gdn_layer.h", "gdn_host.h",
-            "gdn_conv.h", "gdn_pack8.h", "gdn_scan.h", "gdn_scan_host.h", "gdn_scan_bwd.h", "gdn_linattn.h")] + [
+            "gdn_conv.h", "gdn_pack8.h", "gdn_scan.h", "gdn_scan_host.h", "gdn_scan_bwd.h", "gdn_linattn.h", "gdn_norm.h")] + [
     os.path.join(INCLUDE, "gdn.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -625,6 +625,83 @@ gdn_status_t gdn_linattn_bwd(const gdn_linattn_params_t *p, const void *q, const
                              float *d_initial_state, void *workspace, size_t workspace_bytes,
                              void *stream);
 
+/* ---- Norms around a block ----------------------------------------------------------
+ * With r(u) = u / sqrt(mean(u^2) + eps) over a row's channels and silu(z) = z / (1 + e^-z):
+ *   gated norm, of a mixer's output head by head:
+ *     y = r(x) * weight * silu(z)     or (gate_first)  r(x * silu(z)) * weight,
+ *     y = r(x) * weight               with z NULL
+ *   residual norm, between two blocks: the norm behind the one, the scaled residual sum and
+ *   the norm ahead of the next:
+ *     p = r(x) * post_weight  (x with post_weight NULL),   s = residual + scale * p,
+ *     h = r(s) * weight
+ *   x, z          [B][T] rows of H*D values, x_stride, z_stride elements apart (0: H*D), dtype;
+ *                 the norm is over each head's D channels
+ *   x, residual   [B][T] rows of C values, x_stride, residual_stride apart (0: C); x in dtype,
+ *                 the residual in residual_dtype (dtype, or GDN_F32)
+ *   weight        [D] or [C] fp32; post_weight, scale  [C] fp32 or NULL (no norm behind the
+ *                 block; 1)
+ *   y             [B][T][H][D] contiguous, dtype, written
+ *   h             [B][T][C] contiguous, dtype; new_residual [B][T][C] contiguous,
+ *                 residual_dtype: s; both written.  new_residual may be residual (in place,
+ *                 dense) and must not overlap it otherwise
+ * All arithmetic is fp32 and every output is rounded once: h is the norm of s as it was
+ * before new_residual was rounded.  dtype: GDN_F32 or GDN_BF16.  D, C 1 to 16384 and fewer
+ * than 2^31 - 65536 rows (GDN_ERR_UNSUPPORTED otherwise); eps >= 0 (GDN_ERR_SHAPE).
+ * Alignment: element size (rows that split into 16 bytes, weights included, are faster);
+ * workspace 256.  Errors as for gdn_fwd, all checked before anything is enqueued.  Outputs
+ * must not overlap inputs or each other.  The same call gives the same bits.  Enqueued on
+ * `stream`; nothing is allocated. */
+typedef struct {
+  int32_t B, T, H, D;
+  int32_t dtype;      /* gdn_dtype_t of x, z and y */
+  int32_t gate_first; /* 1: the gate is applied ahead of the norm */
+  float eps;
+  int64_t x_stride, z_stride; /* elements between tokens, 0 = dense */
+} gdn_gated_norm_params_t;
+
+gdn_status_t gdn_gated_norm_fwd(const gdn_gated_norm_params_t *p, const void *x,
+                                const float *weight, const void *z, void *y, void *stream);
+
+/* Gradients for L = sum <d_y, y>.
+ *   d_y, dx       [B][T][H][D] contiguous, dtype; dz the same (required with z, unused
+ *                 without); dweight [D] fp32; written
+ *   workspace     gdn_gated_norm_bwd_workspace_size() bytes */
+size_t gdn_gated_norm_bwd_workspace_size(const gdn_gated_norm_params_t *p);
+
+gdn_status_t gdn_gated_norm_bwd(const gdn_gated_norm_params_t *p, const void *x,
+                                const float *weight, const void *z, const void *d_y, void *dx,
+                                void *dz, float *dweight, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+typedef struct {
+  int32_t B, T, C;
+  int32_t dtype;          /* gdn_dtype_t of x and h */
+  int32_t residual_dtype; /* of residual and new_residual: dtype or GDN_F32 */
+  float eps;
+  int64_t x_stride, residual_stride; /* elements between tokens, 0 = dense */
+} gdn_residual_norm_params_t;
+
+gdn_status_t gdn_residual_norm_fwd(const gdn_residual_norm_params_t *p, const void *x,
+                                   const void *residual, const float *weight,
+                                   const float *post_weight, const float *scale, void *h,
+                                   void *new_residual, void *stream);
+
+/* Gradients for L = sum <d_h, h> + <d_new_residual, new_residual>; s is formed again.
+ *   x, residual   as gdn_residual_norm_fwd had them (not what it wrote over them)
+ *   d_h           [B][T][C] contiguous, dtype; d_new_residual [B][T][C] contiguous,
+ *                 residual_dtype, or NULL (0)
+ *   dx            [B][T][C] dtype; dresidual [B][T][C] residual_dtype; dweight [C] fp32;
+ *                 dpost_weight, dscale [C] fp32 or NULL (unused without their inputs); written
+ *   workspace     gdn_residual_norm_bwd_workspace_size() bytes */
+size_t gdn_residual_norm_bwd_workspace_size(const gdn_residual_norm_params_t *p);
+
+gdn_status_t gdn_residual_norm_bwd(const gdn_residual_norm_params_t *p, const void *x,
+                                   const void *residual, const float *weight,
+                                   const float *post_weight, const float *scale, const void *d_h,
+                                   const void *d_new_residual, void *dx, void *dresidual,
+                                   float *dweight, float *dpost_weight, float *dscale,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- Activation checkpoints in 8 bits --------------------------------------------
  * What a training step keeps of an activation until its backward pass, in 1 + 1/32
  * bytes per element.  Each row of C channels is held in blocks of 32 (the last may be

@@ -39,17 +39,19 @@ def linattn_inputs(B, T, H, HV, K, V, dtype, seed, S=None, h0=True):
     return d, dict(d_o=r(B, T, HV, V).to(dtype), d_fin=r(S, HV, K, V) * 0.3), ld
 
 
-def close(got, ref, tol, what, each=None):
+def close(got, ref, tol, what, each=None, size=None):
     """Relative 2-norm within `tol`, and every element within `each` (16 tol unless given)
-    of the larger of its own value and the tensor's root mean square."""
+    of the larger of its own value and the tensor's root mean square; both relative to
+    `size` where that is given."""
     got = got.detach().cpu().to(F64)
     assert got.shape == ref.shape, (what, got.shape, ref.shape)
     if not ref.numel():
         return
     assert torch.isfinite(got).all(), what + ": not finite"
-    err, rms = (got - ref).abs(), float(ref.norm()) / ref.numel() ** 0.5
-    rel = float(err.norm() / ref.norm()) if rms else float(err.norm())
-    worst = float((err / ref.abs().clamp(min=rms)).max()) if rms else float(err.max())
+    size = ref if size is None else size
+    err, rms = (got - ref).abs(), float(size.norm()) / ref.numel() ** 0.5
+    rel = float(err.norm() / size.norm()) if rms else float(err.norm())
+    worst = float((err / size.abs().clamp(min=rms)).max()) if rms else float(err.max())
     print("  %-24s rel_l2=%.2e (%.2e) worst=%.2e" % (what, rel, tol, worst), flush=True)
     assert rel <= tol, (what, rel, tol)
     assert worst <= (16 * tol if each is None else each), (what, worst)
