@@ -27,11 +27,13 @@
 //     dk         v     d_o   q     dH^T       backwards
 //
 // Sequences are cut into segments of whole chunks, which run side by side: one launch forms
-// each segment's own contribution to the state, a second joins them (the decay of a segment
-// is known without its data), a third runs every segment from its true start.  Where the
-// heads and sequences alone fill the device there is one segment per sequence and only the
-// third launch.
+// what each segment adds to the state, the next runs every segment from its true start, which
+// it sums from what the segments ahead of it added (their decays are known without their data)
+// -- or, where sequences have many segments, a launch in between forms the starts.  Where the
+// heads and sequences alone fill the device there is one segment per sequence and one launch.
 #pragma once
+#include <type_traits>
+
 #include "gdn_layer.h"
 
 namespace gdn {
@@ -52,13 +54,17 @@ struct AttnRows {
   int div;
 };
 
-// What a pass does with the states: element [i][j] of a head's (rows as operand b, columns as
-// operand c) at i rs + j cs.
+// What a pass does with the states.  The caller's are [sequences][HV][..] with element [i][j]
+// of a head (row as operand b, column as operand c) at i rs + j cs.  Those of segments are in
+// the workspace, [slots][HV] of them, in the order in which lanes hold them (state_place).
+enum { kWholeSequence, kSumSegments, kJoined };
 struct AttnState {
-  const float* start;  // [starts][HV][..], or nullptr: zero
-  float* end;          // [ends][HV][..], or nullptr: not written
+  const float* start;  // or nullptr: zero
+  float* end;          // or nullptr: not written
   int rs, cs;
-  bool by_slot;        // start and end by segment (else by sequence)
+  float* w;            // what segments add to the state, or (kJoined) their starts
+  int mode;
+  bool transposed;     // w was written by a pass whose b and c were the other way round
 };
 
 // log_decay as the base-2 exponent; a^n for a whole n >= 0 (a = 0: 0^0 = 1).
@@ -66,14 +72,15 @@ __device__ __forceinline__ float decay_power(float l2, int n) {
   return n == 0 ? 1.f : __builtin_amdgcn_exp2f((float)n * l2);
 }
 
-// The segment of a slot: sequence n, its number in the sequence, tokens [t0, t0 + len).
+// The segment of a slot: sequence n, its number i of `count` in the sequence, tokens
+// [t0, t0 + len).
 //
 // Packed sequences have slot floor(cu[n] / L) + n + i for segment i of sequence n (L tokens
 // per segment): ceil((y - x) / L) <= floor(y / L) - floor(x / L) + 1 keeps the sequences'
 // slots apart, and no table has to be made on the device first; T / L + N slots hold all.
 // The search for n compares 64 offsets at a time.
 struct Segment {
-  int n, i, t0, len;
+  int n, i, count, t0, len;
 
   __device__ __forceinline__ static int seq_slot(const AttnGeo& g, int n) {
     return (seq_offset(g.cu, n, g.T) / kChunk) / g.chunks + n;
@@ -102,6 +109,7 @@ struct Segment {
       end = max((int64_t)seq_offset(g.cu, n + 1, g.T), start);
       i = slot - seq_slot(g, n);
     }
+    count = (int)((end - start + L - 1) / L);
     t0 = len = 0;
     const int64_t at = start + i * L;
     if (i < 0 || at >= end) return false;
@@ -111,65 +119,111 @@ struct Segment {
   }
 };
 
-// A chunk's rows in LDS: 64 rows of D, padded so that the transposed reads below (four rows
-// of 32 bytes per 16 lanes, two such groups at a time) meet no bank twice.
-template <typename E, int D> struct AttnTile {
-  static constexpr int LD = D + (sizeof(E) == 2 ? 16 : 4);
-  static constexpr int VECS = D * (int)sizeof(E) / 16;  // 16-byte vectors per row
-  static constexpr int PER = kChunk * VECS / 256;       // per thread
-  E x[kChunk * LD];
+// Block id -> (slot, value head): the G value heads of a (slot, key head) go to one XCD
+// (workgroups are dispatched to the 8 XCDs round-robin by id), one after the other, so that
+// the query and key rows they share come through one L2.  False for the ids that fill up the
+// last group of eight.
+__device__ __forceinline__ bool attn_block(const AttnGeo& g, int b, int& slot, int& hv) {
+  const int j = b >> 3, unit = j / g.G * 8 + (b & 7);
+  slot = unit / g.H;
+  hv = (unit - slot * g.H) * g.G + j % g.G;
+  return slot < g.slots;
+}
+
+// A state of KD x VD lies in the lanes as tiles of 16 x 16: tile kt = 2 kb + j holds, in lane
+// (g, m) and element r, row 32 kb + 8 g + 4 j + r and column 16 ct + m, so that the two tiles
+// of a block of 32 rows are a fragment whose lane holds eight consecutive rows, which an
+// operand's fragment reads from LDS as 16 bytes.
+__device__ __forceinline__ int state_row(int kt) { return 32 * (kt >> 1) + 8 * (lane_id() >> 4) + 4 * (kt & 1); }
+// A lane's four elements of a tile in the workspace.
+__device__ __forceinline__ int state_place(int kt, int ct, int cts) { return ((kt * cts + ct) * 64 + lane_id()) * 4; }
+// The same of a state that was written the other way round, with KD columns: its element [col][row]
+// for a lane's row (state_row(kt) + r) and column (c + m, c a multiple of 16), as a lane's part
+// (in bytes) and a uniform one.
+template <int KD> __device__ __forceinline__ uint32_t state_lane_transposed() {
+  const int g = lane_id() >> 4, m = lane_id() & 15;
+  return 4 * ((((m >> 2 & 1) * (KD / 16) + (g >> 1)) * 64 + (m >> 3) * 16 + 8 * (g & 1)) * 4 + (m & 3));
+}
+template <int KD> __device__ __forceinline__ int state_transposed(int kt, int r, int c) {
+  return ((c / 32 * 2 * (KD / 16) + (kt >> 1) * 2) * 64 + c / 8 % 4 * 16 + 4 * (kt & 1) + r) * 4;
+}
+
+// A wave per 16 columns of the state.
+constexpr int attn_threads(int vd) { return 4 * vd; }
+
+// A chunk's rows in LDS: 64 rows of D elements in 16-byte pieces, whose places within a row are
+// exchanged (piece c of row r is at c ^ turn(r)) so that neither reads of one piece of 16 rows
+// nor the transposed reads below (two or four pieces of four rows) meet a bank twice.
+template <typename E, int D, int THREADS> struct AttnTile {
+  static constexpr int VECS = D * (int)sizeof(E) / 16;     // pieces per row
+  static constexpr int STEP = THREADS / VECS;              // rows between a thread's pieces
+  static constexpr int PER = kChunk / STEP;                // pieces per thread
+  E x[kChunk * D];
+  __device__ __forceinline__ static int turn(int row) {
+    if (sizeof(E) == 4) return (row >> 3 & 3) << 2 | (row & 3);  // (its columns are read element by element)
+    return VECS == 8 ? (row >> 1 & 1) << 2 | (row >> 2 & 3) : (row & 3) << 2 | (row >> 2 & 3);
+  }
+  // the elements from [row][col] on, to the end of their piece
+  __device__ __forceinline__ E* at(int row, int col) {
+    constexpr int N = 16 / (int)sizeof(E);
+    return x + row * D + ((col / N) ^ turn(row)) * N + col % N;
+  }
+  __device__ __forceinline__ const E* at(int row, int col) const { return const_cast<AttnTile*>(this)->at(row, col); }
+  struct Rows {
+    u32x4 r[PER];
+  };
+  // The rows of a chunk, as loaded: rows from `len` on are the last one's again (whatever is
+  // formed from them is not used), so that no row of another sequence is read.  `base` is
+  // uniform, `ld` in bytes (offsets within a chunk are 32 bits).
+  __device__ __forceinline__ static void fetch(Rows& f, const void* base, uint32_t ld, int len) {
+    const int row = threadIdx.x / VECS, col = threadIdx.x % VECS * 16;
+    Global<const char> p = (Global<const char>)base;
+    if (len == kChunk) {
+      const uint32_t off = lane_offset(row * ld + col);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) f.r[i] = *(Global<const u32x4>)(p + (uint64_t)(i * STEP) * ld + off);
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        f.r[i] = *(Global<const u32x4>)(p + lane_offset(min(row + i * STEP, len - 1) * ld + col));
+    }
+  }
+  __device__ __forceinline__ void place(const Rows& f) {
+    const int row = threadIdx.x / VECS, col = threadIdx.x % VECS * (16 / (int)sizeof(E));
+#pragma unroll
+    for (int i = 0; i < PER; ++i) *reinterpret_cast<u32x4*>(at(row + i * STEP, col)) = f.r[i];
+  }
+  // k32 fragment of a row, whose lane holds eight consecutive elements: 32 kb + 8 g on
+  __device__ __forceinline__ Frag<E> of_row(int row, int kb) const {
+    const int c = 32 * kb + 8 * (lane_id() >> 4);
+    if constexpr (sizeof(E) == 2) return {*reinterpret_cast<const bf16x8*>(at(row, c))};
+    else return {*reinterpret_cast<const f32x4*>(at(row, c)), *reinterpret_cast<const f32x4*>(at(row, c + 4))};
+  }
+  // k32 fragment of rows s0 .. s0 + 31 in the same order, the lane's column c0 + APART (m / 4) +
+  // m % 4: ds_read_b64_tr_b16 gives lane m of a group of 16 element m % 4 of what its lanes
+  // 4 i + m / 4 (i = 0..3) address
+  template <int APART> __device__ __forceinline__ Frag<E> of_columns(int s0, int c0) const {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    const int g = lane_id() >> 4, m = lane_id() & 15;
+    if constexpr (sizeof(E) == 2) {
+      const int row = s0 + 8 * g + (m >> 2), col = c0 + APART * (m & 3);
+      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at(row, col));
+      const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at(row + 4, col));
+      const auto both = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+      return {__builtin_bit_cast(bf16x8, both)};
+    } else {
+      const int row = s0 + 8 * g, col = c0 + APART * (m >> 2) + (m & 3);
+      Frag<E> f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f.lo[i] = *at(row + i, col);
+        f.hi[i] = *at(row + 4 + i, col);
+      }
+      return f;
+    }
+  }
 };
-
-constexpr int kAttnThreads = 256;
-
-// The rows of a chunk, as loaded: rows from `len` on are the last one's again (whatever is
-// formed from them is not used), so that no row of another sequence is read.
-template <typename E, int D, int PER>
-__device__ __forceinline__ void attn_fetch(u32x4 (&r)[PER], const E* base, int64_t ld, int len) {
-  using Tl = AttnTile<E, D>;
-  static_assert(PER == Tl::PER, "");
-#pragma unroll
-  for (int i = 0; i < Tl::PER; ++i) {
-    const int idx = threadIdx.x + kAttnThreads * i;
-    const int row = min(idx / Tl::VECS, len - 1), col = idx % Tl::VECS;
-    r[i] = *reinterpret_cast<const u32x4*>(base + row * ld + col * (16 / (int)sizeof(E)));
-  }
-}
-template <typename E, int D, int PER>
-__device__ __forceinline__ void attn_place(AttnTile<E, D>& t, const u32x4 (&r)[PER]) {
-  using Tl = AttnTile<E, D>;
-  static_assert(PER == Tl::PER, "");
-#pragma unroll
-  for (int i = 0; i < Tl::PER; ++i) {
-    const int idx = threadIdx.x + kAttnThreads * i;
-    *reinterpret_cast<u32x4*>(t.x + idx / Tl::VECS * Tl::LD + idx % Tl::VECS * (16 / (int)sizeof(E))) = r[i];
-  }
-}
-
-// k32 fragment of 32 rows from s0 on, the lane's column c0 + lane % 16: ds_read_b64_tr_b16
-// gives a lane of a group of 16 the four values of its column from the four rows that the
-// group's lanes address (four lanes of 8 bytes per row).
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ Frag<bf16> frag_from_columns(const bf16* x, int ld, int s0, int c0) {
-  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-  const int g = lane_id() >> 4, m = lane_id() & 15;
-  const bf16* p = x + (s0 + 4 * g + (m >> 2)) * ld + c0 + 4 * (m & 3);
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * ld));
-  const auto both = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-  return {__builtin_bit_cast(bf16x8, both)};
-}
-__device__ __forceinline__ Frag<float> frag_from_columns(const float* x, int ld, int s0, int c0) {
-  const int g = lane_id() >> 4, m = lane_id() & 15;
-  const float* p = x + (s0 + 4 * g) * ld + c0 + m;
-  Frag<float> f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f.lo[i] = p[i * ld];
-    f.hi[i] = p[(16 + i) * ld];
-  }
-  return f;
-}
 
 // c_s w_s as a sum of NP fragments.  A bf16 operand of the state's update is c_s (8 bits)
 // times an fp32 weight: one bf16 would leave 2^-9 of every state, which fp32 states must not
@@ -196,227 +250,378 @@ __device__ __forceinline__ void weighted_parts(const Frag<float>& c, const float
   }
 }
 
-// Rows [from, T) of head hv of the output set to 0, shared out over the slots.
+// Rows behind the last sequence, of head hv's columns of the output, set to 0: shared out over
+// the slots.
 template <typename OT, int D>
 __device__ __forceinline__ void attn_zero_rest(const AttnGeo& g, int hv, int slot, OT* out) {
-  constexpr int PER_ROW = D * (int)sizeof(OT) / 16, ROWS = kAttnThreads / PER_ROW;
+  constexpr int PER_ROW = D * (int)sizeof(OT) / 16, ROWS = attn_threads(D) / PER_ROW;
   const int sub = threadIdx.x / PER_ROW, col = threadIdx.x % PER_ROW;
   for (int64_t t = seq_offset(g.cu, g.N, g.T) + (int64_t)slot * ROWS + sub; t < g.T; t += (int64_t)g.slots * ROWS)
     *reinterpret_cast<u32x4*>(out + (t * g.HV + hv) * D + col * (16 / (int)sizeof(OT))) = u32x4{0, 0, 0, 0};
 }
 
-// One pass over a segment of one value head by four waves; wave w owns columns
-// [w VD/4, (w+1) VD/4) of the state and of the output.  KD, VD: widths of operands a and b,
-// and of c.  OUT: rows of the output are formed (else the state alone, from zero).  NP: parts
-// of the update's operands.
-template <typename E, int KD, int VD, bool OUT> struct AttnLds {
-  AttnTile<E, KD> b;
-  AttnTile<E, VD> c;
+// The phases of a chunk stay apart: mixed by the scheduler they need more registers than there are.
+#define ATTN_PHASE __builtin_amdgcn_sched_barrier(0)
+
+// Within a phase (bf16): `ahead` reads of LDS, then per step `mfma` products and `reads` more, so
+// that products find their operands there.  Left alone the scheduler saves registers and waits
+// for every read.
+template <typename E, int AHEAD, int STEPS, int MFMA, int READS> __device__ __forceinline__ void attn_interleave() {
+  if constexpr (sizeof(E) == 2) {
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, MFMA, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+    }
+  }
+}
+
+// H <- a H + b^T (c weighted), H the state's tiles: NP parts of the weighted operand.
+template <int NP, typename E, int KT, typename B, typename C>
+__device__ __forceinline__ void attn_update(f32x4 (&H)[KT], const B& b, const C& c, int col0, const float* weight) {
+  const int g = lane_id() >> 4;
+#pragma unroll
+  for (int sb = 0; sb < kChunk / 32; ++sb) {
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      const f32x4 q = *reinterpret_cast<const f32x4*>(weight + 32 * sb + 8 * g + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[i + j] = q[j];
+    }
+    Frag<E> vw[NP];
+    weighted_parts<NP>(c.template of_columns<4>(32 * sb, col0), w, vw);
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+      const Frag<E> k = b.template of_columns<8>(32 * sb, 32 * (kt >> 1) + 4 * (kt & 1));
+#pragma unroll
+      for (int p = 0; p < NP; ++p) mma_k32(H[kt], k, vw[p]);
+    }
+    attn_interleave<E, 4 + 6, KT, NP, 2>();
+  }
+}
+
+// One pass over a segment of one value head; a wave per 16 columns of the state and of the
+// output.  KD, VD: widths of operands a and b, and of c.  OUT: rows of the output are formed
+// (else what the segment adds to the state).
+//
+// Per chunk: rows from registers (loaded a chunk ahead) to LDS; the weighted products a.b, tiles of
+// 16 x 16 shared out over the waves, to LDS as the next product's operand; the state's part and
+// the products' part of the output, whose rows go through LDS to be stored whole; the state's
+// update.  Powers of the decay are formed by one lane each and read from LDS: of the products
+// (`gap`) once, the weights of a chunk's update and of the state in each of its rows per chunk.
+template <typename E, typename OT, int KD, int VD, bool OUT> struct AttnLds {
+  AttnTile<E, KD, attn_threads(VD)> b;
+  AttnTile<E, VD, attn_threads(VD)> c;
+  float update[kChunk];
 };
-template <typename E, int KD, int VD> struct AttnLds<E, KD, VD, true> {
-  AttnTile<E, KD> b;
-  AttnTile<E, VD> c;
-  AttnTile<E, KD> a;
-  static constexpr int PLD = kChunk + (sizeof(E) == 2 ? 8 : 4);
-  E p[kChunk * PLD];
+template <typename E, typename OT, int KD, int VD> struct AttnLds<E, OT, KD, VD, true> {
+  AttnTile<E, KD, attn_threads(VD)> b;
+  AttnTile<E, VD, attn_threads(VD)> c;
+  AttnTile<E, KD, attn_threads(VD)> a;
+  AttnTile<OT, VD, attn_threads(VD)> o;
+  AttnTile<E, kChunk, attn_threads(VD)> p;
+  float update[kChunk], inter[kChunk], gap[2 * kChunk];  // gap: 0 for rows that are not seen
 };
 
-template <typename E, typename OT, int KD, int VD, bool REV, bool OUT, int NP>
-__global__ __launch_bounds__(kAttnThreads, sizeof(E) == 2 ? 2 : 1) void gdn_linattn_kernel(
-    AttnGeo geo, AttnRows ar, AttnRows br, AttnRows cr, const float* __restrict__ log_decay, AttnState st,
-    OT* __restrict__ out, float s_intra, float s_inter, float s_update) {
-  constexpr int CT = VD / 64, KT = KD / 16, TT = kChunk / 16;
-  using Lds = AttnLds<E, KD, VD, OUT>;
-  __shared__ __attribute__((aligned(16))) char smem[sizeof(Lds)];
+struct AttnPass {
+  AttnRows a, b, c;
+  AttnState st;
+  void* out;
+  float s_intra, s_inter, s_update;  // what products a.b, the state's part and its update are scaled by
+};
+
+template <typename E, typename OT, int KD, int VD, bool REV, bool OUT>
+__device__ __forceinline__ void attn_pass(const AttnGeo& geo, int block, const AttnPass& x,
+                                          const float* __restrict__ log_decay, char* smem) {
+  const AttnRows &ar = x.a, &br = x.b, &cr = x.c;
+  const AttnState& st = x.st;
+  OT* out = static_cast<OT*>(x.out);
+  const float s_intra = x.s_intra, s_inter = x.s_inter, s_update = x.s_update;
+  constexpr int KT = KD / 16, TT = kChunk / 16, THREADS = attn_threads(VD), WAVES = VD / 16;
+  using Lds = AttnLds<E, OT, KD, VD, OUT>;
+  using KTile = AttnTile<E, KD, THREADS>;
+  using VTile = AttnTile<E, VD, THREADS>;
+  using OTile = AttnTile<OT, VD, THREADS>;
   Lds& L = *reinterpret_cast<Lds*>(smem);
 
   int hv, slot;
-  xcd_slot_block(blockIdx.x, geo.H, geo.G, geo.slots, hv, slot);
+  if (!attn_block(geo, block, slot, hv)) return;
   if constexpr (OUT) {
     if (geo.cu && geo.zero) attn_zero_rest<OT, VD>(geo, hv, slot, out);
   }
   Segment seg;
-  // (a sequence without tokens passes its state on)
-  if (!seg.find(geo, slot) && (!st.end || st.by_slot || seg.i != 0)) return;
+  const bool tokens = seg.find(geo, slot);
+  // in the order of the pass: segments done before this one, and whether it is the last
+  const int before = REV ? seg.count - 1 - seg.i : seg.i;
+  const bool last = before >= seg.count - 1;
+  if constexpr (OUT) {
+    // (a sequence without tokens passes its state on)
+    if (!tokens && !(st.end && seg.i == 0)) return;
+  } else {
+    if (!tokens || last) return;  // nobody asks what the last segment adds
+  }
   const int nch = (seg.len + kChunk - 1) / kChunk;
   const int lane = lane_id(), g = lane >> 4, m = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col0 = wave * 16 * CT;
+  const int col0 = 16 * wave;
   const float l2 = log_decay[hv] * kLog2e;
 
   const E* ap = static_cast<const E*>(ar.p) + (int64_t)seg.t0 * ar.ld + (hv / ar.div) * KD;
   const E* bp = static_cast<const E*>(br.p) + (int64_t)seg.t0 * br.ld + (hv / br.div) * KD;
   const E* cp = static_cast<const E*>(cr.p) + (int64_t)seg.t0 * cr.ld + (hv / cr.div) * VD;
 
-  // the state: tile kt holds rows 16 kt + 4 g + r, column col0 + 16 ct + m
-  f32x4 H[KT][CT];
-  const int64_t sbase = ((int64_t)(st.by_slot ? slot : seg.n) * geo.HV + hv) * (KD * VD);
-#pragma unroll
-  for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      H[kt][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (OUT && st.start) {
-        const float* s = st.start + sbase + (int64_t)(16 * kt + 4 * g) * st.rs + (col0 + 16 * ct + m) * st.cs;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) H[kt][ct][r] = s[r * st.rs];
-      }
-    }
-
-  u32x4 ra[OUT ? AttnTile<E, KD>::PER : 1], rb[AttnTile<E, KD>::PER], rc[AttnTile<E, VD>::PER];
-  auto fetch = [&](int c) {
-    const int n = min(kChunk, seg.len - c * kChunk);
-    if constexpr (OUT) attn_fetch<E, KD>(ra, ap + (int64_t)c * kChunk * ar.ld, ar.ld, n);
-    attn_fetch<E, KD>(rb, bp + (int64_t)c * kChunk * br.ld, br.ld, n);
-    attn_fetch<E, VD>(rc, cp + (int64_t)c * kChunk * cr.ld, cr.ld, n);
+  struct Rows {
+    typename KTile::Rows a, b;
+    typename VTile::Rows c;
   };
-  if (nch > 0) fetch(REV ? nch - 1 : 0);
+  Rows ahead;  // the next chunk's
+  auto fetch_ab = [&](int it) {
+    const int c = REV ? nch - 1 - it : it, n = min(kChunk, seg.len - c * kChunk);
+    if constexpr (OUT) KTile::fetch(ahead.a, ap + (int64_t)c * kChunk * ar.ld, (uint32_t)(ar.ld * sizeof(E)), n);
+    KTile::fetch(ahead.b, bp + (int64_t)c * kChunk * br.ld, (uint32_t)(br.ld * sizeof(E)), n);
+  };
+  auto fetch_c = [&](int it) {
+    const int c = REV ? nch - 1 - it : it, n = min(kChunk, seg.len - c * kChunk);
+    VTile::fetch(ahead.c, cp + (int64_t)c * kChunk * cr.ld, (uint32_t)(cr.ld * sizeof(E)), n);
+  };
+  if (nch > 0) {
+    fetch_ab(0);
+    fetch_c(0);
+  }
 
-  for (int it = 0; it < nch; ++it) {
-    const int c = REV ? nch - 1 - it : it;
-    const int n = min(kChunk, seg.len - c * kChunk);
-    __syncthreads();  // the last chunk's reads are done
-    if constexpr (OUT) attn_place<E, KD>(L.a, ra);
-    attn_place<E, KD>(L.b, rb);
-    attn_place<E, VD>(L.c, rc);
-    __syncthreads();
-    if (it + 1 < nch) fetch(REV ? c - 1 : c + 1);
-
-    if constexpr (OUT) {
-      constexpr int ALD = AttnTile<E, KD>::LD;
-      // rows of operand a: tile `wave`; the weighted products with every row of b that they see
-      {
-        const int t = 16 * wave + m;
-        Frag<E> fa[KD / 32];
+  f32x4 H[KT];
 #pragma unroll
-        for (int kb = 0; kb < KD / 32; ++kb) fa[kb] = frag_from_row(L.a.x + t * ALD + 32 * kb);
-#pragma unroll
-        for (int sg = 0; sg < TT; ++sg) {
-          f32x4 p = {0.f, 0.f, 0.f, 0.f};
-          if (REV ? sg >= wave : sg <= wave) {
-#pragma unroll
-            for (int kb = 0; kb < KD / 32; ++kb)
-              mma_k32(p, frag_from_row(L.b.x + (16 * sg + m) * ALD + 32 * kb), fa[kb]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int s = 16 * sg + 4 * g + r, gap = REV ? s - t : t - s;
-              // (a select, so that nothing of a masked product stays)
-              p[r] = gap >= 0 && s < n ? p[r] * (s_intra * decay_power(l2, gap)) : 0.f;
-            }
-          }
-          // rows in blocks of 32 of which at least one is seen are read below
-          if (REV ? sg >= (wave & ~1) : sg <= (wave | 1))
-            *reinterpret_cast<Quad<E>*>(L.p + t * Lds::PLD + 16 * sg + 4 * g) = make_quad<E>(p);
-        }
-      }
-      // the state's part: O^T = H^T a^T, then weighted by row
-      f32x4 acc[CT][TT];
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int tt = 0; tt < TT; ++tt) acc[ct][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int kb = 0; kb < KD / 32; ++kb) {
-        Frag<E> h[CT];
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) h[ct] = frag_from_tiles<E>(H[2 * kb][ct], H[2 * kb + 1][ct]);
-#pragma unroll
-        for (int tt = 0; tt < TT; ++tt) {
-          const Frag<E> a = frag_from_row(L.a.x + (16 * tt + m) * ALD + 32 * kb);
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) mma_k32(acc[ct][tt], h[ct], a);
-        }
-      }
-#pragma unroll
-      for (int tt = 0; tt < TT; ++tt) {
-        const int t = 16 * tt + m;
-        const float w = s_inter * decay_power(l2, REV ? max(n - 1 - t, 0) : t + 1);
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) acc[ct][tt] *= w;
-      }
-      __syncthreads();  // the weighted products are there
-#pragma unroll
-      for (int sb = 0; sb < kChunk / 32; ++sb) {
-        Frag<E> v[CT];
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) v[ct] = frag_from_columns(L.c.x, AttnTile<E, VD>::LD, 32 * sb, col0 + 16 * ct);
-#pragma unroll
-        for (int tt = 0; tt < TT; ++tt) {
-          if (REV ? 2 * sb + 1 < tt : 2 * sb > tt) continue;
-          const Frag<E> p = frag_from_row(L.p + (16 * tt + m) * Lds::PLD + 32 * sb);
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) mma_k32(acc[ct][tt], v[ct], p);
-        }
-      }
-      OT* orow = out + ((int64_t)(seg.t0 + c * kChunk) * geo.HV + hv) * VD + col0;
-#pragma unroll
-      for (int tt = 0; tt < TT; ++tt) {
-        const int t = 16 * tt + m;
-        if (t < n) {
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct)
-            *reinterpret_cast<Quad<OT>*>(orow + (int64_t)t * geo.HV * VD + 16 * ct + 4 * g) = make_quad<OT>(acc[ct][tt]);
-        }
-      }
-    }
-
-    if (!OUT || st.end || it + 1 < nch) {
-      const float a = decay_power(l2, n);
+  for (int kt = 0; kt < KT; ++kt) H[kt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if constexpr (OUT) {
+    const bool joined = st.mode == kJoined && tokens;
+    if (st.start && !joined) {
+      const float* s = st.start + ((int64_t)seg.n * geo.HV + hv) * (KD * VD) + (col0 + m) * st.cs;
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) H[kt][ct] *= a;
+        for (int r = 0; r < 4; ++r) H[kt][r] = s[(state_row(kt) + r) * st.rs];
+    }
+    // H <- a^len H + what the segment adds, over the segments done before, AHEAD of them loaded
+    // at a time; or the start itself
+    const int sums = joined ? 1 : st.mode == kSumSegments ? before : 0;
+    constexpr int AHEAD = sizeof(E) == 2 ? 4 : 1;
+    for (int j0 = 0; j0 < sums; j0 += AHEAD) {
+      f32x4 e[AHEAD][KT];
 #pragma unroll
-      for (int sb = 0; sb < kChunk / 32; ++sb) {
-        float w[8];
+      for (int j = 0; j < AHEAD; ++j) {
+        const int k = min(j0 + j, sums - 1);
+        const int at = joined ? slot : REV ? slot + before - k : slot - before + k;
+        const float* w = st.w + ((int64_t)at * geo.HV + hv) * (KD * VD);
+        if (!st.transposed) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int s = 32 * sb + (i < 4 ? 4 * g + i : 12 + 4 * g + i);
-          w[i] = s < n ? s_update * decay_power(l2, REV ? s + 1 : n - 1 - s) : 0.f;
+          for (int kt = 0; kt < KT; ++kt) e[j][kt] = *reinterpret_cast<const f32x4*>(w + state_place(kt, wave, VD / 16));
+        } else {
+          const uint32_t off = lane_offset(state_lane_transposed<KD>());
+#pragma unroll
+          for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              e[j][kt][r] = *(Global<const float>)((Global<const char>)(w + state_transposed<KD>(kt, r, col0)) + off);
         }
-        Frag<E> v[CT][NP];
+      }
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-          weighted_parts<NP>(frag_from_columns(L.c.x, AttnTile<E, VD>::LD, 32 * sb, col0 + 16 * ct), w, v[ct]);
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-          const Frag<E> k = frag_from_columns(L.b.x, AttnTile<E, KD>::LD, 32 * sb, 16 * kt);
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-            for (int p = 0; p < NP; ++p) mma_k32(H[kt][ct], k, v[ct][p]);
+      for (int j = 0; j < AHEAD; ++j) {
+        if (j0 + j >= sums) break;
+        const int64_t len = (int64_t)geo.chunks * kChunk;
+        // (backwards, the sequence's last segment may be short; forwards those before are whole)
+        int64_t n = len;
+        if (REV && j0 + j == 0) {
+          const int64_t end = geo.cu ? seq_offset(geo.cu, seg.n + 1, geo.T) : (int64_t)(seg.n + 1) * geo.T;
+          n = end - (seg.t0 - (int64_t)seg.i * len) - (int64_t)(seg.count - 1) * len;
         }
+        // (a start replaces what is there: nothing, times 0)
+        const float a = joined ? 0.f : decay_power(l2, (int)n);
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) H[kt] = H[kt] * a + e[j][kt];
       }
     }
+    if (wave < 2) L.gap[threadIdx.x] = wave == 0 ? 0.f : s_intra * decay_power(l2, lane);
   }
 
-  if (st.end) {
+  // the output's rows of chunk `it`, from LDS
+  auto store = [&](int it) {
+    if constexpr (OUT) {
+      const int c = REV ? nch - 1 - it : it, n = min(kChunk, seg.len - c * kChunk);
+      const uint32_t row = (uint32_t)(geo.HV * VD * sizeof(OT));
+      Global<char> o = (Global<char>)(out + ((int64_t)(seg.t0 + c * kChunk) * geo.HV + hv) * VD);
+      const int r0 = threadIdx.x / OTile::VECS, col = threadIdx.x % OTile::VECS * 16;
+      const uint32_t off = lane_offset(r0 * row + col);
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        float* s = st.end + sbase + (int64_t)(16 * kt + 4 * g) * st.rs + (col0 + 16 * ct + m) * st.cs;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) s[r * st.rs] = H[kt][ct][r];
+      for (int i = 0; i < OTile::PER; ++i) {
+        const int r = r0 + i * OTile::STEP;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(L.o.at(r, col / (int)sizeof(OT)));
+        if (r < n) *(Global<u32x4>)(o + (uint64_t)(i * OTile::STEP) * row + off) = v;
       }
+    }
+  };
+
+  auto chunk = [&](int it, auto more) {
+    const int c = REV ? nch - 1 - it : it;
+    const int n = min(kChunk, seg.len - c * kChunk);
+    if (it) __syncthreads();  // the last chunk's reads are done, its rows of the output written
+    if constexpr (OUT) L.a.place(ahead.a);
+    L.b.place(ahead.b);
+    L.c.place(ahead.c);
+    if (wave == 0) L.update[lane] = lane < n ? s_update * decay_power(l2, REV ? lane + 1 : n - 1 - lane) : 0.f;
+    if constexpr (OUT) {
+      if (wave == 1) L.inter[lane] = lane < n ? s_inter * decay_power(l2, REV ? n - 1 - lane : lane + 1) : 0.f;
+    }
+    __syncthreads();
+    if constexpr (decltype(more)::value) fetch_ab(it + 1);
+    if constexpr (!OUT && decltype(more)::value) fetch_c(it + 1);
+    if (it) store(it - 1);
+
+    if constexpr (OUT) {
+      // the weighted products of a tile of rows of a with those rows of b that they see, two
+      // tiles of b at a time; two waves share a tile of a where there are eight
+      {
+        constexpr int SHARE = WAVES / TT;
+        const int tt = wave / SHARE, t = 16 * tt + m;
+        Frag<E> fa[KD / 32];
+#pragma unroll
+        for (int kb = 0; kb < KD / 32; ++kb) fa[kb] = L.a.of_row(t, kb);
+#pragma unroll
+        for (int i = 0; i < 2 / SHARE; ++i) {
+          const int sb = SHARE == 2 ? wave % 2 : i;
+          // (blocks of 32 rows of which none is seen are not read below)
+          if (REV ? 2 * sb + 1 < tt : 2 * sb > tt) continue;
+          f32x4 p[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+          float w[2][4];
+          const int apart = 32 * sb + 4 * g - t;  // s - t at j = r = 0
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) w[j][r] = L.gap[kChunk + (REV ? 1 : -1) * (apart + 16 * j + r)];
+#pragma unroll
+          for (int kb = 0; kb < KD / 32; ++kb)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) mma_k32(p[j], L.b.of_row(32 * sb + 16 * j + m, kb), fa[kb]);
+          attn_interleave<E, 16, KD / 32, 2, 0>();
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              asm("" : "+v"(w[j][r]));  // (read above, and not behind a branch here)
+              // (a select, so that nothing of a masked product stays)
+              const int gap = apart + 16 * j + r;
+              p[j][r] = (REV ? gap >= 0 && 32 * sb + 4 * g + 16 * j + r < n : gap <= 0) ? p[j][r] * w[j][r] : 0.f;
+            }
+            *reinterpret_cast<Quad<E>*>(L.p.at(t, 32 * sb + 16 * j + 4 * g)) = make_quad<E>(p[j]);
+          }
+          ATTN_PHASE;
+        }
+      }
+      if constexpr (decltype(more)::value) fetch_c(it + 1);  // (apart from the others: loads queue)
+      // the state's part: O^T = H^T a^T, then weighted by row
+      f32x4 acc[TT];
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt) acc[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kb = 0; kb < KD / 32; ++kb) {
+        const Frag<E> h = frag_from_tiles<E>(H[2 * kb], H[2 * kb + 1]);
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) mma_k32(acc[tt], h, L.a.of_row(16 * tt + m, kb));
+      }
+      attn_interleave<E, 6, (KD / 32) * TT, 1, 1>();
+      ATTN_PHASE;
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt) acc[tt] *= L.inter[16 * tt + m];
+      __syncthreads();  // the weighted products are there
+#pragma unroll
+      for (int sb = 0; sb < kChunk / 32; ++sb) {
+        const Frag<E> v = L.c.template of_columns<4>(32 * sb, col0);
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) {
+          if (REV ? 2 * sb + 1 < tt : 2 * sb > tt) continue;
+          mma_k32(acc[tt], v, L.p.of_row(16 * tt + m, sb));
+        }
+      }
+      attn_interleave<E, 10, 1, 6, 0>();
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt)
+        *reinterpret_cast<Quad<OT>*>(L.o.at(16 * tt + m, col0 + 4 * g)) = make_quad<OT>(acc[tt]);
+    }
+    ATTN_PHASE;
+    const bool end = OUT && last && st.end;
+    if (!OUT || end || it + 1 < nch) {
+      const float a = decay_power(l2, n);
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) H[kt] *= a;
+      // three parts where the states go out as fp32, two where they only meet bf16 operands
+      if constexpr (sizeof(E) == 4) attn_update<1, E>(H, L.b, L.c, col0, L.update);
+      else if (!OUT || end) attn_update<3, E>(H, L.b, L.c, col0, L.update);
+      else attn_update<2, E>(H, L.b, L.c, col0, L.update);
+    }
+  };
+  // (the loop's loads are unconditional: the compiler then knows how many are under way)
+  int it = 0;
+  for (; it + 1 < nch; ++it) chunk(it, std::true_type{});
+  if (nch > 0) chunk(it, std::false_type{});
+
+  if constexpr (OUT) {
+    if (nch > 0) {
+      __syncthreads();
+      store(nch - 1);
+    }
+    if (last && st.end) {
+      float* s = st.end + ((int64_t)seg.n * geo.HV + hv) * (KD * VD) + (col0 + m) * st.cs;
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[(state_row(kt) + r) * st.rs] = H[kt][r];
+    }
+  } else {
+    float* w = st.w + ((int64_t)slot * geo.HV + hv) * (KD * VD);
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(w + state_place(kt, wave, VD / 16)) = H[kt];
   }
 }
 
-// Segments joined: per sequence, head and four elements of the state, in the segments' order
-// (REV: from the last),  w[segment] <- cur;  cur <- a^len cur + (what w[segment] held),
-// from `start` (or 0); the last cur goes to `end`.  Sequences without tokens pass `start` on
-// (w is not read where there is no token at all).
-// Loads run kAttnAhead segments ahead.
+template <typename E, int VD, bool OUT> constexpr int attn_waves() {  // per SIMD, that registers are left for
+  return sizeof(E) == 4 || (VD == 64 && OUT) ? 1 : 2;
+}
+
+template <typename E, typename OT, int KD, int VD, bool REV, bool OUT>
+__global__ __launch_bounds__(attn_threads(VD), (attn_waves<E, VD, OUT>())) void gdn_linattn_kernel(
+    AttnGeo geo, AttnPass x, const float* __restrict__ log_decay) {
+  __shared__ __attribute__((aligned(16))) char smem[sizeof(AttnLds<E, OT, KD, VD, OUT>)];
+  attn_pass<E, OT, KD, VD, REV, OUT>(geo, blockIdx.x, x, log_decay, smem);
+}
+
+// The backward pass's passes of one kind in one launch, `blocks` workgroups each, where keys and
+// values are of one width D: what segments add to H^T and dH (two passes), or dq, dk and dv.
+// OT: the type of dq and dk.
+template <typename E, typename OT, int D, bool OUT>
+__global__ __launch_bounds__(attn_threads(D), (attn_waves<E, D, OUT>())) void gdn_linattn_bwd_kernel(
+    AttnGeo geo, AttnPass q, AttnPass k, AttnPass v, const float* __restrict__ log_decay, int blocks) {
+  __shared__ __attribute__((aligned(16))) char smem[sizeof(AttnLds<E, OT, D, D, OUT>)];
+  static_assert(sizeof(smem) >= sizeof(AttnLds<E, E, D, D, OUT>), "");
+  const int role = blockIdx.x / blocks, block = blockIdx.x - role * blocks;
+  if (role == 0) attn_pass<E, OT, D, D, false, OUT>(geo, block, q, log_decay, smem);
+  else if (OUT && role == 1) attn_pass<E, OT, D, D, true, OUT>(geo, block, k, log_decay, smem);
+  else attn_pass<E, E, D, D, true, OUT>(geo, block, v, log_decay, smem);
+}
+
+// The starts of sequences' segments: per sequence, head and four elements of the state, in the
+// segments' order (REV: from the last),  w[segment] <- cur;  cur <- a^len cur + (what
+// w[segment] held),  from `start` (or 0).  Loads run kAttnAhead segments ahead.
 constexpr int kAttnAhead = 8;
 
-template <int KV, bool REV>
+template <int KD, int VD, bool REV>
 __global__ __launch_bounds__(256) void gdn_linattn_join_kernel(AttnGeo geo, const float* __restrict__ log_decay,
-                                                               const float* __restrict__ start, float* w,
-                                                               float* __restrict__ end) {
-  constexpr int PER = KV / 4 / 256;  // workgroups per head
+                                                               const float* __restrict__ start, int rs, int cs,
+                                                               float* w) {
+  constexpr int KV = KD * VD, PER = KV / 4 / 256;  // workgroups per head
   const int part = blockIdx.x % PER, unit = blockIdx.x / PER;
   const int hv = unit % geo.HV, n = unit / geo.HV;
-  const int64_t at = 4 * ((int64_t)part * 256 + threadIdx.x);
+  const int tile = part * 4 + (threadIdx.x >> 6), at = (tile * 64 + lane_id()) * 4;
   const float l2 = log_decay[hv] * kLog2e;
   int64_t t0, t1;
   int first;
@@ -431,37 +636,50 @@ __global__ __launch_bounds__(256) void gdn_linattn_join_kernel(AttnGeo geo, cons
   }
   const int64_t L = (int64_t)geo.chunks * kChunk;
   const int count = (int)((t1 - t0 + L - 1) / L);
-  const int64_t head = ((int64_t)n * geo.HV + hv) * KV + at;
   f32x4 cur = {0.f, 0.f, 0.f, 0.f};
-  if (start) cur = *reinterpret_cast<const f32x4*>(start + head);
+  if (start) {
+    const float* s = start + ((int64_t)n * geo.HV + hv) * KV + (tile % (VD / 16) * 16 + (lane_id() & 15)) * cs;
+    const int row = state_row(tile / (VD / 16));
+#pragma unroll
+    for (int r = 0; r < 4; ++r) cur[r] = s[(row + r) * rs];
+  }
   auto place = [&](int i) {
     return reinterpret_cast<f32x4*>(w + ((int64_t)(first + (REV ? count - 1 - i : i)) * geo.HV + hv) * KV + at);
   };
   const float whole = decay_power(l2, (int)min(L, t1 - t0));
   const float tail = decay_power(l2, (int)(t1 - t0 - (int64_t)(count - 1) * L));
   for (int i = 0; i < count; i += kAttnAhead) {
-    f32x4 own[kAttnAhead];
+    f32x4 add[kAttnAhead];
 #pragma unroll
     for (int j = 0; j < kAttnAhead; ++j)
-      if (i + j < count) own[j] = *place(i + j);
+      if (i + j + 1 < count) add[j] = *place(i + j);  // (the last segment's is not formed)
 #pragma unroll
     for (int j = 0; j < kAttnAhead; ++j)
       if (i + j < count) {
         *place(i + j) = cur;
-        cur = cur * ((REV ? i + j == 0 : i + j == count - 1) ? tail : whole) + own[j];
+        if (i + j + 1 < count) cur = cur * (REV && i + j == 0 ? tail : whole) + add[j];
       }
   }
-  if (end) *reinterpret_cast<f32x4*>(end + head) = cur;
+}
+
+// States without a token: start (or 0) passed to end.
+static __global__ __launch_bounds__(256) void gdn_linattn_copy_kernel(const float* __restrict__ start,
+                                                                      float* __restrict__ end, int64_t quads) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < quads; i += (int64_t)gridDim.x * 256)
+    reinterpret_cast<f32x4*>(end)[i] = start ? reinterpret_cast<const f32x4*>(start)[i] : f32x4{0.f, 0.f, 0.f, 0.f};
 }
 
 // Gradients of shared key heads: out[row][h][k] = sum over the G value heads of part[row][h G + j][k],
-// in their order.
+// in their order; of dq, and (second row of the grid) of dk.
 template <typename E>
-__global__ __launch_bounds__(256) void gdn_linattn_sum_kernel(const float* __restrict__ part, E* __restrict__ out,
-                                                              int64_t quads, int G, int KQ) {
+__global__ __launch_bounds__(256) void gdn_linattn_sum_kernel(const float* __restrict__ partq, const float* __restrict__ partk,
+                                                              E* __restrict__ dq, E* __restrict__ dk, int64_t quads,
+                                                              int G, int KQ) {
+  const f32x4* part = reinterpret_cast<const f32x4*>(blockIdx.y ? partk : partq);
+  E* out = blockIdx.y ? dk : dq;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < quads; i += (int64_t)gridDim.x * 256) {
     const int64_t row = i / KQ;
-    const f32x4* p = reinterpret_cast<const f32x4*>(part) + row * G * KQ + (i - row * KQ);
+    const f32x4* p = part + row * G * KQ + (i - row * KQ);
     f32x4 s = p[0];
     for (int j = 1; j < G; ++j) s += p[(int64_t)j * KQ];
     *reinterpret_cast<Quad<E>*>(out + 4 * i) = make_quad<E>(s);

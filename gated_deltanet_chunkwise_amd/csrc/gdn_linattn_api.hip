@@ -6,9 +6,15 @@
 namespace {
 
 using gdn::AttnGeo;
+using gdn::AttnPass;
 using gdn::AttnRows;
 using gdn::AttnState;
 using gdn::kChunk;
+
+// Segments of a sequence up to which each sums its start itself; chunks that a segment has at
+// least.
+constexpr int kSumMost = 8;
+constexpr int64_t kLeast = 2;
 
 struct AttnPlan {
   AttnGeo geo;
@@ -32,14 +38,14 @@ gdn_status_t attn_sizes(const gdn_linattn_params_t* p, bool packed, AttnPlan* ou
   if ((p->K != 64 && p->K != 128) || (p->V != 64 && p->V != 128)) return GDN_ERR_UNSUPPORTED;
   AttnPlan pl{};
   pl.esz = dtype == GDN_BF16 ? 2 : 4;
-  // token's offsets within a row are 32 bits, and so are sums over rows of all heads below
-  if (p->HV > INT32_MAX / 1024) return GDN_ERR_UNSUPPORTED;
   const int64_t qk = (int64_t)p->H * p->K, vw = (int64_t)p->HV * p->V;
   auto bad = [](int64_t ld, int64_t least) { return ld != 0 && ld < least; };
   if (bad(p->q_stride, qk) || bad(p->k_stride, qk) || bad(p->v_stride, vw)) return GDN_ERR_SHAPE;
   pl.ldq = p->q_stride ? p->q_stride : qk;
   pl.ldk = p->k_stride ? p->k_stride : qk;
   pl.ldv = p->v_stride ? p->v_stride : vw;
+  // a chunk's rows are 32-bit byte offsets apart
+  if (std::max({pl.ldq, pl.ldk, pl.ldv, vw}) > (int64_t)UINT32_MAX / (kChunk * 4)) return GDN_ERR_UNSUPPORTED;
   AttnGeo& g = pl.geo;
   g.B = p->B; g.T = p->T; g.H = p->H; g.HV = p->HV;
   g.G = p->HV / p->H;
@@ -52,12 +58,13 @@ gdn_status_t attn_sizes(const gdn_linattn_params_t* p, bool packed, AttnPlan* ou
   // beyond any memory: states, and tokens' partial sums, counted in 64 bits below
   if ((int64_t)g.N * g.HV > (int64_t)1 << 40 || pl.tok > ((int64_t)1 << 48) / g.HV) return GDN_ERR_UNSUPPORTED;
 
-  // Segments: about kWorkgroups of them over all heads, of kLeast chunks at least.
-  constexpr int64_t kWorkgroups = 512, kLeast = 2;
+  // Chunks per segment: a workgroup for each of 256 CUs (taken for granted, so that the workspace
+  // is the same on every device), for the chunks of all heads; two of them once segments are of
+  // 16 chunks: each costs four transfers of a state, as much as a chunk's rows.
   const int64_t chunks = ceil_div(std::max(g.T, 1), kChunk);  // of a sequence, or of the packed row
-  const int64_t units = std::max<int64_t>((int64_t)(packed ? 1 : std::max(g.B, 1)) * g.HV, 1);
-  const int64_t want = std::max<int64_t>(kWorkgroups / units, 1);
-  g.chunks = (int)std::min(std::max(ceil_div(chunks, want), kLeast), chunks);
+  const int64_t all = chunks * (packed ? 1 : std::max(g.B, 1)) * g.HV;
+  const int64_t len = std::max(ceil_div(all, 512), std::min<int64_t>(ceil_div(all, 256), 16));
+  g.chunks = (int)std::min(std::max(len, kLeast), chunks);
   g.nseg = (int)ceil_div(chunks, g.chunks);
   const int64_t slots = packed ? (int64_t)g.T / kChunk / g.chunks + g.N : (int64_t)g.nseg * g.N;
   if (slots > INT32_MAX) return GDN_ERR_UNSUPPORTED;
@@ -73,58 +80,54 @@ size_t attn_states(const AttnPlan& pl) {
   return align_up((size_t)pl.geo.slots * pl.geo.HV * pl.K * pl.V * 4);
 }
 size_t attn_partial(const AttnPlan& pl) {
-  return pl.geo.G == 1 ? 0 : align_up((size_t)pl.tok * pl.geo.HV * pl.K * 4);
+  return pl.geo.G == 1 ? 0 : align_up((size_t)pl.tok * pl.geo.HV * pl.K * 4 * 2);
 }
 
+int64_t attn_blocks(const AttnGeo& g) { return ceil_div((int64_t)g.slots * g.H, 8) * 8 * g.G; }
 bool attn_fits(const AttnPlan& pl) {
-  return grid_fits((int64_t)pl.geo.slots * pl.geo.HV, gdn::kAttnThreads) &&
+  return grid_fits(attn_blocks(pl.geo), gdn::attn_threads(128)) &&
          grid_fits((int64_t)pl.geo.N * pl.geo.HV * (pl.K * pl.V / 1024), 256);
 }
 
-struct Weights {
-  float intra, inter, update;
-};
-
-template <typename E, typename OT, int KD, int VD, bool REV, bool OUT>
-hipError_t pass_run(const AttnGeo& g, AttnRows a, AttnRows b, AttnRows c, const float* ld, AttnState st, OT* out,
-                    Weights w, hipStream_t s) {
-  // three parts where states go out as fp32
-  constexpr bool exact = sizeof(E) == 4;
-  const dim3 grid((unsigned)((int64_t)g.slots * g.HV)), block(gdn::kAttnThreads);
-  if constexpr (exact)
-    return launch(gdn::gdn_linattn_kernel<E, OT, KD, VD, REV, OUT, 1>, grid, block, s, g, a, b, c, ld, st, out,
-                  w.intra, w.inter, w.update);
-  else if (st.end)
-    return launch(gdn::gdn_linattn_kernel<E, OT, KD, VD, REV, OUT, 3>, grid, block, s, g, a, b, c, ld, st, out,
-                  w.intra, w.inter, w.update);
-  else
-    return launch(gdn::gdn_linattn_kernel<E, OT, KD, VD, REV, OUT, 2>, grid, block, s, g, a, b, c, ld, st, out,
-                  w.intra, w.inter, w.update);
+// `f` for widths KD and VD.
+template <typename F> hipError_t sized(int KD, int VD, F&& f) {
+  using S = std::integral_constant<int, 64>;
+  using L = std::integral_constant<int, 128>;
+  if (KD == 64) return VD == 64 ? f(S{}, S{}) : f(S{}, L{});
+  return VD == 64 ? f(L{}, S{}) : f(L{}, L{});
 }
 
 template <typename E, typename OT, bool REV, bool OUT>
-hipError_t pass(const AttnPlan& pl, int KD, int VD, AttnRows a, AttnRows b, AttnRows c, const float* ld,
-                AttnState st, void* out, Weights w, hipStream_t s) {
-  OT* o = static_cast<OT*>(out);
-  if (KD == 64)
-    return VD == 64 ? pass_run<E, OT, 64, 64, REV, OUT>(pl.geo, a, b, c, ld, st, o, w, s)
-                    : pass_run<E, OT, 64, 128, REV, OUT>(pl.geo, a, b, c, ld, st, o, w, s);
-  return VD == 64 ? pass_run<E, OT, 128, 64, REV, OUT>(pl.geo, a, b, c, ld, st, o, w, s)
-                  : pass_run<E, OT, 128, 128, REV, OUT>(pl.geo, a, b, c, ld, st, o, w, s);
+hipError_t pass(const AttnPlan& pl, int KD, int VD, const float* ld, const AttnPass& x, hipStream_t s) {
+  return sized(KD, VD, [&](auto kd, auto vd) {
+    constexpr int K = decltype(kd)::value, V = decltype(vd)::value;
+    return launch(gdn::gdn_linattn_kernel<E, OT, K, V, REV, OUT>, dim3((unsigned)attn_blocks(pl.geo)),
+                  dim3(gdn::attn_threads(V)), s, pl.geo, x, ld);
+  });
 }
 
+// The starts of all segments, where a sequence may have too many of them to be summed by each.
 template <bool REV>
-hipError_t join(const AttnPlan& pl, const float* ld, const float* start, float* w, float* end, hipStream_t s) {
-  const int kv = pl.K * pl.V;
-  const dim3 grid((unsigned)((int64_t)pl.geo.N * pl.geo.HV * (kv / 1024))), block(256);
-  auto kern = kv == 4096 ? gdn::gdn_linattn_join_kernel<4096, REV>
-              : kv == 8192 ? gdn::gdn_linattn_join_kernel<8192, REV> : gdn::gdn_linattn_join_kernel<16384, REV>;
-  return launch(kern, grid, block, s, pl.geo, ld, start, w, end);
+hipError_t join(const AttnPlan& pl, int KD, int VD, const float* ld, const AttnState& st, hipStream_t s) {
+  if (st.mode != gdn::kJoined) return hipSuccess;
+  const dim3 grid((unsigned)((int64_t)pl.geo.N * pl.geo.HV * (KD * VD / 1024))), block(256);
+  return sized(KD, VD, [&](auto kd, auto vd) {
+    return launch(gdn::gdn_linattn_join_kernel<decltype(kd)::value, decltype(vd)::value, REV>, grid, block, s, pl.geo,
+                  ld, st.start, st.rs, st.cs, st.w);
+  });
 }
 
-// The states alone pass to `end` where there is no token.
-hipError_t pass_on(const AttnPlan& pl, const float* ld, const float* start, float* end, hipStream_t s) {
-  return end && pl.geo.N > 0 ? join<false>(pl, ld, start, nullptr, end, s) : hipSuccess;
+// Without any token the states pass through.
+hipError_t pass_on(const AttnPlan& pl, const float* start, float* end, hipStream_t s) {
+  const int64_t n = (int64_t)pl.geo.N * pl.geo.HV * pl.K * pl.V / 4;
+  if (!end || n == 0) return hipSuccess;
+  const int64_t blocks = std::min(ceil_div(n, 256), (int64_t)device_cus() * 16);
+  return launch(gdn::gdn_linattn_copy_kernel, dim3((unsigned)blocks), dim3(256), s, start, end, n);
+}
+
+// How segments get their starts.
+int attn_mode(const AttnPlan& pl) {
+  return pl.one ? gdn::kWholeSequence : pl.geo.nseg <= kSumMost ? gdn::kSumSegments : gdn::kJoined;
 }
 
 template <typename E>
@@ -136,16 +139,16 @@ gdn_status_t fwd_run(const AttnPlan& pl, const void* q, const void* k, const voi
   };
   const AttnRows a{q, pl.ldq, pl.geo.G}, b{k, pl.ldk, pl.geo.G}, c{v, pl.ldv, 1};
   const int K = pl.K, V = pl.V;
-  const Weights w{pl.scale, pl.scale, 1.f};
+  const AttnState st{h0, fin, V, 1, static_cast<float*>(ws), attn_mode(pl), false};
+  const AttnPass x{a, b, c, st, o, pl.scale, pl.scale, 1.f};
   if (pl.tok == 0) {
-    ok(pass_on(pl, ld, h0, fin, s));
-  } else if (pl.one) {
-    ok(pass<E, E, false, true>(pl, K, V, a, b, c, ld, {h0, fin, V, 1, false}, o, w, s));
+    ok(pass_on(pl, h0, fin, s));
   } else {
-    float* st = static_cast<float*>(ws);
-    ok(pass<E, E, false, false>(pl, K, V, a, b, c, ld, {nullptr, st, V, 1, true}, nullptr, w, s));
-    ok(join<false>(pl, ld, h0, st, fin, s));
-    ok(pass<E, E, false, true>(pl, K, V, a, b, c, ld, {st, nullptr, V, 1, true}, o, w, s));
+    if (!pl.one) {
+      ok(pass<E, E, false, false>(pl, K, V, ld, x, s));
+      ok(join<false>(pl, K, V, ld, st, s));
+    }
+    ok(pass<E, E, false, true>(pl, K, V, ld, x, s));
   }
   return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
@@ -167,47 +170,63 @@ gdn_status_t bwd_run(AttnPlan pl, const AttnBwd& x, void* ws, hipStream_t s) {
   };
   const int K = pl.K, V = pl.V, G = pl.geo.G;
   const AttnRows q{x.q, pl.ldq, G}, k{x.k, pl.ldk, G}, v{x.v, pl.ldv, 1}, d_o{x.d_o, (int64_t)pl.geo.HV * V, 1};
-  const Weights fw{pl.scale, pl.scale, 1.f}, bw{pl.scale, 1.f, pl.scale};
   pl.geo.zero = pl.packed;
   if (pl.tok == 0) {
-    ok(pass_on(pl, x.ld, x.d_fin, x.dh0, s));
+    ok(pass_on(pl, x.d_fin, x.dh0, s));
     return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
   }
   char* base = static_cast<char*>(ws);
-  float* part = reinterpret_cast<float*>(base + 2 * attn_states(pl));
-  AttnState sq, sk, sv;  // the states of the passes that form dq, dk and dv
-  if (pl.one) {
-    sq = {x.h0, nullptr, 1, V, false};
-    sk = {x.d_fin, nullptr, 1, V, false};
-    sv = {x.d_fin, x.dh0, V, 1, false};
-  } else {
-    float* sth = reinterpret_cast<float*>(base);
-    float* std_ = reinterpret_cast<float*>(base + attn_states(pl));
-    ok(pass<E, E, false, false>(pl, K, V, q, k, v, x.ld, {nullptr, sth, V, 1, true}, nullptr, fw, s));
-    ok(pass<E, E, true, false>(pl, K, V, k, q, d_o, x.ld, {nullptr, std_, V, 1, true}, nullptr, bw, s));
-    ok(join<false>(pl, x.ld, x.h0, sth, nullptr, s));
-    ok(join<true>(pl, x.ld, x.d_fin, std_, x.dh0, s));
-    sq = {sth, nullptr, 1, V, true};
-    sk = {std_, nullptr, 1, V, true};
-    sv = {std_, nullptr, V, 1, true};
+  float* part = reinterpret_cast<float*>(base + 2 * attn_states(pl));  // of dq, then of dk
+  float* wh = reinterpret_cast<float*>(base);
+  float* wd = reinterpret_cast<float*>(base + attn_states(pl));
+  const int mode = attn_mode(pl);
+  const int64_t row = pl.tok * pl.geo.HV * K;
+  // dq goes by H^T, dk by dH^T, dv by dH
+  const AttnPass xq{d_o, v, k, {x.h0, nullptr, 1, V, wh, mode, false}, G == 1 ? x.dq : part, pl.scale, pl.scale, 1.f};
+  const AttnPass xk{v, d_o, q, {x.d_fin, nullptr, 1, V, wd, mode, true}, G == 1 ? x.dk : part + row, pl.scale, 1.f, pl.scale};
+  const AttnPass xv{k, q, d_o, {x.d_fin, x.dh0, V, 1, wd, mode, false}, x.dv, pl.scale, 1.f, pl.scale};
+  const int blocks = (int)attn_blocks(pl.geo);
+  // both states' passes, and all three of the gradients, in one launch each where their widths agree
+  auto together = [&](auto d, auto ot, auto out) {
+    constexpr int D = decltype(d)::value;
+    constexpr bool OUT = decltype(out)::value;
+    ok(launch(gdn::gdn_linattn_bwd_kernel<E, decltype(ot), D, OUT>, dim3((unsigned)blocks * (OUT ? 3 : 2)),
+              dim3(gdn::attn_threads(D)), s, pl.geo, xq, xk, xv, x.ld, blocks));
+  };
+  auto same_width = [&](auto ot, auto out) {
+    if (K == 64) together(std::integral_constant<int, 64>{}, ot, out);
+    else together(std::integral_constant<int, 128>{}, ot, out);
+  };
+  if (!pl.one) {
+    if (K == V) {
+      same_width(E{}, std::false_type{});
+    } else {
+      ok(pass<E, E, false, false>(pl, V, K, x.ld, xq, s));
+      ok(pass<E, E, true, false>(pl, K, V, x.ld, xv, s));
+    }
+    ok(join<false>(pl, V, K, x.ld, xq.st, s));
+    ok(join<true>(pl, K, V, x.ld, xv.st, s));
   }
-  // gradients of shared heads: each value head's own, then their sum
-  auto shared = [&](void* out) {
-    const int64_t quads = pl.tok * pl.geo.H * (K / 4);
-    const int64_t blocks = std::min(ceil_div(quads, 256), (int64_t)device_cus() * 16);
-    ok(launch(gdn::gdn_linattn_sum_kernel<E>, dim3((unsigned)blocks), dim3(256), s, part, static_cast<E*>(out), quads,
-              G, K / 4));
+  auto gradients = [&](auto ot) {
+    using OT = decltype(ot);
+    if (K == V) {
+      same_width(ot, std::true_type{});
+    } else {
+      ok(pass<E, OT, false, true>(pl, V, K, x.ld, xq, s));
+      ok(pass<E, OT, true, true>(pl, V, K, x.ld, xk, s));
+      ok(pass<E, E, true, true>(pl, K, V, x.ld, xv, s));
+    }
   };
   if (G == 1) {
-    ok(pass<E, E, false, true>(pl, V, K, d_o, v, k, x.ld, sq, x.dq, fw, s));
-    ok(pass<E, E, true, true>(pl, V, K, v, d_o, q, x.ld, sk, x.dk, bw, s));
+    gradients(E{});
   } else {
-    ok(pass<E, float, false, true>(pl, V, K, d_o, v, k, x.ld, sq, part, fw, s));
-    shared(x.dq);
-    ok(pass<E, float, true, true>(pl, V, K, v, d_o, q, x.ld, sk, part, bw, s));
-    shared(x.dk);
+    // of shared heads: each value head's own, then their sum
+    gradients(0.f);
+    const int64_t quads = pl.tok * pl.geo.H * (K / 4);
+    const int64_t grid = std::min(ceil_div(quads, 256), (int64_t)device_cus() * 16);
+    ok(launch(gdn::gdn_linattn_sum_kernel<E>, dim3((unsigned)grid, 2), dim3(256), s, part, part + row,
+              static_cast<E*>(x.dq), static_cast<E*>(x.dk), quads, G, K / 4));
   }
-  ok(pass<E, E, true, true>(pl, K, V, k, q, d_o, x.ld, sv, x.dv, bw, s));
   return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
@@ -295,13 +314,8 @@ gdn_status_t gdn_linattn_decode(const gdn_linattn_params_t* p, const void* q, co
                   AttnRows{k, pl.ldk, pl.geo.G}, AttnRows{v, pl.ldv, 1}, log_decay, state, new_state,
                   static_cast<E*>(o), pl.scale);
   };
-  using S = std::integral_constant<int, 64>;
-  using L = std::integral_constant<int, 128>;
-  auto sized = [&](auto e) {
-    if (p->K == 64) return p->V == 64 ? go(e, S{}, S{}) : go(e, S{}, L{});
-    return p->V == 64 ? go(e, L{}, S{}) : go(e, L{}, L{});
-  };
-  return (pl.esz == 2 ? sized(gdn::bf16{}) : sized(0.f)) == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+  auto typed = [&](auto e) { return sized(p->K, p->V, [&](auto kd, auto vd) { return go(e, kd, vd); }); };
+  return (pl.esz == 2 ? typed(gdn::bf16{}) : typed(0.f)) == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
 }  // extern "C"
