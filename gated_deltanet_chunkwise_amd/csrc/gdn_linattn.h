@@ -252,9 +252,9 @@ __device__ __forceinline__ void weighted_parts(const Frag<float>& c, const float
 
 // Rows behind the last sequence, of head hv's columns of the output, set to 0: shared out over
 // the slots.
-template <typename OT, int D>
+template <typename OT, int D, int THREADS>
 __device__ __forceinline__ void attn_zero_rest(const AttnGeo& g, int hv, int slot, OT* out) {
-  constexpr int PER_ROW = D * (int)sizeof(OT) / 16, ROWS = attn_threads(D) / PER_ROW;
+  constexpr int PER_ROW = D * (int)sizeof(OT) / 16, ROWS = THREADS / PER_ROW;
   const int sub = threadIdx.x / PER_ROW, col = threadIdx.x % PER_ROW;
   for (int64_t t = seq_offset(g.cu, g.N, g.T) + (int64_t)slot * ROWS + sub; t < g.T; t += (int64_t)g.slots * ROWS)
     *reinterpret_cast<u32x4*>(out + (t * g.HV + hv) * D + col * (16 / (int)sizeof(OT))) = u32x4{0, 0, 0, 0};
@@ -311,17 +311,17 @@ __device__ __forceinline__ void attn_update(f32x4 (&H)[KT], const B& b, const C&
 // the products' part of the output, whose rows go through LDS to be stored whole; the state's
 // update.  Powers of the decay are formed by one lane each and read from LDS: of the products
 // (`gap`) once, the weights of a chunk's update and of the state in each of its rows per chunk.
-template <typename E, typename OT, int KD, int VD, bool OUT> struct AttnLds {
-  AttnTile<E, KD, attn_threads(VD)> b;
-  AttnTile<E, VD, attn_threads(VD)> c;
+template <typename E, typename OT, int KD, int VD, int THREADS, bool OUT> struct AttnLds {
+  AttnTile<E, KD, THREADS> b;
+  AttnTile<E, VD, THREADS> c;
   float update[kChunk];
 };
-template <typename E, typename OT, int KD, int VD> struct AttnLds<E, OT, KD, VD, true> {
-  AttnTile<E, KD, attn_threads(VD)> b;
-  AttnTile<E, VD, attn_threads(VD)> c;
-  AttnTile<E, KD, attn_threads(VD)> a;
-  AttnTile<OT, VD, attn_threads(VD)> o;
-  AttnTile<E, kChunk, attn_threads(VD)> p;
+template <typename E, typename OT, int KD, int VD, int THREADS> struct AttnLds<E, OT, KD, VD, THREADS, true> {
+  AttnTile<E, KD, THREADS> b;
+  AttnTile<E, VD, THREADS> c;
+  AttnTile<E, KD, THREADS> a;
+  AttnTile<OT, VD, THREADS> o;
+  AttnTile<E, kChunk, THREADS> p;
   float update[kChunk], inter[kChunk], gap[2 * kChunk];  // gap: 0 for rows that are not seen
 };
 
@@ -332,15 +332,15 @@ struct AttnPass {
   float s_intra, s_inter, s_update;  // what products a.b, the state's part and its update are scaled by
 };
 
-template <typename E, typename OT, int KD, int VD, bool REV, bool OUT>
+template <typename E, typename OT, int KD, int VD, int THREADS, bool REV, bool OUT>
 __device__ __forceinline__ void attn_pass(const AttnGeo& geo, int block, const AttnPass& x,
                                           const float* __restrict__ log_decay, char* smem) {
   const AttnRows &ar = x.a, &br = x.b, &cr = x.c;
   const AttnState& st = x.st;
   OT* out = static_cast<OT*>(x.out);
   const float s_intra = x.s_intra, s_inter = x.s_inter, s_update = x.s_update;
-  constexpr int KT = KD / 16, TT = kChunk / 16, THREADS = attn_threads(VD), WAVES = VD / 16;
-  using Lds = AttnLds<E, OT, KD, VD, OUT>;
+  constexpr int KT = KD / 16, TT = kChunk / 16, WAVES = VD / 16;
+  using Lds = AttnLds<E, OT, KD, VD, THREADS, OUT>;
   using KTile = AttnTile<E, KD, THREADS>;
   using VTile = AttnTile<E, VD, THREADS>;
   using OTile = AttnTile<OT, VD, THREADS>;
@@ -349,7 +349,7 @@ __device__ __forceinline__ void attn_pass(const AttnGeo& geo, int block, const A
   int hv, slot;
   if (!attn_block(geo, block, slot, hv)) return;
   if constexpr (OUT) {
-    if (geo.cu && geo.zero) attn_zero_rest<OT, VD>(geo, hv, slot, out);
+    if (geo.cu && geo.zero) attn_zero_rest<OT, VD, THREADS>(geo, hv, slot, out);
   }
   Segment seg;
   const bool tokens = seg.find(geo, slot);
@@ -365,7 +365,9 @@ __device__ __forceinline__ void attn_pass(const AttnGeo& geo, int block, const A
   const int nch = (seg.len + kChunk - 1) / kChunk;
   const int lane = lane_id(), g = lane >> 4, m = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col0 = 16 * wave;
+  // (waves beyond the columns, where another pass of the launch has more, load and store)
+  const bool owner = THREADS == attn_threads(VD) || wave < WAVES;
+  const int col0 = owner ? 16 * wave : 0;
   const float l2 = log_decay[hv] * kLog2e;
 
   const E* ap = static_cast<const E*>(ar.p) + (int64_t)seg.t0 * ar.ld + (hv / ar.div) * KD;
@@ -416,7 +418,7 @@ __device__ __forceinline__ void attn_pass(const AttnGeo& geo, int block, const A
         const float* w = st.w + ((int64_t)at * geo.HV + hv) * (KD * VD);
         if (!st.transposed) {
 #pragma unroll
-          for (int kt = 0; kt < KT; ++kt) e[j][kt] = *reinterpret_cast<const f32x4*>(w + state_place(kt, wave, VD / 16));
+          for (int kt = 0; kt < KT; ++kt) e[j][kt] = *reinterpret_cast<const f32x4*>(w + state_place(kt, col0 / 16, VD / 16));
         } else {
           const uint32_t off = lane_offset(state_lane_transposed<KD>());
 #pragma unroll
@@ -478,7 +480,9 @@ __device__ __forceinline__ void attn_pass(const AttnGeo& geo, int block, const A
     if constexpr (!OUT && decltype(more)::value) fetch_c(it + 1);
     if (it) store(it - 1);
 
-    if constexpr (OUT) {
+    f32x4 acc[TT];
+    if constexpr (OUT && decltype(more)::value) fetch_c(it + 1);
+    if constexpr (OUT) if (owner) {
       // the weighted products of a tile of rows of a with those rows of b that they see, two
       // tiles of b at a time; two waves share a tile of a where there are eight
       {
@@ -518,9 +522,7 @@ __device__ __forceinline__ void attn_pass(const AttnGeo& geo, int block, const A
           ATTN_PHASE;
         }
       }
-      if constexpr (decltype(more)::value) fetch_c(it + 1);  // (apart from the others: loads queue)
       // the state's part: O^T = H^T a^T, then weighted by row
-      f32x4 acc[TT];
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) acc[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -533,7 +535,9 @@ __device__ __forceinline__ void attn_pass(const AttnGeo& geo, int block, const A
       ATTN_PHASE;
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) acc[tt] *= L.inter[16 * tt + m];
-      __syncthreads();  // the weighted products are there
+    }
+    if constexpr (OUT) __syncthreads();  // the weighted products are there
+    if constexpr (OUT) if (owner) {
 #pragma unroll
       for (int sb = 0; sb < kChunk / 32; ++sb) {
         const Frag<E> v = L.c.template of_columns<4>(32 * sb, col0);
@@ -550,7 +554,7 @@ __device__ __forceinline__ void attn_pass(const AttnGeo& geo, int block, const A
     }
     ATTN_PHASE;
     const bool end = OUT && last && st.end;
-    if (!OUT || end || it + 1 < nch) {
+    if (owner && (!OUT || end || it + 1 < nch)) {
       const float a = decay_power(l2, n);
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) H[kt] *= a;
@@ -570,17 +574,17 @@ __device__ __forceinline__ void attn_pass(const AttnGeo& geo, int block, const A
       __syncthreads();
       store(nch - 1);
     }
-    if (last && st.end) {
+    if (last && st.end && owner) {
       float* s = st.end + ((int64_t)seg.n * geo.HV + hv) * (KD * VD) + (col0 + m) * st.cs;
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
         for (int r = 0; r < 4; ++r) s[(state_row(kt) + r) * st.rs] = H[kt][r];
     }
-  } else {
+  } else if (owner) {
     float* w = st.w + ((int64_t)slot * geo.HV + hv) * (KD * VD);
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(w + state_place(kt, wave, VD / 16)) = H[kt];
+    for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(w + state_place(kt, col0 / 16, VD / 16)) = H[kt];
   }
 }
 
@@ -591,22 +595,23 @@ template <typename E, int VD, bool OUT> constexpr int attn_waves() {  // per SIM
 template <typename E, typename OT, int KD, int VD, bool REV, bool OUT>
 __global__ __launch_bounds__(attn_threads(VD), (attn_waves<E, VD, OUT>())) void gdn_linattn_kernel(
     AttnGeo geo, AttnPass x, const float* __restrict__ log_decay) {
-  __shared__ __attribute__((aligned(16))) char smem[sizeof(AttnLds<E, OT, KD, VD, OUT>)];
-  attn_pass<E, OT, KD, VD, REV, OUT>(geo, blockIdx.x, x, log_decay, smem);
+  __shared__ __attribute__((aligned(16))) char smem[sizeof(AttnLds<E, OT, KD, VD, attn_threads(VD), OUT>)];
+  attn_pass<E, OT, KD, VD, attn_threads(VD), REV, OUT>(geo, blockIdx.x, x, log_decay, smem);
 }
 
-// The backward pass's passes of one kind in one launch, `blocks` workgroups each, where keys and
-// values are of one width D: what segments add to H^T and dH (two passes), or dq, dk and dv.
-// OT: the type of dq and dk.
-template <typename E, typename OT, int D, bool OUT>
-__global__ __launch_bounds__(attn_threads(D), (attn_waves<E, D, OUT>())) void gdn_linattn_bwd_kernel(
+// The backward pass's passes of one kind in one launch, `blocks` workgroups each: what segments
+// add to H^T and dH (two passes), or dq, dk and dv.  OT: the type of dq and dk.  Workgroups have
+// the threads that the wider of keys and values takes.
+template <typename E, typename OT, int K, int V, bool OUT>
+__global__ __launch_bounds__(attn_threads(K > V ? K : V), (attn_waves<E, (K > V ? K : V), OUT>())) void gdn_linattn_bwd_kernel(
     AttnGeo geo, AttnPass q, AttnPass k, AttnPass v, const float* __restrict__ log_decay, int blocks) {
-  __shared__ __attribute__((aligned(16))) char smem[sizeof(AttnLds<E, OT, D, D, OUT>)];
-  static_assert(sizeof(smem) >= sizeof(AttnLds<E, E, D, D, OUT>), "");
+  constexpr int THREADS = attn_threads(K > V ? K : V);
+  constexpr size_t QK = sizeof(AttnLds<E, OT, V, K, THREADS, OUT>), VV = sizeof(AttnLds<E, E, K, V, THREADS, OUT>);
+  __shared__ __attribute__((aligned(16))) char smem[QK > VV ? QK : VV];
   const int role = blockIdx.x / blocks, block = blockIdx.x - role * blocks;
-  if (role == 0) attn_pass<E, OT, D, D, false, OUT>(geo, block, q, log_decay, smem);
-  else if (OUT && role == 1) attn_pass<E, OT, D, D, true, OUT>(geo, block, k, log_decay, smem);
-  else attn_pass<E, E, D, D, true, OUT>(geo, block, v, log_decay, smem);
+  if (role == 0) attn_pass<E, OT, V, K, THREADS, false, OUT>(geo, block, q, log_decay, smem);
+  else if (OUT && role == 1) attn_pass<E, OT, V, K, THREADS, true, OUT>(geo, block, k, log_decay, smem);
+  else attn_pass<E, E, K, V, THREADS, true, OUT>(geo, block, v, log_decay, smem);
 }
 
 // The starts of sequences' segments: per sequence, head and four elements of the state, in the
@@ -615,10 +620,11 @@ __global__ __launch_bounds__(attn_threads(D), (attn_waves<E, D, OUT>())) void gd
 constexpr int kAttnAhead = 8;
 
 template <int KD, int VD, bool REV>
-__global__ __launch_bounds__(256) void gdn_linattn_join_kernel(AttnGeo geo, const float* __restrict__ log_decay,
-                                                               const float* __restrict__ start, int rs, int cs,
-                                                               float* w) {
+__device__ __forceinline__ void attn_join(const AttnGeo& geo, const float* __restrict__ log_decay, const AttnState& st) {
   constexpr int KV = KD * VD, PER = KV / 4 / 256;  // workgroups per head
+  const float* start = st.start;
+  float* w = st.w;
+  const int rs = st.rs, cs = st.cs;
   const int part = blockIdx.x % PER, unit = blockIdx.x / PER;
   const int hv = unit % geo.HV, n = unit / geo.HV;
   const int tile = part * 4 + (threadIdx.x >> 6), at = (tile * 64 + lane_id()) * 4;
@@ -660,6 +666,18 @@ __global__ __launch_bounds__(256) void gdn_linattn_join_kernel(AttnGeo geo, cons
         if (i + j + 1 < count) cur = cur * (REV && i + j == 0 ? tail : whole) + add[j];
       }
   }
+}
+
+template <int K, int V>
+__global__ __launch_bounds__(256) void gdn_linattn_join_kernel(AttnGeo geo, AttnState h, const float* __restrict__ log_decay) {
+  attn_join<K, V, false>(geo, log_decay, h);
+}
+// H^T and (second row of the grid) dH of the backward pass.
+template <int K, int V>
+__global__ __launch_bounds__(256) void gdn_linattn_bwd_join_kernel(AttnGeo geo, AttnState ht, AttnState dh,
+                                                                   const float* __restrict__ log_decay) {
+  if (blockIdx.y == 0) attn_join<V, K, false>(geo, log_decay, ht);
+  else attn_join<K, V, true>(geo, log_decay, dh);
 }
 
 // States without a token: start (or 0) passed to end.

@@ -27,6 +27,32 @@ struct AttnPlan {
   int64_t ldq, ldk, ldv;
 };
 
+// Chunks per segment, for sequences of `chunks` in `units` (sequence, head) pairs or, packed, one
+// row of them per head that holds `packed` sequences.  256 CUs are taken for granted, so that the
+// workspace is the same on every device; a CU runs one workgroup of the last launch at a time.
+// For 1 to 8 rounds of workgroups, the least of: a round's chunks (about 3.7 us each at B=2,
+// T=2048, 16 heads of 128 bf16) with its start; and, with several segments, the launch that forms
+// what they add, two workgroups per CU, and the third.  (us, by whole segments of 16 chunks and by
+// this: 16 sequences of 2048 tokens, 16 heads 207 and 153; 32768 packed tokens in 12 sequences, 16
+// heads 228 and 225.)
+int64_t segment_chunks(int64_t chunks, int64_t units, int64_t packed) {
+  int64_t best = chunks;
+  double least = 1e300;
+  for (int rounds = 1; rounds <= 8; ++rounds) {
+    // segments per row of chunks that fill so many rounds; sequences end half a segment each
+    const int64_t fill = std::max<int64_t>(256 * rounds / units - packed / 2, 1);
+    const int64_t len = std::min(std::max(ceil_div(chunks, fill), kLeast), chunks);
+    const int64_t n = ceil_div(chunks, len), wgs = units * (n + packed / 2);
+    double cost = (double)ceil_div(wgs, 256) * (len + 1.5 + 0.25 * std::min<int64_t>(n, 8));
+    if (n > 1) cost += ceil_div(wgs, 512) * (len * (wgs > 256 ? 0.9 : 0.6) + 1.) + 0.8 + (n > kSumMost ? 3. : 0.);
+    if (cost < least) {
+      least = cost;
+      best = len;
+    }
+  }
+  return best;
+}
+
 // Sizes only.
 gdn_status_t attn_sizes(const gdn_linattn_params_t* p, bool packed, AttnPlan* out) {
   if (!p) return GDN_ERR_NULL;
@@ -58,13 +84,8 @@ gdn_status_t attn_sizes(const gdn_linattn_params_t* p, bool packed, AttnPlan* ou
   // beyond any memory: states, and tokens' partial sums, counted in 64 bits below
   if ((int64_t)g.N * g.HV > (int64_t)1 << 40 || pl.tok > ((int64_t)1 << 48) / g.HV) return GDN_ERR_UNSUPPORTED;
 
-  // Chunks per segment: a workgroup for each of 256 CUs (taken for granted, so that the workspace
-  // is the same on every device), for the chunks of all heads; two of them once segments are of
-  // 16 chunks: each costs four transfers of a state, as much as a chunk's rows.
   const int64_t chunks = ceil_div(std::max(g.T, 1), kChunk);  // of a sequence, or of the packed row
-  const int64_t all = chunks * (packed ? 1 : std::max(g.B, 1)) * g.HV;
-  const int64_t len = std::max(ceil_div(all, 512), std::min<int64_t>(ceil_div(all, 256), 16));
-  g.chunks = (int)std::min(std::max(len, kLeast), chunks);
+  g.chunks = (int)segment_chunks(chunks, packed ? g.HV : (int64_t)std::max(g.B, 1) * g.HV, packed ? g.N : 0);
   g.nseg = (int)ceil_div(chunks, g.chunks);
   const int64_t slots = packed ? (int64_t)g.T / kChunk / g.chunks + g.N : (int64_t)g.nseg * g.N;
   if (slots > INT32_MAX) return GDN_ERR_UNSUPPORTED;
@@ -84,9 +105,10 @@ size_t attn_partial(const AttnPlan& pl) {
 }
 
 int64_t attn_blocks(const AttnGeo& g) { return ceil_div((int64_t)g.slots * g.H, 8) * 8 * g.G; }
+int64_t join_blocks(const AttnPlan& pl) { return (int64_t)pl.geo.N * pl.geo.HV * (pl.K * pl.V / 1024); }
 bool attn_fits(const AttnPlan& pl) {
-  return grid_fits(attn_blocks(pl.geo), gdn::attn_threads(128)) &&
-         grid_fits((int64_t)pl.geo.N * pl.geo.HV * (pl.K * pl.V / 1024), 256);
+  return grid_fits(attn_blocks(pl.geo) * 3, gdn::attn_threads(128)) &&
+         grid_fits(join_blocks(pl), 256);
 }
 
 // `f` for widths KD and VD.
@@ -95,26 +117,6 @@ template <typename F> hipError_t sized(int KD, int VD, F&& f) {
   using L = std::integral_constant<int, 128>;
   if (KD == 64) return VD == 64 ? f(S{}, S{}) : f(S{}, L{});
   return VD == 64 ? f(L{}, S{}) : f(L{}, L{});
-}
-
-template <typename E, typename OT, bool REV, bool OUT>
-hipError_t pass(const AttnPlan& pl, int KD, int VD, const float* ld, const AttnPass& x, hipStream_t s) {
-  return sized(KD, VD, [&](auto kd, auto vd) {
-    constexpr int K = decltype(kd)::value, V = decltype(vd)::value;
-    return launch(gdn::gdn_linattn_kernel<E, OT, K, V, REV, OUT>, dim3((unsigned)attn_blocks(pl.geo)),
-                  dim3(gdn::attn_threads(V)), s, pl.geo, x, ld);
-  });
-}
-
-// The starts of all segments, where a sequence may have too many of them to be summed by each.
-template <bool REV>
-hipError_t join(const AttnPlan& pl, int KD, int VD, const float* ld, const AttnState& st, hipStream_t s) {
-  if (st.mode != gdn::kJoined) return hipSuccess;
-  const dim3 grid((unsigned)((int64_t)pl.geo.N * pl.geo.HV * (KD * VD / 1024))), block(256);
-  return sized(KD, VD, [&](auto kd, auto vd) {
-    return launch(gdn::gdn_linattn_join_kernel<decltype(kd)::value, decltype(vd)::value, REV>, grid, block, s, pl.geo,
-                  ld, st.start, st.rs, st.cs, st.w);
-  });
 }
 
 // Without any token the states pass through.
@@ -138,17 +140,21 @@ gdn_status_t fwd_run(const AttnPlan& pl, const void* q, const void* k, const voi
     if (e != hipSuccess && err == hipSuccess) err = e;
   };
   const AttnRows a{q, pl.ldq, pl.geo.G}, b{k, pl.ldk, pl.geo.G}, c{v, pl.ldv, 1};
-  const int K = pl.K, V = pl.V;
-  const AttnState st{h0, fin, V, 1, static_cast<float*>(ws), attn_mode(pl), false};
+  const AttnState st{h0, fin, pl.V, 1, static_cast<float*>(ws), attn_mode(pl), false};
   const AttnPass x{a, b, c, st, o, pl.scale, pl.scale, 1.f};
   if (pl.tok == 0) {
     ok(pass_on(pl, h0, fin, s));
   } else {
-    if (!pl.one) {
-      ok(pass<E, E, false, false>(pl, K, V, ld, x, s));
-      ok(join<false>(pl, K, V, ld, st, s));
-    }
-    ok(pass<E, E, false, true>(pl, K, V, ld, x, s));
+    ok(sized(pl.K, pl.V, [&](auto kd, auto vd) {
+      constexpr int K = decltype(kd)::value, V = decltype(vd)::value;
+      const dim3 grid((unsigned)attn_blocks(pl.geo)), block(gdn::attn_threads(V));
+      if (!pl.one) {
+        ok(launch(gdn::gdn_linattn_kernel<E, E, K, V, false, false>, grid, block, s, pl.geo, x, ld));
+        if (st.mode == gdn::kJoined)
+          ok(launch(gdn::gdn_linattn_join_kernel<K, V>, dim3((unsigned)join_blocks(pl)), dim3(256), s, pl.geo, st, ld));
+      }
+      return launch(gdn::gdn_linattn_kernel<E, E, K, V, false, true>, grid, block, s, pl.geo, x, ld);
+    }));
   }
   return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
@@ -185,48 +191,26 @@ gdn_status_t bwd_run(AttnPlan pl, const AttnBwd& x, void* ws, hipStream_t s) {
   const AttnPass xq{d_o, v, k, {x.h0, nullptr, 1, V, wh, mode, false}, G == 1 ? x.dq : part, pl.scale, pl.scale, 1.f};
   const AttnPass xk{v, d_o, q, {x.d_fin, nullptr, 1, V, wd, mode, true}, G == 1 ? x.dk : part + row, pl.scale, 1.f, pl.scale};
   const AttnPass xv{k, q, d_o, {x.d_fin, x.dh0, V, 1, wd, mode, false}, x.dv, pl.scale, 1.f, pl.scale};
-  const int blocks = (int)attn_blocks(pl.geo);
-  // both states' passes, and all three of the gradients, in one launch each where their widths agree
-  auto together = [&](auto d, auto ot, auto out) {
-    constexpr int D = decltype(d)::value;
-    constexpr bool OUT = decltype(out)::value;
-    ok(launch(gdn::gdn_linattn_bwd_kernel<E, decltype(ot), D, OUT>, dim3((unsigned)blocks * (OUT ? 3 : 2)),
-              dim3(gdn::attn_threads(D)), s, pl.geo, xq, xk, xv, x.ld, blocks));
-  };
-  auto same_width = [&](auto ot, auto out) {
-    if (K == 64) together(std::integral_constant<int, 64>{}, ot, out);
-    else together(std::integral_constant<int, 128>{}, ot, out);
-  };
-  if (!pl.one) {
-    if (K == V) {
-      same_width(E{}, std::false_type{});
-    } else {
-      ok(pass<E, E, false, false>(pl, V, K, x.ld, xq, s));
-      ok(pass<E, E, true, false>(pl, K, V, x.ld, xv, s));
+  ok(sized(K, V, [&](auto kd, auto vd) {
+    constexpr int KD = decltype(kd)::value, VD = decltype(vd)::value;
+    const int blocks = (int)attn_blocks(pl.geo);
+    const dim3 block(gdn::attn_threads(std::max(KD, VD)));
+    if (!pl.one) {
+      ok(launch(gdn::gdn_linattn_bwd_kernel<E, E, KD, VD, false>, dim3((unsigned)blocks * 2), block, s, pl.geo, xq, xk,
+                xv, x.ld, blocks));
+      if (mode == gdn::kJoined)
+        ok(launch(gdn::gdn_linattn_bwd_join_kernel<KD, VD>, dim3((unsigned)join_blocks(pl), 2), dim3(256), s, pl.geo,
+                  xq.st, xv.st, x.ld));
     }
-    ok(join<false>(pl, V, K, x.ld, xq.st, s));
-    ok(join<true>(pl, K, V, x.ld, xv.st, s));
-  }
-  auto gradients = [&](auto ot) {
-    using OT = decltype(ot);
-    if (K == V) {
-      same_width(ot, std::true_type{});
-    } else {
-      ok(pass<E, OT, false, true>(pl, V, K, x.ld, xq, s));
-      ok(pass<E, OT, true, true>(pl, V, K, x.ld, xk, s));
-      ok(pass<E, E, true, true>(pl, K, V, x.ld, xv, s));
-    }
-  };
-  if (G == 1) {
-    gradients(E{});
-  } else {
+    const dim3 grid((unsigned)blocks * 3);
+    if (G == 1) return launch(gdn::gdn_linattn_bwd_kernel<E, E, KD, VD, true>, grid, block, s, pl.geo, xq, xk, xv, x.ld, blocks);
     // of shared heads: each value head's own, then their sum
-    gradients(0.f);
+    ok(launch(gdn::gdn_linattn_bwd_kernel<E, float, KD, VD, true>, grid, block, s, pl.geo, xq, xk, xv, x.ld, blocks));
     const int64_t quads = pl.tok * pl.geo.H * (K / 4);
-    const int64_t grid = std::min(ceil_div(quads, 256), (int64_t)device_cus() * 16);
-    ok(launch(gdn::gdn_linattn_sum_kernel<E>, dim3((unsigned)grid, 2), dim3(256), s, part, part + row,
-              static_cast<E*>(x.dq), static_cast<E*>(x.dk), quads, G, K / 4));
-  }
+    const int64_t n = std::min(ceil_div(quads, 256), (int64_t)device_cus() * 16);
+    return launch(gdn::gdn_linattn_sum_kernel<E>, dim3((unsigned)n, 2), dim3(256), s, part, part + row,
+                  static_cast<E*>(x.dq), static_cast<E*>(x.dk), quads, G, K / 4);
+  }));
   return err == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 

@@ -542,26 +542,54 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_residual_norm_bwd_kerne
   norm_partials<VEC, LPR, NV, 3>(acc, partial, g.D);
 }
 
-// out[k][c] = sum over the rows of partial[row][k][c], for the K outputs that are wanted: 16
-// groups of rows of 64 channels each, then the groups in order.
+// out[k][c] = sum over the rows of partial[row][k][c], for the K outputs that are wanted.  A
+// workgroup has 64 channels of one output, VEC of them per lane and so 16 VEC groups of rows;
+// their sums are added in the groups' order.
 struct NormSums {
   float* out[3];
 };
-static __global__ __launch_bounds__(1024) void gdn_norm_sums_kernel(const float* __restrict__ partial, int rows, int K,
-                                                                    int D, NormSums o) {
-  __shared__ float s[16][64];
-  const int groups = (D + 63) / 64, k = blockIdx.x / groups;
-  const int c = (blockIdx.x - k * groups) * 64 + lane_id(), w = threadIdx.x >> 6;
-  float a = 0.f;
-  if (o.out[k] && c < D)
-    for (int r = w; r < rows; r += 16) a += partial[((int64_t)r * K + k) * D + c];
-  s[w][lane_id()] = a;
-  __syncthreads();
-  if (w == 0 && o.out[k] && c < D) {
-    a = 0.f;
+constexpr int kSumAhead = 8;  // rows of a group that are loaded at a time
+template <int VEC>
+__global__ __launch_bounds__(1024) void gdn_norm_sums_kernel(const float* __restrict__ partial, int rows, int K, int D,
+                                                             NormSums o) {
+  constexpr int LANES = 64 / VEC, GROUPS = 1024 / LANES;
+  __shared__ float s[GROUPS][64 + 1], t[16][64 + 1];
+  const int blocks = (D + 63) / 64, k = blockIdx.x / blocks, c0 = (blockIdx.x - k * blocks) * 64;
+  if (!o.out[k]) return;
+  const int g = threadIdx.x / LANES, x = threadIdx.x % LANES * VEC;
+  float a[VEC] = {};
+  if (c0 + x < D) {
+    const float* p = partial + (int64_t)k * D + c0 + x;
+    for (int r = g; r < rows; r += GROUPS * kSumAhead) {
+      Chan<float, VEC> v[kSumAhead];
 #pragma unroll
-    for (int r = 0; r < 16; ++r) a += s[r][lane_id()];
-    o.out[k][c] = a;
+      for (int i = 0; i < kSumAhead; ++i) {
+        v[i].zero();
+        if (r + i * GROUPS < rows) v[i].load(p + (int64_t)(r + i * GROUPS) * K * D);
+      }
+#pragma unroll
+      for (int i = 0; i < kSumAhead; ++i) {
+        float f[VEC];
+        v[i].get(f);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) a[j] += f[j];
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) s[g][x + j] = a[j];
+  __syncthreads();
+  const int w = threadIdx.x >> 6, c = lane_id();
+  float b = 0.f;
+#pragma unroll
+  for (int r = 0; r < GROUPS / 16; ++r) b += s[w * (GROUPS / 16) + r][c];
+  t[w][c] = b;
+  __syncthreads();
+  if (w == 0 && c0 + c < D) {
+    b = 0.f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) b += t[r][c];
+    o.out[k][c0 + c] = b;
   }
 }
 

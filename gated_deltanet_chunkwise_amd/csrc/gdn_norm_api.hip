@@ -100,7 +100,7 @@ size_t norm_ws(const NormPlan& pl, int K) {
 }
 
 hipError_t norm_sums(const NormPlan& pl, const float* partial, int64_t rows, int K, gdn::NormSums o, hipStream_t s) {
-  return launch(gdn::gdn_norm_sums_kernel, dim3((unsigned)(K * ceil_div(pl.geo.D, 64))), dim3(1024), s, partial,
+  return launch(pl.geo.D % 4 ? gdn::gdn_norm_sums_kernel<1> : gdn::gdn_norm_sums_kernel<4>, dim3((unsigned)(K * ceil_div(pl.geo.D, 64))), dim3(1024), s, partial,
                 (int)rows, K, pl.geo.D, o);
 }
 
