@@ -30,6 +30,8 @@ struct AttnPlan {
 // Chunks per segment, for sequences of `chunks` in `units` (sequence, head) pairs or, packed, one
 // row of them per head that holds `packed` sequences.  256 CUs are taken for granted, so that the
 // workspace is the same on every device; a CU runs one workgroup of the last launch at a time.
+// Packed sequences end half a segment early each; no more than 32 are counted, since offsets may
+// be padded with empty ones, which cost nothing.
 // For 1 to 8 rounds of workgroups, the least of: a round's chunks (about 3.7 us each at B=2,
 // T=2048, 16 heads of 128 bf16) with its start; and, with several segments, the launch that forms
 // what they add, two workgroups per CU, and the third.  (us, by whole segments of 16 chunks and by
@@ -38,11 +40,12 @@ struct AttnPlan {
 int64_t segment_chunks(int64_t chunks, int64_t units, int64_t packed) {
   int64_t best = chunks;
   double least = 1e300;
+  const int64_t ends = std::min<int64_t>(packed, 32) / 2;
   for (int rounds = 1; rounds <= 8; ++rounds) {
-    // segments per row of chunks that fill so many rounds; sequences end half a segment each
-    const int64_t fill = std::max<int64_t>(256 * rounds / units - packed / 2, 1);
+    // segments per row of chunks that fill so many rounds
+    const int64_t fill = std::max<int64_t>(256 * rounds / units - ends, 1);
     const int64_t len = std::min(std::max(ceil_div(chunks, fill), kLeast), chunks);
-    const int64_t n = ceil_div(chunks, len), wgs = units * (n + packed / 2);
+    const int64_t n = ceil_div(chunks, len), wgs = units * (n + ends);
     double cost = (double)ceil_div(wgs, 256) * (len + 1.5 + 0.25 * std::min<int64_t>(n, 8));
     if (n > 1) cost += ceil_div(wgs, 512) * (len * (wgs > 256 ? 0.9 : 0.6) + 1.) + 0.8 + (n > kSumMost ? 3. : 0.);
     if (cost < least) {

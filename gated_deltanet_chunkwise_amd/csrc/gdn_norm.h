@@ -427,7 +427,7 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_residual_norm_bwd_kerne
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < VEC; ++j) acc[k][i][j] = 0.f;
-  auto vec = [&](const float* p, int c, float (&v)[VEC]) {
+  auto read = [&](const float* p, int c, float (&v)[VEC]) {
     Chan<float, VEC> t;
     if (p && c < g.D) {
       t.load(p + c);
@@ -437,26 +437,61 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_residual_norm_bwd_kerne
       for (int j = 0; j < VEC; ++j) v[j] = 1.f;
     }
   };
-  for (int64_t base = (int64_t)blockIdx.x * RPB; base < g.rows; base += (int64_t)gridDim.x * RPB) {
-    const int64_t row = base + sub;
-    const bool live = row < g.rows;
-    const int64_t at = live ? row : 0;
-    Chan<E, VEC> xv[NV], hv[NV];
-    Chan<R, VEC> rv[NV], sv[NV];
+  // Where a lane has one vector, it keeps the weights' as well, and loads a row ahead of its use
+  // (B=4, T=4096, C=2048 bf16: 108 us without either in 1024 workgroups, 86 with both in 512).
+  constexpr bool HOLD = NV == 1 && LPR <= 512;
+  float held[3][VEC];
+  if constexpr (HOLD) {
+    read(w, l * VEC, held[0]);
+    read(post, l * VEC, held[1]);
+    read(scale, l * VEC, held[2]);
+  }
+  auto vec = [&](auto which, int c, float (&v)[VEC]) {
+    constexpr int k = decltype(which)::value;
+    if constexpr (HOLD) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[j] = held[k][j];
+    } else {
+      read(k == 0 ? w : k == 1 ? post : scale, c, v);
+    }
+  };
+  constexpr std::integral_constant<int, 0> kW{};
+  constexpr std::integral_constant<int, 1> kPost{};
+  constexpr std::integral_constant<int, 2> kScale{};
+  struct Row {
+    Chan<E, VEC> x[NV], h[NV];
+    Chan<R, VEC> r[NV], s[NV];
+  };
+  auto load = [&](Row& o, int64_t row) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * LPR + l) * VEC;
-      xv[i].zero();
-      hv[i].zero();
-      rv[i].zero();
-      sv[i].zero();
-      if (c < g.D && live) {
-        xv[i].load(x + at * g.ldx + c);
-        rv[i].load(residual + at * g.ldz + c);
-        hv[i].load(dh + at * g.D + c);
-        if (ds) sv[i].load(ds + at * g.D + c);
+      o.x[i].zero();
+      o.h[i].zero();
+      o.r[i].zero();
+      o.s[i].zero();
+      if (c < g.D && row < g.rows) {
+        o.x[i].load(x + row * g.ldx + c);
+        o.r[i].load(residual + row * g.ldz + c);
+        o.h[i].load(dh + row * g.D + c);
+        if (ds) o.s[i].load(ds + row * g.D + c);
       }
     }
+  };
+  Row next;
+  if constexpr (HOLD) load(next, (int64_t)blockIdx.x * RPB + sub);
+  for (int64_t base = (int64_t)blockIdx.x * RPB; base < g.rows; base += (int64_t)gridDim.x * RPB) {
+    const int64_t row = base + sub;
+    const bool live = row < g.rows;
+    Row cur;
+    if constexpr (HOLD) {
+      cur = next;
+      load(next, row + (int64_t)gridDim.x * RPB);
+    } else {
+      load(cur, row);
+    }
+    const auto &xv = cur.x, &hv = cur.h;
+    const auto &rv = cur.r, &sv = cur.s;
     float cp = 1.f;
     if (post) {
       float ss = 0.f;
@@ -476,8 +511,8 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_residual_norm_bwd_kerne
       float xf[VEC], pf[VEC], cf[VEC];
       xv[i].get(xf);
       rv[i].get(s[i]);
-      vec(post, c, pf);
-      vec(scale, c, cf);
+      vec(kPost, c, pf);
+      vec(kScale, c, cf);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         s[i][j] += cf[j] * (xf[j] * cp * pf[j]);
@@ -490,7 +525,7 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_residual_norm_bwd_kerne
     for (int i = 0; i < NV; ++i) {
       float hf[VEC], wf[VEC];
       hv[i].get(hf);
-      vec(w, (i * LPR + l) * VEC, wf);
+      vec(kW, (i * LPR + l) * VEC, wf);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         const float n = s[i][j] * c;
@@ -508,9 +543,9 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_residual_norm_bwd_kerne
       hv[i].get(hf);
       sv[i].get(d);
       xv[i].get(xf);
-      vec(w, ch, wf);
-      vec(post, ch, pf);
-      vec(scale, ch, cf);
+      vec(kW, ch, wf);
+      vec(kPost, ch, pf);
+      vec(kScale, ch, cf);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         const float n = s[i][j] * c;
@@ -531,8 +566,8 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_residual_norm_bwd_kerne
       if (ch >= g.D) continue;
       float xf[VEC], pf[VEC], cf[VEC];
       xv[i].get(xf);
-      vec(post, ch, pf);
-      vec(scale, ch, cf);
+      vec(kPost, ch, pf);
+      vec(kScale, ch, cf);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) xf[j] = cp * (s[i][j] * cf[j] * pf[j] - xf[j] * cp * q);
       chan_store<R, VEC>(dr + row * g.D + ch, s[i]);
