@@ -205,15 +205,19 @@ template <typename E, int D, int THREADS> struct AttnTile {
   template <int APART> __device__ __forceinline__ Frag<E> of_columns(int s0, int c0) const {
     typedef short s16x4 __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-    const int g = lane_id() >> 4, m = lane_id() & 15;
     if constexpr (sizeof(E) == 2) {
+      const int g = lane_id() >> 4, m = lane_id() & 15;
       const int row = s0 + 8 * g + (m >> 2), col = c0 + APART * (m & 3);
       const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at(row, col));
       const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at(row + 4, col));
       const auto both = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
       return {__builtin_bit_cast(bf16x8, both)};
     } else {
-      const int row = s0 + 8 * g, col = c0 + APART * (m >> 2) + (m & 3);
+      int lane = lane_id();
+      // where the tiles are of two widths, addresses kept from chunk to chunk need more registers
+      // than there are: formed here each time
+      if constexpr (D * 4 != THREADS) asm volatile("" : "+v"(lane));
+      const int row = s0 + 8 * (lane >> 4), col = c0 + APART * ((lane & 15) >> 2) + (lane & 3);
       Frag<E> f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -482,11 +486,12 @@ __device__ __forceinline__ void attn_pass(const AttnGeo& geo, int block, const A
 
     f32x4 acc[TT];
     if constexpr (OUT && decltype(more)::value) fetch_c(it + 1);
-    if constexpr (OUT) if (owner) {
+    if constexpr (OUT) {
       // the weighted products of a tile of rows of a with those rows of b that they see, two
-      // tiles of b at a time; two waves share a tile of a where there are eight
+      // tiles of b at a time; two waves share a tile of a where there are eight (all of them, also
+      // those beyond the columns)
       {
-        constexpr int SHARE = WAVES / TT;
+        constexpr int SHARE = THREADS / 64 / TT;
         const int tt = wave / SHARE, t = 16 * tt + m;
         Frag<E> fa[KD / 32];
 #pragma unroll
@@ -522,6 +527,8 @@ __device__ __forceinline__ void attn_pass(const AttnGeo& geo, int block, const A
           ATTN_PHASE;
         }
       }
+    }
+    if constexpr (OUT) if (owner) {
       // the state's part: O^T = H^T a^T, then weighted by row
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) acc[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -617,7 +624,7 @@ __global__ __launch_bounds__(attn_threads(K > V ? K : V), (attn_waves<E, (K > V 
 // The starts of sequences' segments: per sequence, head and four elements of the state, in the
 // segments' order (REV: from the last),  w[segment] <- cur;  cur <- a^len cur + (what
 // w[segment] held),  from `start` (or 0).  Loads run kAttnAhead segments ahead.
-constexpr int kAttnAhead = 8;
+constexpr int kAttnAhead = 16;
 
 template <int KD, int VD, bool REV>
 __device__ __forceinline__ void attn_join(const AttnGeo& geo, const float* __restrict__ log_decay, const AttnState& st) {

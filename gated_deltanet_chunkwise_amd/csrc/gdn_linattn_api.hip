@@ -1,5 +1,7 @@
 // gdn_linattn_api.hip -- entry points of linear attention with a decay for each head:
 // validation, segments and launches.  See include/gdn.h.
+#include <cmath>
+
 #include "gdn_host.h"
 #include "gdn_linattn.h"
 
@@ -11,10 +13,8 @@ using gdn::AttnRows;
 using gdn::AttnState;
 using gdn::kChunk;
 
-// Segments of a sequence up to which each sums its start itself; chunks that a segment has at
-// least.
+// Segments of a sequence up to which each sums its start itself.
 constexpr int kSumMost = 8;
-constexpr int64_t kLeast = 2;
 
 struct AttnPlan {
   AttnGeo geo;
@@ -28,26 +28,42 @@ struct AttnPlan {
 };
 
 // Chunks per segment, for sequences of `chunks` in `units` (sequence, head) pairs or, packed, one
-// row of them per head that holds `packed` sequences.  256 CUs are taken for granted, so that the
-// workspace is the same on every device; a CU runs one workgroup of the last launch at a time.
-// Packed sequences end half a segment early each; no more than 32 are counted, since offsets may
-// be padded with empty ones, which cost nothing.
-// For 1 to 8 rounds of workgroups, the least of: a round's chunks (about 3.7 us each at B=2,
-// T=2048, 16 heads of 128 bf16) with its start; and, with several segments, the launch that forms
-// what they add, two workgroups per CU, and the third.  (us, by whole segments of 16 chunks and by
-// this: 16 sequences of 2048 tokens, 16 heads 207 and 153; 32768 packed tokens in 12 sequences, 16
-// heads 228 and 225.)
-int64_t segment_chunks(int64_t chunks, int64_t units, int64_t packed) {
+// row of them per head that holds `packed` sequences; `passes` in one launch (3 backwards); G heads
+// share a key head.  256 CUs in 8 XCDs are taken for granted, so that the workspace is the same on
+// every device; a CU runs one workgroup of the last launch at a time.  Packed sequences end with a short segment each; no more
+// than 32 are counted, since offsets may be padded with empty ones, which cost nothing.
+//
+// The least time of one segment and of 1 to 8 rounds of workgroups, by figures in us as measured: a chunk in the last
+// launch 4.1 (bf16: memory and LDS; a quarter less where few CUs are busy) or 14 (fp32, 128 x 128:
+// matrix cores), in the first 2 or 4; a workgroup's own start 5, a state that it reads for it 0.7;
+// the launches in between 3, and the states that the join reads and writes.  Segments of one
+// length run in whole rounds of an XCD; those of packed sequences in whatever order, a part of one
+// behind the mean.
+// Measured (us; by the forward pass's rounds alone with two chunks at least, and by this): backward,
+// 2 sequences of 2048 tokens, 16 heads of 128 bf16, 98 and 89 (4 and 7 chunks); 5003 packed tokens,
+// 8 value heads of 128 x 64, 72 and 69 (2 and 5); 3 sequences of 777 tokens, 5 heads of 64 x 128
+// fp32, 33 and 28 (2 and 1).
+int64_t segment_chunks(int64_t chunks, int64_t units, int64_t packed, int G, int passes, int K, int V, bool fp32) {
   int64_t best = chunks;
   double least = 1e300;
-  const int64_t ends = std::min<int64_t>(packed, 32) / 2;
-  for (int rounds = 1; rounds <= 8; ++rounds) {
-    // segments per row of chunks that fill so many rounds
-    const int64_t fill = std::max<int64_t>(256 * rounds / units - ends, 1);
-    const int64_t len = std::min(std::max(ceil_div(chunks, fill), kLeast), chunks);
-    const int64_t n = ceil_div(chunks, len), wgs = units * (n + ends);
-    double cost = (double)ceil_div(wgs, 256) * (len + 1.5 + 0.25 * std::min<int64_t>(n, 8));
-    if (n > 1) cost += ceil_div(wgs, 512) * (len * (wgs > 256 ? 0.9 : 0.6) + 1.) + 0.8 + (n > kSumMost ? 3. : 0.);
+  const double ends = (double)std::min<int64_t>(packed, 32), area = K * V / 16384.;
+  const double chunk = fp32 ? 3.5 + 10.5 * area : 4.1, first = fp32 ? 4. * area : 2.;
+  const int sums = passes > 1 ? 2 : 1;  // kinds of states
+  const double row = (double)units * passes / 256.;
+  for (int rounds = 0; rounds <= 8; ++rounds) {
+    // segments per row of chunks that fill so many rounds, or one
+    const int64_t fill = std::max<int64_t>((int64_t)(rounds / row - 0.5 * ends), 1);
+    const int64_t len = ceil_div(chunks, fill), n = ceil_div(chunks, len);
+    const double start = 5. + 0.7 * area * (n == 1 ? 0 : n <= kSumMost ? n : 2);
+    const double wgs = packed ? row * (n + ends) : ceil_div(units / G * n, 8) * G * passes / 32.;
+    const double one = len * chunk, whole = std::floor(wgs);
+    double cost;
+    if (wgs <= 1.) cost = one * (0.75 + 0.25 * wgs) + start;
+    else if (packed) cost = row * chunks * chunk + wgs * start + 0.3 * (one + start);
+    else cost = whole * (one + start) + (wgs > whole ? one * (0.75 + 0.25 * (wgs - whole)) + start : 0.);
+    const double states = units * (n + 0.5 * ends) * sums;
+    if (n > 1) cost += 3. + len * first * std::max(1., (states - units * sums) / 256.);
+    if (n > kSumMost) cost += 3. + states * area * (16384. * 4 * 3 / 5e6);
     if (cost < least) {
       least = cost;
       best = len;
@@ -56,8 +72,8 @@ int64_t segment_chunks(int64_t chunks, int64_t units, int64_t packed) {
   return best;
 }
 
-// Sizes only.
-gdn_status_t attn_sizes(const gdn_linattn_params_t* p, bool packed, AttnPlan* out) {
+// Sizes only; `passes` of the last launch.
+gdn_status_t attn_sizes(const gdn_linattn_params_t* p, bool packed, int passes, AttnPlan* out) {
   if (!p) return GDN_ERR_NULL;
   const int32_t dtype = p->dtype & ~GDN_ZERO_REST;
   if (dtype != GDN_F32 && dtype != GDN_BF16) return GDN_ERR_DTYPE;
@@ -88,7 +104,8 @@ gdn_status_t attn_sizes(const gdn_linattn_params_t* p, bool packed, AttnPlan* ou
   if ((int64_t)g.N * g.HV > (int64_t)1 << 40 || pl.tok > ((int64_t)1 << 48) / g.HV) return GDN_ERR_UNSUPPORTED;
 
   const int64_t chunks = ceil_div(std::max(g.T, 1), kChunk);  // of a sequence, or of the packed row
-  g.chunks = (int)segment_chunks(chunks, packed ? g.HV : (int64_t)std::max(g.B, 1) * g.HV, packed ? g.N : 0);
+  g.chunks = (int)segment_chunks(chunks, packed ? g.HV : (int64_t)std::max(g.B, 1) * g.HV, packed ? g.N : 0,
+                                 g.G, passes, pl.K, pl.V, pl.esz == 4);
   g.nseg = (int)ceil_div(chunks, g.chunks);
   const int64_t slots = packed ? (int64_t)g.T / kChunk / g.chunks + g.N : (int64_t)g.nseg * g.N;
   if (slots > INT32_MAX) return GDN_ERR_UNSUPPORTED;
@@ -232,14 +249,14 @@ extern "C" {
 
 size_t gdn_linattn_fwd_workspace_size(const gdn_linattn_params_t* p, int packed) {
   AttnPlan pl;
-  return attn_sizes(p, packed != 0, &pl) == GDN_OK ? attn_states(pl) : 0;
+  return attn_sizes(p, packed != 0, 1, &pl) == GDN_OK ? attn_states(pl) : 0;
 }
 
 gdn_status_t gdn_linattn_fwd(const gdn_linattn_params_t* p, const void* q, const void* k, const void* v,
                              const float* log_decay, const int64_t* cu_seqlens, const float* initial_state, void* o,
                              float* final_state, void* workspace, size_t workspace_bytes, void* stream) {
   AttnPlan pl;
-  gdn_status_t st = attn_sizes(p, cu_seqlens != nullptr, &pl);
+  gdn_status_t st = attn_sizes(p, cu_seqlens != nullptr, 1, &pl);
   if (st != GDN_OK) return st;
   if (!log_decay || (pl.tok > 0 && (!q || !k || !v || !o))) return GDN_ERR_NULL;
   const size_t need = attn_states(pl);
@@ -257,7 +274,7 @@ gdn_status_t gdn_linattn_fwd(const gdn_linattn_params_t* p, const void* q, const
 
 size_t gdn_linattn_bwd_workspace_size(const gdn_linattn_params_t* p, int packed) {
   AttnPlan pl;
-  return attn_sizes(p, packed != 0, &pl) == GDN_OK ? 2 * attn_states(pl) + attn_partial(pl) : 0;
+  return attn_sizes(p, packed != 0, 3, &pl) == GDN_OK ? 2 * attn_states(pl) + attn_partial(pl) : 0;
 }
 
 gdn_status_t gdn_linattn_bwd(const gdn_linattn_params_t* p, const void* q, const void* k, const void* v,
@@ -265,7 +282,7 @@ gdn_status_t gdn_linattn_bwd(const gdn_linattn_params_t* p, const void* q, const
                              const void* d_o, const float* d_final_state, void* dq, void* dk, void* dv,
                              float* d_initial_state, void* workspace, size_t workspace_bytes, void* stream) {
   AttnPlan pl;
-  gdn_status_t st = attn_sizes(p, cu_seqlens != nullptr, &pl);
+  gdn_status_t st = attn_sizes(p, cu_seqlens != nullptr, 3, &pl);
   if (st != GDN_OK) return st;
   if (!log_decay || (pl.tok > 0 && (!q || !k || !v || !d_o || !dq || !dk || !dv))) return GDN_ERR_NULL;
   const size_t need = 2 * attn_states(pl) + attn_partial(pl);
@@ -284,7 +301,7 @@ gdn_status_t gdn_linattn_bwd(const gdn_linattn_params_t* p, const void* q, const
 gdn_status_t gdn_linattn_decode(const gdn_linattn_params_t* p, const void* q, const void* k, const void* v,
                                 const float* log_decay, const float* state, float* new_state, void* o, void* stream) {
   AttnPlan pl;
-  gdn_status_t st = attn_sizes(p, false, &pl);
+  gdn_status_t st = attn_sizes(p, false, 1, &pl);
   if (st != GDN_OK) return st;
   if (p->num_seqs != 0) return GDN_ERR_SHAPE;
   if (p->B > 0 && (!state || !new_state || !log_decay)) return GDN_ERR_NULL;
