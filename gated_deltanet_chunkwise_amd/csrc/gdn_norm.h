@@ -20,22 +20,33 @@ namespace gdn {
 
 enum { kGateNone = 0, kGateAfter = 1, kGateFirst = 2 };
 
-// VEC channels of a row as loaded.
+// VEC channels of a row as loaded.  Rows of any width are read and written 16 bytes at a time: the
+// device takes such accesses at any element's address, and only the row's last vector, where
+// `left` channels are fewer than VEC, is put together (zeros behind them).
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 template <int BYTES> struct RawBytes;
 template <> struct RawBytes<32> { u32x4 a, b; };
 template <> struct RawBytes<16> { u32x4 a; };
-template <> struct RawBytes<8> { u32x2 a; };
 template <> struct RawBytes<4> { uint32_t a; };
 template <> struct RawBytes<2> { uint16_t a; };
 template <typename E, int VEC> struct Chan {
   RawBytes<VEC * (int)sizeof(E)> r;
-  __device__ __forceinline__ void load(const E* p) {
-    using R = RawBytes<VEC * (int)sizeof(E)>;
-    if constexpr (sizeof(R) == 32) {  // (16-byte alignment is asked for, not 32)
-      r.a = reinterpret_cast<const u32x4*>(p)[0];
-      r.b = reinterpret_cast<const u32x4*>(p)[1];
-    } else {
+  __device__ __forceinline__ void load(const E* p, int left) {
+    if constexpr (VEC == 1) {
       r.a = *reinterpret_cast<const decltype(r.a)*>(p);
+    } else if (left >= VEC) {
+      r.a = *reinterpret_cast<const u32x4_any*>(p);
+      if constexpr (sizeof(r) == 32) r.b = *reinterpret_cast<const u32x4_any*>(p + 4);
+    } else if constexpr (sizeof(E) == 2) {  // the row's last VEC channels, moved down
+      typedef unsigned __int128 bits;
+      const bits v = __builtin_bit_cast(bits, (u32x4)*reinterpret_cast<const u32x4_any*>(p + left - VEC));
+      r.a = __builtin_bit_cast(u32x4, v >> (16 * (VEC - left)));
+    } else {
+      uint32_t v[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = i < left ? __float_as_uint(p[i]) : 0;
+      r.a = u32x4{v[0], v[1], v[2], v[3]};
+      if constexpr (sizeof(r) == 32) r.b = u32x4{v[4], v[5], v[6], v[7]};
     }
   }
   __device__ __forceinline__ void zero() { r = {}; }
@@ -56,18 +67,23 @@ template <typename E, int VEC> struct Chan {
     }
   }
 };
-template <typename E, int VEC> __device__ __forceinline__ void chan_store(E* p, const float (&v)[VEC]) {
+template <typename E, int VEC> __device__ __forceinline__ void chan_store(E* p, const float (&v)[VEC], int left) {
   if constexpr (VEC == 1) {
     *p = (E)v[0];
+  } else if (left < VEC) {
+#pragma unroll
+    for (int i = 0; i < VEC - 1; ++i)
+      if (i < left) p[i] = (E)v[i];
   } else if constexpr (VEC * sizeof(E) == 32) {
-    reinterpret_cast<f32x4*>(p)[0] = f32x4{v[0], v[1], v[2], v[3]};
-    reinterpret_cast<f32x4*>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
+    typedef float any __attribute__((ext_vector_type(4), aligned(4)));
+    reinterpret_cast<any*>(p)[0] = f32x4{v[0], v[1], v[2], v[3]};
+    reinterpret_cast<any*>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
   } else {
     typedef E vec __attribute__((ext_vector_type(VEC)));
     vec x;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) x[i] = (E)v[i];
-    *reinterpret_cast<vec*>(p) = x;
+    *reinterpret_cast<u32x4_any*>(p) = __builtin_bit_cast(u32x4, x);
   }
 }
 
@@ -96,10 +112,8 @@ template <int LPR> struct RowSum {
       return v;
     } else {
       v = row16_sum(v);
-      if constexpr (LPR >= 64) {
-        v += __shfl_xor(v, 16);
-        v += __shfl_xor(v, 32);
-      }
+      if constexpr (LPR >= 32) v += __shfl_xor(v, 16);
+      if constexpr (LPR >= 64) v += __shfl_xor(v, 32);
       if constexpr (LPR > 64) {
         constexpr int W = LPR / 64;
         if (lane_id() == 0) slot[turn][threadIdx.x >> 6] = v;
@@ -129,10 +143,13 @@ __device__ __forceinline__ int64_t norm_row(const NormGeo& g, int64_t row, int64
   return t * ld + ((uint32_t)row - t * g.H) * (int64_t)g.D;
 }
 
+// Channels of a row of D from c on, as a vector's load or store asks (WHOLE: D is a multiple of VEC).
+template <bool WHOLE, int VEC> __device__ __forceinline__ int channels_left(int D, int c) { return WHOLE ? VEC : D - c; }
+
 // Threads of a workgroup, and the rows that it holds at a time.
 constexpr int norm_threads(int lpr) { return lpr <= 256 ? 256 : lpr; }
 
-template <typename E, int VEC, int LPR, int NV>
+template <typename E, int VEC, int LPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(norm_threads(LPR)) void gdn_gated_norm_kernel(NormGeo g, const E* __restrict__ x,
                                                                           const float* __restrict__ w,
                                                                           const E* __restrict__ z, E* __restrict__ y) {
@@ -144,7 +161,7 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_gated_norm_kernel(NormG
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * LPR + l) * VEC;
-    if (c < g.D) wv[i].load(w + c);
+    if (c < g.D) wv[i].load(w + c, channels_left<WHOLE, VEC>(g.D, c));
     else wv[i].zero();
   }
   for (int64_t base = (int64_t)blockIdx.x * RPB; base < g.rows; base += (int64_t)gridDim.x * RPB) {
@@ -159,8 +176,8 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_gated_norm_kernel(NormG
       xv[i].zero();
       zv[i].zero();
       if (c < g.D && live) {
-        xv[i].load(xr + c);
-        if (z) zv[i].load(zr + c);
+        xv[i].load(xr + c, channels_left<WHOLE, VEC>(g.D, c));
+        if (z) zv[i].load(zr + c, channels_left<WHOLE, VEC>(g.D, c));
       }
     }
     float u[NV][VEC], gate[NV][VEC], ss = 0.f;
@@ -188,13 +205,13 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_gated_norm_kernel(NormG
         out[j] = u[i][j] * c * wf[j];
         if (g.mode == kGateAfter) out[j] *= gate[i][j];
       }
-      if (ch < g.D) chan_store<E, VEC>(yr + ch, out);
+      if (ch < g.D) chan_store<E, VEC>(yr + ch, out, channels_left<WHOLE, VEC>(g.D, ch));
     }
   }
 }
 
 // The workgroup's sums of K weights' gradients, from its row groups, to partial[block][k][D].
-template <int VEC, int LPR, int NV, int K>
+template <int VEC, int LPR, int NV, bool WHOLE, int K>
 __device__ __forceinline__ void norm_partials(float (&acc)[K][NV][VEC], float* __restrict__ partial, int D) {
   constexpr int RPB = norm_threads(LPR) / LPR;
   const int sub = threadIdx.x / LPR, l = threadIdx.x % LPR;
@@ -204,7 +221,7 @@ __device__ __forceinline__ void norm_partials(float (&acc)[K][NV][VEC], float* _
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * LPR + l) * VEC;
-        if (c < D) chan_store<float, VEC>(partial + ((int64_t)blockIdx.x * K + k) * D + c, acc[k][i]);
+        if (c < D) chan_store<float, VEC>(partial + ((int64_t)blockIdx.x * K + k) * D + c, acc[k][i], channels_left<WHOLE, VEC>(D, c));
       }
   } else {
     __shared__ float sums[norm_threads(LPR) * VEC];
@@ -227,7 +244,7 @@ __device__ __forceinline__ void norm_partials(float (&acc)[K][NV][VEC], float* _
   }
 }
 
-template <typename E, int VEC, int LPR, int NV>
+template <typename E, int VEC, int LPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(norm_threads(LPR)) void gdn_gated_norm_bwd_kernel(
     NormGeo g, const E* __restrict__ x, const float* __restrict__ w, const E* __restrict__ z,
     const E* __restrict__ dy, E* __restrict__ dx, E* __restrict__ dz, float* __restrict__ partial) {
@@ -240,7 +257,7 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_gated_norm_bwd_kernel(
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * LPR + l) * VEC;
-    if (c < g.D) wv[i].load(w + c);
+    if (c < g.D) wv[i].load(w + c, channels_left<WHOLE, VEC>(g.D, c));
     else wv[i].zero();
 #pragma unroll
     for (int j = 0; j < VEC; ++j) acc[0][i][j] = 0.f;
@@ -260,9 +277,9 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_gated_norm_bwd_kernel(
       zv[i].zero();
       dv[i].zero();
       if (c < g.D && live) {
-        xv[i].load(xr + c);
-        dv[i].load(dy + at * g.D + c);
-        if (z) zv[i].load(zr + c);
+        xv[i].load(xr + c, channels_left<WHOLE, VEC>(g.D, c));
+        dv[i].load(dy + at * g.D + c, channels_left<WHOLE, VEC>(g.D, c));
+        if (z) zv[i].load(zr + c, channels_left<WHOLE, VEC>(g.D, c));
       }
     }
     float u[NV][VEC], ss = 0.f;
@@ -320,15 +337,15 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_gated_norm_bwd_kernel(
         }
       }
       if (ch < g.D) {
-        chan_store<E, VEC>(dx + row * g.D + ch, ox);
-        if (z) chan_store<E, VEC>(dz + row * g.D + ch, oz);
+        chan_store<E, VEC>(dx + row * g.D + ch, ox, channels_left<WHOLE, VEC>(g.D, ch));
+        if (z) chan_store<E, VEC>(dz + row * g.D + ch, oz, channels_left<WHOLE, VEC>(g.D, ch));
       }
     }
   }
-  norm_partials<VEC, LPR, NV, 1>(acc, partial, g.D);
+  norm_partials<VEC, LPR, NV, WHOLE, 1>(acc, partial, g.D);
 }
 
-template <typename E, typename R, int VEC, int LPR, int NV>
+template <typename E, typename R, int VEC, int LPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(norm_threads(LPR)) void gdn_residual_norm_kernel(
     NormGeo g, const E* __restrict__ x, const R* residual, const float* __restrict__ w,
     const float* __restrict__ post, const float* __restrict__ scale, E* __restrict__ h, R* out) {
@@ -350,8 +367,8 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_residual_norm_kernel(
       xv[i].zero();
       rv[i].zero();
       if (c < g.D && live) {
-        xv[i].load(xr + c);
-        rv[i].load(rr + c);
+        xv[i].load(xr + c, channels_left<WHOLE, VEC>(g.D, c));
+        rv[i].load(rr + c, channels_left<WHOLE, VEC>(g.D, c));
       }
     }
     float s[NV][VEC];
@@ -378,8 +395,8 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_residual_norm_kernel(
       pv.zero();
       sv.zero();
       if (c < g.D) {
-        if (post) pv.load(post + c);
-        if (scale) sv.load(scale + c);
+        if (post) pv.load(post + c, channels_left<WHOLE, VEC>(g.D, c));
+        if (scale) sv.load(scale + c, channels_left<WHOLE, VEC>(g.D, c));
       }
       pv.get(pf);
       sv.get(sf);
@@ -398,19 +415,19 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_residual_norm_kernel(
       if (ch >= g.D) continue;
       Chan<float, VEC> wv;
       float wf[VEC], hf[VEC];
-      wv.load(w + ch);
+      wv.load(w + ch, channels_left<WHOLE, VEC>(g.D, ch));
       wv.get(wf);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) hf[j] = s[i][j] * c * wf[j];
-      chan_store<R, VEC>(out + row * g.D + ch, s[i]);
-      chan_store<E, VEC>(h + row * g.D + ch, hf);
+      chan_store<R, VEC>(out + row * g.D + ch, s[i], channels_left<WHOLE, VEC>(g.D, ch));
+      chan_store<E, VEC>(h + row * g.D + ch, hf, channels_left<WHOLE, VEC>(g.D, ch));
     }
   }
 }
 
 // s is formed again from x and the residual, in fp32, so that the gradients are those of the
 // values that h was formed from (and not of s as it was rounded).
-template <typename E, typename R, int VEC, int LPR, int NV>
+template <typename E, typename R, int VEC, int LPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(norm_threads(LPR)) void gdn_residual_norm_bwd_kernel(
     NormGeo g, const E* __restrict__ x, const R* __restrict__ residual, const float* __restrict__ w,
     const float* __restrict__ post, const float* __restrict__ scale, const E* __restrict__ dh,
@@ -430,7 +447,7 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_residual_norm_bwd_kerne
   auto read = [&](const float* p, int c, float (&v)[VEC]) {
     Chan<float, VEC> t;
     if (p && c < g.D) {
-      t.load(p + c);
+      t.load(p + c, channels_left<WHOLE, VEC>(g.D, c));
       t.get(v);
     } else {
 #pragma unroll
@@ -471,10 +488,10 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_residual_norm_bwd_kerne
       o.r[i].zero();
       o.s[i].zero();
       if (c < g.D && row < g.rows) {
-        o.x[i].load(x + row * g.ldx + c);
-        o.r[i].load(residual + row * g.ldz + c);
-        o.h[i].load(dh + row * g.D + c);
-        if (ds) o.s[i].load(ds + row * g.D + c);
+        o.x[i].load(x + row * g.ldx + c, channels_left<WHOLE, VEC>(g.D, c));
+        o.r[i].load(residual + row * g.ldz + c, channels_left<WHOLE, VEC>(g.D, c));
+        o.h[i].load(dh + row * g.D + c, channels_left<WHOLE, VEC>(g.D, c));
+        if (ds) o.s[i].load(ds + row * g.D + c, channels_left<WHOLE, VEC>(g.D, c));
       }
     }
   };
@@ -570,11 +587,11 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_residual_norm_bwd_kerne
       vec(kScale, ch, cf);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) xf[j] = cp * (s[i][j] * cf[j] * pf[j] - xf[j] * cp * q);
-      chan_store<R, VEC>(dr + row * g.D + ch, s[i]);
-      chan_store<E, VEC>(dx + row * g.D + ch, xf);
+      chan_store<R, VEC>(dr + row * g.D + ch, s[i], channels_left<WHOLE, VEC>(g.D, ch));
+      chan_store<E, VEC>(dx + row * g.D + ch, xf, channels_left<WHOLE, VEC>(g.D, ch));
     }
   }
-  norm_partials<VEC, LPR, NV, 3>(acc, partial, g.D);
+  norm_partials<VEC, LPR, NV, WHOLE, 3>(acc, partial, g.D);
 }
 
 // out[k][c] = sum over the rows of partial[row][k][c], for the K outputs that are wanted.  A
@@ -600,7 +617,7 @@ __global__ __launch_bounds__(1024) void gdn_norm_sums_kernel(const float* __rest
 #pragma unroll
       for (int i = 0; i < kSumAhead; ++i) {
         v[i].zero();
-        if (r + i * GROUPS < rows) v[i].load(p + (int64_t)(r + i * GROUPS) * K * D);
+        if (r + i * GROUPS < rows) v[i].load(p + (int64_t)(r + i * GROUPS) * K * D, VEC);
       }
 #pragma unroll
       for (int i = 0; i < kSumAhead; ++i) {
