@@ -30,30 +30,32 @@ struct AttnPlan {
 // Chunks per segment, for sequences of `chunks` in `units` (sequence, head) pairs or, packed, one
 // row of them per head that holds `packed` sequences; `passes` in one launch (3 backwards); G heads
 // share a key head.  256 CUs in 8 XCDs are taken for granted, so that the workspace is the same on
-// every device; a CU runs one workgroup of the last launch at a time.  Packed sequences end with a short segment each; no more
-// than 32 are counted, since offsets may be padded with empty ones, which cost nothing.
+// every device; a CU runs one workgroup of the last launch at a time.  Packed sequences end with a
+// short segment each; no more than 32 are counted, since offsets may be padded with empty ones,
+// which cost nothing.
 //
-// The least time of one segment and of 1 to 8 rounds of workgroups, by figures in us as measured: a chunk in the last
-// launch 4.1 (bf16: memory and LDS; a quarter less where few CUs are busy) or 14 (fp32, 128 x 128:
-// matrix cores), in the first 2 or 4; a workgroup's own start 5, a state that it reads for it 0.7;
-// the launches in between 3, and the states that the join reads and writes.  Segments of one
-// length run in whole rounds of an XCD; those of packed sequences in whatever order, a part of one
-// behind the mean.
-// Measured (us; by the forward pass's rounds alone with two chunks at least, and by this): backward,
-// 2 sequences of 2048 tokens, 16 heads of 128 bf16, 98 and 89 (4 and 7 chunks); 5003 packed tokens,
-// 8 value heads of 128 x 64, 72 and 69 (2 and 5); 3 sequences of 777 tokens, 5 heads of 64 x 128
-// fp32, 33 and 28 (2 and 1).
+// Of the lengths that fill 1 to 8 rounds of workgroups and the shortest ones, that of the least time
+// by figures in us as measured: a chunk in the last launch 4.1 (bf16: memory and LDS; a quarter less
+// where few CUs are busy) or 14 (fp32, 128 x 128: matrix cores), in the first 2 or 5.5; a
+// workgroup's own start 5, a state that it reads for it 0.7; the first launch 5, the join 6, 0.065
+// per segment of a sequence and the states that it reads and writes.  Segments of one length run in
+// whole rounds of an XCD; those of packed sequences in whatever order, a part of one behind the mean.
+//
+// Measured (us; with the forward pass's rounds alone and two chunks at least, and so): backward, 2
+// sequences of 2048 tokens, 16 heads of 128 bf16, 98 and 89 (4 and 7 chunks); 5003 packed tokens, 8
+// value heads of 128 x 64, 72 and 69 (2 and 5); 3 sequences of 777 tokens, 5 heads of 64 x 128 fp32,
+// 33 and 28 (2 and 1); one of 32768, one head of 64 bf16 46 and 39 (2 and 3; with 5 it would take 36).
 int64_t segment_chunks(int64_t chunks, int64_t units, int64_t packed, int G, int passes, int K, int V, bool fp32) {
   int64_t best = chunks;
   double least = 1e300;
   const double ends = (double)std::min<int64_t>(packed, 32), area = K * V / 16384.;
-  const double chunk = fp32 ? 3.5 + 10.5 * area : 4.1, first = fp32 ? 4. * area : 2.;
+  const double chunk = fp32 ? 3.5 + 10.5 * area : 4.1, first = fp32 ? 1.5 + 4. * area : 2.;
   const int sums = passes > 1 ? 2 : 1;  // kinds of states
   const double row = (double)units * passes / 256.;
-  for (int rounds = 0; rounds <= 8; ++rounds) {
-    // segments per row of chunks that fill so many rounds, or one
-    const int64_t fill = std::max<int64_t>((int64_t)(rounds / row - 0.5 * ends), 1);
-    const int64_t len = ceil_div(chunks, fill), n = ceil_div(chunks, len);
+  for (int i = 0; i <= 16; ++i) {
+    // as many segments per row of chunks as fill 0 (one segment) to 8 rounds; 1 to 8 chunks each
+    const int64_t fill = std::max<int64_t>((int64_t)(i / row - 0.5 * ends), 1);
+    const int64_t len = i <= 8 ? ceil_div(chunks, fill) : std::min<int64_t>(i - 8, chunks), n = ceil_div(chunks, len);
     const double start = 5. + 0.7 * area * (n == 1 ? 0 : n <= kSumMost ? n : 2);
     const double wgs = packed ? row * (n + ends) : ceil_div(units / G * n, 8) * G * passes / 32.;
     const double one = len * chunk, whole = std::floor(wgs);
@@ -62,8 +64,8 @@ int64_t segment_chunks(int64_t chunks, int64_t units, int64_t packed, int G, int
     else if (packed) cost = row * chunks * chunk + wgs * start + 0.3 * (one + start);
     else cost = whole * (one + start) + (wgs > whole ? one * (0.75 + 0.25 * (wgs - whole)) + start : 0.);
     const double states = units * (n + 0.5 * ends) * sums;
-    if (n > 1) cost += 3. + len * first * std::max(1., (states - units * sums) / 256.);
-    if (n > kSumMost) cost += 3. + states * area * (16384. * 4 * 3 / 5e6);
+    if (n > 1) cost += 5. + len * first * std::max(1., (states - units * sums) / 256.);
+    if (n > kSumMost) cost += 6. + 0.065 * n / std::max(ends, 1.) + states * area * (16384. * 4 * 3 / 5e6);
     if (cost < least) {
       least = cost;
       best = len;

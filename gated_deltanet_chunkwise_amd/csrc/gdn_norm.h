@@ -13,6 +13,11 @@
 // sums over all rows: a lane keeps its channels' sums over the rows that its workgroup walks,
 // the workgroup writes them to its row of `partial`, and a second kernel adds those rows, in a
 // fixed order.
+//
+// Measured (us and TB/s of a pass; 5.2 is a copy's, more comes from the caches), bf16: gated norm of
+// B=4, T=8192, 16 heads of 128: 74 and 5.4; of a token of 64 sequences 3.0 (a launch).  Its backward
+// pass, B=2, T=2048: 18.5 and 4.5, with 4.6 of sums.  Residual norm, T=5003, C=1000 fp32: 13.8 and
+// 5.8; backward, B=4, T=4096, C=2048: 78 and 5.2, with 4.8 of sums.
 #pragma once
 #include "gdn_layer.h"
 
@@ -21,8 +26,9 @@ namespace gdn {
 enum { kGateNone = 0, kGateAfter = 1, kGateFirst = 2 };
 
 // VEC channels of a row as loaded.  Rows of any width are read and written 16 bytes at a time: the
-// device takes such accesses at any element's address, and only the row's last vector, where
-// `left` channels are fewer than VEC, is put together (zeros behind them).
+// device takes such accesses at any element's address, and only the row's last vector, where `left`
+// channels are fewer than VEC, is put together, zeros behind them (gated norm's backward pass over
+// 8M channels in bf16 rows of 2049: 39 us, by single channels 961).
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 template <int BYTES> struct RawBytes;
 template <> struct RawBytes<32> { u32x4 a, b; };

@@ -583,8 +583,9 @@ gdn_status_t gdn_scan_bwd(const gdn_scan_params_t *p, const void *x, const uint8
  * row of its sequence and head from the start of its chunk on.
  * Alignment: rows (pointers and strides) and states 16 bytes, log_decay 4, cu_seqlens 8,
  * workspace 256.  B * T below 2^31 - 4096.  Errors as for gdn_fwd, all checked before
- * anything is enqueued; GDN_ERR_UNSUPPORTED for another K or V, and for sizes that would take
- * 2^32 threads or more in one launch.  Outputs must not overlap inputs or each other
+ * anything is enqueued; GDN_ERR_UNSUPPORTED for another K or V, for rows (q, k, v or o) 2^24
+ * elements or more apart, and for sizes that would take 2^32 threads or more in one launch.
+ * Outputs must not overlap inputs or each other
  * (gdn_linattn_decode: new_state may be state).  The same call gives the same bits.
  * Enqueued on `stream`; nothing is allocated. */
 typedef struct {
@@ -647,8 +648,7 @@ gdn_status_t gdn_linattn_bwd(const gdn_linattn_params_t *p, const void *q, const
  * All arithmetic is fp32 and every output is rounded once: h is the norm of s as it was
  * before new_residual was rounded.  dtype: GDN_F32 or GDN_BF16.  D, C 1 to 16384 and fewer
  * than 2^31 - 65536 rows (GDN_ERR_UNSUPPORTED otherwise); eps >= 0 (GDN_ERR_SHAPE).
- * Alignment: element size (rows that split into 16 bytes, weights included, are faster);
- * workspace 256.  Errors as for gdn_fwd, all checked before anything is enqueued.  Outputs
+ * Alignment: element size (rows of whole 16 bytes are faster); workspace 256.  Errors as for gdn_fwd, all checked before anything is enqueued.  Outputs
  * must not overlap inputs or each other.  The same call gives the same bits.  Enqueued on
  * `stream`; nothing is allocated. */
 typedef struct {
