@@ -1,6 +1,6 @@
 """MI355X (gfx950) Gated DeltaNet chunkwise forward and backward passes, and the layer
-operators around them: short causal convolution, selective state space scan and 8-bit
-activation checkpoints.
+operators around them: short causal convolution, selective state space scan, linear
+attention with a decay per head, the norms around a block and 8-bit activation checkpoints.
 
 Thin Python binding of libgdn.so (C ABI in include/gdn.h).  It only marshals
 arguments: every step of every pass runs in the library's HIP kernels.
