@@ -245,15 +245,22 @@ template <typename E, int D, int THREADS> struct AttnTile {
 // have; two parts leave 2^-17 (states that only ever meet bf16 operands), three 2^-25.
 template <int NP>
 __device__ __forceinline__ void weighted_parts(const Frag<bf16>& c, const float (&w)[8], Frag<bf16> (&out)[NP]) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const u32x4 x = __builtin_bit_cast(u32x4, c.x);
+  u32x4 part[NP];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float f = (float)c.x[i] * w[i];
+  for (int i = 0; i < 4; ++i) {  // two at a time, which one instruction rounds
+    float lo = __uint_as_float(x[i] << 16) * w[2 * i], hi = __uint_as_float(x[i] & 0xffff0000u) * w[2 * i + 1];
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-      out[p].x[i] = (bf16)f;
-      f -= (float)out[p].x[i];
+      part[p][i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+      lo -= __uint_as_float(part[p][i] << 16);
+      hi -= __uint_as_float(part[p][i] & 0xffff0000u);
     }
   }
+#pragma unroll
+  for (int p = 0; p < NP; ++p) out[p].x = __builtin_bit_cast(bf16x8, part[p]);
 }
 template <int NP>
 __device__ __forceinline__ void weighted_parts(const Frag<float>& c, const float (&w)[8], Frag<float> (&out)[NP]) {
