@@ -36,11 +36,12 @@
 // outputs (64 KB per workgroup: 4.1 TB/s, where a copy from memory reaches 5.2), with 64 or fewer
 // 3.2, of which a seventh is matrix instructions and most is LDS: every wave reads all rows of a and,
 // transposed at half rate, of b.  A workgroup's start takes 5 us before its first chunk.
-//     B=2, T=2048, 16 heads: outputs 26 us, what segments add 14 (backward 67 and 25)
-//     32768 packed tokens, 16 value heads: 161 and 64, the join 12
+//     B=2, T=2048, 16 heads: outputs 26 us, what segments add 13 (backward 68 and 24)
+//     32768 packed tokens, 16 value heads: 160 and 60, the join 12
 // Tried and slower: four waves of 32 columns, two workgroups per CU (43 to 48 us for the first shape,
 // 41 with eight of 16); loads two chunks ahead (44; backward 111 for 99); the backward pass's three
-// passes next to one another in the grid (102 for 97).  No faster: c's columns held from the
+// passes next to one another in the grid (102 for 97); segments' sums by waves of 32 columns and half
+// of the rows (packed 243 for 225).  No faster: c's columns held from the
 // outputs' product for the update.
 #pragma once
 #include <type_traits>
@@ -242,7 +243,9 @@ template <typename E, int D, int THREADS> struct AttnTile {
 
 // c_s w_s as a sum of NP fragments.  A bf16 operand of the state's update is c_s (8 bits)
 // times an fp32 weight: one bf16 would leave 2^-9 of every state, which fp32 states must not
-// have; two parts leave 2^-17 (states that only ever meet bf16 operands), three 2^-25.
+// have; two parts leave 2^-17 (states that only ever meet bf16 operands), three 2^-25.  They are
+// rounded two elements at a time: the vector unit is half busy here (packed, as above: 225 us one at a
+// time, 219 so).
 template <int NP>
 __device__ __forceinline__ void weighted_parts(const Frag<bf16>& c, const float (&w)[8], Frag<bf16> (&out)[NP]) {
   typedef float f32x2 __attribute__((ext_vector_type(2)));
