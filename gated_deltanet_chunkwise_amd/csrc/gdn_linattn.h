@@ -243,7 +243,8 @@ template <typename E, int D, int THREADS> struct AttnTile {
 
 // c_s w_s as a sum of NP fragments.  A bf16 operand of the state's update is c_s (8 bits)
 // times an fp32 weight: one bf16 would leave 2^-9 of every state, which fp32 states must not
-// have; two parts leave 2^-17 (states that only ever meet bf16 operands), three 2^-25.  They are
+// have; two parts leave 2^-17 (as operand_parts does of a state that only ever meets bf16 rows),
+// three 2^-25.  They are
 // rounded two elements at a time: the vector unit is half busy here (packed, as above: 225 us one at a
 // time, 219 so).
 template <int NP>
@@ -272,6 +273,31 @@ __device__ __forceinline__ void weighted_parts(const Frag<float>& c, const float
   for (int i = 0; i < 4; ++i) {
     out[0].lo[i] = c.lo[i] * w[i];
     out[0].hi[i] = c.hi[i] * w[i + 4];
+  }
+}
+
+// What fp32 values become as operands (a chunk's weighted products, and the state where it meets
+// rows), as a sum of NP fragments.  Of bf16 there are two, which leave 2^-17, so that a result's own
+// rounding is the one that it shows: with one part results were off by 0.0023 where that rounding
+// alone is 0.0017.  Times with one and with two (us): B=2, T=2048, 16 heads of 128 37 and 40, its
+// backward pass 87 and 96; 32768 packed tokens, 16 value heads 219 and 244.
+template <typename E> constexpr int attn_parts() { return sizeof(E) == 2 ? 2 : 1; }
+template <typename E, int NP> __device__ __forceinline__ void operand_parts(f32x4 x, Quad<E> (&out)[NP]) {
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    out[p] = make_quad<E>(x);
+    if (p + 1 < NP) x -= quad_f32(out[p]);
+  }
+}
+// The same of two tiles of a state, which are a fragment's halves.
+template <typename E, int NP> __device__ __forceinline__ void state_parts(f32x4 d0, f32x4 d1, Frag<E> (&out)[NP]) {
+  Quad<E> lo[NP], hi[NP];
+  operand_parts(d0, lo);
+  operand_parts(d1, hi);
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    if constexpr (sizeof(E) == 2) out[p] = {__builtin_shufflevector(lo[p].x, hi[p].x, 0, 1, 2, 3, 4, 5, 6, 7)};
+    else out[p] = {lo[p].x, hi[p].x};
   }
 }
 
@@ -346,7 +372,7 @@ template <typename E, typename OT, int KD, int VD, int THREADS> struct AttnLds<E
   AttnTile<E, VD, THREADS> c;
   AttnTile<E, KD, THREADS> a;
   AttnTile<OT, VD, THREADS> o;
-  AttnTile<E, kChunk, THREADS> p;
+  AttnTile<E, kChunk, THREADS> p[attn_parts<E>()];
   float update[kChunk], inter[kChunk], gap[2 * kChunk];  // gap: 0 for rows that are not seen
 };
 
@@ -364,7 +390,7 @@ __device__ __forceinline__ void attn_pass(const AttnGeo& geo, int block, const A
   const AttnState& st = x.st;
   OT* out = static_cast<OT*>(x.out);
   const float s_intra = x.s_intra, s_inter = x.s_inter, s_update = x.s_update;
-  constexpr int KT = KD / 16, TT = kChunk / 16, WAVES = VD / 16;
+  constexpr int KT = KD / 16, TT = kChunk / 16, WAVES = VD / 16, NP = attn_parts<E>();
   using Lds = AttnLds<E, OT, KD, VD, THREADS, OUT>;
   using KTile = AttnTile<E, KD, THREADS>;
   using VTile = AttnTile<E, VD, THREADS>;
@@ -543,7 +569,10 @@ __device__ __forceinline__ void attn_pass(const AttnGeo& geo, int block, const A
               const int gap = apart + 16 * j + r;
               p[j][r] = (REV ? gap >= 0 && 32 * sb + 4 * g + 16 * j + r < n : gap <= 0) ? p[j][r] * w[j][r] : 0.f;
             }
-            *reinterpret_cast<Quad<E>*>(L.p.at(t, 32 * sb + 16 * j + 4 * g)) = make_quad<E>(p[j]);
+            Quad<E> part[NP];
+            operand_parts(p[j], part);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) *reinterpret_cast<Quad<E>*>(L.p[i].at(t, 32 * sb + 16 * j + 4 * g)) = part[i];
           }
           ATTN_PHASE;
         }
@@ -555,11 +584,16 @@ __device__ __forceinline__ void attn_pass(const AttnGeo& geo, int block, const A
       for (int tt = 0; tt < TT; ++tt) acc[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int kb = 0; kb < KD / 32; ++kb) {
-        const Frag<E> h = frag_from_tiles<E>(H[2 * kb], H[2 * kb + 1]);
+        Frag<E> h[NP];
+        state_parts(H[2 * kb], H[2 * kb + 1], h);
 #pragma unroll
-        for (int tt = 0; tt < TT; ++tt) mma_k32(acc[tt], h, L.a.of_row(16 * tt + m, kb));
+        for (int tt = 0; tt < TT; ++tt) {
+          const Frag<E> q = L.a.of_row(16 * tt + m, kb);
+#pragma unroll
+          for (int i = 0; i < NP; ++i) mma_k32(acc[tt], h[i], q);
+        }
       }
-      attn_interleave<E, 6, (KD / 32) * TT, 1, 1>();
+      attn_interleave<E, 6, (KD / 32) * TT * NP, 1, 1>();
       ATTN_PHASE;
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) acc[tt] *= L.inter[16 * tt + m];
@@ -572,10 +606,11 @@ __device__ __forceinline__ void attn_pass(const AttnGeo& geo, int block, const A
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt) {
           if (REV ? 2 * sb + 1 < tt : 2 * sb > tt) continue;
-          mma_k32(acc[tt], v, L.p.of_row(16 * tt + m, sb));
+#pragma unroll
+          for (int i = 0; i < NP; ++i) mma_k32(acc[tt], v, L.p[i].of_row(16 * tt + m, sb));
         }
       }
-      attn_interleave<E, 10, 1, 6, 0>();
+      attn_interleave<E, 8, 12, 1, 1>();
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt)
         *reinterpret_cast<Quad<OT>*>(L.o.at(16 * tt + m, col0 + 4 * g)) = make_quad<OT>(acc[tt]);

@@ -576,9 +576,10 @@ gdn_status_t gdn_scan_bwd(const gdn_scan_params_t *p, const void *x, const uint8
  *   initial_state, final_state  [sequences][HV][K][V] fp32 or NULL
  *   o             [B][T][HV][V] contiguous, dtype, written
  *   workspace     gdn_linattn_fwd_workspace_size() bytes
- * dtype: GDN_F32 or GDN_BF16.  bf16: products of bf16 operands summed in fp32; a chunk's
- * weighted products q.k, and the state where it meets q, are rounded to bf16; the states
- * themselves are held and returned to fp32's precision.  An infinity or NaN in q reaches
+ * dtype: GDN_F32 or GDN_BF16.  bf16: products of bf16 operands summed in fp32, the results
+ * rounded to bf16 once; a chunk's weighted products q.k, and the state where it meets q, are
+ * taken as sums of two bf16 parts, to 2^-17 of themselves; the states that are returned have
+ * fp32's precision.  An infinity or NaN in q reaches
  * its own row of o (and in the gradients what depends on it); one in k or v reaches every
  * row of its sequence and head from the start of its chunk on.
  * Alignment: rows (pointers and strides) and states 16 bytes, log_decay 4, cu_seqlens 8,
