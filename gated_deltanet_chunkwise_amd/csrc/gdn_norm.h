@@ -250,6 +250,12 @@ __device__ __forceinline__ void norm_partials(float (&acc)[K][NV][VEC], float* _
   }
 }
 
+// The factor of a row's norm from its mean square.  Rows behind the last one (not live) hold zeros,
+// which without an eps have an infinite one: theirs is 0, so that what they add to the sums is 0.
+__device__ __forceinline__ float row_factor(float mean, const NormGeo& g, bool live) {
+  return live ? __builtin_amdgcn_rsqf(mean + g.eps) : 0.f;
+}
+
 template <typename E, int VEC, int LPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(norm_threads(LPR)) void gdn_gated_norm_bwd_kernel(
     NormGeo g, const E* __restrict__ x, const float* __restrict__ w, const E* __restrict__ z,
@@ -301,7 +307,7 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_gated_norm_bwd_kernel(
 #pragma unroll
       for (int j = 0; j < VEC; ++j) ss += u[i][j] * u[i][j];
     }
-    const float c = __builtin_amdgcn_rsqf(sum(ss) * inv + g.eps);
+    const float c = row_factor(sum(ss) * inv, g, live);
     // n = u c;  m = mean(n dn), dn = dy w (times the gate behind the norm)
     float dn[NV][VEC], m = 0.f;
 #pragma unroll
@@ -525,7 +531,7 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_residual_norm_bwd_kerne
 #pragma unroll
         for (int j = 0; j < VEC; ++j) ss += xf[j] * xf[j];
       }
-      cp = __builtin_amdgcn_rsqf(sum(ss) * inv + g.eps);
+      cp = row_factor(sum(ss) * inv, g, live);
     }
     float s[NV][VEC], ss = 0.f;
 #pragma unroll
@@ -542,7 +548,7 @@ __global__ __launch_bounds__(norm_threads(LPR)) void gdn_residual_norm_bwd_kerne
         ss += s[i][j] * s[i][j];
       }
     }
-    const float c = __builtin_amdgcn_rsqf(sum(ss) * inv + g.eps);
+    const float c = row_factor(sum(ss) * inv, g, live);
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {

@@ -648,8 +648,8 @@ gdn_status_t gdn_linattn_bwd(const gdn_linattn_params_t *p, const void *q, const
  *                 dense) and must not overlap it otherwise
  * All arithmetic is fp32 and every output is rounded once: h is the norm of s as it was
  * before new_residual was rounded.  The squares are fp32's too: a row beyond about 1e19
- * overflows its mean and is normed to 0, and with eps 0 one below about 1e-19 is not normed
- * rightly (nor one of zeros: 0 / 0).  dtype: GDN_F32 or GDN_BF16.  D, C 1 to 16384 and fewer
+ * overflows its mean and is normed to 0, and with eps below 1.2e-38 one below about 1e-19 is
+ * not normed rightly (nor one of zeros: 0 / 0).  dtype: GDN_F32 or GDN_BF16.  D, C 1 to 16384 and fewer
  * than 2^31 - 65536 rows (GDN_ERR_UNSUPPORTED otherwise); eps >= 0 (GDN_ERR_SHAPE).
  * Alignment: element size (rows of whole 16 bytes are faster); workspace 256.  Errors as for gdn_fwd, all checked before anything is enqueued.  Outputs
  * must not overlap inputs or each other.  The same call gives the same bits.  Enqueued on
