@@ -54,7 +54,7 @@ struct AttnGeo {
   int B, T, H, HV, G, N;  // N sequences; G = HV / H
   int chunks;             // chunks per segment
   int nseg;               // segments per sequence (without offsets)
-  int slots;              // segments in all, or (packed) an upper bound
+  int slots;              // segments in all, or (packed) an upper bound that counts empty sequences too
   const int64_t* cu;
   bool zero;              // rows of the output behind the last sequence are set to 0
 };
@@ -68,7 +68,7 @@ struct AttnRows {
 
 // What a pass does with the states.  The caller's are [sequences][HV][..] with element [i][j]
 // of a head (row as operand b, column as operand c) at i rs + j cs.  Those of segments are in
-// the workspace, [slots][HV] of them, in the order in which lanes hold them (state_place).
+// the workspace, [Segment::state][HV] of them, in the order in which lanes hold them (state_place).
 enum { kWholeSequence, kSumSegments, kJoined };
 struct AttnState {
   const float* start;  // or nullptr: zero
@@ -91,11 +91,23 @@ __device__ __forceinline__ float decay_power(float l2, int n) {
 // per segment): ceil((y - x) / L) <= floor(y / L) - floor(x / L) + 1 keeps the sequences'
 // slots apart, and no table has to be made on the device first; T / L + N slots hold all.
 // The search for n compares 64 offsets at a time.
+//
+// States in the workspace are those of sequences of several segments alone, whose x < y are more
+// than L apart: with f = floor(x / L), theirs are f + min(n, f) + i, which are apart as well (such a
+// sequence takes f a step further, and so min(n, f)) and below T / L + min(N, T / L), however many
+// short sequences there are.
 struct Segment {
   int n, i, count, t0, len;
+  int state;  // place of the segment's state, where the sequence has several
 
-  __device__ __forceinline__ static int seq_slot(const AttnGeo& g, int n) {
-    return (seq_offset(g.cu, n, g.T) / kChunk) / g.chunks + n;
+  __device__ __forceinline__ static int whole(const AttnGeo& g, int n) {
+    return (seq_offset(g.cu, n, g.T) / kChunk) / g.chunks;
+  }
+  __device__ __forceinline__ static int seq_slot(const AttnGeo& g, int n) { return whole(g, n) + n; }
+  // the place of a sequence's first state
+  __device__ __forceinline__ static int seq_state(const AttnGeo& g, int n) {
+    const int f = whole(g, n);
+    return f + min(n, f);
   }
   // False for a slot that no token is in: i == 0 then still tells a sequence without tokens.
   __device__ __forceinline__ bool find(const AttnGeo& g, int slot) {
@@ -106,6 +118,7 @@ struct Segment {
       i = slot - n * g.nseg;
       start = (int64_t)n * g.T;
       end = start + g.T;
+      state = slot;
     } else {
       int lo = 0, hi = g.N;  // slot(lo) <= slot is taken for granted
       while (hi - lo > 1) {
@@ -119,7 +132,9 @@ struct Segment {
       n = __builtin_amdgcn_readfirstlane(lo);
       start = seq_offset(g.cu, n, g.T);
       end = max((int64_t)seq_offset(g.cu, n + 1, g.T), start);
-      i = slot - seq_slot(g, n);
+      const int f = whole(g, n);
+      i = slot - (f + n);
+      state = f + min(n, f) + i;
     }
     count = (int)((end - start + L - 1) / L);
     t0 = len = 0;
@@ -448,7 +463,7 @@ __device__ __forceinline__ void attn_pass(const AttnGeo& geo, int block, const A
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt) H[kt] = f32x4{0.f, 0.f, 0.f, 0.f};
   if constexpr (OUT) {
-    const bool joined = st.mode == kJoined && tokens;
+    const bool joined = st.mode == kJoined && seg.count > 1;
     if (st.start && !joined) {
       const float* s = st.start + ((int64_t)seg.n * geo.HV + hv) * (KD * VD) + (col0 + m) * st.cs;
 #pragma unroll
@@ -465,7 +480,7 @@ __device__ __forceinline__ void attn_pass(const AttnGeo& geo, int block, const A
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) {
         const int k = min(j0 + j, sums - 1);
-        const int at = joined ? slot : REV ? slot + before - k : slot - before + k;
+        const int at = joined ? seg.state : REV ? seg.state + before - k : seg.state - before + k;
         const float* w = st.w + ((int64_t)at * geo.HV + hv) * (KD * VD);
         if (!st.transposed) {
 #pragma unroll
@@ -645,7 +660,7 @@ __device__ __forceinline__ void attn_pass(const AttnGeo& geo, int block, const A
         for (int r = 0; r < 4; ++r) s[(state_row(kt) + r) * st.rs] = H[kt][r];
     }
   } else if (owner) {
-    float* w = st.w + ((int64_t)slot * geo.HV + hv) * (KD * VD);
+    float* w = st.w + ((int64_t)seg.state * geo.HV + hv) * (KD * VD);
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(w + state_place(kt, col0 / 16, VD / 16)) = H[kt];
   }
@@ -677,11 +692,13 @@ __global__ __launch_bounds__(attn_threads(K > V ? K : V), (attn_waves<E, (K > V 
   else attn_pass<E, E, K, V, THREADS, true, OUT>(geo, block, v, log_decay, smem);
 }
 
-// The starts of sequences' segments: per sequence, head and four elements of the state, in the
-// segments' order (REV: from the last),  w[segment] <- cur;  cur <- a^len cur + (what
-// w[segment] held),  from `start` (or 0).  Loads run kAttnAhead segments ahead (backward, 5003
+// The starts of the segments of sequences that have several: per sequence, head and four elements
+// of the state, in the segments' order (REV: from the last),  w[segment] <- cur;  cur <- a^len cur +
+// (what w[segment] held),  from `start` (or 0).  Loads run kAttnAhead segments ahead (backward, 5003
 // packed tokens, 8 value heads of 128 x 64 in segments of two chunks: 8 ahead 76.8 us, 16 74.9, 32
-// 76.1).  Bound by the states' bytes: 80 MB read and written in 12 us at 32768 tokens, 16 heads.
+// 76.1).  Bound by the states' bytes: 75 MB read and written in 10 us at 32768 tokens, 16 heads.
+// Packed sequences of one segment are passed over: their states would go to the workspace and back
+// (1000 of 64 tokens, 16 heads of 128 bf16: 1272 and 887 us a call, backward 3471 and 2673).
 constexpr int kAttnAhead = 16;
 
 template <int KD, int VD, bool REV>
@@ -694,18 +711,19 @@ __device__ __forceinline__ void attn_join(const AttnGeo& geo, const float* __res
   const int hv = unit % geo.HV, n = unit / geo.HV;
   const int tile = part * 4 + (threadIdx.x >> 6), at = (tile * 64 + lane_id()) * 4;
   const float l2 = log_decay[hv] * kLog2e;
+  const int64_t L = (int64_t)geo.chunks * kChunk;
   int64_t t0, t1;
   int first;
   if (geo.cu) {
     t0 = seq_offset(geo.cu, n, geo.T);
     t1 = max((int64_t)seq_offset(geo.cu, n + 1, geo.T), t0);
-    first = Segment::seq_slot(geo, n);
+    if (t1 - t0 <= L) return;  // (its one segment starts from `start` itself)
+    first = Segment::seq_state(geo, n);
   } else {
     t0 = 0;
     t1 = geo.T;
     first = n * geo.nseg;
   }
-  const int64_t L = (int64_t)geo.chunks * kChunk;
   const int count = (int)((t1 - t0 + L - 1) / L);
   f32x4 cur = {0.f, 0.f, 0.f, 0.f};
   if (start) {

@@ -23,6 +23,7 @@ struct AttnPlan {
   int64_t tok;  // tokens in all
   bool packed;
   bool one;     // no sequence has more than one segment
+  int64_t states;  // of segments, per head, in the workspace
   float scale;
   int64_t ldq, ldk, ldv;
 };
@@ -31,8 +32,8 @@ struct AttnPlan {
 // row of them per head that holds `packed` sequences; `passes` in one launch (3 backwards); G heads
 // share a key head.  256 CUs in 8 XCDs are taken for granted, so that the workspace is the same on
 // every device; a CU runs one workgroup of the last launch at a time.  Packed sequences end with a
-// short segment each; no more than 32 are counted, since offsets may be padded with empty ones,
-// which cost nothing.
+// short segment each; no more than 32 are counted, since offsets may be padded with empty ones, which
+// cost a workgroup per head that ends at once.
 //
 // Of the lengths that fill 1 to 8 rounds of workgroups and the shortest ones, that of the least time
 // by figures in us as measured: a chunk in the last launch 4.1 (bf16: memory and LDS; a quarter less
@@ -113,15 +114,14 @@ gdn_status_t attn_sizes(const gdn_linattn_params_t* p, bool packed, int passes, 
   if (slots > INT32_MAX) return GDN_ERR_UNSUPPORTED;
   g.slots = (int)slots;
   pl.one = g.nseg == 1;
+  const int64_t whole = (int64_t)g.T / kChunk / g.chunks;
+  pl.states = pl.one || pl.tok == 0 ? 0 : packed ? whole + std::min<int64_t>(g.N, whole) : slots;  // (Segment)
   *out = pl;
   return GDN_OK;
 }
 
 // Bytes of the segments' states; workspaces of both passes.
-size_t attn_states(const AttnPlan& pl) {
-  if (pl.one || pl.tok == 0) return 0;
-  return align_up((size_t)pl.geo.slots * pl.geo.HV * pl.K * pl.V * 4);
-}
+size_t attn_states(const AttnPlan& pl) { return align_up((size_t)pl.states * pl.geo.HV * pl.K * pl.V * 4); }
 size_t attn_partial(const AttnPlan& pl) {
   return pl.geo.G == 1 ? 0 : align_up((size_t)pl.tok * pl.geo.HV * pl.K * 4 * 2);
 }
