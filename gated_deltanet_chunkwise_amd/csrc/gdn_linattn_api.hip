@@ -128,10 +128,6 @@ size_t attn_partial(const AttnPlan& pl) {
 
 int64_t attn_blocks(const AttnGeo& g) { return ceil_div((int64_t)g.slots * g.H, 8) * 8 * g.G; }
 int64_t join_blocks(const AttnPlan& pl) { return (int64_t)pl.geo.N * pl.geo.HV * (pl.K * pl.V / 1024); }
-bool attn_fits(const AttnPlan& pl) {
-  return grid_fits(attn_blocks(pl.geo) * 3, gdn::attn_threads(128)) &&
-         grid_fits(join_blocks(pl), 256);
-}
 
 // `f` for widths KD and VD.
 template <typename F> hipError_t sized(int KD, int VD, F&& f) {
@@ -152,6 +148,13 @@ hipError_t pass_on(const AttnPlan& pl, const float* start, float* end, hipStream
 // How segments get their starts.
 int attn_mode(const AttnPlan& pl) {
   return pl.one ? gdn::kWholeSequence : pl.geo.nseg <= kSumMost ? gdn::kSumSegments : gdn::kJoined;
+}
+
+// Whether the launches of a call with `passes` in its last one (3 backwards) fit the grid.
+bool attn_fits(const AttnPlan& pl, int passes) {
+  if (pl.tok == 0) return true;
+  return grid_fits(attn_blocks(pl.geo) * passes, gdn::attn_threads(passes == 1 ? pl.V : std::max(pl.K, pl.V))) &&
+         (attn_mode(pl) != gdn::kJoined || grid_fits(join_blocks(pl), 256));
 }
 
 template <typename E>
@@ -267,7 +270,7 @@ gdn_status_t gdn_linattn_fwd(const gdn_linattn_params_t* p, const void* q, const
       !aligned(cu_seqlens, 8) || !aligned(workspace, kWsAlign))
     return GDN_ERR_ALIGN;
   if (workspace_bytes < need) return GDN_ERR_WORKSPACE;
-  if (!attn_fits(pl)) return GDN_ERR_UNSUPPORTED;
+  if (!attn_fits(pl, 1)) return GDN_ERR_UNSUPPORTED;
   pl.geo.cu = cu_seqlens;
   hipStream_t s = static_cast<hipStream_t>(stream);
   return pl.esz == 2 ? fwd_run<gdn::bf16>(pl, q, k, v, log_decay, initial_state, o, final_state, workspace, s)
@@ -293,7 +296,7 @@ gdn_status_t gdn_linattn_bwd(const gdn_linattn_params_t* p, const void* q, const
                pl.esz) || !aligned(log_decay, 4) || !aligned(cu_seqlens, 8) || !aligned(workspace, kWsAlign))
     return GDN_ERR_ALIGN;
   if (workspace_bytes < need) return GDN_ERR_WORKSPACE;
-  if (!attn_fits(pl)) return GDN_ERR_UNSUPPORTED;
+  if (!attn_fits(pl, 3)) return GDN_ERR_UNSUPPORTED;
   pl.geo.cu = cu_seqlens;
   const AttnBwd x{q, k, v, log_decay, initial_state, d_o, d_final_state, dq, dk, dv, d_initial_state};
   hipStream_t s = static_cast<hipStream_t>(stream);
