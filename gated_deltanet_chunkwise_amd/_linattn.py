@@ -179,10 +179,11 @@ def _function():
 def linear_attention(q, k, v, log_decay, cu_seqlens=None, initial_state=None, scale=1.0, checkpoint_bits=None):
     """linear_attn_fwd() as a differentiable torch op: returns (o, final_state); gradients
     reach q, k, v and initial_state through gdn_linattn_bwd, which forms the states again.
-    log_decay is a constant of the model: one that requires a gradient is refused.
+    log_decay is a constant of the model: one that requires a gradient is refused where gradients
+    are recorded.
     checkpoint_bits=8 keeps q, k and v for the backward pass as 8-bit checkpoints (pack8): the
     gradients are then those at the values the checkpoints stand for."""
-    if log_decay.requires_grad:
+    if log_decay.requires_grad and _torch().is_grad_enabled():
         raise ValueError("log_decay takes no gradient: pass it detached")
     bits = _layers.kept_bits(checkpoint_bits, q, k, v, initial_state)
     return _function().apply(q, k, v, log_decay, cu_seqlens, initial_state, scale, bits)
