@@ -208,6 +208,13 @@ def _check_placement(named, device):
             raise ValueError("%s must be contiguous" % name)
 
 
+def _gradient(t, dtype):
+    """A gradient as the library takes it: dense, of that dtype and on 16 bytes.  torch may hand
+    over expanded or strided ones, or part of a longer tensor from any element on."""
+    t = t.to(dtype).contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _check_forward_inputs(plan, q, k, v, g_raw, beta, A_log, dt_bias, cu_seqlens,
                           initial_state):
     """The forward inputs against a plan's sizes and dtype (include/gdn.h layouts)."""

@@ -8,7 +8,7 @@ current stream of the tensors' GPU.
 import ctypes
 
 from . import _layers
-from ._binding import _dtype_code
+from ._binding import _dtype_code, _gradient
 from ._layers import GDN_ZERO_REST, _call, _fit, _lib, _like, _need, _on, _p, _place, _row_stride, _sequences, _torch, _workspace, _written
 
 
@@ -167,8 +167,8 @@ def _function():
                 qd, qs, kd, ks, vd, vs, log_decay, cu, h0 = ctx.saved_tensors
                 q, k, v = (t if sc is None else _layers.unpack8(_layers.Packed8(t, sc, ctx.dtype))
                            for t, sc in ((qd, qs), (kd, ks), (vd, vs)))
-                d_o = torch.zeros(v.shape, dtype=ctx.dtype, device=v.device) if d_o is None else d_o.to(ctx.dtype).contiguous()
-                d_fin = None if d_fin is None else d_fin.to(torch.float32).contiguous()
+                d_o = torch.zeros(v.shape, dtype=ctx.dtype, device=v.device) if d_o is None else _gradient(d_o, ctx.dtype)
+                d_fin = None if d_fin is None else _gradient(d_fin, torch.float32)
                 g = linear_attn_bwd(q, k, v, log_decay, d_o, d_fin, cu, h0, ctx.scale)
                 return (g["dq"], g["dk"], g["dv"], None, None, g["dh0"] if h0 is not None else None, None, None)
 
