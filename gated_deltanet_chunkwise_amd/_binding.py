@@ -615,13 +615,11 @@ def _gated_delta_rule_fn():
                            for t, sc in ((qd, qs), (kd, ks), (vd, vs)))
                 B, T = q.shape[0], q.shape[1]
                 HV, V = v.shape[2], v.shape[3]
-                # torch may hand over expanded or strided gradients; the library
-                # takes dense row-major buffers
                 if d_o is None:
                     d_o = torch.zeros((B, T, HV, V), dtype=q.dtype, device=q.device)
-                d_o = d_o.to(q.dtype).contiguous()
+                d_o = _gradient(d_o, q.dtype)
                 if d_fin is not None:
-                    d_fin = d_fin.to(torch.float32).contiguous()
+                    d_fin = _gradient(d_fin, torch.float32)
                 gr = bwd(q, k, v, g_raw, beta, A_log, dt_bias, d_o, d_fin,
                          cu_seqlens=cu_seqlens, initial_state=h0, scale=ctx.scale)
                 return (gr["dq"], gr["dk"], gr["dv"], gr["dg_raw"], gr["dbeta"], gr["dA_log"],
