@@ -32,12 +32,17 @@
 // -- or, where sequences have many segments, a launch in between forms the starts.  Where the
 // heads and sequences alone fill the device there is one segment per sequence and one launch.
 //
-// Measured, bf16, 128 x 128.  With 256 workgroups a chunk takes 4.1 us of the launch that forms
-// outputs (64 KB per workgroup: 4.1 TB/s, where a copy from memory reaches 5.2), with 64 or fewer
-// 3.2, of which a seventh is matrix instructions and most is LDS: every wave reads all rows of a and,
-// transposed at half rate, of b.  A workgroup's start takes 5 us before its first chunk.
-//     B=2, T=2048, 16 heads: outputs 26 us, what segments add 13 (backward 68 and 24)
-//     32768 packed tokens, 16 value heads: 160 and 60, the join 12
+// Measured, bf16, 128 x 128.  With 256 workgroups a chunk takes 4.6 us of the launch that forms
+// outputs (64 KB per workgroup: 3.6 TB/s, where a copy from memory reaches 5.2; 5.0 where final states
+// are asked for, in three parts), with 64 3.8.  Matrix instructions are a fifth to a quarter of it;
+// the rest is reads of LDS, barriers and waits: every wave reads all rows of a and, transposed at half
+// rate, of b.  Of 64 x 64 a chunk takes 2.1.  A workgroup's start, and the states that it writes, take 4
+// to 7 us.
+//     B=2, T=2048, 16 heads: outputs 30 us, what segments add 13 (backward 76 and 24)
+//     32768 packed tokens, 16 value heads: 190 and 61, the join 10
+// The comparisons that follow, and those at weighted_parts, attn_join and segment_chunks, were made
+// with one bf16 part of what operand_parts now gives in two, which takes 7 to 12 % less time on
+// either side of each.
 // Tried and slower: four waves of 32 columns, two workgroups per CU (43 to 48 us for the first shape,
 // 41 with eight of 16); loads two chunks ahead (44; backward 111 for 99); the backward pass's three
 // passes next to one another in the grid (102 for 97); segments' sums by waves of 32 columns and half
@@ -294,8 +299,9 @@ __device__ __forceinline__ void weighted_parts(const Frag<float>& c, const float
 // What fp32 values become as operands (a chunk's weighted products, and the state where it meets
 // rows), as a sum of NP fragments.  Of bf16 there are two, which leave 2^-17, so that a result's own
 // rounding is the one that it shows: with one part results were off by 0.0023 where that rounding
-// alone is 0.0017.  Times with one and with two (us): B=2, T=2048, 16 heads of 128 37 and 40, its
-// backward pass 87 and 96; 32768 packed tokens, 16 value heads 219 and 244.
+// alone is 0.0017.  Times with one and with two (us): B=2, T=2048, 16 heads of 128 38 and 40, its
+// backward pass 87 and 96; 32768 packed tokens, 16 value heads 220 and 245 (239 since the join passes
+// over single segments).
 template <typename E> constexpr int attn_parts() { return sizeof(E) == 2 ? 2 : 1; }
 template <typename E, int NP> __device__ __forceinline__ void operand_parts(f32x4 x, Quad<E> (&out)[NP]) {
 #pragma unroll

@@ -31,13 +31,17 @@ struct AttnPlan {
 // Chunks per segment, for sequences of `chunks` in `units` (sequence, head) pairs or, packed, one
 // row of them per head that holds `packed` sequences; `passes` in one launch (3 backwards); G heads
 // share a key head.  256 CUs in 8 XCDs are taken for granted, so that the workspace is the same on
-// every device; a CU runs one workgroup of the last launch at a time.  Packed sequences end with a
+// every device, and that a CU runs one workgroup of the last launch at a time: so it is but for bf16
+// 64 x 64, of which two or three fit, and the forward pass of 128 x 64, two, which the rounds below do
+// not count.  Packed sequences end with a
 // short segment each; no more than 32 are counted, since offsets may be padded with empty ones, which
 // cost a workgroup per head that ends at once.
 //
 // Of the lengths that fill 1 to 8 rounds of workgroups and the shortest ones, that of the least time
-// by figures in us as measured: a chunk in the last launch 4.1 (bf16: memory and LDS; a quarter less
-// where few CUs are busy) or 14 (fp32, 128 x 128: matrix cores), in the first 2 or 5.5; a
+// by figures in us as measured at widths of 128: a chunk in the last launch 4.1 (bf16, with operands in
+// one part; a quarter less where few CUs are busy) or 14 (fp32: matrix cores), in the first 2 or 5.5.
+// In two parts a bf16 chunk takes 4.6, with which one call in twenty would choose another length; of
+// narrower widths it takes down to 2.1, and lengths are then up to a fifth off the best.  Further: a
 // workgroup's own start 5, a state that it reads for it 0.7; the first launch 5, the join 6, 0.065
 // per segment of a sequence and the states that it reads and writes.  Segments of one length run in
 // whole rounds of an XCD; those of packed sequences in whatever order, a part of one behind the mean.

@@ -53,7 +53,9 @@ inline size_t esize(int32_t dtype) { return dtype == GDN_BF16 ? 2 : 4; }
 
 // f(VEC, LPR, NV, WHOLE) for the lanes and vectors of 16 bytes that hold a row: one vector per lane
 // as long as 1024 lanes hold the row, so that the three sums of a backward pass stay in registers,
-// then as few as do.  WHOLE: no vector is cut off by the row's end, which spares the passes the
+// then as few as do.  Beyond 8192 channels they do not stay there: the backward kernels spill 74 to
+// 176 registers (8M channels bf16 in rows of 8192 and of 16384: gated norm 36 and 84 us, residual norm
+// 49 and 159).  WHOLE: no vector is cut off by the row's end, which spares the passes the
 // question (backward of a residual norm, B=4, T=4096, C=2048 bf16: 89 us with it, 82 without).  Rows
 // below 16 bytes go by channels.
 template <typename E, typename F> hipError_t norm_shape(int D, F&& f) {
@@ -81,10 +83,12 @@ template <typename E, typename F> hipError_t norm_shape(int D, F&& f) {
 
 template <int LPR> int64_t rows_per_block() { return gdn::norm_threads(LPR) / LPR; }
 
-// Workgroups of a backward pass, each with a row of partial sums: as many as fill the device (256
-// CUs are taken for granted, so that the workspace is the same on every device).  us, 512, 768
-// and 1024: gated norm of B=2, T=2048, 16 heads of 128 bf16 23.3, 22.1 and 21.4; residual norm of
-// B=4, T=4096, C=2048 bf16 86, 88 and 104 (three workgroups of it fit a CU).
+// Workgroups of a backward pass, each with a row of partial sums: as many as fill the device at the
+// rows they were measured with (256 CUs are taken for granted, so that the workspace is the same on
+// every device).  us, 512, 768 and 1024: gated norm of B=2, T=2048, 16 heads of 128 bf16 23.3, 22.1 and
+// 21.4; residual norm of B=4, T=4096, C=2048 bf16 86, 88 and 104 (three workgroups of it fit a CU).
+// Wide rows take more than they need, since a workgroup of 1024 lanes fills a CU by itself: at 8192
+// channels the partial sums are as many bytes as the data of 8M channels.
 constexpr int64_t kGatedBlocks = 1024, kResidualBlocks = 512;
 int64_t norm_blocks(const NormPlan& pl, int64_t rpb, int64_t most) { return std::min(ceil_div(pl.geo.rows, rpb), most); }
 size_t norm_ws(const NormPlan& pl, int K, int64_t most) {

@@ -580,8 +580,9 @@ gdn_status_t gdn_scan_bwd(const gdn_scan_params_t *p, const void *x, const uint8
  * rounded to bf16 once; a chunk's weighted products q.k, and the state where it meets q, are
  * taken as sums of two bf16 parts, to 2^-17 of themselves; the states that are returned have
  * fp32's precision.  An infinity or NaN in q reaches
- * its own row of o (and in the gradients what depends on it); one in k or v reaches every
- * row of its sequence and head from the start of its chunk on.
+ * its own row of o (and in the gradients what depends on it); one in k or v may reach any
+ * row of its sequence and head from the start of its chunk on, so that rows which pad a
+ * sequence have to be finite.
  * Alignment: rows (pointers and strides) and states 16 bytes, log_decay 4, cu_seqlens 8,
  * workspace 256.  B * T below 2^31 - 4096.  Errors as for gdn_fwd, all checked before
  * anything is enqueued; GDN_ERR_UNSUPPORTED for another K or V, for rows (q, k, v or o) 2^24
