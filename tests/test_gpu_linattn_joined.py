@@ -77,3 +77,35 @@ def test_the_same_sequences_alone():
     a = gdn.linear_attn_bwd(row(g["q"]), row(g["k"]), row(g["v"]), ldc, row(s["d_o"]), s["d_fin"], cu, g["h0"])
     b = gdn.linear_attn_bwd(g["q"], g["k"], g["v"], ldc, s["d_o"], s["d_fin"], None, g["h0"])
     assert torch.equal(a["dh0"], b["dh0"]) and all(torch.equal(a[k], row(b[k])) for k in ("dq", "dk", "dv"))
+
+
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 64)])
+def test_a_captured_call_under_other_offsets(K, V):
+    """Segments, their states' places and which sequences have several follow from the offsets on the
+    device: a captured forward and backward pass is replayed under offsets of other lengths."""
+    T, N = 1500, 12
+    d, seeds, ld = bo.linattn_inputs(1, T, 1, 2, K, V, BF16, 43, N)
+    g, s, ldc = lo.cuda(d), lo.cuda(seeds), ld.cuda()
+
+    def passes(cu):
+        o, fin = gdn.linear_attn_fwd(g["q"], g["k"], g["v"], ldc, cu, g["h0"])
+        return [o, fin, *gdn.linear_attn_bwd(g["q"], g["k"], g["v"], ldc, s["d_o"], s["d_fin"], cu, g["h0"]).values()]
+    kinds = [[125] * 12, [1500] + [0] * 11, [0] * 11 + [1500], [64] * 12, [1, 0, 700, 0, 0, 65, 63, 64, 600, 0, 2, 0], [0] * 12]
+    cu = lo.offsets(kinds[0]).cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        passes(cu)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = passes(cu)
+    for lengths in kinds + kinds[::-1]:
+        cu.copy_(lo.offsets(lengths))
+        for t in out:
+            t.fill_(float("nan"))
+        graph.replay()
+        want = passes(cu.clone())
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), lengths
+        assert all(t.isfinite().all() for t in out)
